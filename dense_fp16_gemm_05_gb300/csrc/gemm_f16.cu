@@ -21,6 +21,7 @@
 #include "attention_launch.cuh"
 #include "gemm_fp8_launch.cuh"
 #include "gemm_launch.cuh"
+#include "gemm_mxfp4_launch.cuh"
 
 using namespace gemm_sm103;
 
@@ -231,6 +232,35 @@ int encode_matrix_u8(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t 
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fns.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+int encode_codes_u4(CUtensorMap *map, const void *ptr, int64_t rows, int64_t K, uint32_t box_rows)
+{
+    const DriverFns &fns = driver();
+    if (!fns.ok) return GEMM_ERR_CUDA;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>((K + 1) / 2), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(mx4_row_bytes(K))};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fns.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+int encode_scale_tiles(CUtensorMap *map, const void *ptr, int64_t rows, int64_t K, uint32_t box_k, uint32_t box_rows)
+{
+    const DriverFns &fns = driver();
+    if (!fns.ok) return GEMM_ERR_CUDA;
+    const cuuint64_t kt = static_cast<cuuint64_t>(mx4_k_tiles(K));
+    cuuint64_t dims[3] = {kMx4TileBytes / 4, kt, static_cast<cuuint64_t>(mx4_row_tiles(rows))};
+    cuuint64_t strides[2] = {kMx4TileBytes, kt * kMx4TileBytes};
+    cuuint32_t box[3] = {kMx4TileBytes / 4, box_k, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fns.encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
@@ -761,6 +791,103 @@ extern "C" int gemm_mxfp8_block_scaled(const void *A, const uint8_t *SA, const v
     a.status = status_word(dev.device);
     if (a.status == nullptr) return GEMM_ERR_CUDA;
     return launch_mxfp8(a);
+}
+
+namespace {
+
+// Bytes of an element of a gemm_f16_type, 0 for an unknown type.
+uint32_t type_bytes(int type)
+{
+    switch (type) {
+    case GEMM_TYPE_F16:
+    case GEMM_TYPE_BF16: return 2;
+    case GEMM_TYPE_F32: return 4;
+    default: return 0;
+    }
+}
+
+}  // namespace
+
+extern "C" int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, void *V, int64_t rows, int64_t K,
+                              int trans, void *stream)
+{
+    int st = check_sizes(rows, 0, K, 0);
+    if (st != GEMM_OK) return st;
+    const uint32_t el = type_bytes(type);
+    if (el == 0) return reject(GEMM_ERR_INVALID_ARG, "type is not a gemm_f16_type");
+    if (trans != 0 && trans != 1) return reject(GEMM_ERR_INVALID_ARG, "trans is not 0 or 1");
+    if (rows == 0 || K == 0) return GEMM_OK;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint64_t x_bytes = static_cast<uint64_t>(rows) * static_cast<uint64_t>(K) * el;
+    const uint64_t q_bytes = mx4_code_bytes(rows, K), s_bytes = mx4_scale_bytes(rows, K);
+    if ((st = check_device_buffer(X, x_bytes, dev.device, el)) != GEMM_OK) return st;
+    if ((st = check_device_buffer(Q, q_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer(S, s_bytes, dev.device)) != GEMM_OK) return st;
+    if (V != nullptr && (st = check_device_buffer(V, x_bytes, dev.device, el)) != GEMM_OK) return st;
+    if (ranges_overlap(Q, q_bytes, X, x_bytes) || ranges_overlap(S, s_bytes, X, x_bytes) ||
+        ranges_overlap(Q, q_bytes, S, s_bytes) ||
+        (V != nullptr && (ranges_overlap(V, x_bytes, X, x_bytes) || ranges_overlap(V, x_bytes, Q, q_bytes) ||
+                          ranges_overlap(V, x_bytes, S, s_bytes))))
+        return reject(GEMM_ERR_INVALID_ARG, "Q, S or V overlaps another buffer");
+    Mx4QuantArgs a;
+    a.X = X;
+    a.Q = Q;
+    a.S = S;
+    a.V = V;
+    a.rows = rows;
+    a.K = K;
+    a.type = type;
+    a.trans = trans;
+    a.sm_count = dev.sm_count;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_mxfp4_quantize(a);
+}
+
+extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C, int64_t M,
+                          int64_t N, int64_t K, int relu, void *stream)
+{
+    int st = check_sizes(M, N, K, relu);
+    if (st != GEMM_OK) return st;
+    if (M == 0 || N == 0) return GEMM_OK;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const uint64_t c_bytes = static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * 2u;
+    if ((st = check_device_buffer(C, c_bytes, dev.device)) != GEMM_OK) return st;
+    if (K == 0) {
+        // Empty sum: every output is R(+0) = +0.
+        if (cudaMemsetAsync(C, 0, c_bytes, s) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        return GEMM_OK;
+    }
+    if ((N % 8) != 0) return reject(GEMM_ERR_ALIGNMENT, "N is not a multiple of 8 (the fp16 row pitch of C)");
+    const uint64_t a_bytes = mx4_code_bytes(M, K), w_bytes = mx4_code_bytes(N, K);
+    const uint64_t sa_bytes = mx4_scale_bytes(M, K), sw_bytes = mx4_scale_bytes(N, K);
+    if ((st = check_device_buffer(A, a_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer(W, w_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer(SA, sa_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer(SW, sw_bytes, dev.device)) != GEMM_OK) return st;
+    if (ranges_overlap(C, c_bytes, A, a_bytes) || ranges_overlap(C, c_bytes, W, w_bytes) ||
+        ranges_overlap(C, c_bytes, SA, sa_bytes) || ranges_overlap(C, c_bytes, SW, sw_bytes))
+        return reject(GEMM_ERR_INVALID_ARG, "C overlaps an input");
+    Mx4LaunchArgs a;
+    a.A = A;
+    a.SA = SA;
+    a.W = W;
+    a.SW = SW;
+    a.C = C;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.relu = relu;
+    a.dev = dev;
+    a.stream = s;
+    a.status = status_word(dev.device);
+    if (a.status == nullptr) return GEMM_ERR_CUDA;
+    return launch_mxfp4(a);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

@@ -1,0 +1,118 @@
+// gemm_mxfp4.cu -- host-side launch of the 4-bit microscaled GEMM
+// (gemm_mxfp4_kernel.cuh).  The C ABI entry, gemm_mxfp4 in gemm_f16.cu,
+// validates every argument and calls launch_mxfp4.
+#include "gemm_mxfp4_launch.cuh"
+
+#include "gemm_mxfp4_kernel.cuh"
+
+namespace gemm_sm103 {
+
+namespace {
+
+// Per device and ReLU variant: the shared-memory attribute is set once and
+// the number of co-resident CTA pairs cached (one CTA per SM).
+template <bool kRelu>
+struct Mx4Prepared {
+    static std::atomic<int> slots[kMaxDevices];
+
+    static int get(int dev, int sm_count)
+    {
+        int v = slots[dev].load(std::memory_order_acquire);
+        if (v > 0) return v;
+        auto kern = gemm_mxfp4_sm103a<kRelu>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Mx4Cfg::SMEM_BYTES) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        v = sm_count / 2;
+        cudaLaunchConfig_t lc{};
+        lc.blockDim = dim3(Mx4Cfg::THREADS, 1, 1);
+        lc.dynamicSmemBytes = Mx4Cfg::SMEM_BYTES;
+        lc.gridDim = dim3(2 * v, 1, 1);
+        cudaLaunchAttribute attrs[1];
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = 2;
+        attrs[0].val.clusterDim.y = 1;
+        attrs[0].val.clusterDim.z = 1;
+        lc.attrs = attrs;
+        lc.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kern, &lc) == cudaSuccess && clusters > 0)
+            v = clusters < v ? clusters : v;
+        else
+            cudaGetLastError();
+        if (v > 0) slots[dev].store(v, std::memory_order_release);
+        return v;
+    }
+
+    static void forget(int dev) { slots[dev].store(0, std::memory_order_release); }
+};
+
+template <bool kRelu>
+std::atomic<int> Mx4Prepared<kRelu>::slots[kMaxDevices];
+
+template <bool kRelu>
+int launch_pairs(const Mx4LaunchArgs &a)
+{
+    using Cfg = Mx4Cfg;
+    CUtensorMap ta, tw, tsa, tsw, tc;
+    int st;
+    if ((st = encode_codes_u4(&ta, a.A, a.M, a.K, Cfg::BM)) != GEMM_OK) return st;
+    if ((st = encode_codes_u4(&tw, a.W, a.N, a.K, Cfg::BN_CTA)) != GEMM_OK) return st;
+    if ((st = encode_scale_tiles(&tsa, a.SA, a.M, a.K, Cfg::SF_TILES, 1)) != GEMM_OK) return st;
+    if ((st = encode_scale_tiles(&tsw, a.SW, a.N, a.K, Cfg::SF_TILES, 2)) != GEMM_OK) return st;
+    if ((st = encode_matrix(&tc, a.C, a.M, a.N, Cfg::EPI_COLS, 32)) != GEMM_OK) return st;
+
+    Mx4Params p{};
+    p.M = static_cast<int32_t>(a.M);
+    p.N = static_cast<int32_t>(a.N);
+    p.num_m_blocks = static_cast<int32_t>((a.M + Cfg::TILE_M - 1) / Cfg::TILE_M);
+    p.num_n_blocks = static_cast<int32_t>((a.N + Cfg::BN - 1) / Cfg::BN);
+    p.num_k_blocks = static_cast<int32_t>((a.K + Cfg::BK - 1) / Cfg::BK);
+    const int64_t tiles = static_cast<int64_t>(p.num_m_blocks) * p.num_n_blocks;
+    if (tiles > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+    p.num_tiles = static_cast<int32_t>(tiles);
+    p.group_m = 8;   // 2048-row panels, as the fp16 kernels
+    p.timeout_cycles = timeout_cycles_for(a.K);
+    p.status = a.status;
+
+    using Prep = Mx4Prepared<kRelu>;
+    const int64_t slots = Prep::get(a.dev.device, a.dev.sm_count);
+    if (slots <= 0) return GEMM_ERR_LAUNCH;
+    const int64_t clusters = tiles < slots ? tiles : slots;
+    auto kern = gemm_mxfp4_sm103a<kRelu>;
+    cudaLaunchConfig_t lc{};
+    lc.blockDim = dim3(Cfg::THREADS, 1, 1);
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = a.stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = 2;
+    attrs[0].val.clusterDim.y = 1;
+    attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // programmatic dependent launch
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attrs;
+    lc.numAttrs = 2;
+    lc.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
+    if (cudaLaunchKernelEx(&lc, kern, ta, tw, tsa, tsw, tc, p) != cudaSuccess) {
+        cudaGetLastError();
+        Prep::forget(a.dev.device);
+        if (Prep::get(a.dev.device, a.dev.sm_count) <= 0 ||
+            cudaLaunchKernelEx(&lc, kern, ta, tw, tsa, tsw, tc, p) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+    }
+    return GEMM_OK;
+}
+
+}  // namespace
+
+int launch_mxfp4(const Mx4LaunchArgs &a)
+{
+    return a.relu ? launch_pairs<true>(a) : launch_pairs<false>(a);
+}
+
+}  // namespace gemm_sm103

@@ -1,0 +1,485 @@
+// gemm_mxfp4_kernel.cuh -- microscaled 4-bit GEMM (MXFP4: E2M1 elements, one
+// E8M0 scale per 32 elements along K) with a fused ReLU, for sm_103a:
+//
+//   C[i,j] = R( sum_b 2^(sa[i,b] - 127) * 2^(sw[j,b] - 127) * sum_{k in block b} A[i,k] W[j,k] )
+//
+// A (M,K) and W (N,K) hold two codes per byte (element 2i in the low half),
+// row pitch 16 ceil(K/32) bytes; the scale bytes come in 512-byte tiles of 128
+// rows x 4 blocks, byte (r % 32) * 16 + (r / 32) * 4 + b, tiles of a row block
+// adjacent along K.  That order is what one tcgen05.cp.32x128b.warpx4 moves
+// into four TMEM columns: row r's word at lane r % 32, column r / 32, its four
+// bytes the scales of four K blocks.  tcgen05.mma.kind::mxf4 (K = 64, two
+// scales per row) then takes bytes 0-1 or 2-3 of the words, as the instruction
+// descriptor's scale ids 0 or 2 say.  So scales go from global memory to the
+// MMA without passing through a register: a TMA load beside the operands' and
+// one copy instruction per tile.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "gemm_kernel.cuh"
+
+namespace gemm_sm103 {
+
+// ---------------------------------------------------------------- PTX
+
+// D[tmem] (+)= (A[smem] x scale_A) * (B[smem] x scale_B), E2M1 operands, two
+// E8M0 scales per row of A and of B for the instruction's K = 64, fp32
+// accumulator.
+template <int kCtaGroup>
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    if constexpr (kCtaGroup == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+            : "memory");
+}
+
+// Copies one 512-byte scale tile from shared memory into four TMEM columns,
+// repeated for each of the four 32-lane quarters (in both CTAs of a pair for
+// cta_group::2, each from its own shared memory at the same offset).  Ordered
+// before the MMAs that this thread issues after it.
+template <int kCtaGroup>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t s_desc)
+{
+    if constexpr (kCtaGroup == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
+// 3-D tiled load of one box (coordinates x, y, z), completion counted on a
+// barrier of this CTA, or (pair form) of either CTA of a pair.
+__device__ __forceinline__ void tma_load_3d_cta(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                                int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Shared-memory descriptor of a 512-byte scale tile for tcgen05.cp: no
+// swizzle, 8-row groups of 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;           // leading-dimension offset: one 16-byte row wide, not used
+    d |= static_cast<uint64_t>(128 >> 4) << 32;    // stride between 8-row groups
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;
+}
+
+// Instruction descriptor for tcgen05.mma.kind::mxf4: E2M1 A and B (format 1 in
+// bits 7-9 and 10-11), both K-major, N >> 3 (17-22), E8M0 scales (bit 23),
+// M >> 7 (27-28), K = 64 (bit 31 = 0); scale ids (4-5 for B, 29-30 for A) are
+// added per MMA.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N)
+{
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(M >> 7) << 27);
+}
+
+// ---------------------------------------------------------------- CTA pairs, 256 x 256 tiles
+
+// One CTA per SM, a cluster = one CTA pair, a persistent grid over 256 x 256
+// output tiles in grouped raster order; each CTA holds 128 rows of the tile's
+// accumulator.  A stage is 256 elements of K: a 128-byte swizzle row of A and
+// W per row, four MMAs.
+struct Mx4Cfg {
+    static constexpr int BM = 128;             // rows of C per CTA (TMEM lanes)
+    static constexpr int TILE_M = 256;         // rows per pair tile (the MMA's M)
+    static constexpr int BN = 256;             // columns of C per tile (the MMA's N)
+    static constexpr int BN_CTA = BN / 2;      // rows of W each CTA loads
+    static constexpr int BK = 256;             // elements per K block = one 128-byte swizzle row
+    static constexpr int ROW_BYTES = BK / 2;
+    static constexpr int UMMA_K = 64;
+    static constexpr int STEP_BYTES = UMMA_K / 2;
+    static constexpr int SF_TILE = 512;        // bytes of a scale tile: 128 rows x 4 blocks of 32
+    static constexpr int SF_TILES = BK / 128;  // scale tiles per row block and K block
+    static constexpr int STAGES = 5;
+    static constexpr int THREADS = 192;
+    static constexpr int A_STAGE_BYTES = BM * ROW_BYTES;                // 16 KiB
+    static constexpr int W_STAGE_BYTES = BN_CTA * ROW_BYTES;            // 16 KiB
+    static constexpr int SFA_STAGE_BYTES = SF_TILES * SF_TILE;          // this CTA's 128 rows
+    static constexpr int SFW_STAGE_BYTES = 2 * SF_TILES * SF_TILE;      // all 256 columns, in each CTA
+    static constexpr int STAGE_TX_BYTES = A_STAGE_BYTES + W_STAGE_BYTES + SFA_STAGE_BYTES + SFW_STAGE_BYTES;
+    static constexpr int SF_SLOTS = 2;         // scale slots in TMEM, used in turn
+    static constexpr int SFW_COL = 4 * SF_TILES;                        // W words after A's in a slot
+    static constexpr int SF_SLOT_COLS = 4 * SF_TILES + 8 * SF_TILES;    // 24 columns
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int SF_COL0 = TMEM_COLS - SF_SLOTS * SF_SLOT_COLS; // 464
+    static constexpr int ACC1_COL = SF_COL0 - BN;                       // 208
+    static constexpr int EPI_COLS = 64;
+    static constexpr int EPI_CHUNKS = BN / EPI_COLS;    // 4
+    static constexpr int C_BUF_BYTES = 32 * EPI_COLS * 2;   // one warp's 32 rows of one chunk
+    static constexpr int SMEM_A_OFF = 0;
+    static constexpr int SMEM_W_OFF = STAGES * A_STAGE_BYTES;
+    static constexpr int SMEM_C_OFF = SMEM_W_OFF + STAGES * W_STAGE_BYTES;
+    static constexpr int SMEM_SFA_OFF = SMEM_C_OFF + 4 * 2 * C_BUF_BYTES;
+    static constexpr int SMEM_SFW_OFF = SMEM_SFA_OFF + STAGES * SFA_STAGE_BYTES;
+    static constexpr int SMEM_CTL_OFF = SMEM_SFW_OFF + STAGES * SFW_STAGE_BYTES;
+    static constexpr int SMEM_CTL_BYTES = 256;
+    static constexpr int SMEM_BYTES = 1024 + SMEM_CTL_OFF + SMEM_CTL_BYTES;
+    static constexpr uint32_t IDESC = idesc_mxf4(TILE_M, BN);
+
+    // The two accumulators share the columns [ACC1_COL, BN): the epilogue reads
+    // those first.
+    static_assert(ACC1_COL + EPI_COLS >= BN && ACC1_COL >= BN - EPI_COLS, "the shared columns lie in one chunk");
+    static_assert((2 * STAGES + 4) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
+};
+
+struct Mx4Params {
+    int32_t M, N;
+    int32_t num_m_blocks;   // ceil(M / 256)
+    int32_t num_n_blocks;   // ceil(N / 256)
+    int32_t num_k_blocks;   // ceil(K / 256)
+    int32_t num_tiles;
+    int32_t group_m;        // rasterisation panel height, in tiles
+    uint64_t timeout_cycles;
+    unsigned long long *status;
+};
+
+__device__ __forceinline__ void mx4_tile_coords(int t, const Mx4Params &p, int &mb, int &nb)
+{
+    const int per_group = p.group_m * p.num_n_blocks;
+    const int g = t / per_group;
+    const int first_m = g * p.group_m;
+    const int rows = min(p.num_m_blocks - first_m, p.group_m);
+    const int r = t - g * per_group;
+    mb = first_m + r % rows;
+    nb = r / rows;
+}
+
+// Roles per CTA:
+//   warp 0, one lane   TMA producer: per K block a box of A and of W (128 bytes
+//                      x 128 rows each) and the scale tiles of A's 128 rows and
+//                      of the tile's 256 columns, completing on the pair
+//                      leader's "full" barrier
+//   warp 1, one lane   (leader CTA only) copies the scale tiles into TMEM and
+//                      issues the MMAs, M = 256, N = 256, K = 64
+//   warps 2..5         epilogue: accumulator -> R -> fp16 -> shared memory ->
+//                      TMA store
+// TMEM (512 columns): two accumulators of 256 columns and two scale slots of
+// 24 do not fit beside each other, so the accumulators overlap in 48 columns.
+// The epilogue reads the chunk that holds those columns first and then lets the
+// next tile's MMAs start, which run while it reads and stores the rest.
+// Ragged edges: TMA zero-fills operands and scales outside A and W (a zero
+// scale byte is 2^-127, not NaN); rows and columns outside C are not stored.
+// Every wait is bounded; on expiry the site is recorded in the device status
+// word and all roles leave.
+template <bool kRelu>
+__global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
+    gemm_mxfp4_sm103a(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                      const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sw,
+                      const __grid_constant__ CUtensorMap tmap_c, const Mx4Params p)
+{
+    using Cfg = Mx4Cfg;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;   // SW128 atoms need 1024-byte alignment
+    uint8_t *base_ptr = smem_raw + (base - raw);
+
+    const uint32_t sA = base + Cfg::SMEM_A_OFF;
+    const uint32_t sW = base + Cfg::SMEM_W_OFF;
+    const uint32_t sC = base + Cfg::SMEM_C_OFF;
+    const uint32_t sSFA = base + Cfg::SMEM_SFA_OFF;
+    const uint32_t sSFW = base + Cfg::SMEM_SFW_OFF;
+    const uint32_t ctl = base + Cfg::SMEM_CTL_OFF;
+    constexpr int S = Cfg::STAGES;
+    auto full_bar = [&](int s) { return ctl + 8u * s; };
+    auto empty_bar = [&](int s) { return ctl + 8u * (S + s); };
+    const uint32_t tfull_bar = ctl + 8u * (2 * S);
+    const uint32_t tempty_bar = ctl + 8u * (2 * S + 1);
+    const uint32_t drain_bar = ctl + 8u * (2 * S + 2);
+    const uint32_t tmem_slot = ctl + 8u * (2 * S + 3);
+    const uint32_t abort_addr = tmem_slot + 4;
+    volatile uint32_t *tmem_slot_ptr =
+        reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (2 * S + 3));
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();   // 0: the pair leader, which issues the MMAs
+    const bool leader = rank == 0;
+    constexpr uint16_t kPairMask = 0x3u;
+
+    AbortFlag abort;
+    abort.local = reinterpret_cast<volatile int *>(tmem_slot_ptr + 1);
+    abort.status = p.status;
+    abort.addr = abort_addr;
+    abort.cluster = 2;
+    abort.rank = rank;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 2);    // each CTA's arrive.expect_tx (used on the leader)
+            mbar_init(empty_bar(s), 1);   // one MMA commit, sent to both CTAs
+        }
+        mbar_init(tfull_bar, 1);          // one MMA commit, sent to both CTAs
+        mbar_init(tempty_bar, 8);         // one arrive per epilogue warp of both CTAs
+        mbar_init(drain_bar, 1);
+        *abort.local = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmap_a);
+        prefetch_tensormap(&tmap_w);
+        prefetch_tensormap(&tmap_sa);
+        prefetch_tensormap(&tmap_sw);
+        prefetch_tensormap(&tmap_c);
+    }
+    if (warp == 1) {
+        tmem_alloc<2>(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish<2>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    // Both CTAs' barriers are initialised and their TMEM allocated before
+    // either signals the other.
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after_sync();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint64_t limit = p.timeout_cycles;
+    const int KB = p.num_k_blocks;
+    const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t issued_mask = 0, issued_parity = 0;
+            bool ok = true;
+            const uint32_t full_base = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
+            griddep_wait();   // A, W and the scales may come from the kernel just before
+            for (int t = first; ok && t < p.num_tiles; t += stride) {
+                int mb, nb;
+                mx4_tile_coords(t, p, mb, nb);
+                const int m0 = mb * Cfg::TILE_M + static_cast<int>(rank) * Cfg::BM;
+                const int n0 = nb * Cfg::BN + static_cast<int>(rank) * Cfg::BN_CTA;
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_phase(empty_bar(s), ph ^ 1u, abort, limit, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    // Both CTAs' bytes are counted on the leader's barrier; each
+                    // announces its own.
+                    const uint32_t fb = full_base + 8u * s;
+                    if (leader) mbar_arrive_expect_tx(fb, Cfg::STAGE_TX_BYTES);
+                    else mbar_arrive_expect_tx_cluster(fb, Cfg::STAGE_TX_BYTES);
+                    tma_load_2d_pair(sA + s * Cfg::A_STAGE_BYTES, &tmap_a, fb, kb * Cfg::ROW_BYTES, m0);
+                    tma_load_2d_pair(sW + s * Cfg::W_STAGE_BYTES, &tmap_w, fb, kb * Cfg::ROW_BYTES, n0);
+                    // Scale tiles: (word in the tile, tile along K, row block).
+                    tma_load_3d_pair(sSFA + s * Cfg::SFA_STAGE_BYTES, &tmap_sa, fb, 0, kb * Cfg::SF_TILES,
+                                     mb * 2 + static_cast<int>(rank));
+                    tma_load_3d_pair(sSFW + s * Cfg::SFW_STAGE_BYTES, &tmap_sw, fb, 0, kb * Cfg::SF_TILES, nb * 2);
+                    issued_mask |= 1u << s;
+                    issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                if (leader) {
+                    // Let the loads in flight land before the CTA exits.
+                    for (int i = 0; i < S; ++i)
+                        if (issued_mask & (1u << i))
+                            wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads,
+                                             p.status);
+                } else {
+                    // This CTA's loads complete on the leader's barrier, which it
+                    // cannot probe: give them a bounded time (~1e6 cycles) to land.
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < 1000000) {
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (leader CTA)
+        if (lane == 0 && leader) {
+            int s = 0;
+            uint32_t ph = 0, acc_it = 0, blk = 0;
+            bool ok = true, issued_any = false;
+            // K-major SW128 operands: 8-row groups 1024 B apart; a K step of 64
+            // elements is +32 B inside the swizzle row.
+            const uint64_t a_desc0 = smem_desc_sw128(sA, 16, 1024);
+            const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
+            const uint64_t sfa_desc0 = smem_desc_scales(sSFA);
+            const uint64_t sfw_desc0 = smem_desc_scales(sSFW);
+            for (int t = first; ok && t < p.num_tiles; t += stride, ++acc_it) {
+                // The epilogue has read the columns that this tile's accumulator
+                // shares with the previous one's (and all of the one before).
+                if (acc_it > 0 && !wait_phase(tempty_bar, (acc_it - 1) & 1u, abort, limit, kSiteMmaTmemEmpty)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t acc = tmem_base + ((acc_it & 1u) ? Cfg::ACC1_COL : 0);
+                for (int kb = 0; kb < KB; ++kb, ++blk) {
+                    // The scale slot was last used two K blocks ago: its MMAs have
+                    // completed once that block's ring slot is free.
+                    if (blk >= Cfg::SF_SLOTS) {
+                        const uint32_t old = blk - Cfg::SF_SLOTS;
+                        if (!wait_phase(empty_bar(old % S), (old / S) & 1u, abort, limit, kSiteMmaFull)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t sf =
+                        tmem_base + Cfg::SF_COL0 + (blk % Cfg::SF_SLOTS) * static_cast<uint32_t>(Cfg::SF_SLOT_COLS);
+                    const uint64_t sfa_st = sfa_desc0 + static_cast<uint64_t>((s * Cfg::SFA_STAGE_BYTES) >> 4);
+                    const uint64_t sfw_st = sfw_desc0 + static_cast<uint64_t>((s * Cfg::SFW_STAGE_BYTES) >> 4);
+                    // In shared memory the W tiles are ordered (row block, K tile);
+                    // in TMEM the eight columns of one K tile are adjacent.
+#pragma unroll
+                    for (int i = 0; i < Cfg::SF_TILES; ++i) {
+                        tmem_copy_scales<2>(sf + 4u * i, sfa_st + static_cast<uint64_t>((i * Cfg::SF_TILE) >> 4));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tmem_copy_scales<2>(sf + Cfg::SFW_COL + 8u * i + 4u * h,
+                                                sfw_st + static_cast<uint64_t>(
+                                                             ((h * Cfg::SF_TILES + i) * Cfg::SF_TILE) >> 4));
+                    }
+                    const uint64_t a_st = a_desc0 + static_cast<uint64_t>((s * Cfg::A_STAGE_BYTES) >> 4);
+                    const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < Cfg::BK / Cfg::UMMA_K; ++ks) {
+                        const uint64_t step = static_cast<uint64_t>((ks * Cfg::STEP_BYTES) >> 4);
+                        const uint32_t id = (ks & 1) * 2;   // bytes 0-1 or 2-3 of the words
+                        mma_mxf4<2>(acc, a_st + step, w_st + step, Cfg::IDESC | (id << 4) | (id << 29),
+                                    sf + 4u * (ks / 2), sf + Cfg::SFW_COL + 8u * (ks / 2),
+                                    (kb != 0 || ks != 0) ? 1u : 0u);
+                    }
+                    issued_any = true;
+                    // Operand slot s is free in both CTAs once these MMAs have read it.
+                    mma_commit_pair_mc(empty_bar(s), kPairMask);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit_pair_mc(tfull_bar, kPairMask);   // the tile's accumulator is complete in both CTAs
+            }
+            if (!ok && issued_any) {
+                // Wait for this thread's MMAs before the TMEM is freed.
+                mma_commit_pair_mc(drain_bar, static_cast<uint16_t>(1u << rank));
+                wait_phase_drain(drain_bar, 0, limit, kSiteDrainMma, p.status);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue (warps 2..5)
+        const int ew = warp - 2;       // owner of smem staging buffers
+        const int q = warp & 3;        // TMEM lane quarter this warp may access
+        const uint32_t row_off = static_cast<uint32_t>(lane) * 128u;
+        const uint32_t sw = static_cast<uint32_t>(lane & 7);
+        const uint32_t tempty_leader = leader ? tempty_bar : mapa_shared(tempty_bar, 0);
+        const uint32_t cbuf0 = sC + static_cast<uint32_t>(ew * 2 * Cfg::C_BUF_BYTES);
+        uint32_t acc_it = 0;
+        for (int t = first; t < p.num_tiles; t += stride, ++acc_it) {
+            int mb, nb;
+            mx4_tile_coords(t, p, mb, nb);
+            int ok = 1;
+            if (lane == 0) ok = wait_phase(tfull_bar, acc_it & 1u, abort, limit, kSiteEpilogueTmemFull) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (acc_it == 0) griddep_wait();   // before this warp's first store of C
+            tc_fence_after_sync();
+            const int row0 = mb * Cfg::TILE_M + static_cast<int>(rank) * Cfg::BM + q * 32;
+            const uint32_t odd = acc_it & 1u;
+            const uint32_t acc_addr =
+                tmem_base + (odd ? Cfg::ACC1_COL : 0) + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+            for (int i = 0; i < Cfg::EPI_CHUNKS; ++i) {
+                // The shared columns lie in the last chunk of accumulator 0 and
+                // the first of accumulator 1.
+                const int c = odd ? i : Cfg::EPI_CHUNKS - 1 - i;
+                uint32_t r[64];
+                tmem_load_32x32b_x64(acc_addr + static_cast<uint32_t>(c * Cfg::EPI_COLS), r);
+                if (i == 0) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(tempty_bar);
+                        else mbar_arrive_cluster(tempty_leader);
+                    }
+                }
+                // The store that used this staging buffer two chunks ago has read it.
+                if (lane == 0) bulk_wait_group_read<1>();
+                __syncwarp();
+                const uint32_t cbuf = cbuf0 + static_cast<uint32_t>((i & 1) * Cfg::C_BUF_BYTES);
+                // 16-byte piece jj of a row at piece jj ^ (row % 8): the layout a
+                // SWIZZLE_128B tensor-map store expects.
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj)
+                    st_shared_v4(cbuf + row_off + ((static_cast<uint32_t>(jj) ^ sw) << 4),
+                                 pack_f16x2<kRelu>(r[8 * jj + 0], r[8 * jj + 1]),
+                                 pack_f16x2<kRelu>(r[8 * jj + 2], r[8 * jj + 3]),
+                                 pack_f16x2<kRelu>(r[8 * jj + 4], r[8 * jj + 5]),
+                                 pack_f16x2<kRelu>(r[8 * jj + 6], r[8 * jj + 7]));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    const int col0 = nb * Cfg::BN + c * Cfg::EPI_COLS;
+                    if (row0 < p.M && col0 < p.N) tma_store_2d(&tmap_c, cbuf, col0, row0);
+                    bulk_commit_group();
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_group<0>();
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    // Neither CTA exits while the other may still signal its barriers or its
+    // MMAs may still use this CTA's shared or tensor memory.
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc<2>(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+}  // namespace gemm_sm103

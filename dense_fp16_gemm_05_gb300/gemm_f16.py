@@ -112,6 +112,10 @@ def lib() -> ctypes.CDLL:
     L.gemm_fp8_block_scaled.restype = ci
     L.gemm_mxfp8_block_scaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
     L.gemm_mxfp8_block_scaled.restype = ci
+    L.mxfp4_quantize.argtypes = [vp, ci, vp, vp, vp, i64, i64, ci, vp]
+    L.mxfp4_quantize.restype = ci
+    L.gemm_mxfp4.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
+    L.gemm_mxfp4.restype = ci
     pi = ctypes.POINTER(ctypes.c_int)
     L.gemm_fp8_launch_info.argtypes = [i64, i64, i64, pi, pi]
     L.gemm_fp8_launch_info.restype = ci
@@ -483,6 +487,119 @@ def gemm_mxfp8_block_scaled(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, 
                                        M, N, K, int(bool(relu)), _stream_handle(stream, A.device))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mxfp8_block_scaled")
+    return C
+
+
+TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # enum gemm_f16_type
+MXFP4_BLOCK = 32
+
+
+def mxfp4_shapes(rows: int, K: int) -> tuple[tuple[int, int], tuple[int, int, int]]:
+    """Shapes of the codes and of the scale tiles of a (rows, K) MXFP4 matrix (see gemm_f16.h)."""
+    return (rows, 16 * -(-K // MXFP4_BLOCK)), (-(-rows // 128), -(-K // 128), 512)
+
+
+def mxfp4_tile_scales(E: torch.Tensor) -> torch.Tensor:
+    """Scale bytes E (rows, blocks), one per row and block of 32, in the tile order of gemm_mxfp4.
+
+    A layout change in torch, on E's device: for weights that come with
+    row-major scales.  Fill bytes are zero.
+    """
+    if not isinstance(E, torch.Tensor) or E.dtype != torch.uint8 or E.dim() != 2:
+        raise ValueError("E must be a 2-D uint8 tensor")
+    rows, KB = E.shape
+    RB, KT = -(-rows // 128), -(-KB // 4)
+    full = torch.zeros((RB * 128, KT * 4), dtype=torch.uint8, device=E.device)
+    full[:rows, :KB] = E
+    return full.reshape(RB, 4, 32, KT, 4).permute(0, 3, 2, 1, 4).reshape(RB, KT, 512).contiguous()
+
+
+def mxfp4_row_scales(S: torch.Tensor, rows: int, K: int) -> torch.Tensor:
+    """The inverse of mxfp4_tile_scales: scale bytes (rows, ceil(K/32)) of tiles S."""
+    if not isinstance(S, torch.Tensor) or S.dtype != torch.uint8 or tuple(S.shape) != mxfp4_shapes(rows, K)[1]:
+        raise ValueError(f"S must be a uint8 tensor of shape {mxfp4_shapes(rows, K)[1]}")
+    RB, KT, _ = S.shape
+    full = S.reshape(RB, KT, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(RB * 128, KT * 4)
+    return full[:rows, :-(-K // MXFP4_BLOCK)].contiguous()
+
+
+def _check_like(t, name: str, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = False, Q: torch.Tensor | None = None,
+                   S: torch.Tensor | None = None, V: torch.Tensor | None = None, stream=None):
+    """MXFP4 codes and scale tiles (Q, S) of the (rows, K) matrix X, or (Q, S, V) with ``values``.
+
+    X: contiguous 2-D float16, bfloat16 or float32 CUDA tensor; with
+    ``transpose`` it is (K, rows) and its columns are quantised (a weight
+    stored in-features x out-features becomes gemm_mxfp4's W).  V holds the
+    values the codes stand for, (rows, K) of X's type.  Q, S and V are
+    allocated when not given; formats and rounding as in gemm_f16.h.
+    Asynchronous on ``stream``.
+    """
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    if X.dtype not in TYPES or X.dim() != 2 or not X.is_contiguous():
+        raise ValueError("X must be a contiguous 2-D float16, bfloat16 or float32 tensor, "
+                         f"got {X.dtype} {tuple(X.shape)}")
+    rows, K = (X.shape[1], X.shape[0]) if transpose else (X.shape[0], X.shape[1])
+    q_shape, s_shape = mxfp4_shapes(rows, K)
+    dev = X.device
+    if Q is None:
+        Q = torch.empty(q_shape, dtype=torch.uint8, device=dev)
+    if S is None:
+        S = torch.empty(s_shape, dtype=torch.uint8, device=dev)
+    if V is None and values:
+        V = torch.empty((rows, K), dtype=X.dtype, device=dev)
+    _check_like(Q, "Q", torch.uint8, q_shape, dev)
+    _check_like(S, "S", torch.uint8, s_shape, dev)
+    if V is not None:
+        _check_like(V, "V", X.dtype, (rows, K), dev)
+    L = lib()
+    with _device_scope(dev):
+        st = L.mxfp4_quantize(X.data_ptr(), TYPES[X.dtype], Q.data_ptr(), S.data_ptr(),
+                              None if V is None else V.data_ptr(), rows, K, int(bool(transpose)),
+                              _stream_handle(stream, dev))
+    if st != GEMM_OK:
+        raise GemmError(st, "mxfp4_quantize")
+    return (Q, S) if V is None else (Q, S, V)
+
+
+def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Tensor, C: torch.Tensor | None = None,
+               relu: bool = False, K: int | None = None, stream=None) -> torch.Tensor:
+    """C = R(A @ W^T) from MXFP4 operands (codes and scale tiles of mxfp4_quantize), C float16.
+
+    A, SA: packed (M,K); W, SW: packed (N,K).  K defaults to the codes' width,
+    2 A.shape[1] (give it when K is not a multiple of 32).  C (M,N) is
+    allocated when not given.  Asynchronous on ``stream``.
+    """
+    for t, name in ((A, "A"), (W, "W")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-D uint8 tensor, got {tuple(t.shape)}")
+    M, N = A.shape[0], W.shape[0]
+    if K is None:
+        K = 2 * A.shape[1]
+    dev = A.device
+    for t, s, name, rows in ((A, SA, "A", M), (W, SW, "W", N)):
+        q_shape, s_shape = mxfp4_shapes(rows, K)
+        _check_like(t, name, torch.uint8, q_shape, dev)
+        _check_like(s, "S" + name, torch.uint8, s_shape, dev)
+    if C is None:
+        C = torch.empty((M, N), dtype=torch.float16, device=dev)
+    _check_like(C, "C", torch.float16, (M, N), dev)
+    L = lib()
+    with _device_scope(dev):
+        st = L.gemm_mxfp4(A.data_ptr(), SA.data_ptr(), W.data_ptr(), SW.data_ptr(), C.data_ptr(), M, N, int(K),
+                          int(bool(relu)), _stream_handle(stream, dev))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_mxfp4")
     return C
 
 

@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define GEMM_F16_VERSION 7
+#define GEMM_F16_VERSION 8
 
 /* Return codes.  0 is success; every error is negative. */
 enum gemm_f16_status {
@@ -308,6 +308,71 @@ int gemm_fp8_block_scaled(const void *A, const float *SA, const void *W, const f
  */
 int gemm_mxfp8_block_scaled(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C,
                             int64_t M, int64_t N, int64_t K, int relu, void *stream);
+
+/* Element types of the entry points that take one. */
+enum gemm_f16_type {
+    GEMM_TYPE_F16 = 0,    /* IEEE binary16 */
+    GEMM_TYPE_BF16 = 1,   /* bfloat16 */
+    GEMM_TYPE_F32 = 2     /* IEEE binary32 */
+};
+
+/*
+ * MXFP4 matrices (OCP microscaling formats, version 1.0: E2M1 elements, one
+ * E8M0 scale of value 2^(byte - 127) per 32 elements along K).  The packed
+ * form of a (rows, K) matrix is two device buffers:
+ *
+ *   Q  codes, (rows, 16 ceil(K/32)) bytes row-major: element 2i of a row in
+ *      the low half of byte i, element 2i + 1 in the high half.  Codes past K
+ *      are zero.  16-byte aligned.
+ *   S  scales, (ceil(rows/128), ceil(K/128), 512) bytes: the byte of row r and
+ *      block b (elements 32 b .. 32 b + 31) at tile [r / 128][b / 4], byte
+ *      (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4.  Bytes of blocks past K are
+ *      zero (any value but 0xFF, NaN, serves); bytes of rows past `rows` are
+ *      not used.  16-byte aligned.
+ *
+ * The scale order is the one the tensor core's scale memory is filled from:
+ * a tile is 32 rows of 16 bytes, four words for rows r, r + 32, r + 64, r + 96.
+ *
+ * mxfp4_quantize -- X -> (Q, S).  Per block: e = floor(log2 max|x|) - 2, kept
+ * within -127 .. 127, scale byte e + 127; element = x 2^-e rounded to the
+ * nearest E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), ties to even,
+ * magnitudes above 6 to 6.  A block of zeros gets scale byte 0.  A block that
+ * holds an infinity or a NaN gets scale byte 0xFF (NaN) and zero codes.
+ *
+ *   X      device pointer, elements of type `type` (enum gemm_f16_type),
+ *          row-major: (rows, K) for trans = 0; (K, rows) for trans = 1, whose
+ *          columns become the rows of the packed form (the weight of a linear
+ *          layer stored in-features x out-features).  Aligned to its element.
+ *   V      NULL, or a buffer like the (rows, K) matrix of X's type, row-major,
+ *          that receives the values the codes stand for, rounded once to that
+ *          type (exact in bfloat16 and binary32): what the product will see,
+ *          for a quantisation error or a straight-through gradient
+ *   rows, K  0 .. INT32_MAX; either 0: no-op
+ *
+ * Q, S and V overlap neither X nor each other.  Only enqueues on `stream`.
+ * The pages name per-block scaling as the FP8 layer's preparation (nxmr.cn,
+ * section 7; 7yue.com, section 8.2); the 4-bit form is this library's.
+ */
+int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, void *V, int64_t rows, int64_t K, int trans,
+                   void *stream);
+
+/*
+ * gemm_mxfp4 -- C = R(A @ W^T) from MXFP4 operands, fp16 C:
+ *
+ *   C[i,j] = R( sum_b 2^(sa[i,b]-127) * 2^(sw[j,b]-127) * sum_{k in block b} A[i,k] * W[j,k] )
+ *
+ * accumulated in fp32 by the block-scaled 4-bit MMA and rounded once to fp16
+ * (R as for gemm_f16; a NaN scale gives NaN without ReLU, +0 with it).
+ * A, SA: the packed form of a (M,K) matrix; W, SW: of a (N,K) matrix (a linear
+ * layer's weight, out-features x in-features); C (M,N) row-major.
+ *
+ * Checks as for gemm_mxfp8_block_scaled, with any K and N a
+ * multiple of 8 (GEMM_ERR_ALIGNMENT), SA and SW 16-byte aligned.  M == 0 or
+ * N == 0: no-op; K == 0: C = +0.  Only enqueues on `stream`, allocates
+ * nothing; device timeouts are reported by gemm_f16_check.
+ */
+int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C,
+               int64_t M, int64_t N, int64_t K, int relu, void *stream);
 
 /* Launch geometry of gemm_fp8_block_scaled for this problem on the current
  * device: persistent grid in CTAs (CTA pairs over 256 x 256 output tiles) and
