@@ -10,7 +10,10 @@ calls the kernel and whose backward returns ``dA = dC @ B.T`` and
 * dA        dZ @ B^T   (B stored (K,N))          gemm_f16_tx with transb = 1 (NT)
 * dB        A^T @ dZ   (A stored (M,K))          gemm_f16_tx with transa = 1 (TN)
 
-Operands and gradients are float16 (the kernels accumulate in fp32).  No step
+and layer norm, for the layer that feeds them, with layer_norm_fwd and
+layer_norm_bwd.
+
+The GEMMs' operands and gradients are float16 (the kernels accumulate in fp32).  No step
 falls back to torch arithmetic; a missing library raises LibraryNotBuilt.
 """
 from __future__ import annotations
@@ -45,6 +48,39 @@ class GemmF16Function(torch.autograd.Function):
         if ctx.needs_input_grad[1]:
             dB = _g.gemm_f16_t(A, dZ, transa=True, relu=False)     # (K,M) @ (M,N)
         return dA, dB, None
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """Layer norm over the last dimension; its backward is layer_norm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None, eps: float):
+        x = x.contiguous()
+        y, mean, rstd = _g.layer_norm_fwd(x, gamma, beta, eps=eps)
+        ctx.save_for_backward(x, gamma, mean, rstd)
+        ctx.wtype = beta.dtype if gamma is None and beta is not None else None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy: torch.Tensor):
+        x, gamma, mean, rstd = ctx.saved_tensors
+        dy = dy.contiguous()
+        if dy.dtype != x.dtype:
+            dy = dy.to(x.dtype)
+        need_g, need_b = ctx.needs_input_grad[1], ctx.needs_input_grad[2]
+        dx, dgamma, dbeta = _g.layer_norm_bwd(dy, x, mean, rstd, gamma, weights=need_g or need_b, wtype=ctx.wtype)
+        return (dx if ctx.needs_input_grad[0] else None, dgamma if need_g else None, dbeta if need_b else None, None)
+
+
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+               eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable layer norm over x's last dimension on CUDA tensors.
+
+    As with any torch function, capture a training step's backward pass only
+    with its forward pass, after warm-up on the capture stream and with no
+    eager graph of the same leaves alive.
+    """
+    return LayerNormFunction.apply(x, gamma, beta, eps)
 
 
 def gemm_relu(A: torch.Tensor, B: torch.Tensor) -> torch.Tensor:

@@ -22,6 +22,7 @@
 #include "gemm_fp8_launch.cuh"
 #include "gemm_launch.cuh"
 #include "gemm_mxfp4_launch.cuh"
+#include "layer_norm.cuh"
 
 using namespace gemm_sm103;
 
@@ -888,6 +889,152 @@ extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const
     a.status = status_word(dev.device);
     if (a.status == nullptr) return GEMM_ERR_CUDA;
     return launch_mxfp4(a);
+}
+
+namespace {
+
+int check_norm_args(int64_t rows, int64_t dim, int xtype, int wtype)
+{
+    const int st = check_sizes(rows, dim, 0, 0);
+    if (st != GEMM_OK) return st;
+    if (type_bytes(xtype) == 0 || type_bytes(wtype) == 0)
+        return reject(GEMM_ERR_INVALID_ARG, "xtype or wtype is not a gemm_f16_type");
+    if (wtype != xtype && wtype != GEMM_TYPE_F32)
+        return reject(GEMM_ERR_INVALID_ARG, "wtype is neither xtype nor GEMM_TYPE_F32");
+    return GEMM_OK;
+}
+
+struct NormBuffer {
+    const void *p;
+    uint64_t bytes;
+    uintptr_t align;
+    bool written;
+};
+
+// Checks every buffer that is given and that what is written overlaps nothing
+// else.
+int check_norm_buffers(const NormBuffer *b, int n, int dev)
+{
+    for (int i = 0; i < n; ++i) {
+        if (b[i].p == nullptr) continue;
+        const int st = check_device_buffer(b[i].p, b[i].bytes, dev, b[i].align);
+        if (st != GEMM_OK) return st;
+    }
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j) {
+            if (i == j || !b[i].written || b[i].p == nullptr || b[j].p == nullptr) continue;
+            if (ranges_overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
+                return reject(GEMM_ERR_INVALID_ARG, "an output overlaps another buffer");
+        }
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" int layer_norm_fwd(const void *X, const void *gamma, const void *beta, void *Y, float *mean, float *rstd,
+                              int64_t rows, int64_t dim, float eps, int xtype, int wtype, void *stream)
+{
+    int st = check_norm_args(rows, dim, xtype, wtype);
+    if (st != GEMM_OK) return st;
+    if (!std::isfinite(eps) || eps < 0.0f) return reject(GEMM_ERR_INVALID_ARG, "eps is negative or not finite");
+    if (rows == 0 || dim == 0) return GEMM_OK;
+    if (X == nullptr || Y == nullptr) return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint64_t x_bytes = static_cast<uint64_t>(rows) * static_cast<uint64_t>(dim) * type_bytes(xtype);
+    const uint64_t w_bytes = static_cast<uint64_t>(dim) * type_bytes(wtype);
+    const uint64_t r_bytes = static_cast<uint64_t>(rows) * sizeof(float);
+    const NormBuffer b[] = {{X, x_bytes, type_bytes(xtype), false},    {gamma, w_bytes, type_bytes(wtype), false},
+                            {beta, w_bytes, type_bytes(wtype), false}, {Y, x_bytes, type_bytes(xtype), true},
+                            {mean, r_bytes, 4, true},                  {rstd, r_bytes, 4, true}};
+    if ((st = check_norm_buffers(b, 6, dev.device)) != GEMM_OK) return st;
+    LayerNormArgs a;
+    a.X = X;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.Y = Y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.dim = dim;
+    a.eps = eps;
+    a.xtype = xtype;
+    a.wtype = wtype;
+    a.sm_count = dev.sm_count;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_layer_norm_fwd(a);
+}
+
+extern "C" int64_t layer_norm_bwd_workspace(int64_t rows, int64_t dim)
+{
+    int st = check_sizes(rows, dim, 0, 0);
+    if (st != GEMM_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    return 2 * layer_norm_parts(rows, dim, dev.sm_count) * dim * static_cast<int64_t>(sizeof(float));
+}
+
+extern "C" int layer_norm_bwd(const void *dY, const void *X, const void *gamma, const float *mean, const float *rstd,
+                              void *dX, void *dgamma, void *dbeta, int64_t rows, int64_t dim, int xtype, int wtype,
+                              void *workspace, int64_t workspace_bytes, void *stream)
+{
+    int st = check_norm_args(rows, dim, xtype, wtype);
+    if (st != GEMM_OK) return st;
+    if ((dgamma == nullptr) != (dbeta == nullptr))
+        return reject(GEMM_ERR_INVALID_ARG, "one of dgamma and dbeta is NULL and the other is not");
+    if (dim == 0) return GEMM_OK;
+    if (rows > 0 && (dY == nullptr || X == nullptr || mean == nullptr || rstd == nullptr || dX == nullptr))
+        return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    if (rows == 0 && dgamma == nullptr) return GEMM_OK;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const uint64_t x_bytes = static_cast<uint64_t>(rows) * static_cast<uint64_t>(dim) * type_bytes(xtype);
+    const uint64_t w_bytes = static_cast<uint64_t>(dim) * type_bytes(wtype);
+    const uint64_t r_bytes = static_cast<uint64_t>(rows) * sizeof(float);
+    if (rows == 0) {
+        // Empty sums.
+        const NormBuffer b[] = {{dgamma, w_bytes, type_bytes(wtype), true}, {dbeta, w_bytes, type_bytes(wtype), true}};
+        if ((st = check_norm_buffers(b, 2, dev.device)) != GEMM_OK) return st;
+        if (cudaMemsetAsync(dgamma, 0, w_bytes, s) != cudaSuccess ||
+            cudaMemsetAsync(dbeta, 0, w_bytes, s) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        return GEMM_OK;
+    }
+    const uint64_t need =
+        dgamma ? 2 * static_cast<uint64_t>(layer_norm_parts(rows, dim, dev.sm_count)) * static_cast<uint64_t>(dim) * 4u
+               : 0u;
+    if (dgamma && (workspace == nullptr || workspace_bytes < 0 || static_cast<uint64_t>(workspace_bytes) < need))
+        return reject(GEMM_ERR_INVALID_ARG, "the workspace is smaller than layer_norm_bwd_workspace says");
+    const NormBuffer b[] = {{dY, x_bytes, type_bytes(xtype), false},
+                            {X, x_bytes, type_bytes(xtype), false},
+                            {gamma, w_bytes, type_bytes(wtype), false},
+                            {mean, r_bytes, 4, false},
+                            {rstd, r_bytes, 4, false},
+                            {dX, x_bytes, type_bytes(xtype), true},
+                            {dgamma, w_bytes, type_bytes(wtype), true},
+                            {dbeta, w_bytes, type_bytes(wtype), true},
+                            {dgamma ? workspace : nullptr, need, 16, true}};
+    if ((st = check_norm_buffers(b, 9, dev.device)) != GEMM_OK) return st;
+    LayerNormArgs a;
+    a.dY = dY;
+    a.X = X;
+    a.gamma = gamma;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.Y = dX;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.workspace = static_cast<float *>(workspace);
+    a.rows = rows;
+    a.dim = dim;
+    a.xtype = xtype;
+    a.wtype = wtype;
+    a.sm_count = dev.sm_count;
+    a.stream = s;
+    return launch_layer_norm_bwd(a);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

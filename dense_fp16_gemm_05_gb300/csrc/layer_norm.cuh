@@ -1,0 +1,159 @@
+// layer_norm.cuh -- shared pieces of the layer norm kernels (layer_norm_fwd.cu,
+// layer_norm_bwd.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "gemm_f16.h"
+#include "gemm_launch.cuh"
+
+namespace gemm_sm103 {
+
+struct LayerNormArgs {
+    const void *X = nullptr, *gamma = nullptr, *beta = nullptr, *dY = nullptr;
+    void *Y = nullptr;                          // forward output, or dX
+    float *mean = nullptr, *rstd = nullptr;     // written forward, read backward
+    void *dgamma = nullptr, *dbeta = nullptr;
+    float *workspace = nullptr;                 // 2 x parts x dim floats (backward)
+    int64_t rows = 0;
+    int64_t dim = 0;
+    float eps = 0.0f;
+    int xtype = 0, wtype = 0;
+    int sm_count = 0;
+    cudaStream_t stream = nullptr;
+};
+
+int launch_layer_norm_fwd(const LayerNormArgs &a);
+int launch_layer_norm_bwd(const LayerNormArgs &a);
+// Partial sums of the weights' gradients that a backward call writes per column.
+int64_t layer_norm_parts(int64_t rows, int64_t dim, int sm_count);
+
+__device__ __forceinline__ float ln_float(float x) { return x; }
+__device__ __forceinline__ float ln_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float ln_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T>
+__device__ __forceinline__ T ln_round(float x);
+template <>
+__device__ __forceinline__ float ln_round<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half ln_round<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 ln_round<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// V adjacent elements, loaded and stored in pieces of 16 bytes where V elements
+// hold that many (the caller vouches for the alignment), else one by one.
+template <class T, int V>
+struct LnPack {
+    T e[V];
+
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (V * sizeof(T) % 16 == 0) {
+            uint4 raw[V * sizeof(T) / 16];
+#pragma unroll
+            for (unsigned i = 0; i < V * sizeof(T) / 16; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            memcpy(e, raw, sizeof(e));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = __ldg(p + i);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+        if constexpr (V * sizeof(T) % 16 == 0) {
+            uint4 raw[V * sizeof(T) / 16];
+            memcpy(raw, e, sizeof(e));
+#pragma unroll
+            for (unsigned i = 0; i < V * sizeof(T) / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = raw[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = e[i];
+        }
+    }
+    __device__ __forceinline__ void fill(float v)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = ln_round<T>(v);
+    }
+    __device__ __forceinline__ float operator[](int i) const { return ln_float(e[i]); }
+};
+
+__device__ __forceinline__ float ln_warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum over the TPR threads of a row, the same bits in each of them.  TPR = 32:
+// a warp; else the whole block, with `sh` (TPR / 32 floats) not in use by an
+// earlier sum that some thread may still be reading.
+template <int TPR>
+__device__ __forceinline__ float ln_row_sum(float v, float *sh)
+{
+    v = ln_warp_sum(v);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = sh[0];
+#pragma unroll
+        for (int i = 1; i < TPR / 32; ++i) v += sh[i];
+    }
+    return v;
+}
+
+template <int TPR>
+__device__ __forceinline__ float2 ln_row_sum2(float a, float b, float2 *sh)
+{
+    a = ln_warp_sum(a);
+    b = ln_warp_sum(b);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        float2 s = sh[0];
+#pragma unroll
+        for (int i = 1; i < TPR / 32; ++i) {
+            s.x += sh[i].x;
+            s.y += sh[i].y;
+        }
+        return s;
+    }
+    return make_float2(a, b);
+}
+
+// Launch as a programmatic dependent of the previous kernel on the stream (the
+// kernels wait for it before touching memory).
+template <class... Args>
+int ln_launch(void (*kern)(Args...), dim3 grid, unsigned threads, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads, 1, 1);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+// Calls f(T{}, W{}) for the element types of a call: W is X's type or float.
+template <class F>
+int ln_dispatch(int xtype, int wtype, F f)
+{
+    if (xtype == GEMM_TYPE_F32) return f(float{}, float{});
+    if (xtype == GEMM_TYPE_F16) return wtype == GEMM_TYPE_F32 ? f(__half{}, float{}) : f(__half{}, __half{});
+    return wtype == GEMM_TYPE_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+}
+
+}  // namespace gemm_sm103

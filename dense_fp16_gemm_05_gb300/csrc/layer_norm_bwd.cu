@@ -1,0 +1,294 @@
+// layer_norm_bwd.cu -- gradients of layer norm.  With z = (x - mean) rstd and
+// g = dy gamma,
+//
+//   dx     = rstd (g - sum(g) / dim - z sum(g z) / dim)      (sums over a row)
+//   dgamma = sum dy z,   dbeta = sum dy                      (sums over all rows)
+//
+// Bound by memory: dY and X are read once and dX written once.  A block walks
+// rows; a thread always has the same columns, so the columns' sums stay in its
+// registers (fp32) until the block's last row, and only then one partial sum
+// per block and column goes to the workspace.  A second kernel adds the blocks'
+// partial sums in a fixed order: no atomics, the same bits every time.
+#include "layer_norm.cuh"
+
+namespace {
+
+using namespace gemm_sm103;
+
+template <class T, class W>
+struct BwdParams {
+    const T *dY, *X;
+    const W *gamma;   // NULL: ones
+    const float *mean, *rstd;
+    T *dX;
+    float *part;      // (2, parts, dim): dgamma's, then dbeta's; NULL: not wanted
+    int64_t rows;
+    int32_t dim;
+    int32_t parts;    // blocks
+    float inv_dim;
+};
+
+template <class T, class W, int V, int NV, int TPR>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layer_norm_bwd_kernel(BwdParams<T, W> p)
+{
+    constexpr int BT = TPR < 256 ? 256 : TPR;
+    constexpr int R = BT / TPR;   // rows at a time
+    static_assert(TPR == 32 || R == 1, "a warp or a block per row");
+    __shared__ float2 sh[2][TPR / 32];
+    extern __shared__ float comb[];   // R > 1: (R, dim)
+    griddep_wait();
+    griddep_launch_dependents();
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    float dg[NV][V], db[NV][V];
+    LnPack<W, V> pg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int k = (i * TPR + t) * V;
+        if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
+        else pg[i].fill(1.0f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) dg[i][j] = db[i][j] = 0.0f;
+    }
+    int it = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * R + sub; row < p.rows;
+         row += static_cast<int64_t>(gridDim.x) * R, it ^= 1) {
+        const T *x = p.X + row * p.dim;
+        const T *dy = p.dY + row * p.dim;
+        LnPack<T, V> px[NV], pd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (k < p.dim) {
+                px[i].load(x + k);
+                pd[i].load(dy + k);
+            } else {
+                px[i].fill(0.0f);
+                pd[i].fill(0.0f);   // adds nothing to any sum
+            }
+        }
+        const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float z = (i * TPR + t) * V < p.dim ? (px[i][j] - mean) * rstd : 0.0f;
+                const float d = pd[i][j];
+                const float g = d * pg[i][j];
+                s1 += g;
+                s2 = fmaf(g, z, s2);
+                dg[i][j] = fmaf(d, z, dg[i][j]);
+                db[i][j] += d;
+            }
+        const float2 sum = ln_row_sum2<TPR>(s1, s2, sh[it]);
+        const float c1 = sum.x * p.inv_dim, c2 = sum.y * p.inv_dim;
+        T *dx = p.dX + row * p.dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (k >= p.dim) continue;
+            LnPack<T, V> out;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float z = (px[i][j] - mean) * rstd;
+                out.e[j] = ln_round<T>(rstd * (fmaf(pd[i][j], pg[i][j], -c1) - z * c2));
+            }
+            out.store(dx + k);
+        }
+    }
+    if (p.part == nullptr) return;
+    // The block's partial sums, first dgamma's and then dbeta's.
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float *out = p.part + (static_cast<int64_t>(which) * p.parts + blockIdx.x) * p.dim;
+        if constexpr (R == 1) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int k = (i * TPR + t) * V;
+                if (k >= p.dim) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) out[k + j] = which == 0 ? dg[i][j] : db[i][j];
+            }
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int k = (i * TPR + t) * V;
+                if (k >= p.dim) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) comb[sub * p.dim + k + j] = which == 0 ? dg[i][j] : db[i][j];
+            }
+            __syncthreads();
+            for (int k = threadIdx.x; k < p.dim; k += BT) {
+                float s = comb[k];
+#pragma unroll
+                for (int r = 1; r < R; ++r) s += comb[r * p.dim + k];
+                out[k] = s;
+            }
+        }
+    }
+}
+
+// Rows longer than a block holds: dX in two passes over the row ...
+template <class T, class W>
+__global__ void __launch_bounds__(1024) layer_norm_bwd_long(BwdParams<T, W> p)
+{
+    __shared__ float2 sh[2][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, it ^= 1) {
+        const T *x = p.X + row * p.dim;
+        const T *dy = p.dY + row * p.dim;
+        T *dx = p.dX + row * p.dim;
+        const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t k = threadIdx.x; k < p.dim; k += 1024) {
+            const float g = ln_float(dy[k]) * (p.gamma ? ln_float(p.gamma[k]) : 1.0f);
+            s1 += g;
+            s2 = fmaf(g, (ln_float(x[k]) - mean) * rstd, s2);
+        }
+        const float2 sum = ln_row_sum2<1024>(s1, s2, sh[it]);
+        const float c1 = sum.x * p.inv_dim, c2 = sum.y * p.inv_dim;
+        for (int64_t k = threadIdx.x; k < p.dim; k += 1024) {
+            const float g = ln_float(dy[k]) * (p.gamma ? ln_float(p.gamma[k]) : 1.0f);
+            dx[k] = ln_round<T>(rstd * (g - c1 - (ln_float(x[k]) - mean) * rstd * c2));
+        }
+    }
+}
+
+// ... and the columns' partial sums, a thread per column, rows blockIdx.y,
+// blockIdx.y + parts, ...
+template <class T, class W>
+__global__ void __launch_bounds__(256) layer_norm_bwd_columns(BwdParams<T, W> p)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (k >= p.dim) return;
+    for (int64_t part = blockIdx.y; part < p.parts; part += gridDim.y) {
+        float dg = 0.0f, db = 0.0f;
+        for (int64_t row = part; row < p.rows; row += p.parts) {
+            const float d = ln_float(p.dY[row * p.dim + k]);
+            const float z = (ln_float(p.X[row * p.dim + k]) - __ldg(p.mean + row)) * __ldg(p.rstd + row);
+            dg = fmaf(d, z, dg);
+            db += d;
+        }
+        p.part[part * p.dim + k] = dg;
+        p.part[(static_cast<int64_t>(p.parts) + part) * p.dim + k] = db;
+    }
+}
+
+// Adds the parts of 32 columns: 8 warps take every eighth part, then their sums
+// are added in order.
+template <class W>
+__global__ void __launch_bounds__(256) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
+                                                             W *__restrict__ dbeta, int parts, int dim)
+{
+    __shared__ float sh[8][33];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const float *src = part + static_cast<int64_t>(blockIdx.y) * parts * dim;
+    float s = 0.0f;
+    if (k < dim) {
+#pragma unroll 8
+        for (int r = w; r < parts; r += 8) s += src[static_cast<int64_t>(r) * dim + k];
+    }
+    sh[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && k < dim) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sh[i][lane];
+        (blockIdx.y == 0 ? dgamma : dbeta)[k] = ln_round<W>(s);
+    }
+}
+
+template <class T, class W, int V, int NV, int TPR>
+int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
+{
+    constexpr int BT = TPR < 256 ? 256 : TPR;
+    constexpr int R = BT / TPR;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(p.parts), 1, 1);
+    lc.blockDim = dim3(BT, 1, 1);
+    lc.dynamicSmemBytes = R > 1 ? static_cast<size_t>(R) * p.dim * sizeof(float) : 0;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, layer_norm_bwd_kernel<T, W, V, NV, TPR>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+template <class T, class W, int V>
+int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
+{
+    const int packs = (p.dim + V - 1) / V;
+    constexpr int N = V == 1 ? 8 : (sizeof(T) == 2 ? 1 : 2);   // packs of 8 elements
+    // Up to 512 elements a warp per row; layer_norm_parts counts on it.
+    if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
+    if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
+    if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
+    if (packs <= 256 * 2 * N) return launch_one<T, W, V, 2 * N, 256>(p, stream);
+    if (packs <= 512 * 2 * N) return launch_one<T, W, V, 2 * N, 512>(p, stream);
+    if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
+    int st = ln_launch(layer_norm_bwd_long<T, W>, dim3(static_cast<unsigned>(p.parts), 1, 1), 1024, stream, p);
+    if (st != GEMM_OK || p.part == nullptr) return st;
+    return ln_launch(layer_norm_bwd_columns<T, W>,
+                     dim3(static_cast<unsigned>((static_cast<int64_t>(p.dim) + 255) / 256),
+                          static_cast<unsigned>(p.parts), 1),
+                     256, stream, p);
+}
+
+template <class T, class W>
+int backward(const LayerNormArgs &a)
+{
+    BwdParams<T, W> p{};
+    p.dY = static_cast<const T *>(a.dY);
+    p.X = static_cast<const T *>(a.X);
+    p.gamma = static_cast<const W *>(a.gamma);
+    p.mean = a.mean;
+    p.rstd = a.rstd;
+    p.dX = static_cast<T *>(a.Y);
+    p.part = a.dgamma ? a.workspace : nullptr;
+    p.rows = a.rows;
+    p.dim = static_cast<int32_t>(a.dim);
+    p.parts = static_cast<int32_t>(layer_norm_parts(a.rows, a.dim, a.sm_count));
+    p.inv_dim = 1.0f / static_cast<float>(a.dim);
+    constexpr int V = 16 / sizeof(T);
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
+                           reinterpret_cast<uintptr_t>(a.Y) | reinterpret_cast<uintptr_t>(a.gamma);
+    const bool vec = a.dim % V == 0 && (bits & 15u) == 0;
+    int st = vec ? launch_packs<T, W, V>(p, a.stream) : launch_packs<T, W, 1>(p, a.stream);
+    if (st != GEMM_OK || p.part == nullptr) return st;
+    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 256, a.stream,
+                     static_cast<const float *>(p.part), static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta),
+                     p.parts, p.dim);
+}
+
+}  // namespace
+
+namespace gemm_sm103 {
+
+// One part per block of the row kernels: rows of up to 512 elements go eight at
+// a time (a warp each), longer ones one at a time.
+int64_t layer_norm_parts(int64_t rows, int64_t dim, int sm_count)
+{
+    const int64_t per = dim <= 512 ? 8 : 1;
+    const int64_t want = (rows + per - 1) / per, most = 2 * static_cast<int64_t>(sm_count);
+    return want < most ? want : most;
+}
+
+int launch_layer_norm_bwd(const LayerNormArgs &a)
+{
+    return ln_dispatch(a.xtype, a.wtype, [&](auto t, auto w) { return backward<decltype(t), decltype(w)>(a); });
+}
+
+}  // namespace gemm_sm103

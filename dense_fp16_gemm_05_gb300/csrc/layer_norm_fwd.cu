@@ -1,0 +1,170 @@
+// layer_norm_fwd.cu -- layer norm over the last dimension:
+//
+//   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps),
+//   y = (x - mean) rstd gamma + beta,
+//
+// sums in fp32, the second one over deviations of the row that is still in
+// registers (not sum x^2 - mean^2, which cancels).  Bound by memory: X is read
+// once and Y written once.  A row belongs to a warp or to one block, chosen so
+// that a thread holds at most 32 elements; longer rows are read again from L2.
+#include "layer_norm.cuh"
+
+namespace {
+
+using namespace gemm_sm103;
+
+template <class T, class W>
+struct FwdParams {
+    const T *X;
+    const W *gamma;   // NULL: ones
+    const W *beta;    // NULL: zeros
+    T *Y;
+    float *mean, *rstd;   // NULL: not kept
+    int64_t rows;
+    int32_t dim;
+    float inv_dim, eps;
+};
+
+// TPR threads per row, NV packs of V elements per thread, pack i of thread t at
+// element (i TPR + t) V.
+template <class T, class W, int V, int NV, int TPR>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(FwdParams<T, W> p)
+{
+    constexpr int BT = TPR < 128 ? 128 : TPR;
+    __shared__ float sh[2][TPR / 32];
+    griddep_wait();   // X may come from the kernel just before
+    griddep_launch_dependents();
+    const int t = threadIdx.x % TPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (BT / TPR) + threadIdx.x / TPR;
+    if (row >= p.rows) return;   // whole warps (TPR = 32) or no thread
+    const T *x = p.X + row * p.dim;
+    LnPack<T, V> px[NV];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int k = (i * TPR + t) * V;
+        if (k < p.dim) px[i].load(x + k);
+        else px[i].fill(0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += px[i][j];
+    const float mean = ln_row_sum<TPR>(s, sh[0]) * p.inv_dim;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((i * TPR + t) * V < p.dim) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = px[i][j] - mean;
+                s = fmaf(d, d, s);
+            }
+        }
+    const float var = ln_row_sum<TPR>(s, sh[1]) * p.inv_dim;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+    if (t == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    T *y = p.Y + row * p.dim;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int k = (i * TPR + t) * V;
+        if (k >= p.dim) continue;
+        LnPack<W, V> g, b;
+        if (p.gamma) g.load(p.gamma + k);
+        else g.fill(1.0f);
+        if (p.beta) b.load(p.beta + k);
+        else b.fill(0.0f);
+        LnPack<T, V> out;
+#pragma unroll
+        for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(fmaf((px[i][j] - mean) * rstd, g[j], b[j]));
+        out.store(y + k);
+    }
+}
+
+// Rows longer than a block holds: three passes over the row.
+template <class T, class W>
+__global__ void __launch_bounds__(1024) layer_norm_fwd_long(FwdParams<T, W> p)
+{
+    __shared__ float sh[2][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t row = blockIdx.x;
+    const T *x = p.X + row * p.dim;
+    float s = 0.0f;
+    for (int64_t k = threadIdx.x; k < p.dim; k += 1024) s += ln_float(x[k]);
+    const float mean = ln_row_sum<1024>(s, sh[0]) * p.inv_dim;
+    s = 0.0f;
+    for (int64_t k = threadIdx.x; k < p.dim; k += 1024) {
+        const float d = ln_float(x[k]) - mean;
+        s = fmaf(d, d, s);
+    }
+    const float rstd = 1.0f / sqrtf(ln_row_sum<1024>(s, sh[1]) * p.inv_dim + p.eps);
+    if (threadIdx.x == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    T *y = p.Y + row * p.dim;
+    for (int64_t k = threadIdx.x; k < p.dim; k += 1024) {
+        const float g = p.gamma ? ln_float(p.gamma[k]) : 1.0f, b = p.beta ? ln_float(p.beta[k]) : 0.0f;
+        y[k] = ln_round<T>(fmaf((ln_float(x[k]) - mean) * rstd, g, b));
+    }
+}
+
+template <class T, class W, int V, int NV, int TPR>
+int launch_one(const FwdParams<T, W> &p, cudaStream_t stream)
+{
+    constexpr int BT = TPR < 128 ? 128 : TPR;
+    constexpr int R = BT / TPR;
+    return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR>, dim3(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1),
+                     BT, stream, p);
+}
+
+template <class T, class W, int V>
+int launch_packs(const FwdParams<T, W> &p, cudaStream_t stream)
+{
+    const int packs = (p.dim + V - 1) / V;
+    constexpr int N = V == 1 ? 8 : (sizeof(T) == 2 ? 1 : 2);   // packs of the smallest variant
+    if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
+    if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
+    if (packs <= 32 * 4 * N) return launch_one<T, W, V, 4 * N, 32>(p, stream);
+    if (packs <= 128 * 2 * N) return launch_one<T, W, V, 2 * N, 128>(p, stream);
+    if (packs <= 128 * 4 * N) return launch_one<T, W, V, 4 * N, 128>(p, stream);
+    if (packs <= 512 * 2 * N) return launch_one<T, W, V, 2 * N, 512>(p, stream);
+    if (packs <= 512 * 4 * N) return launch_one<T, W, V, 4 * N, 512>(p, stream);
+    return ln_launch(layer_norm_fwd_long<T, W>, dim3(static_cast<unsigned>(p.rows), 1, 1), 1024, stream, p);
+}
+
+template <class T, class W>
+int forward(const LayerNormArgs &a)
+{
+    FwdParams<T, W> p{};
+    p.X = static_cast<const T *>(a.X);
+    p.gamma = static_cast<const W *>(a.gamma);
+    p.beta = static_cast<const W *>(a.beta);
+    p.Y = static_cast<T *>(a.Y);
+    p.mean = a.mean;
+    p.rstd = a.rstd;
+    p.rows = a.rows;
+    p.dim = static_cast<int32_t>(a.dim);
+    p.inv_dim = 1.0f / static_cast<float>(a.dim);
+    p.eps = a.eps;
+    constexpr int V = 16 / sizeof(T);
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.Y) |
+                           reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.beta);
+    if (a.dim % V == 0 && (bits & 15u) == 0) return launch_packs<T, W, V>(p, a.stream);
+    return launch_packs<T, W, 1>(p, a.stream);
+}
+
+}  // namespace
+
+namespace gemm_sm103 {
+
+int launch_layer_norm_fwd(const LayerNormArgs &a)
+{
+    return ln_dispatch(a.xtype, a.wtype, [&](auto t, auto w) { return forward<decltype(t), decltype(w)>(a); });
+}
+
+}  // namespace gemm_sm103

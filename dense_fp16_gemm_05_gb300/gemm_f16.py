@@ -116,6 +116,13 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_quantize.restype = ci
     L.gemm_mxfp4.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
     L.gemm_mxfp4.restype = ci
+    cf = ctypes.c_float
+    L.layer_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, cf, ci, ci, vp]
+    L.layer_norm_fwd.restype = ci
+    L.layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]
+    L.layer_norm_bwd.restype = ci
+    L.layer_norm_bwd_workspace.argtypes = [i64, i64]
+    L.layer_norm_bwd_workspace.restype = i64
     pi = ctypes.POINTER(ctypes.c_int)
     L.gemm_fp8_launch_info.argtypes = [i64, i64, i64, pi, pi]
     L.gemm_fp8_launch_info.restype = ci
@@ -601,6 +608,116 @@ def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Ten
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mxfp4")
     return C
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_rows(X, name: str = "X") -> tuple[int, int]:
+    if not isinstance(X, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if X.dtype not in TYPES or X.dim() < 1 or not X.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 tensor, "
+                         f"got {X.dtype} {tuple(X.shape)}")
+    dim = X.shape[-1]
+    return (X.numel() // dim if dim else math.prod(X.shape[:-1])), dim
+
+
+def _norm_weight_type(X, *weights) -> torch.dtype:
+    wt = next((w.dtype for w in weights if isinstance(w, torch.Tensor)), X.dtype)
+    if wt != X.dtype and wt != torch.float32:
+        raise ValueError(f"weights must be of X's type {X.dtype} or float32, got {wt}")
+    for w in weights:
+        if w is not None:
+            _check_like(w, "a weight", wt, (X.shape[-1],), X.device)
+    return wt
+
+
+def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                   eps: float = 1e-5, Y: torch.Tensor | None = None, stats: bool = True, stream=None):
+    """(Y, mean, rstd) of layer norm over X's last dimension (see gemm_f16.h).
+
+    X: contiguous float16, bfloat16 or float32 CUDA tensor; gamma, beta: None
+    (ones, zeros) or vectors of X's type or float32.  mean and rstd are float32
+    of X's leading shape, or None without ``stats``.  Asynchronous on ``stream``.
+    """
+    rows, dim = _norm_rows(X)
+    wt = _norm_weight_type(X, gamma, beta)
+    if Y is None:
+        Y = torch.empty_like(X)
+    _check_like(Y, "Y", X.dtype, X.shape, X.device)
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+        rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+    L = lib()
+    with _device_scope(X.device):
+        st = L.layer_norm_fwd(X.data_ptr(), _ptr(gamma), _ptr(beta), Y.data_ptr(), _ptr(mean), _ptr(rstd), rows, dim,
+                              float(eps), TYPES[X.dtype], TYPES[wt], _stream_handle(stream, X.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "layer_norm_fwd")
+    return Y, mean, rstd
+
+
+def layer_norm_bwd_workspace(rows: int, dim: int, device=None) -> int:
+    """Bytes of workspace layer_norm_bwd needs."""
+    with _device_scope(torch.cuda.current_device() if device is None else device):
+        n = int(lib().layer_norm_bwd_workspace(rows, dim))
+    if n < 0:
+        raise GemmError(n, "layer_norm_bwd_workspace")
+    return n
+
+
+def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   gamma: torch.Tensor | None = None, dX: torch.Tensor | None = None, weights: bool = True,
+                   wtype: torch.dtype | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(dX, dgamma, dbeta) of layer_norm_fwd; dgamma and dbeta None without ``weights``.
+
+    dY like X; mean, rstd and gamma as given to and returned by
+    layer_norm_fwd.  dgamma and dbeta have gamma's type (``wtype`` without a
+    gamma, X's type by default).  ``workspace``: a float32 vector of
+    layer_norm_bwd_workspace bytes for callers that keep one; made on the
+    launch stream when not given.  Asynchronous on ``stream``.
+    """
+    rows, dim = _norm_rows(X)
+    _check_like(dY, "dY", X.dtype, X.shape, X.device)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _check_like(t, name, torch.float32, X.shape[:-1], X.device)
+    wt = _norm_weight_type(X, gamma)
+    if gamma is None and wtype is not None:
+        wt = wtype
+        if wt not in (X.dtype, torch.float32):
+            raise ValueError(f"wtype must be X's type {X.dtype} or float32, got {wt}")
+    if dX is None:
+        dX = torch.empty_like(X)
+    _check_like(dX, "dX", X.dtype, X.shape, X.device)
+    L = lib()
+    dgamma = dbeta = None
+    need = 0
+    with _device_scope(X.device):
+        if weights:
+            dgamma = torch.empty((dim,), dtype=wt, device=X.device)
+            dbeta = torch.empty((dim,), dtype=wt, device=X.device)
+            need = L.layer_norm_bwd_workspace(rows, dim)
+            if need < 0:
+                raise GemmError(need, "layer_norm_bwd_workspace")
+            if workspace is None:
+                if stream is None:
+                    workspace = torch.empty((need // 4,), dtype=torch.float32, device=X.device)
+                else:
+                    with torch.cuda.stream(_launch_stream(stream, X.device)):
+                        workspace = torch.empty((need // 4,), dtype=torch.float32, device=X.device)
+            elif (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.float32
+                  or not workspace.is_contiguous() or workspace.device != X.device):
+                raise ValueError("workspace must be a contiguous float32 tensor on X's device")
+        st = L.layer_norm_bwd(dY.data_ptr(), X.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
+                              dX.data_ptr(), _ptr(dgamma), _ptr(dbeta), rows, dim, TYPES[X.dtype], TYPES[wt],
+                              _ptr(workspace) if weights else None, 4 * workspace.numel() if weights else 0,
+                              _stream_handle(stream, X.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "layer_norm_bwd")
+    return dX, dgamma, dbeta
 
 
 def fp8_launch_info(M: int, N: int, K: int) -> dict:

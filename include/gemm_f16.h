@@ -374,6 +374,57 @@ int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, void *V, int
 int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C,
                int64_t M, int64_t N, int64_t K, int relu, void *stream);
 
+/*
+ * layer_norm_fwd -- layer norm over rows of `dim` elements (the norm in front of
+ * a feed-forward or attention block; on the roadmap of the TileLang-MUSA
+ * lesson, 7yue.com, section 7, with its backward pass):
+ *
+ *   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
+ *   Y = (X - mean) rstd gamma + beta
+ *
+ * in fp32, rounded once to X's type.
+ *
+ *   X, Y         device pointers, (rows, dim) row-major, type xtype (enum
+ *                gemm_f16_type)
+ *   gamma, beta  NULL (ones, zeros) or dim elements of type wtype: xtype, or
+ *                GEMM_TYPE_F32
+ *   mean, rstd   NULL (not kept) or rows floats, written, for layer_norm_bwd
+ *   eps          finite, >= 0
+ *
+ * Buffers are aligned to their element (16-byte alignment and rows of a
+ * multiple of 16 bytes select the vectorised path); outputs overlap neither
+ * inputs nor each other.  rows == 0 or dim == 0: no-op.  Only enqueues on `stream`.
+ */
+int layer_norm_fwd(const void *X, const void *gamma, const void *beta, void *Y, float *mean, float *rstd,
+                   int64_t rows, int64_t dim, float eps, int xtype, int wtype, void *stream);
+
+/*
+ * layer_norm_bwd -- gradients of layer_norm_fwd.  With z = (X - mean) rstd and
+ * g = dY gamma:
+ *
+ *   dX = rstd (g - mean_row(g) - z mean_row(g z)),  dgamma = sum_rows dY z,  dbeta = sum_rows dY
+ *
+ * in fp32, each output rounded once; the sums over rows are taken in a fixed
+ * order (equal calls give equal bits on one GPU model).
+ *
+ *   dY, X, gamma, mean, rstd  as given to and kept by layer_norm_fwd
+ *   dX             (rows, dim) of type xtype
+ *   dgamma, dbeta  dim elements of type wtype each, or both NULL (not wanted)
+ *   workspace      layer_norm_bwd_workspace(rows, dim) bytes, 16-byte aligned,
+ *                  written before it is read; may be NULL if dgamma is.  Calls
+ *                  that may run at the same time need one each.
+ *
+ * Outputs and the workspace overlap neither inputs nor each other.  rows == 0:
+ * dgamma and dbeta are filled with zeros; dim == 0: no-op.
+ */
+int layer_norm_bwd(const void *dY, const void *X, const void *gamma, const float *mean, const float *rstd, void *dX,
+                   void *dgamma, void *dbeta, int64_t rows, int64_t dim, int xtype, int wtype, void *workspace,
+                   int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace layer_norm_bwd needs for these sizes on the current
+ * device, or a negative status. */
+int64_t layer_norm_bwd_workspace(int64_t rows, int64_t dim);
+
 /* Launch geometry of gemm_fp8_block_scaled for this problem on the current
  * device: persistent grid in CTAs (CTA pairs over 256 x 256 output tiles) and
  * the number of tiles.  Either pointer may be NULL.  Launches nothing. */
