@@ -108,11 +108,94 @@ int launch_pairs(const Mx4LaunchArgs &a)
     return GEMM_OK;
 }
 
+template <bool kRelu, int kBN, int kStages>
+int launch_narrow(const Mx4LaunchArgs &a, int splits)
+{
+    using Cfg = Mx4NarrowCfg<kBN, kStages>;
+    CUtensorMap ta, tw, tsa, tsw;
+    int st;
+    if ((st = encode_codes_u4(&ta, a.A, a.M, a.K, Cfg::BN)) != GEMM_OK) return st;
+    if ((st = encode_codes_u4(&tw, a.W, a.N, a.K, Cfg::BM)) != GEMM_OK) return st;
+    if ((st = encode_scale_tiles(&tsa, a.SA, a.M, a.K, Cfg::SF_TILES, 1)) != GEMM_OK) return st;
+    if ((st = encode_scale_tiles(&tsw, a.SW, a.N, a.K, Cfg::SF_TILES, 1)) != GEMM_OK) return st;
+
+    Mx4NarrowParams p{};
+    p.M = static_cast<int32_t>(a.M);
+    p.N = static_cast<int32_t>(a.N);
+    p.num_m_tiles = static_cast<int32_t>((a.M + Cfg::BN - 1) / Cfg::BN);
+    p.num_k_blocks = static_cast<int32_t>((a.K + Cfg::BK - 1) / Cfg::BK);
+    p.k_per_cta = (p.num_k_blocks + splits - 1) / splits;
+    p.timeout_cycles = timeout_cycles_for(a.K);
+    p.C = static_cast<__half *>(a.C);
+    p.status = a.status;
+    const int64_t ctas = static_cast<int64_t>(p.num_m_tiles) * ((a.N + Cfg::BM - 1) / Cfg::BM) * splits;
+    if (ctas > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+
+    // Per device: the shared-memory attribute is set once.
+    static std::atomic<int> prepared[kMaxDevices];
+    auto kern = gemm_mxfp4_narrow_sm103a<kRelu, kBN, kStages>;
+    for (int attempt = 0;; ++attempt) {
+        if (!prepared[a.dev.device].load(std::memory_order_acquire)) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) !=
+                cudaSuccess) {
+                cudaGetLastError();
+                return GEMM_ERR_LAUNCH;
+            }
+            prepared[a.dev.device].store(1, std::memory_order_release);
+        }
+        cudaLaunchConfig_t lc{};
+        lc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+        lc.blockDim = dim3(Cfg::THREADS, 1, 1);
+        lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+        lc.stream = a.stream;
+        cudaLaunchAttribute attrs[2];
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = static_cast<unsigned>(splits);
+        attrs[0].val.clusterDim.y = 1;
+        attrs[0].val.clusterDim.z = 1;
+        attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[1].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = attrs;
+        lc.numAttrs = 2;
+        if (cudaLaunchKernelEx(&lc, kern, ta, tw, tsa, tsw, p) == cudaSuccess) return GEMM_OK;
+        cudaGetLastError();
+        prepared[a.dev.device].store(0, std::memory_order_release);
+        if (attempt > 0) return GEMM_ERR_LAUNCH;
+    }
+}
+
+// CTAs of a cluster that share a tile's K loop: as many as the idle CTA slots
+// allow (two per SM), up to 8 and at least one K block each.
+int narrow_splits(int64_t tiles, int64_t k_blocks, int sm_count)
+{
+    int s = 1;
+    while (s < 8 && tiles * (2 * s) <= 2 * static_cast<int64_t>(sm_count) && k_blocks >= 2 * s) s *= 2;
+    // No CTA without K blocks: ceil(k_blocks / s) each.
+    while (s > 1 && (k_blocks + s - 1) / s * (s - 1) >= k_blocks) s /= 2;
+    return s;
+}
+
+template <bool kRelu>
+int launch_variant(const Mx4LaunchArgs &a)
+{
+    const int64_t pair_tiles = ((a.M + Mx4Cfg::TILE_M - 1) / Mx4Cfg::TILE_M) * ((a.N + Mx4Cfg::BN - 1) / Mx4Cfg::BN);
+    if (pair_tiles * 2 >= a.dev.sm_count) return launch_pairs<kRelu>(a);
+    const int64_t w_tiles = (a.N + 127) / 128, k_blocks = (a.K + 255) / 256;
+    const int bn = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : (a.M <= 64 ? 64 : 128));
+    const int s = narrow_splits(w_tiles * ((a.M + bn - 1) / bn), k_blocks, a.dev.sm_count);
+    switch (bn) {
+    case 16: return launch_narrow<kRelu, 16, 5>(a, s);
+    case 32: return launch_narrow<kRelu, 32, 4>(a, s);
+    case 64: return launch_narrow<kRelu, 64, 4>(a, s);
+    default: return launch_narrow<kRelu, 128, 3>(a, s);
+    }
+}
+
 }  // namespace
 
 int launch_mxfp4(const Mx4LaunchArgs &a)
 {
-    return a.relu ? launch_pairs<true>(a) : launch_pairs<false>(a);
+    return a.relu ? launch_variant<true>(a) : launch_variant<false>(a);
 }
 
 }  // namespace gemm_sm103

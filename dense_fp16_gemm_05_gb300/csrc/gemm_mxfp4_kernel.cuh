@@ -85,6 +85,24 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// Loads 16 consecutive fp32 columns of the warp's 32 TMEM lanes and waits.
+__device__ __forceinline__ void tmem_load_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Shared-memory descriptor of a 512-byte scale tile for tcgen05.cp: no
 // swizzle, 8-row groups of 16-byte rows 128 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr)
@@ -131,12 +149,12 @@ struct Mx4Cfg {
     static constexpr int SFA_STAGE_BYTES = SF_TILES * SF_TILE;          // this CTA's 128 rows
     static constexpr int SFW_STAGE_BYTES = 2 * SF_TILES * SF_TILE;      // all 256 columns, in each CTA
     static constexpr int STAGE_TX_BYTES = A_STAGE_BYTES + W_STAGE_BYTES + SFA_STAGE_BYTES + SFW_STAGE_BYTES;
-    static constexpr int SF_SLOTS = 2;         // scale slots in TMEM, used in turn
+    static constexpr int SF_SLOTS = STAGES;    // scale slots in TMEM, one per ring slot
     static constexpr int SFW_COL = 4 * SF_TILES;                        // W words after A's in a slot
     static constexpr int SF_SLOT_COLS = 4 * SF_TILES + 8 * SF_TILES;    // 24 columns
     static constexpr int TMEM_COLS = 512;
-    static constexpr int SF_COL0 = TMEM_COLS - SF_SLOTS * SF_SLOT_COLS; // 464
-    static constexpr int ACC1_COL = SF_COL0 - BN;                       // 208
+    static constexpr int SF_COL0 = TMEM_COLS - SF_SLOTS * SF_SLOT_COLS; // 392
+    static constexpr int ACC1_COL = SF_COL0 - BN;                       // 136
     static constexpr int EPI_COLS = 64;
     static constexpr int EPI_CHUNKS = BN / EPI_COLS;    // 4
     static constexpr int C_BUF_BYTES = 32 * EPI_COLS * 2;   // one warp's 32 rows of one chunk
@@ -150,9 +168,10 @@ struct Mx4Cfg {
     static constexpr int SMEM_BYTES = 1024 + SMEM_CTL_OFF + SMEM_CTL_BYTES;
     static constexpr uint32_t IDESC = idesc_mxf4(TILE_M, BN);
 
-    // The two accumulators share the columns [ACC1_COL, BN): the epilogue reads
-    // those first.
-    static_assert(ACC1_COL + EPI_COLS >= BN && ACC1_COL >= BN - EPI_COLS, "the shared columns lie in one chunk");
+    // The two accumulators share the columns [ACC1_COL, BN); the epilogue reads
+    // the RELEASE chunks that hold those first.
+    static constexpr int RELEASE = (BN - ACC1_COL + EPI_COLS - 1) / EPI_COLS;
+    static_assert(ACC1_COL > 0 && RELEASE < EPI_CHUNKS, "part of the epilogue overlaps the next tile's MMAs");
     static_assert((2 * STAGES + 4) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
     static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
 };
@@ -188,10 +207,13 @@ __device__ __forceinline__ void mx4_tile_coords(int t, const Mx4Params &p, int &
 //                      issues the MMAs, M = 256, N = 256, K = 64
 //   warps 2..5         epilogue: accumulator -> R -> fp16 -> shared memory ->
 //                      TMA store
-// TMEM (512 columns): two accumulators of 256 columns and two scale slots of
-// 24 do not fit beside each other, so the accumulators overlap in 48 columns.
-// The epilogue reads the chunk that holds those columns first and then lets the
-// next tile's MMAs start, which run while it reads and stores the rest.
+// TMEM (512 columns): each ring slot has its own scale slot of 24 columns, so
+// that a full ring slot is all the MMA issuer waits for (two scale slots and a
+// wait for the MMAs of two K blocks ago: SLOTS2US against SLOTS5US at 8192^3).  Two
+// accumulators of 256 columns do not fit beside them, so these overlap in 120
+// columns.  The epilogue reads the two chunks that hold those columns first and
+// then lets the next tile's MMAs start, which run while it reads and stores the
+// rest.
 // Ragged edges: TMA zero-fills operands and scales outside A and W (a zero
 // scale byte is 2^-127, not NaN); rows and columns outside C are not stored.
 // Every wait is bounded; on expiry the site is recorded in the device status
@@ -332,7 +354,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         // ------------------------------------------------------------ MMA issuer (leader CTA)
         if (lane == 0 && leader) {
             int s = 0;
-            uint32_t ph = 0, acc_it = 0, blk = 0;
+            uint32_t ph = 0, acc_it = 0;
             bool ok = true, issued_any = false;
             // K-major SW128 operands: 8-row groups 1024 B apart; a K step of 64
             // elements is +32 B inside the swizzle row.
@@ -349,23 +371,13 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 }
                 tc_fence_after_sync();
                 const uint32_t acc = tmem_base + ((acc_it & 1u) ? Cfg::ACC1_COL : 0);
-                for (int kb = 0; kb < KB; ++kb, ++blk) {
-                    // The scale slot was last used two K blocks ago: its MMAs have
-                    // completed once that block's ring slot is free.
-                    if (blk >= Cfg::SF_SLOTS) {
-                        const uint32_t old = blk - Cfg::SF_SLOTS;
-                        if (!wait_phase(empty_bar(old % S), (old / S) & 1u, abort, limit, kSiteMmaFull)) {
-                            ok = false;
-                            break;
-                        }
-                    }
+                for (int kb = 0; kb < KB; ++kb) {
                     if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t sf =
-                        tmem_base + Cfg::SF_COL0 + (blk % Cfg::SF_SLOTS) * static_cast<uint32_t>(Cfg::SF_SLOT_COLS);
+                    const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
                     const uint64_t sfa_st = sfa_desc0 + static_cast<uint64_t>((s * Cfg::SFA_STAGE_BYTES) >> 4);
                     const uint64_t sfw_st = sfw_desc0 + static_cast<uint64_t>((s * Cfg::SFW_STAGE_BYTES) >> 4);
                     // In shared memory the W tiles are ordered (row block, K tile);
@@ -431,12 +443,12 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 tmem_base + (odd ? Cfg::ACC1_COL : 0) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
             for (int i = 0; i < Cfg::EPI_CHUNKS; ++i) {
-                // The shared columns lie in the last chunk of accumulator 0 and
+                // The shared columns lie in the last chunks of accumulator 0 and
                 // the first of accumulator 1.
                 const int c = odd ? i : Cfg::EPI_CHUNKS - 1 - i;
                 uint32_t r[64];
                 tmem_load_32x32b_x64(acc_addr + static_cast<uint32_t>(c * Cfg::EPI_COLS), r);
-                if (i == 0) {
+                if (i == Cfg::RELEASE - 1) {
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
@@ -479,6 +491,330 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         __syncwarp();
         tc_fence_after_sync();
         tmem_dealloc<2>(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- narrow tiles, K divided over a cluster
+
+// For problems that 256 x 256 tiles leave most SMs idle on: few rows of A (one,
+// when tokens are generated one at a time), where the time is that of reading
+// W.  The operands change places: 128 rows of W are the MMA's M (TMEM lanes),
+// kBN rows of A its N, so a single row of A costs an MMA of N = 16 and not a
+// 128-row tile, and the ring holds mostly W.  The K loop of a tile is divided
+// over the S = 1, 2, 4 or 8 CTAs of a cluster; each leaves its fp32 partial tile
+// in its shared memory, and after a cluster barrier every CTA adds a share of
+// the tile over the S partials in rank order (a fixed order: equal calls give
+// equal bits) and stores fp16.  Two CTAs fit on an SM, so the loads of one run
+// under the set-up and the reduction of the other.
+template <int kBN, int kStages>
+struct Mx4NarrowCfg {
+    static constexpr int BM = 128;             // rows of W per tile (TMEM lanes)
+    static constexpr int BN = kBN;             // rows of A per tile
+    static constexpr int BK = 256;
+    static constexpr int ROW_BYTES = BK / 2;
+    static constexpr int UMMA_K = 64;
+    static constexpr int STEP_BYTES = UMMA_K / 2;
+    static constexpr int SF_TILE = 512;
+    static constexpr int SF_TILES = BK / 128;
+    static constexpr int STAGES = kStages;
+    static constexpr int THREADS = 192;
+    static constexpr int MAX_CLUSTER = 8;
+    static constexpr int W_STAGE_BYTES = BM * ROW_BYTES;
+    static constexpr int X_STAGE_BYTES = BN * ROW_BYTES;
+    static constexpr int SF_STAGE_BYTES = SF_TILES * SF_TILE;   // of W and of A each
+    static constexpr int STAGE_TX_BYTES = W_STAGE_BYTES + X_STAGE_BYTES + 2 * SF_STAGE_BYTES;
+    static constexpr int SF_SLOTS = STAGES;                     // one per ring slot
+    static constexpr int SF_SLOT_COLS = 8 * SF_TILES;           // W's words, then A's
+    static constexpr int SF_COL0 = BN;
+    static constexpr int TMEM_USED = BN + SF_SLOTS * SF_SLOT_COLS;
+    static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : (TMEM_USED <= 128 ? 128 : 256);
+    static constexpr int PART_BYTES = BM * BN * 4;              // in the ring, once the MMAs are done
+    static constexpr int SMEM_W_OFF = 0;
+    static constexpr int SMEM_X_OFF = STAGES * W_STAGE_BYTES;
+    static constexpr int SMEM_SFW_OFF = SMEM_X_OFF + STAGES * X_STAGE_BYTES;
+    static constexpr int SMEM_SFX_OFF = SMEM_SFW_OFF + STAGES * SF_STAGE_BYTES;
+    static constexpr int SMEM_CTL_OFF = SMEM_SFX_OFF + STAGES * SF_STAGE_BYTES;
+    static constexpr int SMEM_CTL_BYTES = 256;
+    static constexpr int SMEM_BYTES = 1024 + SMEM_CTL_OFF + SMEM_CTL_BYTES;
+    static constexpr uint32_t IDESC = idesc_mxf4(BM, BN);
+
+    static_assert(BN % 16 == 0 && BN <= 128, "N of the MMA; scale words of one row block");
+    static_assert(PART_BYTES <= STAGES * (W_STAGE_BYTES + X_STAGE_BYTES), "the partial tile fits in the ring");
+    static_assert((2 * STAGES + 2) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct Mx4NarrowParams {
+    int32_t M, N;
+    int32_t num_m_tiles;    // ceil(M / BN)
+    int32_t num_k_blocks;   // ceil(K / 256)
+    int32_t k_per_cta;      // K blocks of each CTA of a cluster
+    uint64_t timeout_cycles;
+    __half *C;
+    unsigned long long *status;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Adds CTA crank's share of the tile over the S partial tiles in rank order.
+// Item i: row i / 16 of A and rows 8 (i % 16) .. + 7 of W, consecutive items to
+// a CTA.  All S pairs of loads are issued before the first is used: one after
+// another they cost S round trips through the cluster (23 us against 12 for
+// 128 x 4096 x 4096).
+template <int S, bool kRelu, int kBN>
+__device__ __forceinline__ void mx4_reduce(const Mx4NarrowParams &p, uint32_t part, uint32_t crank, int m0, int n0,
+                                           int t)
+{
+    constexpr int PER_ROW = 128 / 8;
+    const int items = min(kBN, p.M - m0) * PER_ROW;
+    const int per = (items + S - 1) / S;
+    const int i1 = min(items, per * (static_cast<int>(crank) + 1));
+    uint32_t src[S];
+#pragma unroll
+    for (int c = 0; c < S; ++c) src[c] = S == 1 ? part : mapa_shared(part, static_cast<uint32_t>(c));
+    for (int i = per * static_cast<int>(crank) + t; i < i1; i += 128) {
+        const int j = i / PER_ROW, w8 = i % PER_ROW;
+        if (n0 + 8 * w8 >= p.N) continue;   // N is a multiple of 8
+        const uint32_t off = static_cast<uint32_t>(j * 512 + w8 * 32);
+        float4 lo[S], hi[S];
+#pragma unroll
+        for (int c = 0; c < S; ++c) {
+            lo[c] = ld_cluster_f32x4(src[c] + off);
+            hi[c] = ld_cluster_f32x4(src[c] + off + 16u);
+        }
+#pragma unroll
+        for (int c = 1; c < S; ++c) {
+            lo[0].x += lo[c].x;
+            lo[0].y += lo[c].y;
+            lo[0].z += lo[c].z;
+            lo[0].w += lo[c].w;
+            hi[0].x += hi[c].x;
+            hi[0].y += hi[c].y;
+            hi[0].z += hi[c].z;
+            hi[0].w += hi[c].w;
+        }
+        st_global_v4(p.C + static_cast<int64_t>(m0 + j) * p.N + n0 + 8 * w8,
+                     pack_f16x2<kRelu>(__float_as_uint(lo[0].x), __float_as_uint(lo[0].y)),
+                     pack_f16x2<kRelu>(__float_as_uint(lo[0].z), __float_as_uint(lo[0].w)),
+                     pack_f16x2<kRelu>(__float_as_uint(hi[0].x), __float_as_uint(hi[0].y)),
+                     pack_f16x2<kRelu>(__float_as_uint(hi[0].z), __float_as_uint(hi[0].w)));
+    }
+}
+
+// Warp 0: TMA producer.  Warp 1: scale copies and MMAs.  Warps 2..5: partial
+// tile to shared memory, then the sum over the cluster.
+template <bool kRelu, int kBN, int kStages>
+__global__ void __launch_bounds__(192, 2)
+    gemm_mxfp4_narrow_sm103a(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                             const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sw,
+                             const Mx4NarrowParams p)
+{
+    using Cfg = Mx4NarrowCfg<kBN, kStages>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *base_ptr = smem_raw + (base - raw);
+
+    const uint32_t sW = base + Cfg::SMEM_W_OFF;
+    const uint32_t sX = base + Cfg::SMEM_X_OFF;
+    const uint32_t sSFW = base + Cfg::SMEM_SFW_OFF;
+    const uint32_t sSFX = base + Cfg::SMEM_SFX_OFF;
+    const uint32_t ctl = base + Cfg::SMEM_CTL_OFF;
+    constexpr int S = Cfg::STAGES;
+    auto full_bar = [&](int s) { return ctl + 8u * s; };
+    auto empty_bar = [&](int s) { return ctl + 8u * (S + s); };
+    const uint32_t tfull_bar = ctl + 8u * (2 * S);
+    const uint32_t tmem_slot = ctl + 8u * (2 * S + 1);
+    volatile uint32_t *tmem_slot_ptr =
+        reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (2 * S + 1));
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t ncl = cluster_nctarank();
+
+    AbortFlag abort;
+    abort.local = reinterpret_cast<volatile int *>(tmem_slot_ptr + 1);
+    abort.status = p.status;
+    abort.addr = tmem_slot + 4;
+    abort.cluster = ncl;
+    abort.rank = crank;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(tfull_bar, 1);
+        *abort.local = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmap_w);
+        prefetch_tensormap(&tmap_a);
+        prefetch_tensormap(&tmap_sw);
+        prefetch_tensormap(&tmap_sa);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish<1>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (ncl > 1) {
+        // Every abort flag of the cluster is zero before any CTA may raise one.
+        cluster_arrive();
+        cluster_wait();
+    }
+    tc_fence_after_sync();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint64_t limit = p.timeout_cycles;
+    const int unit = static_cast<int>(blockIdx.x / ncl);
+    const int mt = unit % p.num_m_tiles, wb = unit / p.num_m_tiles;   // neighbours share W's rows
+    const int m0 = mt * Cfg::BN, n0 = wb * Cfg::BM;
+    const int kb0 = static_cast<int>(crank) * p.k_per_cta;
+    const int kb1 = min(p.num_k_blocks, kb0 + p.k_per_cta);   // the launch leaves no CTA without K blocks
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t issued_mask = 0, issued_parity = 0;
+            bool ok = true;
+            griddep_wait();
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_phase(empty_bar(s), ph ^ 1u, abort, limit, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_TX_BYTES);
+                tma_load_2d(sW + s * Cfg::W_STAGE_BYTES, &tmap_w, full_bar(s), kb * Cfg::ROW_BYTES, n0);
+                tma_load_2d(sX + s * Cfg::X_STAGE_BYTES, &tmap_a, full_bar(s), kb * Cfg::ROW_BYTES, m0);
+                tma_load_3d_cta(sSFW + s * Cfg::SF_STAGE_BYTES, &tmap_sw, full_bar(s), 0, kb * Cfg::SF_TILES, wb);
+                tma_load_3d_cta(sSFX + s * Cfg::SF_STAGE_BYTES, &tmap_sa, full_bar(s), 0, kb * Cfg::SF_TILES,
+                                m0 / 128);
+                issued_mask |= 1u << s;
+                issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) {
+                // Let the loads in flight land before the CTA exits.
+                for (int i = 0; i < S; ++i)
+                    if (issued_mask & (1u << i))
+                        wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
+            const uint64_t x_desc0 = smem_desc_sw128(sX, 16, 1024);
+            const uint64_t sfw_desc0 = smem_desc_scales(sSFW);
+            const uint64_t sfx_desc0 = smem_desc_scales(sSFX);
+            // Row m0 of A is at word column (m0 % 128) / 32 of its scale tiles.
+            const uint32_t sfx_word = static_cast<uint32_t>((m0 % 128) / 32);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
+                const uint64_t sfw_st = sfw_desc0 + static_cast<uint64_t>((s * Cfg::SF_STAGE_BYTES) >> 4);
+                const uint64_t sfx_st = sfx_desc0 + static_cast<uint64_t>((s * Cfg::SF_STAGE_BYTES) >> 4);
+#pragma unroll
+                for (int i = 0; i < Cfg::SF_TILES; ++i) {
+                    tmem_copy_scales<1>(sf + 4u * i, sfw_st + static_cast<uint64_t>((i * Cfg::SF_TILE) >> 4));
+                    tmem_copy_scales<1>(sf + 4u * (Cfg::SF_TILES + i),
+                                        sfx_st + static_cast<uint64_t>((i * Cfg::SF_TILE) >> 4));
+                }
+                const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
+                const uint64_t x_st = x_desc0 + static_cast<uint64_t>((s * Cfg::X_STAGE_BYTES) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < Cfg::BK / Cfg::UMMA_K; ++ks) {
+                    const uint64_t step = static_cast<uint64_t>((ks * Cfg::STEP_BYTES) >> 4);
+                    const uint32_t id = (ks & 1) * 2;
+                    mma_mxf4<1>(tmem_base, w_st + step, x_st + step, Cfg::IDESC | (id << 4) | (id << 29),
+                                sf + 4u * (ks / 2), sf + 4u * (Cfg::SF_TILES + ks / 2) + sfx_word,
+                                (kb != kb0 || ks != 0) ? 1u : 0u);
+                }
+                mma_commit(empty_bar(s));
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            // Also after an abort: the wait below frees the TMEM only once this
+            // thread's MMAs are done.
+            mma_commit(tfull_bar);
+            if (!ok) wait_phase_drain(tfull_bar, 0, limit, kSiteDrainMma, p.status);
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3;
+        const int rows = min(Cfg::BN, p.M - m0);   // rows of A in this tile
+        int ok = 1;
+        if (lane == 0) ok = wait_phase(tfull_bar, 0, abort, limit, kSiteEpilogueTmemFull) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok) {
+            tc_fence_after_sync();
+            // Partial tile: value (row j of A, row w of W) at float j * 128 + w.
+            const uint32_t part = sW + static_cast<uint32_t>(q * 32 + lane) * 4u;
+            const uint32_t acc = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+            for (int j0 = 0; j0 < rows; j0 += 16) {
+                uint32_t r[16];
+                tmem_load_32x32b_x16(acc + static_cast<uint32_t>(j0), r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) st_shared_u32(part + static_cast<uint32_t>(j0 + j) * 512u, r[j]);
+            }
+        }
+    }
+
+    // Every partial tile of the cluster is written.
+    tc_fence_before_sync();
+    if (ncl > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    if (warp >= 2 && !abort.raised()) {
+        griddep_wait();   // before this thread's first store of C
+        const int t = static_cast<int>(threadIdx.x) - 64;
+        switch (ncl) {
+        case 1: mx4_reduce<1, kRelu, Cfg::BN>(p, sW, crank, m0, n0, t); break;
+        case 2: mx4_reduce<2, kRelu, Cfg::BN>(p, sW, crank, m0, n0, t); break;
+        case 4: mx4_reduce<4, kRelu, Cfg::BN>(p, sW, crank, m0, n0, t); break;
+        default: mx4_reduce<8, kRelu, Cfg::BN>(p, sW, crank, m0, n0, t); break;
+        }
+    }
+    __syncwarp();
+    if (ncl > 1) {
+        // No CTA exits while another may still read its shared memory.
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem_base, Cfg::TMEM_COLS);
     }
 }
 
