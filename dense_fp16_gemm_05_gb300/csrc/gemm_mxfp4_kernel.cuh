@@ -6,13 +6,19 @@
 // A (M,K) and W (N,K) hold two codes per byte (element 2i in the low half),
 // row pitch 16 ceil(K/32) bytes; the scale bytes come in 512-byte tiles of 128
 // rows x 4 blocks, byte (r % 32) * 16 + (r / 32) * 4 + b, tiles of a row block
-// adjacent along K.  That order is what one tcgen05.cp.32x128b.warpx4 moves
-// into four TMEM columns: row r's word at lane r % 32, column r / 32, its four
-// bytes the scales of four K blocks.  tcgen05.mma.kind::mxf4 (K = 64, two
-// scales per row) then takes bytes 0-1 or 2-3 of the words, as the instruction
-// descriptor's scale ids 0 or 2 say.  So scales go from global memory to the
-// MMA without passing through a register: a TMA load beside the operands' and
-// one copy instruction per tile.
+// adjacent along K.  That is the order of the tensor core's scale memory: four
+// TMEM columns hold a tile, row r's word at lane r % 32 (in each 32-lane
+// quarter), column r / 32, its four bytes the scales of four K blocks of 32.
+// tcgen05.mma.kind::mxf4 (K = 64, two scales per row) takes bytes 0-1 or 2-3 of
+// the words, as the instruction descriptor's scale ids 0 or 2 say.
+//
+// The tiles come by TMA beside the operands; four scale warps, one per quarter,
+// read a tile's rows (16 bytes per lane) from shared memory and store them into
+// TMEM.  tcgen05.cp would move a tile with one instruction, but between the MMAs
+// of one K block and the next it drains the tensor pipe: the copies of a K
+// block cost about 300 cycles beside 512 of MMAs whether they are two or six
+// (8192^3: 231 us with copies, 165 us with the copies left out), while a
+// store from another warp runs beside the MMAs (185 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -50,37 +56,34 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
             : "memory");
 }
 
-// Copies one 512-byte scale tile from shared memory into four TMEM columns,
-// repeated for each of the four 32-lane quarters (in both CTAs of a pair for
-// cta_group::2, each from its own shared memory at the same offset).  Ordered
-// before the MMAs that this thread issues after it.
-template <int kCtaGroup>
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t s_desc)
+__device__ __forceinline__ uint4 ld_shared_u32x4(uint32_t addr)
 {
-    if constexpr (kCtaGroup == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
 }
 
+// Stores two scale tiles (this lane's 16 bytes of each) into eight consecutive
+// columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_store_scales(uint32_t taddr, const uint4 &a, const uint4 &b)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
+// Waits until this thread's TMEM stores are complete.
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // 3-D tiled load of one box (coordinates x, y, z), completion counted on a
-// barrier of this CTA, or (pair form) of either CTA of a pair.
+// barrier of this CTA.
 __device__ __forceinline__ void tma_load_3d_cta(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
                                                 int32_t y, int32_t z)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
             "r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
-                                                 int32_t y, int32_t z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
@@ -101,18 +104,6 @@ __device__ __forceinline__ void tmem_load_32x32b_x16(uint32_t taddr, uint32_t (&
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// Shared-memory descriptor of a 512-byte scale tile for tcgen05.cp: no
-// swizzle, 8-row groups of 16-byte rows 128 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr)
-{
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1) << 16;           // leading-dimension offset: one 16-byte row wide, not used
-    d |= static_cast<uint64_t>(128 >> 4) << 32;    // stride between 8-row groups
-    d |= static_cast<uint64_t>(1) << 46;
-    return d;
 }
 
 // Instruction descriptor for tcgen05.mma.kind::mxf4: E2M1 A and B (format 1 in
@@ -143,12 +134,13 @@ struct Mx4Cfg {
     static constexpr int SF_TILE = 512;        // bytes of a scale tile: 128 rows x 4 blocks of 32
     static constexpr int SF_TILES = BK / 128;  // scale tiles per row block and K block
     static constexpr int STAGES = 5;
-    static constexpr int THREADS = 192;
+    static constexpr int THREADS = 320;
     static constexpr int A_STAGE_BYTES = BM * ROW_BYTES;                // 16 KiB
     static constexpr int W_STAGE_BYTES = BN_CTA * ROW_BYTES;            // 16 KiB
     static constexpr int SFA_STAGE_BYTES = SF_TILES * SF_TILE;          // this CTA's 128 rows
     static constexpr int SFW_STAGE_BYTES = 2 * SF_TILES * SF_TILE;      // all 256 columns, in each CTA
-    static constexpr int STAGE_TX_BYTES = A_STAGE_BYTES + W_STAGE_BYTES + SFA_STAGE_BYTES + SFW_STAGE_BYTES;
+    static constexpr int STAGE_TX_BYTES = A_STAGE_BYTES + W_STAGE_BYTES;
+    static constexpr int SF_TX_BYTES = SFA_STAGE_BYTES + SFW_STAGE_BYTES;
     static constexpr int SF_SLOTS = STAGES;    // scale slots in TMEM, one per ring slot
     static constexpr int SFW_COL = 4 * SF_TILES;                        // W words after A's in a slot
     static constexpr int SF_SLOT_COLS = 4 * SF_TILES + 8 * SF_TILES;    // 24 columns
@@ -172,7 +164,8 @@ struct Mx4Cfg {
     // the RELEASE chunks that hold those first.
     static constexpr int RELEASE = (BN - ACC1_COL + EPI_COLS - 1) / EPI_COLS;
     static_assert(ACC1_COL > 0 && RELEASE < EPI_CHUNKS, "part of the epilogue overlaps the next tile's MMAs");
-    static_assert((2 * STAGES + 4) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert((4 * STAGES + 4) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert(SF_TILES == 2, "the scale warps' stores");
     static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
 };
 
@@ -200,18 +193,19 @@ __device__ __forceinline__ void mx4_tile_coords(int t, const Mx4Params &p, int &
 
 // Roles per CTA:
 //   warp 0, one lane   TMA producer: per K block a box of A and of W (128 bytes
-//                      x 128 rows each) and the scale tiles of A's 128 rows and
-//                      of the tile's 256 columns, completing on the pair
-//                      leader's "full" barrier
-//   warp 1, one lane   (leader CTA only) copies the scale tiles into TMEM and
-//                      issues the MMAs, M = 256, N = 256, K = 64
+//                      x 128 rows each), completing on the pair leader's "full"
+//                      barrier, and the scale tiles of A's 128 rows and of the
+//                      tile's 256 columns, completing on this CTA's "scales
+//                      full" barrier
+//   warp 1, one lane   (leader CTA only) issues the MMAs, M = 256, N = 256, K = 64
 //   warps 2..5         epilogue: accumulator -> R -> fp16 -> shared memory ->
 //                      TMA store
-// TMEM (512 columns): each ring slot has its own scale slot of 24 columns, so
-// that a full ring slot is all the MMA issuer waits for (two scale slots and a
-// wait for the MMAs of two K blocks ago: SLOTS2US against SLOTS5US at 8192^3).  Two
-// accumulators of 256 columns do not fit beside them, so these overlap in 120
-// columns.  The epilogue reads the two chunks that hold those columns first and
+//   warps 6..9         scale warps: tiles from shared memory to TMEM, then an
+//                      arrival on the leader's "scales ready" barrier
+// TMEM (512 columns): each ring slot has its own scale slot of 24 columns, free
+// again when the ring slot is: the scale warps need no barrier of their own for
+// it.  Two accumulators of 256 columns do not fit beside them, so these overlap
+// in 120 columns.  The epilogue reads the two chunks that hold those columns first and
 // then lets the next tile's MMAs start, which run while it reads and stores the
 // rest.
 // Ragged edges: TMA zero-fills operands and scales outside A and W (a zero
@@ -239,13 +233,15 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     constexpr int S = Cfg::STAGES;
     auto full_bar = [&](int s) { return ctl + 8u * s; };
     auto empty_bar = [&](int s) { return ctl + 8u * (S + s); };
-    const uint32_t tfull_bar = ctl + 8u * (2 * S);
-    const uint32_t tempty_bar = ctl + 8u * (2 * S + 1);
-    const uint32_t drain_bar = ctl + 8u * (2 * S + 2);
-    const uint32_t tmem_slot = ctl + 8u * (2 * S + 3);
+    auto sfull_bar = [&](int s) { return ctl + 8u * (2 * S + s); };
+    auto sready_bar = [&](int s) { return ctl + 8u * (3 * S + s); };
+    const uint32_t tfull_bar = ctl + 8u * (4 * S);
+    const uint32_t tempty_bar = ctl + 8u * (4 * S + 1);
+    const uint32_t drain_bar = ctl + 8u * (4 * S + 2);
+    const uint32_t tmem_slot = ctl + 8u * (4 * S + 3);
     const uint32_t abort_addr = tmem_slot + 4;
     volatile uint32_t *tmem_slot_ptr =
-        reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (2 * S + 3));
+        reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (4 * S + 3));
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -264,6 +260,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 2);    // each CTA's arrive.expect_tx (used on the leader)
             mbar_init(empty_bar(s), 1);   // one MMA commit, sent to both CTAs
+            mbar_init(sfull_bar(s), 1);   // this CTA's scale tiles
+            mbar_init(sready_bar(s), 8);  // one arrive per scale warp of both CTAs (used on the leader)
         }
         mbar_init(tfull_bar, 1);          // one MMA commit, sent to both CTAs
         mbar_init(tempty_bar, 8);         // one arrive per epilogue warp of both CTAs
@@ -322,9 +320,11 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                     tma_load_2d_pair(sA + s * Cfg::A_STAGE_BYTES, &tmap_a, fb, kb * Cfg::ROW_BYTES, m0);
                     tma_load_2d_pair(sW + s * Cfg::W_STAGE_BYTES, &tmap_w, fb, kb * Cfg::ROW_BYTES, n0);
                     // Scale tiles: (word in the tile, tile along K, row block).
-                    tma_load_3d_pair(sSFA + s * Cfg::SFA_STAGE_BYTES, &tmap_sa, fb, 0, kb * Cfg::SF_TILES,
-                                     mb * 2 + static_cast<int>(rank));
-                    tma_load_3d_pair(sSFW + s * Cfg::SFW_STAGE_BYTES, &tmap_sw, fb, 0, kb * Cfg::SF_TILES, nb * 2);
+                    mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
+                    tma_load_3d_cta(sSFA + s * Cfg::SFA_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES,
+                                    mb * 2 + static_cast<int>(rank));
+                    tma_load_3d_cta(sSFW + s * Cfg::SFW_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0, kb * Cfg::SF_TILES,
+                                    nb * 2);
                     issued_mask |= 1u << s;
                     issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
                     if (++s == S) {
@@ -334,14 +334,17 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 }
             }
             if (!ok) {
+                // Let the loads in flight land before the CTA exits.
+                for (int i = 0; i < S; ++i)
+                    if (issued_mask & (1u << i))
+                        wait_phase_drain(sfull_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
                 if (leader) {
-                    // Let the loads in flight land before the CTA exits.
                     for (int i = 0; i < S; ++i)
                         if (issued_mask & (1u << i))
                             wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads,
                                              p.status);
                 } else {
-                    // This CTA's loads complete on the leader's barrier, which it
+                    // This CTA's operand loads complete on the leader's barrier, which it
                     // cannot probe: give them a bounded time (~1e6 cycles) to land.
                     const long long t0 = clock64();
                     while (clock64() - t0 < 1000000) {
@@ -360,8 +363,6 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             // elements is +32 B inside the swizzle row.
             const uint64_t a_desc0 = smem_desc_sw128(sA, 16, 1024);
             const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
-            const uint64_t sfa_desc0 = smem_desc_scales(sSFA);
-            const uint64_t sfw_desc0 = smem_desc_scales(sSFW);
             for (int t = first; ok && t < p.num_tiles; t += stride, ++acc_it) {
                 // The epilogue has read the columns that this tile's accumulator
                 // shares with the previous one's (and all of the one before).
@@ -372,25 +373,13 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 tc_fence_after_sync();
                 const uint32_t acc = tmem_base + ((acc_it & 1u) ? Cfg::ACC1_COL : 0);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull)) {
+                    if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull) ||
+                        !wait_phase(sready_bar(s), ph, abort, limit, kSiteMmaFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
-                    const uint64_t sfa_st = sfa_desc0 + static_cast<uint64_t>((s * Cfg::SFA_STAGE_BYTES) >> 4);
-                    const uint64_t sfw_st = sfw_desc0 + static_cast<uint64_t>((s * Cfg::SFW_STAGE_BYTES) >> 4);
-                    // In shared memory the W tiles are ordered (row block, K tile);
-                    // in TMEM the eight columns of one K tile are adjacent.
-#pragma unroll
-                    for (int i = 0; i < Cfg::SF_TILES; ++i) {
-                        tmem_copy_scales<2>(sf + 4u * i, sfa_st + static_cast<uint64_t>((i * Cfg::SF_TILE) >> 4));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tmem_copy_scales<2>(sf + Cfg::SFW_COL + 8u * i + 4u * h,
-                                                sfw_st + static_cast<uint64_t>(
-                                                             ((h * Cfg::SF_TILES + i) * Cfg::SF_TILE) >> 4));
-                    }
                     const uint64_t a_st = a_desc0 + static_cast<uint64_t>((s * Cfg::A_STAGE_BYTES) >> 4);
                     const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
 #pragma unroll
@@ -419,6 +408,44 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             }
         }
         __syncwarp();
+    } else if (warp >= 6) {
+        // ------------------------------------------------------------ scale warps (6..9)
+        const int q = warp & 3;        // TMEM lane quarter this warp may access
+        const uint32_t sready0 = leader ? sready_bar(0) : mapa_shared(sready_bar(0), 0);
+        const uint32_t row = static_cast<uint32_t>(lane) * 16u;
+        const int total = first < p.num_tiles ? (p.num_tiles - first + stride - 1) / stride * KB : 0;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int blk = 0; blk < total; ++blk) {
+            int ok = 1;
+            if (lane == 0) ok = wait_phase(sfull_bar(s), ph, abort, limit, kSiteMmaTmemEmpty) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            // The producer refilled this ring slot after the MMAs that read the
+            // scale slot had completed.
+            tc_fence_after_sync();
+            const uint32_t a = sSFA + static_cast<uint32_t>(s * Cfg::SFA_STAGE_BYTES) + row;
+            const uint32_t w = sSFW + static_cast<uint32_t>(s * Cfg::SFW_STAGE_BYTES) + row;
+            const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS) +
+                                (static_cast<uint32_t>(q * 32) << 16);
+            // Shared memory holds W's tiles as (row block, K tile); in TMEM the
+            // eight columns of one K tile are adjacent.
+            tmem_store_scales(sf, ld_shared_u32x4(a), ld_shared_u32x4(a + Cfg::SF_TILE));
+            tmem_store_scales(sf + Cfg::SFW_COL, ld_shared_u32x4(w), ld_shared_u32x4(w + 2 * Cfg::SF_TILE));
+            tmem_store_scales(sf + Cfg::SFW_COL + 8, ld_shared_u32x4(w + Cfg::SF_TILE),
+                              ld_shared_u32x4(w + 3 * Cfg::SF_TILE));
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(sready_bar(s));
+                else mbar_arrive_cluster(sready0 + 8u * static_cast<uint32_t>(s));
+            }
+            if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
     } else {
         // ------------------------------------------------------------ epilogue (warps 2..5)
         const int ew = warp - 2;       // owner of smem staging buffers
@@ -522,7 +549,8 @@ struct Mx4NarrowCfg {
     static constexpr int W_STAGE_BYTES = BM * ROW_BYTES;
     static constexpr int X_STAGE_BYTES = BN * ROW_BYTES;
     static constexpr int SF_STAGE_BYTES = SF_TILES * SF_TILE;   // of W and of A each
-    static constexpr int STAGE_TX_BYTES = W_STAGE_BYTES + X_STAGE_BYTES + 2 * SF_STAGE_BYTES;
+    static constexpr int STAGE_TX_BYTES = W_STAGE_BYTES + X_STAGE_BYTES;
+    static constexpr int SF_TX_BYTES = 2 * SF_STAGE_BYTES;
     static constexpr int SF_SLOTS = STAGES;                     // one per ring slot
     static constexpr int SF_SLOT_COLS = 8 * SF_TILES;           // W's words, then A's
     static constexpr int SF_COL0 = BN;
@@ -538,9 +566,10 @@ struct Mx4NarrowCfg {
     static constexpr int SMEM_BYTES = 1024 + SMEM_CTL_OFF + SMEM_CTL_BYTES;
     static constexpr uint32_t IDESC = idesc_mxf4(BM, BN);
 
+    static_assert(SF_TILES == 2, "the scale warps' stores");
     static_assert(BN % 16 == 0 && BN <= 128, "N of the MMA; scale words of one row block");
     static_assert(PART_BYTES <= STAGES * (W_STAGE_BYTES + X_STAGE_BYTES), "the partial tile fits in the ring");
-    static_assert((2 * STAGES + 2) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert((4 * STAGES + 2) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
     static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
@@ -609,8 +638,8 @@ __device__ __forceinline__ void mx4_reduce(const Mx4NarrowParams &p, uint32_t pa
     }
 }
 
-// Warp 0: TMA producer.  Warp 1: scale copies and MMAs.  Warps 2..5: partial
-// tile to shared memory, then the sum over the cluster.
+// Warp 0: TMA producer.  Warp 1: MMAs.  Warps 2..5: scale tiles to TMEM; then
+// the partial tile to shared memory and the sum over the cluster.
 template <bool kRelu, int kBN, int kStages>
 __global__ void __launch_bounds__(192, 2)
     gemm_mxfp4_narrow_sm103a(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
@@ -631,10 +660,12 @@ __global__ void __launch_bounds__(192, 2)
     constexpr int S = Cfg::STAGES;
     auto full_bar = [&](int s) { return ctl + 8u * s; };
     auto empty_bar = [&](int s) { return ctl + 8u * (S + s); };
-    const uint32_t tfull_bar = ctl + 8u * (2 * S);
-    const uint32_t tmem_slot = ctl + 8u * (2 * S + 1);
+    auto sfull_bar = [&](int s) { return ctl + 8u * (2 * S + s); };
+    auto sready_bar = [&](int s) { return ctl + 8u * (3 * S + s); };
+    const uint32_t tfull_bar = ctl + 8u * (4 * S);
+    const uint32_t tmem_slot = ctl + 8u * (4 * S + 1);
     volatile uint32_t *tmem_slot_ptr =
-        reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (2 * S + 1));
+        reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (4 * S + 1));
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -652,6 +683,8 @@ __global__ void __launch_bounds__(192, 2)
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(sfull_bar(s), 1);
+            mbar_init(sready_bar(s), 4);   // one arrive per scale warp
         }
         mbar_init(tfull_bar, 1);
         *abort.local = 0;
@@ -699,8 +732,9 @@ __global__ void __launch_bounds__(192, 2)
                 mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_TX_BYTES);
                 tma_load_2d(sW + s * Cfg::W_STAGE_BYTES, &tmap_w, full_bar(s), kb * Cfg::ROW_BYTES, n0);
                 tma_load_2d(sX + s * Cfg::X_STAGE_BYTES, &tmap_a, full_bar(s), kb * Cfg::ROW_BYTES, m0);
-                tma_load_3d_cta(sSFW + s * Cfg::SF_STAGE_BYTES, &tmap_sw, full_bar(s), 0, kb * Cfg::SF_TILES, wb);
-                tma_load_3d_cta(sSFX + s * Cfg::SF_STAGE_BYTES, &tmap_sa, full_bar(s), 0, kb * Cfg::SF_TILES,
+                mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
+                tma_load_3d_cta(sSFW + s * Cfg::SF_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0, kb * Cfg::SF_TILES, wb);
+                tma_load_3d_cta(sSFX + s * Cfg::SF_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES,
                                 m0 / 128);
                 issued_mask |= 1u << s;
                 issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
@@ -712,8 +746,10 @@ __global__ void __launch_bounds__(192, 2)
             if (!ok) {
                 // Let the loads in flight land before the CTA exits.
                 for (int i = 0; i < S; ++i)
-                    if (issued_mask & (1u << i))
+                    if (issued_mask & (1u << i)) {
                         wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+                        wait_phase_drain(sfull_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+                    }
             }
         }
         __syncwarp();
@@ -724,25 +760,16 @@ __global__ void __launch_bounds__(192, 2)
             bool ok = true;
             const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
             const uint64_t x_desc0 = smem_desc_sw128(sX, 16, 1024);
-            const uint64_t sfw_desc0 = smem_desc_scales(sSFW);
-            const uint64_t sfx_desc0 = smem_desc_scales(sSFX);
             // Row m0 of A is at word column (m0 % 128) / 32 of its scale tiles.
             const uint32_t sfx_word = static_cast<uint32_t>((m0 % 128) / 32);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull)) {
+                if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull) ||
+                    !wait_phase(sready_bar(s), ph, abort, limit, kSiteMmaFull)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
                 const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
-                const uint64_t sfw_st = sfw_desc0 + static_cast<uint64_t>((s * Cfg::SF_STAGE_BYTES) >> 4);
-                const uint64_t sfx_st = sfx_desc0 + static_cast<uint64_t>((s * Cfg::SF_STAGE_BYTES) >> 4);
-#pragma unroll
-                for (int i = 0; i < Cfg::SF_TILES; ++i) {
-                    tmem_copy_scales<1>(sf + 4u * i, sfw_st + static_cast<uint64_t>((i * Cfg::SF_TILE) >> 4));
-                    tmem_copy_scales<1>(sf + 4u * (Cfg::SF_TILES + i),
-                                        sfx_st + static_cast<uint64_t>((i * Cfg::SF_TILE) >> 4));
-                }
                 const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
                 const uint64_t x_st = x_desc0 + static_cast<uint64_t>((s * Cfg::X_STAGE_BYTES) >> 4);
 #pragma unroll
@@ -769,7 +796,33 @@ __global__ void __launch_bounds__(192, 2)
         const int q = warp & 3;
         const int rows = min(Cfg::BN, p.M - m0);   // rows of A in this tile
         int ok = 1;
-        if (lane == 0) ok = wait_phase(tfull_bar, 0, abort, limit, kSiteEpilogueTmemFull) ? 1 : 0;
+        // Scale tiles from shared memory to TMEM, as long as there are K blocks.
+        {
+            const uint32_t row = static_cast<uint32_t>(lane) * 16u;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (lane == 0) ok = wait_phase(sfull_bar(s), ph, abort, limit, kSiteMmaTmemEmpty) ? 1 : 0;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t w = sSFW + static_cast<uint32_t>(s * Cfg::SF_STAGE_BYTES) + row;
+                const uint32_t x = sSFX + static_cast<uint32_t>(s * Cfg::SF_STAGE_BYTES) + row;
+                const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS) +
+                                    (static_cast<uint32_t>(q * 32) << 16);
+                tmem_store_scales(sf, ld_shared_u32x4(w), ld_shared_u32x4(w + Cfg::SF_TILE));
+                tmem_store_scales(sf + 8, ld_shared_u32x4(x), ld_shared_u32x4(x + Cfg::SF_TILE));
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sready_bar(s));
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (ok && lane == 0) ok = wait_phase(tfull_bar, 0, abort, limit, kSiteEpilogueTmemFull) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok) {
             tc_fence_after_sync();
