@@ -164,31 +164,41 @@ int launch_narrow(const Mx4LaunchArgs &a, int splits)
     }
 }
 
-// CTAs of a cluster that share a tile's K loop: as many as the idle CTA slots
-// allow (two per SM), up to 8 and at least one K block each.
-int narrow_splits(int64_t tiles, int64_t k_blocks, int sm_count)
+// CTAs of a cluster that divide a tile's K loop, for `tiles` tiles of k_blocks
+// ring slots each: doubled while every CTA still has an SM to itself and at
+// least min_blocks ring slots of K.  A second wave of clusters costs as much as
+// the first (1 x 8192 x 8192: 2 CTAs per tile 9.7 us, 4 CTAs 13.9 us), and
+// clusters of 8 do not pack a GPC's SMs, so those are held to half of them
+// (1 x 2048 x 8192, 16 tiles: 4 CTAs 6.0 us, 8 CTAs 9.2 us).
+int narrow_splits(int64_t tiles, int64_t k_blocks, int64_t min_blocks, int sm_count)
 {
     int s = 1;
-    while (s < 8 && tiles * (2 * s) <= 2 * static_cast<int64_t>(sm_count) && k_blocks >= 2 * s) s *= 2;
+    while (s < 8 && tiles * 2 * s <= (s == 4 ? sm_count / 2 : sm_count) && k_blocks >= 2 * s * min_blocks) s *= 2;
     // No CTA without K blocks: ceil(k_blocks / s) each.
     while (s > 1 && (k_blocks + s - 1) / s * (s - 1) >= k_blocks) s /= 2;
     return s;
 }
 
+// The choice between the two kernels and their tiles.  A narrow tile's time
+// hardly depends on its width (4096 x 4096 weight, 64 rows of A: 7.2 us with one
+// CTA per tile, 512 rows in 128-row tiles 9.5 us), so the narrowest that holds
+// M, or that leaves every tile an SM, is taken; with more tiles than SMs the
+// 256 x 256 pair tiles win (768 x 4096 x 4096: 11.4 us, 192 narrow tiles 18 us; 512 x
+// 4096 x 4096: 11.2 us, 128 narrow tiles 9.5 us).  Dividing K pays where the
+// partial tiles are small (16 rows: 6.4 -> 5.3 us at 4096 x 4096, two ring slots
+// per CTA); for 64 rows the exchange costs what it saves until K is long.
 template <bool kRelu>
 int launch_variant(const Mx4LaunchArgs &a)
 {
-    const int64_t pair_tiles = ((a.M + Mx4Cfg::TILE_M - 1) / Mx4Cfg::TILE_M) * ((a.N + Mx4Cfg::BN - 1) / Mx4Cfg::BN);
-    if (pair_tiles * 2 >= a.dev.sm_count) return launch_pairs<kRelu>(a);
-    const int64_t w_tiles = (a.N + 127) / 128, k_blocks = (a.K + 255) / 256;
-    const int bn = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : (a.M <= 64 ? 64 : 128));
-    const int s = narrow_splits(w_tiles * ((a.M + bn - 1) / bn), k_blocks, a.dev.sm_count);
-    switch (bn) {
-    case 16: return launch_narrow<kRelu, 16, 5>(a, s);
-    case 32: return launch_narrow<kRelu, 32, 4>(a, s);
-    case 64: return launch_narrow<kRelu, 64, 4>(a, s);
-    default: return launch_narrow<kRelu, 128, 3>(a, s);
-    }
+    const int64_t w_tiles = (a.N + 127) / 128, k_blocks = (a.K + 511) / 512;
+    const int64_t sms = a.dev.sm_count;
+    auto tiles = [&](int bn) { return w_tiles * ((a.M + bn - 1) / bn); };
+    auto splits = [&](int bn) { return narrow_splits(tiles(bn), k_blocks, bn <= 32 ? 2 : 8, a.dev.sm_count); };
+    if (a.M <= 16 && tiles(16) <= sms) return launch_narrow<kRelu, 16, 5>(a, splits(16));
+    if (a.M <= 32 && tiles(32) <= sms) return launch_narrow<kRelu, 32, 5>(a, splits(32));
+    if (tiles(64) <= sms) return launch_narrow<kRelu, 64, 4>(a, splits(64));
+    if (tiles(128) <= sms) return launch_narrow<kRelu, 128, 3>(a, splits(128));
+    return launch_pairs<kRelu>(a);
 }
 
 }  // namespace

@@ -531,23 +531,34 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
 // over the S = 1, 2, 4 or 8 CTAs of a cluster; each leaves its fp32 partial tile
 // in its shared memory, and after a cluster barrier every CTA adds a share of
 // the tile over the S partials in rank order (a fixed order: equal calls give
-// equal bits) and stores fp16.  Two CTAs fit on an SM, so the loads of one run
-// under the set-up and the reduction of the other.
+// equal bits) and stores fp16.
+//
+// Few CTAs each with a short K loop make this a matter of latencies.  Timed by
+// clocks written at each step (1 x 4096 x 4096), a K block cost the MMA thread
+// some 670 cycles whatever it held, for two barrier waits, the issue of its
+// MMAs and a commit; so a ring slot holds 512 elements of K, two swizzle rows
+// and eight MMAs (256 elements: 7.9 us with one CTA per tile, 512: 6.4 us).  The
+// first loads are issued before the CTA's other set-up, and the cluster's
+// first barrier is waited for only when the partial tiles are exchanged.
 template <int kBN, int kStages>
 struct Mx4NarrowCfg {
     static constexpr int BM = 128;             // rows of W per tile (TMEM lanes)
     static constexpr int BN = kBN;             // rows of A per tile
-    static constexpr int BK = 256;
-    static constexpr int ROW_BYTES = BK / 2;
+    static constexpr int BK = 512;             // elements of K per ring slot: two swizzle rows
+    static constexpr int HALVES = 2;
+    static constexpr int ROW_BYTES = 128;      // of one half
     static constexpr int UMMA_K = 64;
     static constexpr int STEP_BYTES = UMMA_K / 2;
+    static constexpr int STEPS = 4;            // MMAs per half
     static constexpr int SF_TILE = 512;
     static constexpr int SF_TILES = BK / 128;
     static constexpr int STAGES = kStages;
     static constexpr int THREADS = 192;
     static constexpr int MAX_CLUSTER = 8;
-    static constexpr int W_STAGE_BYTES = BM * ROW_BYTES;
-    static constexpr int X_STAGE_BYTES = BN * ROW_BYTES;
+    static constexpr int W_HALF_BYTES = BM * ROW_BYTES;
+    static constexpr int X_HALF_BYTES = BN * ROW_BYTES;
+    static constexpr int W_STAGE_BYTES = HALVES * W_HALF_BYTES;
+    static constexpr int X_STAGE_BYTES = HALVES * X_HALF_BYTES;
     static constexpr int SF_STAGE_BYTES = SF_TILES * SF_TILE;   // of W and of A each
     static constexpr int STAGE_TX_BYTES = W_STAGE_BYTES + X_STAGE_BYTES;
     static constexpr int SF_TX_BYTES = 2 * SF_STAGE_BYTES;
@@ -562,21 +573,21 @@ struct Mx4NarrowCfg {
     static constexpr int SMEM_SFW_OFF = SMEM_X_OFF + STAGES * X_STAGE_BYTES;
     static constexpr int SMEM_SFX_OFF = SMEM_SFW_OFF + STAGES * SF_STAGE_BYTES;
     static constexpr int SMEM_CTL_OFF = SMEM_SFX_OFF + STAGES * SF_STAGE_BYTES;
-    static constexpr int SMEM_CTL_BYTES = 256;
+    static constexpr int SMEM_CTL_BYTES = 512;
     static constexpr int SMEM_BYTES = 1024 + SMEM_CTL_OFF + SMEM_CTL_BYTES;
     static constexpr uint32_t IDESC = idesc_mxf4(BM, BN);
 
-    static_assert(SF_TILES == 2, "the scale warps' stores");
+    static_assert(SF_TILES == 2 * HALVES && X_HALF_BYTES % 1024 == 0, "tiles of a half; swizzle atoms");
     static_assert(BN % 16 == 0 && BN <= 128, "N of the MMA; scale words of one row block");
     static_assert(PART_BYTES <= STAGES * (W_STAGE_BYTES + X_STAGE_BYTES), "the partial tile fits in the ring");
     static_assert((4 * STAGES + 2) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
-    static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
 };
 
 struct Mx4NarrowParams {
     int32_t M, N;
     int32_t num_m_tiles;    // ceil(M / BN)
-    int32_t num_k_blocks;   // ceil(K / 256)
+    int32_t num_k_blocks;   // ceil(K / 512)
     int32_t k_per_cta;      // K blocks of each CTA of a cluster
     uint64_t timeout_cycles;
     __half *C;
@@ -641,7 +652,7 @@ __device__ __forceinline__ void mx4_reduce(const Mx4NarrowParams &p, uint32_t pa
 // Warp 0: TMA producer.  Warp 1: MMAs.  Warps 2..5: scale tiles to TMEM; then
 // the partial tile to shared memory and the sum over the cluster.
 template <bool kRelu, int kBN, int kStages>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(192, 1)
     gemm_mxfp4_narrow_sm103a(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                              const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sw,
                              const Mx4NarrowParams p)
@@ -679,37 +690,22 @@ __global__ void __launch_bounds__(192, 2)
     abort.cluster = ncl;
     abort.rank = crank;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
-            mbar_init(sfull_bar(s), 1);
-            mbar_init(sready_bar(s), 4);   // one arrive per scale warp
+    if (warp == 0) {
+        // One thread per ring slot: 4 S initialisations one after another would
+        // hold back the first load by some 400 cycles.
+        if (lane < S) {
+            mbar_init(full_bar(lane), 1);
+            mbar_init(empty_bar(lane), 1);
+            mbar_init(sfull_bar(lane), 1);
+            mbar_init(sready_bar(lane), 4);   // one arrive per scale warp
         }
-        mbar_init(tfull_bar, 1);
-        *abort.local = 0;
+        if (lane == 31) {
+            mbar_init(tfull_bar, 1);
+            *abort.local = 0;
+        }
         fence_mbar_init();
+        __syncwarp();
     }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmap_w);
-        prefetch_tensormap(&tmap_a);
-        prefetch_tensormap(&tmap_sw);
-        prefetch_tensormap(&tmap_sa);
-    }
-    if (warp == 1) {
-        tmem_alloc<1>(tmem_slot, Cfg::TMEM_COLS);
-        tmem_relinquish<1>();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    if (ncl > 1) {
-        // Every abort flag of the cluster is zero before any CTA may raise one.
-        cluster_arrive();
-        cluster_wait();
-    }
-    tc_fence_after_sync();
-    griddep_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot_ptr;
     const uint64_t limit = p.timeout_cycles;
     const int unit = static_cast<int>(blockIdx.x / ncl);
     const int mt = unit % p.num_m_tiles, wb = unit / p.num_m_tiles;   // neighbours share W's rows
@@ -717,26 +713,51 @@ __global__ void __launch_bounds__(192, 2)
     const int kb0 = static_cast<int>(crank) * p.k_per_cta;
     const int kb1 = min(p.num_k_blocks, kb0 + p.k_per_cta);   // the launch leaves no CTA without K blocks
 
+    auto load = [&](int kb, int s) {
+        mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_TX_BYTES);
+#pragma unroll
+        for (int h = 0; h < Cfg::HALVES; ++h) {
+            const int x = (kb * Cfg::HALVES + h) * Cfg::ROW_BYTES;   // past K: zeros
+            tma_load_2d(sW + s * Cfg::W_STAGE_BYTES + h * Cfg::W_HALF_BYTES, &tmap_w, full_bar(s), x, n0);
+            tma_load_2d(sX + s * Cfg::X_STAGE_BYTES + h * Cfg::X_HALF_BYTES, &tmap_a, full_bar(s), x, m0);
+        }
+        mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
+        tma_load_3d_cta(sSFW + s * Cfg::SF_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0, kb * Cfg::SF_TILES, wb);
+        tma_load_3d_cta(sSFX + s * Cfg::SF_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES, m0 / 128);
+    };
+    // The thread that initialised the barriers fills the ring before it joins
+    // the others, whose set-up runs while the first loads are on their way.
+    const int filled = min(S, kb1 - kb0);
+    if (threadIdx.x == 0) {
+        griddep_wait();   // A, W and the scales may come from the kernel just before
+        for (int s = 0; s < filled; ++s) load(kb0 + s, s);
+    }
+    if (warp == 1) {
+        tmem_alloc<1>(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish<1>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    // Waited for only when the partial tiles are exchanged: until then no CTA
+    // touches another, but for abort flags raised a second or more from now.
+    if (ncl > 1) cluster_arrive();
+    tc_fence_after_sync();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+
     if (warp == 0) {
         if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            uint32_t issued_mask = 0, issued_parity = 0;
+            // Ring slots in use, and the parity of their last load.
+            uint32_t issued_mask = (1u << filled) - 1u, issued_parity = 0;
             bool ok = true;
-            griddep_wait();
-            for (int kb = kb0; kb < kb1; ++kb) {
+            int s = 0;
+            uint32_t ph = 1;
+            for (int kb = kb0 + filled; kb < kb1; ++kb) {
                 if (!wait_phase(empty_bar(s), ph ^ 1u, abort, limit, kSiteProducerEmpty)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_TX_BYTES);
-                tma_load_2d(sW + s * Cfg::W_STAGE_BYTES, &tmap_w, full_bar(s), kb * Cfg::ROW_BYTES, n0);
-                tma_load_2d(sX + s * Cfg::X_STAGE_BYTES, &tmap_a, full_bar(s), kb * Cfg::ROW_BYTES, m0);
-                mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
-                tma_load_3d_cta(sSFW + s * Cfg::SF_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0, kb * Cfg::SF_TILES, wb);
-                tma_load_3d_cta(sSFX + s * Cfg::SF_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES,
-                                m0 / 128);
-                issued_mask |= 1u << s;
+                load(kb, s);
                 issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
                 if (++s == S) {
                     s = 0;
@@ -773,12 +794,13 @@ __global__ void __launch_bounds__(192, 2)
                 const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
                 const uint64_t x_st = x_desc0 + static_cast<uint64_t>((s * Cfg::X_STAGE_BYTES) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < Cfg::BK / Cfg::UMMA_K; ++ks) {
-                    const uint64_t step = static_cast<uint64_t>((ks * Cfg::STEP_BYTES) >> 4);
+                for (int ks = 0; ks < Cfg::HALVES * Cfg::STEPS; ++ks) {
+                    const int half = ks / Cfg::STEPS, step = (ks % Cfg::STEPS) * Cfg::STEP_BYTES;
                     const uint32_t id = (ks & 1) * 2;
-                    mma_mxf4<1>(tmem_base, w_st + step, x_st + step, Cfg::IDESC | (id << 4) | (id << 29),
-                                sf + 4u * (ks / 2), sf + 4u * (Cfg::SF_TILES + ks / 2) + sfx_word,
-                                (kb != kb0 || ks != 0) ? 1u : 0u);
+                    mma_mxf4<1>(tmem_base, w_st + static_cast<uint64_t>((half * Cfg::W_HALF_BYTES + step) >> 4),
+                                x_st + static_cast<uint64_t>((half * Cfg::X_HALF_BYTES + step) >> 4),
+                                Cfg::IDESC | (id << 4) | (id << 29), sf + 4u * (ks / 2),
+                                sf + 4u * (Cfg::SF_TILES + ks / 2) + sfx_word, (kb != kb0 || ks != 0) ? 1u : 0u);
                 }
                 mma_commit(empty_bar(s));
                 if (++s == S) {
@@ -810,8 +832,13 @@ __global__ void __launch_bounds__(192, 2)
                 const uint32_t x = sSFX + static_cast<uint32_t>(s * Cfg::SF_STAGE_BYTES) + row;
                 const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS) +
                                     (static_cast<uint32_t>(q * 32) << 16);
-                tmem_store_scales(sf, ld_shared_u32x4(w), ld_shared_u32x4(w + Cfg::SF_TILE));
-                tmem_store_scales(sf + 8, ld_shared_u32x4(x), ld_shared_u32x4(x + Cfg::SF_TILE));
+#pragma unroll
+                for (int h = 0; h < Cfg::HALVES; ++h) {
+                    const uint32_t o = static_cast<uint32_t>(2 * h * Cfg::SF_TILE);
+                    tmem_store_scales(sf + 8u * h, ld_shared_u32x4(w + o), ld_shared_u32x4(w + o + Cfg::SF_TILE));
+                    tmem_store_scales(sf + 8u * (Cfg::HALVES + h), ld_shared_u32x4(x + o),
+                                      ld_shared_u32x4(x + o + Cfg::SF_TILE));
+                }
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -841,7 +868,9 @@ __global__ void __launch_bounds__(192, 2)
 
     // Every partial tile of the cluster is written.
     tc_fence_before_sync();
+    __syncwarp();
     if (ncl > 1) {
+        cluster_wait();   // of the arrival after the set-up
         cluster_arrive();
         cluster_wait();
     } else {
