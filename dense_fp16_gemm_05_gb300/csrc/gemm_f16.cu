@@ -71,6 +71,7 @@ constexpr int kNumConfigs = static_cast<int>(sizeof(kConfigs) / sizeof(kConfigs[
 struct DriverFns {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     PFN_cuMemGetAddressRange_v3020 range = nullptr;
+    PFN_cuPointerGetAttributes_v7000 attributes = nullptr;   // may be missing
     bool ok = false;
 };
 
@@ -90,6 +91,14 @@ const DriverFns &driver()
             fns.range = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(f2);
             fns.ok = true;
         }
+        cudaDriverEntryPointQueryResult q3 = cudaDriverEntryPointSymbolNotFound;
+        void *f3 = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &f3, 7000, cudaEnableDefault, &q3) ==
+                cudaSuccess &&
+            q3 == cudaDriverEntryPointSuccess)
+            fns.attributes = reinterpret_cast<PFN_cuPointerGetAttributes_v7000>(f3);
+        else
+            cudaGetLastError();
     });
     return fns;
 }
@@ -183,6 +192,29 @@ int check_device_buffer(const void *p, uint64_t bytes, int dev, uintptr_t align 
     if (off > size || bytes > size - off)
         return reject(GEMM_ERR_INVALID_ARG, "a buffer is smaller than its matrix (runs past its allocation)");
     return GEMM_OK;
+}
+
+// check_device_buffer with one driver call instead of two runtime and driver
+// calls: what it cannot vouch for goes to check_device_buffer, which accepts
+// or names the reason.
+int check_device_buffer_fast(const void *p, uint64_t bytes, int dev, uintptr_t align = 16)
+{
+    const DriverFns &fns = driver();
+    if (fns.attributes != nullptr && p != nullptr && (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0) {
+        unsigned int type = 0;
+        int ordinal = -1;
+        CUdeviceptr base = 0;
+        size_t size = 0;
+        CUpointer_attribute what[4] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                       CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+        void *out[4] = {&type, &ordinal, &base, &size};
+        if (fns.attributes(4, what, out, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS &&
+            type == CU_MEMORYTYPE_DEVICE && ordinal == dev && base != 0) {
+            const uint64_t off = static_cast<uint64_t>(reinterpret_cast<CUdeviceptr>(p) - base);
+            if (off <= size && bytes <= size - off) return GEMM_OK;
+        }
+    }
+    return check_device_buffer(p, bytes, dev, align);
 }
 
 bool ranges_overlap(const void *a, uint64_t abytes, const void *b, uint64_t bbytes)
@@ -822,10 +854,10 @@ extern "C" int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, v
     if ((st = current_device_info(&dev)) != GEMM_OK) return st;
     const uint64_t x_bytes = static_cast<uint64_t>(rows) * static_cast<uint64_t>(K) * el;
     const uint64_t q_bytes = mx4_code_bytes(rows, K), s_bytes = mx4_scale_bytes(rows, K);
-    if ((st = check_device_buffer(X, x_bytes, dev.device, el)) != GEMM_OK) return st;
-    if ((st = check_device_buffer(Q, q_bytes, dev.device)) != GEMM_OK) return st;
-    if ((st = check_device_buffer(S, s_bytes, dev.device)) != GEMM_OK) return st;
-    if (V != nullptr && (st = check_device_buffer(V, x_bytes, dev.device, el)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(X, x_bytes, dev.device, el)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(Q, q_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(S, s_bytes, dev.device)) != GEMM_OK) return st;
+    if (V != nullptr && (st = check_device_buffer_fast(V, x_bytes, dev.device, el)) != GEMM_OK) return st;
     if (ranges_overlap(Q, q_bytes, X, x_bytes) || ranges_overlap(S, s_bytes, X, x_bytes) ||
         ranges_overlap(Q, q_bytes, S, s_bytes) ||
         (V != nullptr && (ranges_overlap(V, x_bytes, X, x_bytes) || ranges_overlap(V, x_bytes, Q, q_bytes) ||
@@ -855,7 +887,7 @@ extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const
     if ((st = current_device_info(&dev)) != GEMM_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const uint64_t c_bytes = static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * 2u;
-    if ((st = check_device_buffer(C, c_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(C, c_bytes, dev.device)) != GEMM_OK) return st;
     if (K == 0) {
         // Empty sum: every output is R(+0) = +0.
         if (cudaMemsetAsync(C, 0, c_bytes, s) != cudaSuccess) {
@@ -867,10 +899,10 @@ extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const
     if ((N % 8) != 0) return reject(GEMM_ERR_ALIGNMENT, "N is not a multiple of 8 (the fp16 row pitch of C)");
     const uint64_t a_bytes = mx4_code_bytes(M, K), w_bytes = mx4_code_bytes(N, K);
     const uint64_t sa_bytes = mx4_scale_bytes(M, K), sw_bytes = mx4_scale_bytes(N, K);
-    if ((st = check_device_buffer(A, a_bytes, dev.device)) != GEMM_OK) return st;
-    if ((st = check_device_buffer(W, w_bytes, dev.device)) != GEMM_OK) return st;
-    if ((st = check_device_buffer(SA, sa_bytes, dev.device)) != GEMM_OK) return st;
-    if ((st = check_device_buffer(SW, sw_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(A, a_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(W, w_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(SA, sa_bytes, dev.device)) != GEMM_OK) return st;
+    if ((st = check_device_buffer_fast(SW, sw_bytes, dev.device)) != GEMM_OK) return st;
     if (ranges_overlap(C, c_bytes, A, a_bytes) || ranges_overlap(C, c_bytes, W, w_bytes) ||
         ranges_overlap(C, c_bytes, SA, sa_bytes) || ranges_overlap(C, c_bytes, SW, sw_bytes))
         return reject(GEMM_ERR_INVALID_ARG, "C overlaps an input");
@@ -917,7 +949,7 @@ int check_norm_buffers(const NormBuffer *b, int n, int dev)
 {
     for (int i = 0; i < n; ++i) {
         if (b[i].p == nullptr) continue;
-        const int st = check_device_buffer(b[i].p, b[i].bytes, dev, b[i].align);
+        const int st = check_device_buffer_fast(b[i].p, b[i].bytes, dev, b[i].align);
         if (st != GEMM_OK) return st;
     }
     for (int i = 0; i < n; ++i)

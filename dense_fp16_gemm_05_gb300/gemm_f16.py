@@ -219,6 +219,28 @@ def _stream_handle(stream, device) -> int:
     return int(stream)
 
 
+# Index of the current device without torch.cuda.current_device's lazy-init
+# check (a CUDA tensor in hand means CUDA is up).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(fn, what: str, device: torch.device, stream, *args):
+    """fn(*args, stream) on ``device``; GemmError for a status that is not GEMM_OK.
+
+    A call on a small problem is bound by the host, so this does what
+    _device_scope and _stream_handle do with as few steps as the common case
+    (a CUDA tensor on the current device, torch's current stream) allows.
+    """
+    idx = device.index
+    if stream is None and idx is not None and _current_raw_stream is not None and idx == _current_device():
+        st = fn(*args, _current_raw_stream(idx))
+    else:
+        with _device_scope(device):
+            st = fn(*args, _stream_handle(stream, device))
+    if st != GEMM_OK:
+        raise GemmError(st, what)
+
+
 def _check_operand(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -533,9 +555,21 @@ def mxfp4_row_scales(S: torch.Tensor, rows: int, K: int) -> torch.Tensor:
 def _check_like(t, name: str, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _like_or_new(t, name: str, dtype, shape, device):
+    """t after _check_like, or a new tensor where t is None."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _check_like(t, name, dtype, shape, device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = False, Q: torch.Tensor | None = None,
@@ -551,29 +585,19 @@ def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = Fals
     """
     if not isinstance(X, torch.Tensor):
         raise TypeError("X must be a torch.Tensor")
-    if X.dtype not in TYPES or X.dim() != 2 or not X.is_contiguous():
-        raise ValueError("X must be a contiguous 2-D float16, bfloat16 or float32 tensor, "
-                         f"got {X.dtype} {tuple(X.shape)}")
-    rows, K = (X.shape[1], X.shape[0]) if transpose else (X.shape[0], X.shape[1])
+    dtype, shape = X.dtype, X.shape
+    code = TYPES.get(dtype)
+    if code is None or len(shape) != 2 or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous 2-D float16, bfloat16 or float32 tensor, got {dtype} {tuple(shape)}")
+    K, rows = shape if transpose else (shape[1], shape[0])
     q_shape, s_shape = mxfp4_shapes(rows, K)
     dev = X.device
-    if Q is None:
-        Q = torch.empty(q_shape, dtype=torch.uint8, device=dev)
-    if S is None:
-        S = torch.empty(s_shape, dtype=torch.uint8, device=dev)
-    if V is None and values:
-        V = torch.empty((rows, K), dtype=X.dtype, device=dev)
-    _check_like(Q, "Q", torch.uint8, q_shape, dev)
-    _check_like(S, "S", torch.uint8, s_shape, dev)
-    if V is not None:
-        _check_like(V, "V", X.dtype, (rows, K), dev)
-    L = lib()
-    with _device_scope(dev):
-        st = L.mxfp4_quantize(X.data_ptr(), TYPES[X.dtype], Q.data_ptr(), S.data_ptr(),
-                              None if V is None else V.data_ptr(), rows, K, int(bool(transpose)),
-                              _stream_handle(stream, dev))
-    if st != GEMM_OK:
-        raise GemmError(st, "mxfp4_quantize")
+    Q = _like_or_new(Q, "Q", torch.uint8, q_shape, dev)
+    S = _like_or_new(S, "S", torch.uint8, s_shape, dev)
+    if values or V is not None:
+        V = _like_or_new(V, "V", dtype, (rows, K), dev)
+    _call((_lib or lib()).mxfp4_quantize, "mxfp4_quantize", dev, stream, X.data_ptr(), code, Q.data_ptr(),
+          S.data_ptr(), _ptr(V), rows, K, 1 if transpose else 0)
     return (Q, S) if V is None else (Q, S, V)
 
 
@@ -590,48 +614,46 @@ def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Ten
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != 2:
             raise ValueError(f"{name} must be a 2-D uint8 tensor, got {tuple(t.shape)}")
-    M, N = A.shape[0], W.shape[0]
-    if K is None:
-        K = 2 * A.shape[1]
+    M, a_bytes = A.shape
+    N = W.shape[0]
+    K = 2 * a_bytes if K is None else int(K)
     dev = A.device
-    for t, s, name, rows in ((A, SA, "A", M), (W, SW, "W", N)):
-        q_shape, s_shape = mxfp4_shapes(rows, K)
-        _check_like(t, name, torch.uint8, q_shape, dev)
-        _check_like(s, "S" + name, torch.uint8, s_shape, dev)
-    if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=dev)
-    _check_like(C, "C", torch.float16, (M, N), dev)
-    L = lib()
-    with _device_scope(dev):
-        st = L.gemm_mxfp4(A.data_ptr(), SA.data_ptr(), W.data_ptr(), SW.data_ptr(), C.data_ptr(), M, N, int(K),
-                          int(bool(relu)), _stream_handle(stream, dev))
-    if st != GEMM_OK:
-        raise GemmError(st, "gemm_mxfp4")
+    u8 = torch.uint8
+    q_shape, s_shape = mxfp4_shapes(M, K)
+    _check_like(A, "A", u8, q_shape, dev)
+    _check_like(SA, "SA", u8, s_shape, dev)
+    q_shape, s_shape = mxfp4_shapes(N, K)
+    _check_like(W, "W", u8, q_shape, dev)
+    _check_like(SW, "SW", u8, s_shape, dev)
+    C = _like_or_new(C, "C", torch.float16, (M, N), dev)
+    _call((_lib or lib()).gemm_mxfp4, "gemm_mxfp4", dev, stream, A.data_ptr(), SA.data_ptr(), W.data_ptr(),
+          SW.data_ptr(), C.data_ptr(), M, N, K, 1 if relu else 0)
     return C
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _norm_rows(X, name: str = "X") -> tuple[int, int]:
+def _norm_input(X, name: str = "X"):
+    """(type code, dtype, shape, rows, dim) of a layer norm input."""
     if not isinstance(X, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if X.dtype not in TYPES or X.dim() < 1 or not X.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 tensor, "
-                         f"got {X.dtype} {tuple(X.shape)}")
-    dim = X.shape[-1]
-    return (X.numel() // dim if dim else math.prod(X.shape[:-1])), dim
+    dtype, shape = X.dtype, X.shape
+    code = TYPES.get(dtype)
+    if code is None or len(shape) < 1 or not X.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 tensor, got {dtype} {tuple(shape)}")
+    dim = shape[-1]
+    return code, dtype, shape, (shape[0] if len(shape) == 2 else math.prod(shape[:-1])), dim
 
 
-def _norm_weight_type(X, *weights) -> torch.dtype:
-    wt = next((w.dtype for w in weights if isinstance(w, torch.Tensor)), X.dtype)
-    if wt != X.dtype and wt != torch.float32:
-        raise ValueError(f"weights must be of X's type {X.dtype} or float32, got {wt}")
+def _norm_weight_type(dtype, dim: int, device, *weights) -> torch.dtype:
+    wt = None
     for w in weights:
-        if w is not None:
-            _check_like(w, "a weight", wt, (X.shape[-1],), X.device)
-    return wt
+        if w is None:
+            continue
+        if wt is None:
+            wt = w.dtype if isinstance(w, torch.Tensor) else dtype
+            if wt != dtype and wt != torch.float32:
+                raise ValueError(f"weights must be of X's type {dtype} or float32, got {wt}")
+        _check_like(w, "a weight", wt, (dim,), device)
+    return dtype if wt is None else wt
 
 
 def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -642,21 +664,17 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
     (ones, zeros) or vectors of X's type or float32.  mean and rstd are float32
     of X's leading shape, or None without ``stats``.  Asynchronous on ``stream``.
     """
-    rows, dim = _norm_rows(X)
-    wt = _norm_weight_type(X, gamma, beta)
-    if Y is None:
-        Y = torch.empty_like(X)
-    _check_like(Y, "Y", X.dtype, X.shape, X.device)
+    code, dtype, shape, rows, dim = _norm_input(X)
+    dev = X.device
+    wt = _norm_weight_type(dtype, dim, dev, gamma, beta)
+    Y = _like_or_new(Y, "Y", dtype, shape, dev)
     mean = rstd = None
     if stats:
-        mean = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-        rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-    L = lib()
-    with _device_scope(X.device):
-        st = L.layer_norm_fwd(X.data_ptr(), _ptr(gamma), _ptr(beta), Y.data_ptr(), _ptr(mean), _ptr(rstd), rows, dim,
-                              float(eps), TYPES[X.dtype], TYPES[wt], _stream_handle(stream, X.device))
-    if st != GEMM_OK:
-        raise GemmError(st, "layer_norm_fwd")
+        lead = shape[:-1]
+        mean = torch.empty(lead, dtype=torch.float32, device=dev)
+        rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+    _call((_lib or lib()).layer_norm_fwd, "layer_norm_fwd", dev, stream, X.data_ptr(), _ptr(gamma), _ptr(beta),
+          Y.data_ptr(), _ptr(mean), _ptr(rstd), rows, dim, eps, code, TYPES[wt])
     return Y, mean, rstd
 
 
@@ -680,43 +698,38 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
     layer_norm_bwd_workspace bytes for callers that keep one; made on the
     launch stream when not given.  Asynchronous on ``stream``.
     """
-    rows, dim = _norm_rows(X)
-    _check_like(dY, "dY", X.dtype, X.shape, X.device)
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _check_like(t, name, torch.float32, X.shape[:-1], X.device)
-    wt = _norm_weight_type(X, gamma)
+    code, dtype, shape, rows, dim = _norm_input(X)
+    dev = X.device
+    _check_like(dY, "dY", dtype, shape, dev)
+    lead = shape[:-1]
+    _check_like(mean, "mean", torch.float32, lead, dev)
+    _check_like(rstd, "rstd", torch.float32, lead, dev)
+    wt = _norm_weight_type(dtype, dim, dev, gamma)
     if gamma is None and wtype is not None:
         wt = wtype
-        if wt not in (X.dtype, torch.float32):
-            raise ValueError(f"wtype must be X's type {X.dtype} or float32, got {wt}")
-    if dX is None:
-        dX = torch.empty_like(X)
-    _check_like(dX, "dX", X.dtype, X.shape, X.device)
-    L = lib()
+        if wt != dtype and wt != torch.float32:
+            raise ValueError(f"wtype must be X's type {dtype} or float32, got {wt}")
+    dX = _like_or_new(dX, "dX", dtype, shape, dev)
+    L = _lib or lib()
     dgamma = dbeta = None
-    need = 0
-    with _device_scope(X.device):
-        if weights:
-            dgamma = torch.empty((dim,), dtype=wt, device=X.device)
-            dbeta = torch.empty((dim,), dtype=wt, device=X.device)
-            need = L.layer_norm_bwd_workspace(rows, dim)
-            if need < 0:
-                raise GemmError(need, "layer_norm_bwd_workspace")
-            if workspace is None:
-                if stream is None:
-                    workspace = torch.empty((need // 4,), dtype=torch.float32, device=X.device)
-                else:
-                    with torch.cuda.stream(_launch_stream(stream, X.device)):
-                        workspace = torch.empty((need // 4,), dtype=torch.float32, device=X.device)
-            elif (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.float32
-                  or not workspace.is_contiguous() or workspace.device != X.device):
-                raise ValueError("workspace must be a contiguous float32 tensor on X's device")
-        st = L.layer_norm_bwd(dY.data_ptr(), X.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
-                              dX.data_ptr(), _ptr(dgamma), _ptr(dbeta), rows, dim, TYPES[X.dtype], TYPES[wt],
-                              _ptr(workspace) if weights else None, 4 * workspace.numel() if weights else 0,
-                              _stream_handle(stream, X.device))
-    if st != GEMM_OK:
-        raise GemmError(st, "layer_norm_bwd")
+    ws_bytes = 0
+    if weights:
+        dgamma = torch.empty((dim,), dtype=wt, device=dev)
+        dbeta = torch.empty((dim,), dtype=wt, device=dev)
+        if workspace is None:
+            need = layer_norm_bwd_workspace(rows, dim, dev)
+            if stream is None:
+                workspace = torch.empty((need // 4,), dtype=torch.float32, device=dev)
+            else:
+                with torch.cuda.stream(_launch_stream(stream, dev)):
+                    workspace = torch.empty((need // 4,), dtype=torch.float32, device=dev)
+        elif (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.float32
+              or not workspace.is_contiguous() or workspace.device != dev):
+            raise ValueError("workspace must be a contiguous float32 tensor on X's device")
+        ws_bytes = 4 * workspace.numel()
+    _call(L.layer_norm_bwd, "layer_norm_bwd", dev, stream, dY.data_ptr(), X.data_ptr(), _ptr(gamma), mean.data_ptr(),
+          rstd.data_ptr(), dX.data_ptr(), _ptr(dgamma), _ptr(dbeta), rows, dim, code, TYPES[wt],
+          _ptr(workspace) if weights else None, ws_bytes)
     return dX, dgamma, dbeta
 
 
