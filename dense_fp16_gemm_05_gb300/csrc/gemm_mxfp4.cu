@@ -184,7 +184,9 @@ int narrow_splits(int64_t tiles, int64_t k_blocks, int64_t min_blocks, int sm_co
 // CTA per tile, 512 rows in 128-row tiles 9.5 us), so the narrowest that holds
 // M, or that leaves every tile an SM, is taken; with more tiles than SMs the
 // 256 x 256 pair tiles win (768 x 4096 x 4096: 11.4 us, 192 narrow tiles 18 us; 512 x
-// 4096 x 4096: 11.2 us, 128 narrow tiles 9.5 us).  Dividing K pays where the
+// 4096 x 4096: 11.2 us, 128 narrow tiles 9.5 us), unless A has so few rows that
+// W's bytes are the time (1 x 131072 x 4096: 54 us against 86 us; 64 x 24576 x 4096:
+// 16.6 against 19.8 us, 64 x 65536 x 2048: 24.8 against 22.9 us).  Dividing K pays where the
 // partial tiles are small (16 rows: 6.4 -> 5.3 us at 4096 x 4096, two ring slots
 // per CTA); for 64 rows the exchange costs what it saves until K is long.
 template <bool kRelu>
@@ -194,9 +196,9 @@ int launch_variant(const Mx4LaunchArgs &a)
     const int64_t sms = a.dev.sm_count;
     auto tiles = [&](int bn) { return w_tiles * ((a.M + bn - 1) / bn); };
     auto splits = [&](int bn) { return narrow_splits(tiles(bn), k_blocks, bn <= 32 ? 2 : 8, a.dev.sm_count); };
-    if (a.M <= 16 && tiles(16) <= sms) return launch_narrow<kRelu, 16, 5>(a, splits(16));
-    if (a.M <= 32 && tiles(32) <= sms) return launch_narrow<kRelu, 32, 5>(a, splits(32));
-    if (tiles(64) <= sms) return launch_narrow<kRelu, 64, 4>(a, splits(64));
+    if (a.M <= 16) return launch_narrow<kRelu, 16, 5>(a, splits(16));
+    if (a.M <= 32) return launch_narrow<kRelu, 32, 5>(a, splits(32));
+    if (tiles(64) <= (a.M <= 64 ? 2 * sms : sms)) return launch_narrow<kRelu, 64, 4>(a, splits(64));
     if (tiles(128) <= sms) return launch_narrow<kRelu, 128, 3>(a, splits(128));
     return launch_pairs<kRelu>(a);
 }

@@ -28,10 +28,15 @@ struct BwdParams {
     float inv_dim;
 };
 
+// Threads of a block, and blocks per SM: some 1024 threads, so that the loads of
+// one block run while another waits for its row's sum.
+__host__ __device__ constexpr int bwd_threads(int tpr) { return tpr == 32 ? 256 : tpr; }
+__host__ __device__ constexpr int bwd_blocks(int tpr) { return tpr == 32 ? 2 : 1024 / tpr; }
+
 template <class T, class W, int V, int NV, int TPR>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layer_norm_bwd_kernel(BwdParams<T, W> p)
+__global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd_blocks(TPR)) layer_norm_bwd_kernel(BwdParams<T, W> p)
 {
-    constexpr int BT = TPR < 256 ? 256 : TPR;
+    constexpr int BT = bwd_threads(TPR);
     constexpr int R = BT / TPR;   // rows at a time
     static_assert(TPR == 32 || R == 1, "a warp or a block per row");
     __shared__ float2 sh[2][TPR / 32];
@@ -49,24 +54,38 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) layer_norm_bwd_kernel(B
 #pragma unroll
         for (int j = 0; j < V; ++j) dg[i][j] = db[i][j] = 0.0f;
     }
-    int it = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * R + sub; row < p.rows;
-         row += static_cast<int64_t>(gridDim.x) * R, it ^= 1) {
+    // The next row's loads are under way while a row's sums are taken.
+    LnPack<T, V> nx[NV], nd[NV];
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto load = [&](int64_t row) {
         const T *x = p.X + row * p.dim;
         const T *dy = p.dY + row * p.dim;
-        LnPack<T, V> px[NV], pd[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
             if (k < p.dim) {
-                px[i].load(x + k);
-                pd[i].load(dy + k);
+                nx[i].load(x + k);
+                nd[i].load(dy + k);
             } else {
-                px[i].fill(0.0f);
-                pd[i].fill(0.0f);   // adds nothing to any sum
+                nx[i].fill(0.0f);
+                nd[i].fill(0.0f);   // adds nothing to any sum
             }
         }
-        const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+        next_mean = __ldg(p.mean + row);
+        next_rstd = __ldg(p.rstd + row);
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * R + sub;
+    if (row < p.rows) load(row);
+    for (int it = 0; row < p.rows; row += step, it ^= 1) {
+        LnPack<T, V> px[NV], pd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            px[i] = nx[i];
+            pd[i] = nd[i];
+        }
+        const float mean = next_mean, rstd = next_rstd;
+        if (row + step < p.rows) load(row + step);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -179,13 +198,13 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_columns(BwdParams<T, W> p)
     }
 }
 
-// Adds the parts of 32 columns: 8 warps take every eighth part, then their sums
-// are added in order.
+// Adds the parts of 32 columns: 16 warps take every sixteenth part, then their
+// sums are added in order.
 template <class W>
-__global__ void __launch_bounds__(256) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
+__global__ void __launch_bounds__(512) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
                                                              W *__restrict__ dbeta, int parts, int dim)
 {
-    __shared__ float sh[8][33];
+    __shared__ float sh[16][33];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -194,13 +213,13 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_finish(const float *__rest
     float s = 0.0f;
     if (k < dim) {
 #pragma unroll 8
-        for (int r = w; r < parts; r += 8) s += src[static_cast<int64_t>(r) * dim + k];
+        for (int r = w; r < parts; r += 16) s += src[static_cast<int64_t>(r) * dim + k];
     }
     sh[w][lane] = s;
     __syncthreads();
     if (w == 0 && k < dim) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sh[i][lane];
+        for (int i = 1; i < 16; ++i) s += sh[i][lane];
         (blockIdx.y == 0 ? dgamma : dbeta)[k] = ln_round<W>(s);
     }
 }
@@ -208,7 +227,7 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_finish(const float *__rest
 template <class T, class W, int V, int NV, int TPR>
 int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
 {
-    constexpr int BT = TPR < 256 ? 256 : TPR;
+    constexpr int BT = bwd_threads(TPR);
     constexpr int R = BT / TPR;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(static_cast<unsigned>(p.parts), 1, 1);
@@ -235,9 +254,10 @@ int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
     // Up to 512 elements a warp per row; layer_norm_parts counts on it.
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
+    if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
     if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
-    if (packs <= 256 * 2 * N) return launch_one<T, W, V, 2 * N, 256>(p, stream);
-    if (packs <= 512 * 2 * N) return launch_one<T, W, V, 2 * N, 512>(p, stream);
+    if (packs <= 512 * N) return launch_one<T, W, V, N, 512>(p, stream);
+    if (packs <= 1024 * N) return launch_one<T, W, V, N, 1024>(p, stream);
     if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
     int st = ln_launch(layer_norm_bwd_long<T, W>, dim3(static_cast<unsigned>(p.parts), 1, 1), 1024, stream, p);
     if (st != GEMM_OK || p.part == nullptr) return st;
@@ -268,7 +288,7 @@ int backward(const LayerNormArgs &a)
     const bool vec = a.dim % V == 0 && (bits & 15u) == 0;
     int st = vec ? launch_packs<T, W, V>(p, a.stream) : launch_packs<T, W, 1>(p, a.stream);
     if (st != GEMM_OK || p.part == nullptr) return st;
-    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 256, a.stream,
+    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 512, a.stream,
                      static_cast<const float *>(p.part), static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta),
                      p.parts, p.dim);
 }
@@ -277,13 +297,20 @@ int backward(const LayerNormArgs &a)
 
 namespace gemm_sm103 {
 
-// One part per block of the row kernels: rows of up to 512 elements go eight at
-// a time (a warp each), longer ones one at a time.
+// One part per block of the row kernels.  Rows of up to 512 elements go eight
+// at a time (a warp each), longer ones one at a time, with the block's threads
+// taking eight elements each: so many blocks that an SM holds some 1024
+// threads, but no more than two per SM or one per eight rows, whichever is
+// more, for a part costs as much as a row's writes.
 int64_t layer_norm_parts(int64_t rows, int64_t dim, int sm_count)
 {
     const int64_t per = dim <= 512 ? 8 : 1;
-    const int64_t want = (rows + per - 1) / per, most = 2 * static_cast<int64_t>(sm_count);
-    return want < most ? want : most;
+    const int64_t blocks = dim <= 512 ? 4 : (dim <= 1024 ? 8 : (dim <= 2048 ? 4 : (dim <= 4096 ? 2 : 1)));
+    const int64_t sms = sm_count;
+    int64_t parts = (rows + per - 1) / per;
+    if (parts > blocks * sms) parts = blocks * sms;
+    const int64_t enough = rows / 8 > 2 * sms ? rows / 8 : 2 * sms;
+    return parts < enough ? parts : enough;
 }
 
 int launch_layer_norm_bwd(const LayerNormArgs &a)

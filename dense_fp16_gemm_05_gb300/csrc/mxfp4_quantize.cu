@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "gemm_f16.h"
 #include "gemm_mxfp4_launch.cuh"
@@ -102,7 +103,29 @@ struct QuantParams {
     int32_t step_groups;
 };
 
-// Eight elements per thread, a block per four neighbouring lanes.
+// Eight adjacent elements of X, zeros past the row's end.
+template <class T, bool kVec>
+struct QuantGroup {
+    static constexpr int W = sizeof(T) * 8 / 16;
+    uint4 raw[W];
+
+    __device__ __forceinline__ void load(const T *x, int k0, int K)
+    {
+        if constexpr (kVec) {   // K is a multiple of 8 and the rows are 16-byte aligned
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                raw[i] = k0 < K ? __ldg(reinterpret_cast<const uint4 *>(x + k0) + i) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            T e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = k0 + i < K ? __ldg(x + k0 + i) : from_float<T>(0.0f);
+            memcpy(raw, e, sizeof(raw));
+        }
+    }
+};
+
+// Eight elements per thread, a block per four neighbouring lanes; the next
+// group's loads are under way while a group is converted.
 template <class T, bool kVec, bool kValues>
 __global__ void __launch_bounds__(256) mxfp4_quantize_rows(const T *__restrict__ X, T *__restrict__ V, QuantParams p)
 {
@@ -111,28 +134,25 @@ __global__ void __launch_bounds__(256) mxfp4_quantize_rows(const T *__restrict__
     const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     int64_t row = first / p.groups;
     int g = static_cast<int>(first - row * p.groups);
+    QuantGroup<T, kVec> next;
+    if (row < p.rows) next.load(X + row * p.K, g * 8, p.K);
     // All four lanes of a block have the same row, so they leave together.
     while (row < p.rows) {
-        const T *x = X + row * p.K;
         const int k0 = g * 8;
         float v[8];
-        if constexpr (kVec) {   // K is a multiple of 8 and the rows are 16-byte aligned
-            if (k0 < p.K) {
-                constexpr int W = sizeof(T) * 8 / 16;
-                uint4 raw[W];
+        {
+            T e[8];
+            memcpy(e, next.raw, sizeof(e));
 #pragma unroll
-                for (int i = 0; i < W; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + k0) + i);
-                const T *e = reinterpret_cast<const T *>(raw);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = k0 + i < p.K ? to_float(x[k0 + i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
         }
+        int64_t next_row = row + p.step_rows;
+        int next_g = g + p.step_groups;
+        if (next_g >= p.groups) {
+            next_g -= p.groups;
+            ++next_row;
+        }
+        if (next_row < p.rows) next.load(X + next_row * p.K, next_g * 8, p.K);
         // Largest magnitude as an integer: NaN's pattern is above infinity's.
         uint32_t amax = 0;
 #pragma unroll
@@ -178,65 +198,121 @@ __global__ void __launch_bounds__(256) mxfp4_quantize_rows(const T *__restrict__
                     if (k0 + i < p.K) out[i] = t[i];
             }
         }
-        row += p.step_rows;
-        g += p.step_groups;
-        if (g >= p.groups) {
-            g -= p.groups;
-            ++row;
-        }
+        row = next_row;
+        g = next_g;
     }
 }
 
-// X stored (K, rows): one thread per column of X (row of the result) and block.
-// The 32 loads of a thread are rows apart, those of a warp adjacent.
-template <class T, bool kValues>
-__global__ void __launch_bounds__(128) mxfp4_quantize_cols(const T *__restrict__ X, T *__restrict__ V, QuantParams p)
+// X stored (K, rows).  A block takes 128 elements of K (one scale tile's four
+// blocks of 32, one per warp) of 32 kCols rows of the result; a thread loads
+// kCols adjacent elements of each of its block's 32 rows of X, so a warp reads
+// 128 bytes at a time.  Its codes and values then lie along K, 16 adjacent bytes
+// here and there in 32 rows: they go through shared memory, so that a row's 64
+// bytes of codes and 128 values are written together (stored by each thread
+// element by element, values took 144 us at 4096 x 4096 fp16, COLUS this way).
+template <class T, int kCols, bool kValues>
+__global__ void __launch_bounds__(128) mxfp4_quantize_cols(const T *__restrict__ X, T *__restrict__ V, QuantParams p,
+                                                           bool v_vec)
 {
+    constexpr int R = 32 * kCols;                                    // rows of the result per block
+    constexpr int CHUNKS = 128 * static_cast<int>(sizeof(T)) / 16;   // 16-byte pieces of a row's values
+    constexpr int PER = 16 / static_cast<int>(sizeof(T));            // values per piece
+    // Piece c of row r lies at piece c ^ ((r / kCols) % 8): a warp's writes, one
+    // piece of every row, then fall into different banks.
+    __shared__ uint4 sv[kValues ? R * CHUNKS : 1];
+    __shared__ uint4 sq[R * 4];
+    __shared__ uint8_t ss[R * 4];
     griddep_wait();
     griddep_launch_dependents();
-    // A warp takes 32 rows of the result, the four warps four blocks along K.
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
-    if (row >= p.rows) return;
-    for (int b = static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x >> 5); b < p.KB;
-         b += static_cast<int>(gridDim.y) * 4) {
-        T x[32];
-        const int k0 = b * 32, n = min(32, p.K - k0);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * R;
+    for (int kt = static_cast<int>(blockIdx.y); kt < p.k_tiles; kt += static_cast<int>(gridDim.y)) {
+        const int k0 = kt * 128 + w * 32;
+        const int n = min(32, p.K - k0);   // <= 0: a block past K
+        const int64_t col = row0 + lane * kCols;
+        T x[32][kCols];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            x[i] = i < n ? X[static_cast<int64_t>(k0 + i) * p.rows + row] : from_float<T>(0.0f);
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) amax = max(amax, __float_as_uint(to_float(x[i])) & 0x7FFFFFFFu);
-        const uint32_t byte = scale_byte(amax);
-        uint32_t codes[4] = {0, 0, 0, 0};
-        if (byte != 255u) {
-            const float inv = inverse_scale(byte);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = to_float(x[8 * j + i]) * inv;
-                codes[j] = e2m1x8(v);
+        for (int i = 0; i < 32; ++i) {
+            const T *src = X + static_cast<int64_t>(k0 + i) * p.rows + col;
+            if constexpr (kCols == 2) {   // rows is even and X 4-byte aligned
+                uint32_t v = 0;
+                if (i < n && col < p.rows) v = __ldg(reinterpret_cast<const uint32_t *>(src));
+                memcpy(x[i], &v, 4);
+            } else {
+                x[i][0] = i < n && col < p.rows ? __ldg(src) : from_float<T>(0.0f);
             }
         }
-        *reinterpret_cast<uint4 *>(p.Q + row * (static_cast<int64_t>(p.KB) * 16) + b * 16) =
-            make_uint4(codes[0], codes[1], codes[2], codes[3]);
-        uint8_t *s = p.S + scale_offset(row, b, p.k_tiles);
-        *s = static_cast<uint8_t>(byte);
-        if (b == p.KB - 1)
-            for (int i = 1; b + i < 4 * p.k_tiles; ++i) s[i] = 0;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            const int r = lane * kCols + c;
+            const int sw = lane & 7;
+            uint32_t amax = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) amax = max(amax, __float_as_uint(to_float(x[i][c])) & 0x7FFFFFFFu);
+            const uint32_t byte = scale_byte(amax);
+            uint32_t codes[4] = {0, 0, 0, 0};
+            if (byte != 255u) {
+                const float inv = inverse_scale(byte);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = to_float(x[8 * j + i][c]) * inv;
+                    codes[j] = e2m1x8(v);
+                }
+            }
+            sq[r * 4 + (w ^ (sw & 3))] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            // A block past K: scale 0, as the blocks that fill up the tile.
+            ss[r * 4 + w] = static_cast<uint8_t>(byte);
+            if constexpr (kValues) {
+                const float sc = scale_value(byte);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float v[8];
+                    e2m1x8_values(codes[j], v);
+                    T t[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t[i] = from_float<T>(v[i] * sc);
+                    constexpr int W = 8 / PER;
+                    uint4 raw[W];
+                    memcpy(raw, t, sizeof(raw));
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        sv[r * CHUNKS + ((w * (CHUNKS / 4) + j * W + i) ^ sw)] = raw[i];
+                }
+            }
+        }
+        __syncthreads();
+        // Codes: 64 bytes per row, as many of them as the row has blocks.
+        for (int i = threadIdx.x; i < R * 4; i += 128) {
+            const int r = i >> 2, b = i & 3;
+            if (row0 + r < p.rows && kt * 4 + b < p.KB)
+                *reinterpret_cast<uint4 *>(p.Q + (row0 + r) * (static_cast<int64_t>(p.KB) * 16) + (kt * 4 + b) * 16) =
+                    sq[r * 4 + (b ^ ((r / kCols) & 3))];
+        }
+        // Scales: a row's four bytes of the tile.
+        if (threadIdx.x < R && row0 + threadIdx.x < p.rows)
+            *reinterpret_cast<uint32_t *>(p.S + scale_offset(row0 + threadIdx.x, kt * 4, p.k_tiles)) =
+                *reinterpret_cast<const uint32_t *>(ss + threadIdx.x * 4);
         if constexpr (kValues) {
-            const float sc = scale_value(byte);
-            T *out = V + row * p.K + k0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v[8];
-                e2m1x8_values(codes[j], v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * j + i < n) out[8 * j + i] = from_float<T>(v[i] * sc);
+            if (v_vec) {
+                for (int i = threadIdx.x; i < R * CHUNKS; i += 128) {
+                    const int r = i / CHUNKS, c = i % CHUNKS;
+                    const int k = kt * 128 + c * PER;
+                    if (row0 + r < p.rows && k < p.K)
+                        *reinterpret_cast<uint4 *>(V + (row0 + r) * p.K + k) = sv[r * CHUNKS + (c ^ ((r / kCols) & 7))];
+                }
+            } else {
+                const T *e = reinterpret_cast<const T *>(sv);
+                for (int i = threadIdx.x; i < R * 128; i += 128) {
+                    const int r = i >> 7, kk = i & 127;
+                    if (row0 + r < p.rows && kt * 128 + kk < p.K)
+                        V[(row0 + r) * p.K + kt * 128 + kk] =
+                            e[(r * CHUNKS + ((kk / PER) ^ ((r / kCols) & 7))) * PER + kk % PER];
+                }
             }
         }
+        __syncthreads();   // before the next tile's writes
     }
 }
 
@@ -273,11 +349,18 @@ int quantize(const Mx4QuantArgs &a)
     const T *X = static_cast<const T *>(a.X);
     T *V = static_cast<T *>(a.V);
     if (a.trans) {
-        const int64_t gx = (a.rows + 31) / 32;
-        const int64_t gy = (p.KB + 3) / 4;
-        const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535), 1);
-        return V ? launch_pdl(mxfp4_quantize_cols<T, true>, grid, 128, a.stream, X, V, p)
-                 : launch_pdl(mxfp4_quantize_cols<T, false>, grid, 128, a.stream, X, V, p);
+        const bool v_vec = a.K % (16 / static_cast<int64_t>(sizeof(T))) == 0 && (reinterpret_cast<uintptr_t>(V) & 15u) == 0;
+        const unsigned gy = static_cast<unsigned>(p.k_tiles < 65535 ? p.k_tiles : 65535);
+        if constexpr (sizeof(T) == 2) {
+            if (a.rows % 2 == 0 && (reinterpret_cast<uintptr_t>(X) & 3u) == 0) {
+                const dim3 grid(static_cast<unsigned>((a.rows + 63) / 64), gy, 1);
+                return V ? launch_pdl(mxfp4_quantize_cols<T, 2, true>, grid, 128, a.stream, X, V, p, v_vec)
+                         : launch_pdl(mxfp4_quantize_cols<T, 2, false>, grid, 128, a.stream, X, V, p, v_vec);
+            }
+        }
+        const dim3 grid(static_cast<unsigned>((a.rows + 31) / 32), gy, 1);
+        return V ? launch_pdl(mxfp4_quantize_cols<T, 1, true>, grid, 128, a.stream, X, V, p, v_vec)
+                 : launch_pdl(mxfp4_quantize_cols<T, 1, false>, grid, 128, a.stream, X, V, p, v_vec);
     }
     const int64_t total = a.rows * p.groups;
     const int64_t max_blocks = static_cast<int64_t>(a.sm_count) * 8;
