@@ -28,6 +28,16 @@ struct BwdParams {
     float inv_dim;
 };
 
+// Elements 2m and 2m + 1 of NV packs in order.
+template <class T, int V, int NV>
+__device__ __forceinline__ float2 ln_pair_of(const LnPack<T, V> (&p)[NV], int m)
+{
+    if constexpr (V == 1) return make_float2(p[2 * m][0], p[2 * m + 1][0]);
+    else return p[m / (V / 2)].pair(m % (V / 2));
+}
+
+__device__ __forceinline__ float half_of(float2 v, int j) { return (j & 1) == 0 ? v.x : v.y; }
+
 // Threads of a block, and blocks per SM: some 1024 threads, so that the loads of
 // one block run while another waits for its row's sum.
 __host__ __device__ constexpr int bwd_threads(int tpr) { return tpr == 32 ? 256 : tpr; }
@@ -44,15 +54,24 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
     griddep_wait();
     griddep_launch_dependents();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float dg[NV][V], db[NV][V];
-    LnPack<W, V> pg[NV];
+    // The arithmetic is done on pairs (two fp32 operations per instruction): with
+    // 16-bit elements the pass is as much a matter of instructions as of bytes
+    // (16384 x 4096 fp16: SCALARUS one by one, PAIRUS in pairs).
+    constexpr int P = V * NV / 2;   // pair m: elements 2m, 2m + 1 of the packs in order
+    float2 dg[P], db[P], gm[P];
+    {
+        LnPack<W, V> pg[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int k = (i * TPR + t) * V;
-        if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
-        else pg[i].fill(1.0f);
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
+            else pg[i].fill(1.0f);
+        }
 #pragma unroll
-        for (int j = 0; j < V; ++j) dg[i][j] = db[i][j] = 0.0f;
+        for (int m = 0; m < P; ++m) {
+            gm[m] = ln_pair_of(pg, m);
+            dg[m] = db[m] = make_float2(0.0f, 0.0f);
+        }
     }
     // The next row's loads are under way while a row's sums are taken.
     LnPack<T, V> nx[NV], nd[NV];
@@ -86,21 +105,26 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
         }
         const float mean = next_mean, rstd = next_rstd;
         if (row + step < p.rows) load(row + step);
-        float s1 = 0.0f, s2 = 0.0f;
+        // z and g stay in registers for the second use.
+        float2 z[P], g[P];
+        float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+        const float2 neg_mean = make_float2(-mean, -mean), rstd2 = make_float2(rstd, rstd);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int m = 0; m < P; ++m) {
+            const float2 d = ln_pair_of(pd, m);
+            // Past the row's end d = 0, so that z does not matter there.
+            z[m] = mul_f32x2(add_f32x2(ln_pair_of(px, m), neg_mean), rstd2);
+            g[m] = mul_f32x2(d, gm[m]);
+            s1 = add_f32x2(s1, g[m]);
+            s2 = fma_f32x2(g[m], z[m], s2);
+            dg[m] = fma_f32x2(d, z[m], dg[m]);
+            db[m] = add_f32x2(db[m], d);
+        }
+        const float2 sum = ln_row_sum2<TPR>(s1.x + s1.y, s2.x + s2.y, sh[it]);
+        const float rc1 = rstd * (sum.x * p.inv_dim), rc2 = rstd * (sum.y * p.inv_dim);
+        const float2 neg_rc1 = make_float2(-rc1, -rc1), neg_rc2 = make_float2(-rc2, -rc2);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float z = (i * TPR + t) * V < p.dim ? (px[i][j] - mean) * rstd : 0.0f;
-                const float d = pd[i][j];
-                const float g = d * pg[i][j];
-                s1 += g;
-                s2 = fmaf(g, z, s2);
-                dg[i][j] = fmaf(d, z, dg[i][j]);
-                db[i][j] += d;
-            }
-        const float2 sum = ln_row_sum2<TPR>(s1, s2, sh[it]);
-        const float c1 = sum.x * p.inv_dim, c2 = sum.y * p.inv_dim;
+        for (int m = 0; m < P; ++m) z[m] = fma_f32x2(z[m], neg_rc2, fma_f32x2(rstd2, g[m], neg_rc1));
         T *dx = p.dX + row * p.dim;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -108,10 +132,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
             if (k >= p.dim) continue;
             LnPack<T, V> out;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float z = (px[i][j] - mean) * rstd;
-                out.e[j] = ln_round<T>(rstd * (fmaf(pd[i][j], pg[i][j], -c1) - z * c2));
-            }
+            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
             out.store(dx + k);
         }
     }
@@ -126,7 +147,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
                 const int k = (i * TPR + t) * V;
                 if (k >= p.dim) continue;
 #pragma unroll
-                for (int j = 0; j < V; ++j) out[k + j] = which == 0 ? dg[i][j] : db[i][j];
+                for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
             }
         } else {
             __syncthreads();
@@ -135,7 +156,8 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
                 const int k = (i * TPR + t) * V;
                 if (k >= p.dim) continue;
 #pragma unroll
-                for (int j = 0; j < V; ++j) comb[sub * p.dim + k + j] = which == 0 ? dg[i][j] : db[i][j];
+                for (int j = 0; j < V; ++j)
+                    comb[sub * p.dim + k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
             }
             __syncthreads();
             for (int k = threadIdx.x; k < p.dim; k += BT) {
@@ -198,13 +220,14 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_columns(BwdParams<T, W> p)
     }
 }
 
-// Adds the parts of 32 columns: 16 warps take every sixteenth part, then their
-// sums are added in order.
+// Adds the parts of 32 columns: 32 warps take every 32nd part, so that a
+// thread's loads (ten for two blocks per SM) are all under way at once, then
+// the warps' sums are added in order.
 template <class W>
-__global__ void __launch_bounds__(512) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
+__global__ void __launch_bounds__(1024) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
                                                              W *__restrict__ dbeta, int parts, int dim)
 {
-    __shared__ float sh[16][33];
+    __shared__ float sh[32][33];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -212,14 +235,14 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_finish(const float *__rest
     const float *src = part + static_cast<int64_t>(blockIdx.y) * parts * dim;
     float s = 0.0f;
     if (k < dim) {
-#pragma unroll 8
-        for (int r = w; r < parts; r += 16) s += src[static_cast<int64_t>(r) * dim + k];
+#pragma unroll 10
+        for (int r = w; r < parts; r += 32) s += src[static_cast<int64_t>(r) * dim + k];
     }
     sh[w][lane] = s;
     __syncthreads();
     if (w == 0 && k < dim) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += sh[i][lane];
+        for (int i = 1; i < 32; ++i) s += sh[i][lane];
         (blockIdx.y == 0 ? dgamma : dbeta)[k] = ln_round<W>(s);
     }
 }
@@ -250,7 +273,7 @@ template <class T, class W, int V>
 int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
-    constexpr int N = V == 1 ? 8 : (sizeof(T) == 2 ? 1 : 2);   // packs of 8 elements
+    constexpr int N = 8 / V;   // packs of 8 elements
     // Up to 512 elements a warp per row; layer_norm_parts counts on it.
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
@@ -282,13 +305,15 @@ int backward(const LayerNormArgs &a)
     p.dim = static_cast<int32_t>(a.dim);
     p.parts = static_cast<int32_t>(layer_norm_parts(a.rows, a.dim, a.sm_count));
     p.inv_dim = 1.0f / static_cast<float>(a.dim);
-    constexpr int V = 16 / sizeof(T);
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
-                           reinterpret_cast<uintptr_t>(a.Y) | reinterpret_cast<uintptr_t>(a.gamma);
-    const bool vec = a.dim % V == 0 && (bits & 15u) == 0;
-    int st = vec ? launch_packs<T, W, V>(p, a.stream) : launch_packs<T, W, 1>(p, a.stream);
+                           reinterpret_cast<uintptr_t>(a.Y) | reinterpret_cast<uintptr_t>(a.gamma) |
+                           (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    constexpr int V = 16 / sizeof(T);
+    int st = (bits & 15u) == 0          ? launch_packs<T, W, V>(p, a.stream)
+             : (bits & 3u) == 0 && V > 4 ? launch_packs<T, W, V / 4>(p, a.stream)
+                                         : launch_packs<T, W, 1>(p, a.stream);
     if (st != GEMM_OK || p.part == nullptr) return st;
-    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 512, a.stream,
+    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 1024, a.stream,
                      static_cast<const float *>(p.part), static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta),
                      p.parts, p.dim);
 }

@@ -126,14 +126,23 @@ template <class T, class W, int V>
 int launch_packs(const FwdParams<T, W> &p, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
-    constexpr int N = V == 1 ? 8 : (sizeof(T) == 2 ? 1 : 2);   // packs of the smallest variant
+    constexpr int N = 8 / V;   // packs of 8 elements
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
-    if (packs <= 32 * 4 * N) return launch_one<T, W, V, 4 * N, 32>(p, stream);
-    if (packs <= 128 * 2 * N) return launch_one<T, W, V, 2 * N, 128>(p, stream);
-    if (packs <= 128 * 4 * N) return launch_one<T, W, V, 4 * N, 128>(p, stream);
-    if (packs <= 512 * 2 * N) return launch_one<T, W, V, 2 * N, 512>(p, stream);
-    if (packs <= 512 * 4 * N) return launch_one<T, W, V, 4 * N, 512>(p, stream);
+    if constexpr (V > 2) {
+        if (packs <= 32 * 4 * N) return launch_one<T, W, V, 4 * N, 32>(p, stream);
+        if (packs <= 128 * 2 * N) return launch_one<T, W, V, 2 * N, 128>(p, stream);
+        if (packs <= 128 * 4 * N) return launch_one<T, W, V, 4 * N, 128>(p, stream);
+        if (packs <= 512 * 2 * N) return launch_one<T, W, V, 2 * N, 512>(p, stream);
+        if (packs <= 512 * 4 * N) return launch_one<T, W, V, 4 * N, 512>(p, stream);
+    } else {
+        // Narrow loads: eight elements per thread, as many threads as that takes.
+        if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
+        if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
+        if (packs <= 512 * N) return launch_one<T, W, V, N, 512>(p, stream);
+        if (packs <= 1024 * N) return launch_one<T, W, V, N, 1024>(p, stream);
+        if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
+    }
     return ln_launch(layer_norm_fwd_long<T, W>, dim3(static_cast<unsigned>(p.rows), 1, 1), 1024, stream, p);
 }
 
@@ -151,10 +160,12 @@ int forward(const LayerNormArgs &a)
     p.dim = static_cast<int32_t>(a.dim);
     p.inv_dim = 1.0f / static_cast<float>(a.dim);
     p.eps = a.eps;
-    constexpr int V = 16 / sizeof(T);
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.Y) |
-                           reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.beta);
-    if (a.dim % V == 0 && (bits & 15u) == 0) return launch_packs<T, W, V>(p, a.stream);
+                           reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.beta) |
+                           (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    constexpr int V = 16 / sizeof(T);
+    if ((bits & 15u) == 0) return launch_packs<T, W, V>(p, a.stream);
+    if ((bits & 3u) == 0 && V > 4) return launch_packs<T, W, V / 4>(p, a.stream);
     return launch_packs<T, W, 1>(p, a.stream);
 }
 

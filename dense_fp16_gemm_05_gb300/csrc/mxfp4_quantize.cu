@@ -20,6 +20,7 @@
 
 #include "gemm_f16.h"
 #include "gemm_mxfp4_launch.cuh"
+#include "sm103_ptx.cuh"
 
 namespace {
 
@@ -72,6 +73,29 @@ __device__ __forceinline__ void e2m1x8_values(uint32_t codes, float (&v)[8])
     }
 }
 
+// Largest magnitude of sixteen elements as an fp32 bit pattern; NaN's pattern is
+// above infinity's.  16-bit elements are compared two at a time.
+__device__ __forceinline__ uint32_t max_magnitude(const float (&e)[16])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(e[i]) & 0x7FFFFFFFu);
+    return m;
+}
+template <class T>
+__device__ __forceinline__ uint32_t max_magnitude(const T (&e)[16])
+{
+    uint32_t raw[8];
+    memcpy(raw, e, sizeof(raw));
+    uint32_t m = raw[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, raw[i] & 0x7FFF7FFFu);
+    const uint16_t top = static_cast<uint16_t>(max(m & 0xFFFFu, m >> 16));
+    T t;
+    memcpy(&t, &top, sizeof(top));
+    return __float_as_uint(to_float(t)) & 0x7FFFFFFFu;
+}
+
 // Scale byte of a block whose largest |x| has the bit pattern `amax` (fp32).
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax)
 {
@@ -88,89 +112,102 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);   // 2^-127 is subnormal
 }
 
-__device__ __forceinline__ int64_t scale_offset(int64_t row, int b, int k_tiles)
+__device__ __forceinline__ int64_t scale_offset(int row, int b, int k_tiles)
 {
-    return ((row >> 7) * k_tiles + (b >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (b & 3);
+    return static_cast<int64_t>(row >> 7) * (static_cast<int64_t>(k_tiles) * 512) +
+           static_cast<int64_t>(b >> 2) * 512 + ((row & 31) * 16 + ((row >> 5) & 3) * 4 + (b & 3));
 }
 
 struct QuantParams {
     uint8_t *Q;
     uint8_t *S;
-    int64_t rows;
+    int32_t rows;
     int32_t K, KB, k_tiles;
-    int32_t groups;        // 8-element groups per row, 4 KB
-    int64_t step_rows;     // grid stride in groups = step_rows * groups + step_groups
+    int32_t groups;        // 16-element groups per row, 2 KB
+    int32_t step_rows;     // grid stride in groups = step_rows * groups + step_groups
     int32_t step_groups;
+    int64_t step_x;        // the same stride in elements of X
 };
 
-// Eight adjacent elements of X, zeros past the row's end.
+// Sixteen adjacent elements of X, of which the row has `left`, zeros past its end.
 template <class T, bool kVec>
 struct QuantGroup {
-    static constexpr int W = sizeof(T) * 8 / 16;
+    static constexpr int W = sizeof(T);   // pieces of 16 bytes
     uint4 raw[W];
 
-    __device__ __forceinline__ void load(const T *x, int k0, int K)
+    __device__ __forceinline__ void load(const T *x, int left)
     {
-        if constexpr (kVec) {   // K is a multiple of 8 and the rows are 16-byte aligned
+        if constexpr (kVec) {   // rows are whole pieces, 16-byte aligned
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                raw[i] = k0 < K ? __ldg(reinterpret_cast<const uint4 *>(x + k0) + i) : make_uint4(0u, 0u, 0u, 0u);
+                raw[i] = left > 16 / W * i ? __ldg(reinterpret_cast<const uint4 *>(x) + i) : make_uint4(0u, 0u, 0u, 0u);
         } else {
-            T e[8];
+            T e[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = k0 + i < K ? __ldg(x + k0 + i) : from_float<T>(0.0f);
+            for (int i = 0; i < 16; ++i) e[i] = i < left ? __ldg(x + i) : from_float<T>(0.0f);
             memcpy(raw, e, sizeof(raw));
         }
     }
 };
 
-// Eight elements per thread, a block per four neighbouring lanes; the next
-// group's loads are under way while a group is converted.
+// Blocks per SM (one wave): as many as the registers allow without spilling.
+__host__ __device__ constexpr int quant_blocks(size_t el, bool vec) { return el == 2 && vec ? 5 : 4; }
+
+// Sixteen elements per thread, a block per two neighbouring lanes; the next
+// group's loads are under way while a group is converted.  By counters the
+// pass is bound by instructions before it is by bytes (issue slots 75 % busy
+// with eight elements per thread), hence the longer groups, the comparison of
+// magnitudes as packed integers and offsets that are carried along.
 template <class T, bool kVec, bool kValues>
-__global__ void __launch_bounds__(256) mxfp4_quantize_rows(const T *__restrict__ X, T *__restrict__ V, QuantParams p)
+__global__ void __launch_bounds__(256, quant_blocks(sizeof(T), kVec)) mxfp4_quantize_rows(const T *__restrict__ X, T *__restrict__ V, QuantParams p)
 {
     griddep_wait();   // X may come from the kernel just before
     griddep_launch_dependents();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    int64_t row = first / p.groups;
-    int g = static_cast<int>(first - row * p.groups);
+    int row = static_cast<int>(first / p.groups);
+    int g = static_cast<int>(first - static_cast<int64_t>(row) * p.groups);
+    // Offsets of the thread's group in X (and V) and in Q, whose rows are whole
+    // groups.
+    int64_t at = static_cast<int64_t>(row) * p.K + g * 16;
+    uint8_t *q = p.Q + first * 8;
+    const int64_t step_q = static_cast<int64_t>(gridDim.x) * blockDim.x * 8;
     QuantGroup<T, kVec> next;
-    if (row < p.rows) next.load(X + row * p.K, g * 8, p.K);
-    // All four lanes of a block have the same row, so they leave together.
+    if (row < p.rows) next.load(X + at, p.K - g * 16);
+    // Both lanes of a block have the same row, so they leave together.
     while (row < p.rows) {
-        const int k0 = g * 8;
-        float v[8];
-        {
-            T e[8];
-            memcpy(e, next.raw, sizeof(e));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
-        }
-        int64_t next_row = row + p.step_rows;
+        const int left = p.K - g * 16;   // elements of the row from here on
+        T e[16];
+        memcpy(e, next.raw, sizeof(e));
+        // Unsigned: rows of the next group may pass 2^31 after the last one.
+        uint32_t next_row = static_cast<uint32_t>(row) + static_cast<uint32_t>(p.step_rows);
+        int64_t next_at = at + p.step_x;
         int next_g = g + p.step_groups;
         if (next_g >= p.groups) {
             next_g -= p.groups;
             ++next_row;
+            next_at += p.K - p.groups * 16;
         }
-        if (next_row < p.rows) next.load(X + next_row * p.K, next_g * 8, p.K);
-        // Largest magnitude as an integer: NaN's pattern is above infinity's.
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        const uint32_t lanes = 0xFu << (threadIdx.x & 28u);
-        amax = max(amax, __shfl_xor_sync(lanes, amax, 1));
-        amax = max(amax, __shfl_xor_sync(lanes, amax, 2));
+        if (next_row < static_cast<uint32_t>(p.rows)) next.load(X + next_at, p.K - next_g * 16);
+        uint32_t amax = max_magnitude(e);
+        amax = max(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30u), amax, 1));
         const uint32_t byte = scale_byte(amax);
-        uint32_t codes = 0;
-        if (byte != 255u) {
-            const float inv = inverse_scale(byte);
+        const float inv = inverse_scale(byte);
+        uint32_t codes[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= inv;
-            codes = e2m1x8(v);
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 s = mul_f32x2(make_float2(to_float(e[8 * h + i]), to_float(e[8 * h + i + 1])),
+                                           make_float2(inv, inv));
+                v[i] = s.x;
+                v[i + 1] = s.y;
+            }
+            codes[h] = byte != 255u ? e2m1x8(v) : 0u;
         }
-        *reinterpret_cast<uint32_t *>(p.Q + row * (static_cast<int64_t>(p.KB) * 16) + g * 4) = codes;
-        if ((g & 3) == 0) {
-            const int b = g >> 2;
+        *reinterpret_cast<uint2 *>(q) = make_uint2(codes[0], codes[1]);
+        if ((g & 1) == 0) {
+            const int b = g >> 1;
             uint8_t *s = p.S + scale_offset(row, b, p.k_tiles);
             *s = static_cast<uint8_t>(byte);
             // The blocks that fill up the last tile multiply zero operands: not NaN.
@@ -179,27 +216,33 @@ __global__ void __launch_bounds__(256) mxfp4_quantize_rows(const T *__restrict__
         }
         if constexpr (kValues) {
             const float sc = scale_value(byte);
-            e2m1x8_values(codes, v);
-            T *out = V + row * p.K + k0;
-            T t[8];
+            T *out = V + at;
+            T t[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = from_float<T>(v[i] * sc);
+            for (int h = 0; h < 2; ++h) {
+                float v[8];
+                e2m1x8_values(codes[h], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[8 * h + i] = from_float<T>(v[i] * sc);
+            }
             if constexpr (kVec) {
-                constexpr int W = sizeof(T) * 8 / 16;
-                if (k0 < p.K) {
-                    uint4 raw[W];
-                    memcpy(raw, t, sizeof(raw));
+                constexpr int W = sizeof(T);
+                uint4 raw[W];
+                memcpy(raw, t, sizeof(raw));
 #pragma unroll
-                    for (int i = 0; i < W; ++i) reinterpret_cast<uint4 *>(out)[i] = raw[i];
-                }
+                for (int i = 0; i < W; ++i)
+                    if (left > 16 / W * i) reinterpret_cast<uint4 *>(out)[i] = raw[i];
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (k0 + i < p.K) out[i] = t[i];
+                for (int i = 0; i < 16; ++i)
+                    if (i < left) out[i] = t[i];
             }
         }
-        row = next_row;
+        if (next_row >= static_cast<uint32_t>(p.rows)) break;
+        row = static_cast<int>(next_row);
         g = next_g;
+        at = next_at;
+        q += step_q;
     }
 }
 
@@ -292,7 +335,7 @@ __global__ void __launch_bounds__(128) mxfp4_quantize_cols(const T *__restrict__
         }
         // Scales: a row's four bytes of the tile.
         if (threadIdx.x < R && row0 + threadIdx.x < p.rows)
-            *reinterpret_cast<uint32_t *>(p.S + scale_offset(row0 + threadIdx.x, kt * 4, p.k_tiles)) =
+            *reinterpret_cast<uint32_t *>(p.S + scale_offset(static_cast<int>(row0) + static_cast<int>(threadIdx.x), kt * 4, p.k_tiles)) =
                 *reinterpret_cast<const uint32_t *>(ss + threadIdx.x * 4);
         if constexpr (kValues) {
             if (v_vec) {
@@ -341,11 +384,11 @@ int quantize(const Mx4QuantArgs &a)
     QuantParams p{};
     p.Q = a.Q;
     p.S = a.S;
-    p.rows = a.rows;
+    p.rows = static_cast<int32_t>(a.rows);
     p.K = static_cast<int32_t>(a.K);
     p.KB = static_cast<int32_t>((a.K + 31) / 32);
     p.k_tiles = static_cast<int32_t>(mx4_k_tiles(a.K));
-    p.groups = p.KB * 4;
+    p.groups = p.KB * 2;
     const T *X = static_cast<const T *>(a.X);
     T *V = static_cast<T *>(a.V);
     if (a.trans) {
@@ -362,15 +405,17 @@ int quantize(const Mx4QuantArgs &a)
         return V ? launch_pdl(mxfp4_quantize_cols<T, 1, true>, grid, 128, a.stream, X, V, p, v_vec)
                  : launch_pdl(mxfp4_quantize_cols<T, 1, false>, grid, 128, a.stream, X, V, p, v_vec);
     }
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.V) |
+                           (static_cast<uintptr_t>(a.K) * sizeof(T));
+    const bool vec = (bits & 15u) == 0;
     const int64_t total = a.rows * p.groups;
-    const int64_t max_blocks = static_cast<int64_t>(a.sm_count) * 8;
+    const int64_t max_blocks = static_cast<int64_t>(a.sm_count) * quant_blocks(sizeof(T), vec);
     int64_t blocks = (total + 255) / 256;
     if (blocks > max_blocks) blocks = max_blocks;
     const int64_t step = blocks * 256;
-    p.step_rows = step / p.groups;
+    p.step_rows = static_cast<int32_t>(step / p.groups);
     p.step_groups = static_cast<int32_t>(step % p.groups);
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.V);
-    const bool vec = (a.K % 8) == 0 && (bits & 15u) == 0;
+    p.step_x = static_cast<int64_t>(p.step_rows) * a.K + static_cast<int64_t>(p.step_groups) * 16;
     const dim3 grid(static_cast<unsigned>(blocks), 1, 1);
     if (vec)
         return V ? launch_pdl(mxfp4_quantize_rows<T, true, true>, grid, 256, a.stream, X, V, p)
