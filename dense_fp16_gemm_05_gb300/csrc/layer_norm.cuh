@@ -107,6 +107,17 @@ struct LnPack {
         for (int i = 0; i < V; ++i) e[i] = ln_round<T>(v);
     }
     __device__ __forceinline__ float operator[](int i) const { return ln_float(e[i]); }
+    // Hides from the compiler that the elements are the ones it has seen.
+    __device__ __forceinline__ void opaque()
+    {
+        if constexpr (V * sizeof(T) % 4 == 0) {
+            uint32_t raw[V * sizeof(T) / 4];
+            memcpy(raw, e, sizeof(e));
+#pragma unroll
+            for (unsigned i = 0; i < V * sizeof(T) / 4; ++i) asm volatile("" : "+r"(raw[i]));
+            memcpy(e, raw, sizeof(e));
+        }
+    }
     // Elements 2i and 2i + 1.
     __device__ __forceinline__ float2 pair(int i) const
     {
@@ -120,22 +131,24 @@ struct LnPack {
     }
 };
 
+// Sum over N neighbouring lanes.
+template <int N = 32>
 __device__ __forceinline__ float ln_warp_sum(float v)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// Sums over the TPR threads of a row, the same bits in each of them.  TPR = 32:
-// a warp; else the whole block, through `sh` (TPR / 32 entries), not in use by
+// Sums over the TPR threads of a row, the same bits in each of them.  TPR <= 32:
+// lanes of a warp; else the whole block, through `sh` (TPR / 32 entries), not in use by
 // an earlier sum that some thread may still be reading.  Every warp adds the
 // warps' sums by shuffles: reading them one by one costs TPR / 32 loads and adds
 // in every thread, a third of the backward pass's instructions for 512 threads.
 template <int TPR>
 __device__ __forceinline__ float ln_row_sum(float v, float *sh)
 {
-    v = ln_warp_sum(v);
+    v = ln_warp_sum<(TPR < 32 ? TPR : 32)>(v);
     if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
         __syncthreads();
@@ -149,8 +162,8 @@ __device__ __forceinline__ float ln_row_sum(float v, float *sh)
 template <int TPR>
 __device__ __forceinline__ float2 ln_row_sum2(float a, float b, float2 *sh)
 {
-    a = ln_warp_sum(a);
-    b = ln_warp_sum(b);
+    a = ln_warp_sum<(TPR < 32 ? TPR : 32)>(a);
+    b = ln_warp_sum<(TPR < 32 ? TPR : 32)>(b);
     if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();

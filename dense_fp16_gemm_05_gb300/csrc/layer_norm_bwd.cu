@@ -40,26 +40,36 @@ __device__ __forceinline__ float half_of(float2 v, int j) { return (j & 1) == 0 
 
 // Threads of a block, and blocks per SM: some 1024 threads, so that the loads of
 // one block run while another waits for its row's sum.
-__host__ __device__ constexpr int bwd_threads(int tpr) { return tpr == 32 ? 256 : tpr; }
-__host__ __device__ constexpr int bwd_blocks(int tpr) { return tpr == 32 ? 2 : 1024 / tpr; }
+__host__ __device__ constexpr int bwd_threads(int tpr) { return tpr <= 32 ? 256 : tpr; }
+__host__ __device__ constexpr int bwd_blocks(int tpr, int v, int per)
+{
+    if (tpr <= 32) return per <= 8 ? 4 : 2;
+    return v == 1 ? 1 : 1024 / tpr;
+}
 
 template <class T, class W, int V, int NV, int TPR>
-__global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd_blocks(TPR)) layer_norm_bwd_kernel(BwdParams<T, W> p)
+__global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) layer_norm_bwd_kernel(BwdParams<T, W> p)
 {
     constexpr int BT = bwd_threads(TPR);
     constexpr int R = BT / TPR;   // rows at a time
-    static_assert(TPR == 32 || R == 1, "a warp or a block per row");
-    __shared__ float2 sh[2][TPR / 32];
+    static_assert(TPR <= 32 || R == 1, "lanes of a warp or a block per row");
+    __shared__ float2 sh[2][TPR < 32 ? 1 : TPR / 32];
     extern __shared__ float comb[];   // R > 1: (R, dim)
     griddep_wait();
     griddep_launch_dependents();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     // The arithmetic is done on pairs (two fp32 operations per instruction): with
     // 16-bit elements the pass is as much a matter of instructions as of bytes
-    // (16384 x 4096 fp16: SCALARUS one by one, PAIRUS in pairs).
+    // (16384 x 4096 fp16: 90 us one by one, 83 us in pairs).
     constexpr int P = V * NV / 2;   // pair m: elements 2m, 2m + 1 of the packs in order
+    // What a thread keeps is weighed against registers: fp32 rows and 16 elements
+    // per thread read gamma again for every row (from L1), and 16 elements in a
+    // block of 1024 threads, which has 64 registers for each, also neither
+    // prefetch nor keep z and g.
+    constexpr bool kReload = sizeof(T) == 4 || V * NV > 8;
+    constexpr bool kLean = TPR == 1024 && V * NV > 8;
     float2 dg[P], db[P], gm[P];
-    {
+    auto load_gamma = [&]() {
         LnPack<W, V> pg[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -68,21 +78,22 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
             else pg[i].fill(1.0f);
         }
 #pragma unroll
-        for (int m = 0; m < P; ++m) {
-            gm[m] = ln_pair_of(pg, m);
-            dg[m] = db[m] = make_float2(0.0f, 0.0f);
-        }
-    }
+        for (int m = 0; m < P; ++m) gm[m] = ln_pair_of(pg, m);
+    };
+    if constexpr (!kReload) load_gamma();
+#pragma unroll
+    for (int m = 0; m < P; ++m) dg[m] = db[m] = make_float2(0.0f, 0.0f);
     // The next row's loads are under way while a row's sums are taken.
     LnPack<T, V> nx[NV], nd[NV];
     float next_mean = 0.0f, next_rstd = 0.0f;
     auto load = [&](int64_t row) {
         const T *x = p.X + row * p.dim;
         const T *dy = p.dY + row * p.dim;
+        const bool in = TPR >= 32 || row < p.rows;   // else the loop has seen to it
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (k < p.dim) {
+            if (in && k < p.dim) {
                 nx[i].load(x + k);
                 nd[i].load(dy + k);
             } else {
@@ -90,21 +101,26 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
                 nd[i].fill(0.0f);   // adds nothing to any sum
             }
         }
-        next_mean = __ldg(p.mean + row);
-        next_rstd = __ldg(p.rstd + row);
+        next_mean = in ? __ldg(p.mean + row) : 0.0f;
+        next_rstd = in ? __ldg(p.rstd + row) : 0.0f;
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * R;
     int64_t row = static_cast<int64_t>(blockIdx.x) * R + sub;
-    if (row < p.rows) load(row);
-    for (int it = 0; row < p.rows; row += step, it ^= 1) {
+    // Lanes of a warp with several rows stay together for the shuffles: `lead`
+    // is the warp's first row, and a lane without a row adds zeros.
+    int64_t lead = row - (TPR < 32 ? sub % (32 / TPR) : 0);
+    if (!kLean && (TPR < 32 || row < p.rows)) load(row);
+    for (int it = 0; lead < p.rows; lead += step, row += step, it ^= 1) {
         LnPack<T, V> px[NV], pd[NV];
+        if constexpr (kLean) load(row);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             px[i] = nx[i];
             pd[i] = nd[i];
         }
         const float mean = next_mean, rstd = next_rstd;
-        if (row + step < p.rows) load(row + step);
+        if (!kLean && (TPR < 32 || row + step < p.rows)) load(row + step);
+        if constexpr (kReload) load_gamma();
         // z and g stay in registers for the second use.
         float2 z[P], g[P];
         float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
@@ -123,13 +139,28 @@ __global__ void __launch_bounds__(bwd_threads(TPR), V == 1 && TPR > 32 ? 1 : bwd
         const float2 sum = ln_row_sum2<TPR>(s1.x + s1.y, s2.x + s2.y, sh[it]);
         const float rc1 = rstd * (sum.x * p.inv_dim), rc2 = rstd * (sum.y * p.inv_dim);
         const float2 neg_rc1 = make_float2(-rc1, -rc1), neg_rc2 = make_float2(-rc2, -rc2);
+        if constexpr (kLean) {
+            // From the packed elements again; the barrier keeps the compiler from
+            // holding (and spilling) the first values instead.
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                px[i].opaque();
+                pd[i].opaque();
+            }
+            load_gamma();
+#pragma unroll
+            for (int m = 0; m < P; ++m) {
+                z[m] = mul_f32x2(add_f32x2(ln_pair_of(px, m), neg_mean), rstd2);
+                g[m] = mul_f32x2(ln_pair_of(pd, m), gm[m]);
+            }
+        }
 #pragma unroll
         for (int m = 0; m < P; ++m) z[m] = fma_f32x2(z[m], neg_rc2, fma_f32x2(rstd2, g[m], neg_rc1));
         T *dx = p.dX + row * p.dim;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (k >= p.dim) continue;
+            if (k >= p.dim || (TPR < 32 && row >= p.rows)) continue;
             LnPack<T, V> out;
 #pragma unroll
             for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
@@ -220,14 +251,13 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_columns(BwdParams<T, W> p)
     }
 }
 
-// Adds the parts of 32 columns: 32 warps take every 32nd part, so that a
-// thread's loads (ten for two blocks per SM) are all under way at once, then
-// the warps' sums are added in order.
+// Adds the parts of 32 columns: 16 warps take every sixteenth part, then their
+// sums are added in order.
 template <class W>
-__global__ void __launch_bounds__(1024) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
+__global__ void __launch_bounds__(512) layer_norm_bwd_finish(const float *__restrict__ part, W *__restrict__ dgamma,
                                                              W *__restrict__ dbeta, int parts, int dim)
 {
-    __shared__ float sh[32][33];
+    __shared__ float sh[16][33];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -236,13 +266,13 @@ __global__ void __launch_bounds__(1024) layer_norm_bwd_finish(const float *__res
     float s = 0.0f;
     if (k < dim) {
 #pragma unroll 10
-        for (int r = w; r < parts; r += 32) s += src[static_cast<int64_t>(r) * dim + k];
+        for (int r = w; r < parts; r += 16) s += src[static_cast<int64_t>(r) * dim + k];
     }
     sh[w][lane] = s;
     __syncthreads();
     if (w == 0 && k < dim) {
 #pragma unroll
-        for (int i = 1; i < 32; ++i) s += sh[i][lane];
+        for (int i = 1; i < 16; ++i) s += sh[i][lane];
         (blockIdx.y == 0 ? dgamma : dbeta)[k] = ln_round<W>(s);
     }
 }
@@ -275,6 +305,11 @@ int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
     // Up to 512 elements a warp per row; layer_norm_parts counts on it.
+    if constexpr (V > 2) {
+        // Short rows (a head's width) share a warp.
+        if (packs <= 8 * N) return launch_one<T, W, V, N, 8>(p, stream);
+        if (packs <= 16 * N) return launch_one<T, W, V, N, 16>(p, stream);
+    }
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
     if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
@@ -313,7 +348,7 @@ int backward(const LayerNormArgs &a)
              : (bits & 3u) == 0 && V > 4 ? launch_packs<T, W, V / 4>(p, a.stream)
                                          : launch_packs<T, W, 1>(p, a.stream);
     if (st != GEMM_OK || p.part == nullptr) return st;
-    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 1024, a.stream,
+    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 512, a.stream,
                      static_cast<const float *>(p.part), static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta),
                      p.parts, p.dim);
 }

@@ -27,16 +27,18 @@ struct FwdParams {
 
 // TPR threads per row, NV packs of V elements per thread, pack i of thread t at
 // element (i TPR + t) V.
-template <class T, class W, int V, int NV, int TPR>
+template <class T, class W, int V, int NV, int TPR, bool kGamma, bool kBeta>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(FwdParams<T, W> p)
 {
     constexpr int BT = TPR < 128 ? 128 : TPR;
-    __shared__ float sh[2][TPR / 32];
+    __shared__ float sh[2][TPR < 32 ? 1 : TPR / 32];
     griddep_wait();   // X may come from the kernel just before
     griddep_launch_dependents();
     const int t = threadIdx.x % TPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (BT / TPR) + threadIdx.x / TPR;
-    if (row >= p.rows) return;   // whole warps (TPR = 32) or no thread
+    int64_t row = static_cast<int64_t>(blockIdx.x) * (BT / TPR) + threadIdx.x / TPR;
+    // Lanes without a row take the last one along, for the sake of the shuffles.
+    const bool in = row < p.rows;
+    if (!in) row = p.rows - 1;
     const T *x = p.X + row * p.dim;
     LnPack<T, V> px[NV];
     float s = 0.0f;
@@ -63,6 +65,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(F
         }
     const float var = ln_row_sum<TPR>(s, sh[1]) * p.inv_dim;
     const float rstd = 1.0f / sqrtf(var + p.eps);
+    if (!in) return;
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -71,11 +74,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(F
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int k = (i * TPR + t) * V;
-        if (k >= p.dim) continue;
+        if (k >= p.dim) break;
         LnPack<W, V> g, b;
-        if (p.gamma) g.load(p.gamma + k);
+        if (kGamma) g.load(p.gamma + k);
         else g.fill(1.0f);
-        if (p.beta) b.load(p.beta + k);
+        if (kBeta) b.load(p.beta + k);
         else b.fill(0.0f);
         LnPack<T, V> out;
 #pragma unroll
@@ -118,8 +121,13 @@ int launch_one(const FwdParams<T, W> &p, cudaStream_t stream)
 {
     constexpr int BT = TPR < 128 ? 128 : TPR;
     constexpr int R = BT / TPR;
-    return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR>, dim3(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1),
-                     BT, stream, p);
+    // The usual case, both weights, has its own kernel: a branch on each pointer
+    // at every element is a tenth of the narrow variants' instructions.
+    const dim3 grid(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1);
+    if (p.gamma && p.beta) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, true, true>, grid, BT, stream, p);
+    if (p.gamma) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, true, false>, grid, BT, stream, p);
+    if (p.beta) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, false, true>, grid, BT, stream, p);
+    return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, false, false>, grid, BT, stream, p);
 }
 
 template <class T, class W, int V>
@@ -127,6 +135,11 @@ int launch_packs(const FwdParams<T, W> &p, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
+    if constexpr (V > 2) {
+        // Short rows (a head's width) share a warp.
+        if (packs <= 8 * N) return launch_one<T, W, V, N, 8>(p, stream);
+        if (packs <= 16 * N) return launch_one<T, W, V, N, 16>(p, stream);
+    }
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
     if constexpr (V > 2) {
