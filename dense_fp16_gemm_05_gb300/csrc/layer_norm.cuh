@@ -140,21 +140,32 @@ __device__ __forceinline__ float ln_warp_sum(float v)
     return v;
 }
 
-// Sums over the TPR threads of a row, the same bits in each of them.  TPR <= 32:
-// lanes of a warp; else the whole block, through `sh` (TPR / 32 entries), not in use by
-// an earlier sum that some thread may still be reading.  Every warp adds the
-// warps' sums by shuffles: reading them one by one costs TPR / 32 loads and adds
-// in every thread, a third of the backward pass's instructions for 512 threads.
+// Threads of a row, as a template argument: TPR <= 32, lanes of a warp; TPR > 32
+// (a power of 2), a block; TPR < 0, a block of whole warps chosen at launch, up
+// to -TPR threads, so that rows of any length leave few threads idle.
+template <int TPR>
+__device__ __forceinline__ int ln_threads()
+{
+    if constexpr (TPR > 0) return TPR;
+    else return static_cast<int>(blockDim.x);
+}
+__host__ __device__ constexpr int ln_warps(int tpr) { return tpr < 0 ? -tpr / 32 : (tpr <= 32 ? 1 : tpr / 32); }
+
+// Sums over the threads of a row, the same bits in each of them; for a block
+// through `sh` (ln_warps entries), not in use by an earlier sum that some thread
+// may still be reading.  Every warp adds the warps' sums by shuffles: reading
+// them one by one costs a load and an add per warp in every thread, a third of
+// the backward pass's instructions for 512 threads.
 template <int TPR>
 __device__ __forceinline__ float ln_row_sum(float v, float *sh)
 {
-    v = ln_warp_sum<(TPR < 32 ? TPR : 32)>(v);
-    if constexpr (TPR > 32) {
-        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    v = ln_warp_sum<(TPR > 0 && TPR < 32 ? TPR : 32)>(v);
+    if constexpr (TPR > 32 || TPR < 0) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) sh[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = sh[threadIdx.x & (TPR / 32 - 1)];
-#pragma unroll
-        for (int o = TPR / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if constexpr (TPR > 0) v = ln_warp_sum<TPR / 32>(sh[lane & (TPR / 32 - 1)]);
+        else v = ln_warp_sum<32>(lane < static_cast<int>(blockDim.x >> 5) ? sh[lane] : 0.0f);
     }
     return v;
 }
@@ -162,18 +173,20 @@ __device__ __forceinline__ float ln_row_sum(float v, float *sh)
 template <int TPR>
 __device__ __forceinline__ float2 ln_row_sum2(float a, float b, float2 *sh)
 {
-    a = ln_warp_sum<(TPR < 32 ? TPR : 32)>(a);
-    b = ln_warp_sum<(TPR < 32 ? TPR : 32)>(b);
-    if constexpr (TPR > 32) {
-        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+    a = ln_warp_sum<(TPR > 0 && TPR < 32 ? TPR : 32)>(a);
+    b = ln_warp_sum<(TPR > 0 && TPR < 32 ? TPR : 32)>(b);
+    if constexpr (TPR > 32 || TPR < 0) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
-        float2 s = sh[threadIdx.x & (TPR / 32 - 1)];
-#pragma unroll
-        for (int o = TPR / 64; o > 0; o >>= 1) {
-            s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-            s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+        float2 s = make_float2(0.0f, 0.0f);
+        if constexpr (TPR > 0) {
+            s = sh[lane & (TPR / 32 - 1)];
+            return make_float2(ln_warp_sum<TPR / 32>(s.x), ln_warp_sum<TPR / 32>(s.y));
+        } else {
+            if (lane < static_cast<int>(blockDim.x >> 5)) s = sh[lane];
+            return make_float2(ln_warp_sum<32>(s.x), ln_warp_sum<32>(s.y));
         }
-        return s;
     }
     return make_float2(a, b);
 }

@@ -40,24 +40,28 @@ __device__ __forceinline__ float half_of(float2 v, int j) { return (j & 1) == 0 
 
 // Threads of a block, and blocks per SM: some 1024 threads, so that the loads of
 // one block run while another waits for its row's sum.
-__host__ __device__ constexpr int bwd_threads(int tpr) { return tpr <= 32 ? 256 : tpr; }
+__host__ __device__ constexpr int bwd_threads(int tpr) { return tpr < 0 ? -tpr : (tpr <= 32 ? 256 : tpr); }
 __host__ __device__ constexpr int bwd_blocks(int tpr, int v, int per)
 {
-    if (tpr <= 32) return per <= 8 ? 4 : 2;
-    return v == 1 ? 1 : 1024 / tpr;
+    if (tpr < 0) return 1;
+    if (tpr <= 32) return per <= 8 ? (v > 2 ? 4 : 2) : 2;
+    return 1024 / tpr;
 }
 
 template <class T, class W, int V, int NV, int TPR>
 __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) layer_norm_bwd_kernel(BwdParams<T, W> p)
 {
-    constexpr int BT = bwd_threads(TPR);
-    constexpr int R = BT / TPR;   // rows at a time
+    constexpr int R = TPR > 0 ? bwd_threads(TPR) / TPR : 1;   // rows at a time
     static_assert(TPR <= 32 || R == 1, "lanes of a warp or a block per row");
-    __shared__ float2 sh[2][TPR < 32 ? 1 : TPR / 32];
+    // Rows of lanes without one: a warp holds several.
+    constexpr bool kShared = TPR > 0 && TPR < 32;
+    __shared__ float2 sh[2][ln_warps(TPR)];
     extern __shared__ float comb[];   // R > 1: (R, dim)
     griddep_wait();
     griddep_launch_dependents();
-    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int tpr = ln_threads<TPR>();
+    const int t = R > 1 ? static_cast<int>(threadIdx.x) % tpr : static_cast<int>(threadIdx.x);
+    const int sub = R > 1 ? static_cast<int>(threadIdx.x) / tpr : 0;
     // The arithmetic is done on pairs (two fp32 operations per instruction): with
     // 16-bit elements the pass is as much a matter of instructions as of bytes
     // (16384 x 4096 fp16: 90 us one by one, 83 us in pairs).
@@ -67,13 +71,13 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
     // block of 1024 threads, which has 64 registers for each, also neither
     // prefetch nor keep z and g.
     constexpr bool kReload = sizeof(T) == 4 || V * NV > 8;
-    constexpr bool kLean = TPR == 1024 && V * NV > 8;
+    constexpr bool kLean = (TPR == 1024 || TPR == -1024) && V * NV > 8;
     float2 dg[P], db[P], gm[P];
     auto load_gamma = [&]() {
         LnPack<W, V> pg[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int k = (i * TPR + t) * V;
+            const int k = (i * tpr + t) * V;
             if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
             else pg[i].fill(1.0f);
         }
@@ -89,10 +93,10 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
     auto load = [&](int64_t row) {
         const T *x = p.X + row * p.dim;
         const T *dy = p.dY + row * p.dim;
-        const bool in = TPR >= 32 || row < p.rows;   // else the loop has seen to it
+        const bool in = !kShared || row < p.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int k = (i * TPR + t) * V;
+            const int k = (i * tpr + t) * V;
             if (in && k < p.dim) {
                 nx[i].load(x + k);
                 nd[i].load(dy + k);
@@ -108,8 +112,11 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
     int64_t row = static_cast<int64_t>(blockIdx.x) * R + sub;
     // Lanes of a warp with several rows stay together for the shuffles: `lead`
     // is the warp's first row, and a lane without a row adds zeros.
-    int64_t lead = row - (TPR < 32 ? sub % (32 / TPR) : 0);
-    if (!kLean && (TPR < 32 || row < p.rows)) load(row);
+    int64_t lead = row - (kShared ? sub % (32 / (TPR > 0 ? TPR : 32)) : 0);
+    // A row that is not there is loaded as the last one, and not used: loads
+    // without a condition can be issued ahead.
+    auto there = [&](int64_t r) { return kShared || r < p.rows ? r : p.rows - 1; };
+    if constexpr (!kLean) load(there(row));
     for (int it = 0; lead < p.rows; lead += step, row += step, it ^= 1) {
         LnPack<T, V> px[NV], pd[NV];
         if constexpr (kLean) load(row);
@@ -119,7 +126,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
             pd[i] = nd[i];
         }
         const float mean = next_mean, rstd = next_rstd;
-        if (!kLean && (TPR < 32 || row + step < p.rows)) load(row + step);
+        if constexpr (!kLean) load(there(row + step));
         if constexpr (kReload) load_gamma();
         // z and g stay in registers for the second use.
         float2 z[P], g[P];
@@ -159,8 +166,8 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
         T *dx = p.dX + row * p.dim;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int k = (i * TPR + t) * V;
-            if (k >= p.dim || (TPR < 32 && row >= p.rows)) continue;
+            const int k = (i * tpr + t) * V;
+            if (k >= p.dim || (kShared && row >= p.rows)) continue;
             LnPack<T, V> out;
 #pragma unroll
             for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
         if constexpr (R == 1) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int k = (i * TPR + t) * V;
+                const int k = (i * tpr + t) * V;
                 if (k >= p.dim) continue;
 #pragma unroll
                 for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
@@ -184,14 +191,14 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int k = (i * TPR + t) * V;
+                const int k = (i * tpr + t) * V;
                 if (k >= p.dim) continue;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     comb[sub * p.dim + k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
             }
             __syncthreads();
-            for (int k = threadIdx.x; k < p.dim; k += BT) {
+            for (int k = threadIdx.x; k < p.dim; k += static_cast<int>(blockDim.x)) {
                 float s = comb[k];
 #pragma unroll
                 for (int r = 1; r < R; ++r) s += comb[r * p.dim + k];
@@ -280,8 +287,10 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_finish(const float *__rest
 template <class T, class W, int V, int NV, int TPR>
 int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
 {
-    constexpr int BT = bwd_threads(TPR);
-    constexpr int R = BT / TPR;
+    // Threads: those of the template, or the whole warps that NV packs each need.
+    const int packs = (p.dim + V - 1) / V;
+    const int BT = TPR > 0 ? bwd_threads(TPR) : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    constexpr int R = TPR > 0 ? bwd_threads(TPR) / TPR : 1;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(static_cast<unsigned>(p.parts), 1, 1);
     lc.blockDim = dim3(BT, 1, 1);
@@ -304,19 +313,29 @@ int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
-    // Up to 512 elements a warp per row; layer_norm_parts counts on it.
     if constexpr (V > 2) {
         // Short rows (a head's width) share a warp.
         if (packs <= 8 * N) return launch_one<T, W, V, N, 8>(p, stream);
         if (packs <= 16 * N) return launch_one<T, W, V, N, 16>(p, stream);
     }
+    // Up to 512 elements a warp per row; layer_norm_parts counts on it.
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
-    if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
-    if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
-    if (packs <= 512 * N) return launch_one<T, W, V, N, 512>(p, stream);
-    if (packs <= 1024 * N) return launch_one<T, W, V, N, 1024>(p, stream);
-    if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
+    if constexpr (V > 2) {
+        if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
+        if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
+        if (packs <= 512 * N) return launch_one<T, W, V, N, 512>(p, stream);
+        if (packs <= 1024 * N) return launch_one<T, W, V, N, 1024>(p, stream);
+        if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
+    } else {
+        // Narrow loads are bound by instructions, so no more threads than eight
+        // elements each take (16384 x 4097 fp16: 347 us with the next power of 2,
+        // 171 us this way).
+        if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
+        if (packs <= 768 * N) return launch_one<T, W, V, N, -768>(p, stream);
+        if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
+        if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, -1024>(p, stream);
+    }
     int st = ln_launch(layer_norm_bwd_long<T, W>, dim3(static_cast<unsigned>(p.parts), 1, 1), 1024, stream, p);
     if (st != GEMM_OK || p.part == nullptr) return st;
     return ln_launch(layer_norm_bwd_columns<T, W>,

@@ -25,17 +25,21 @@ struct FwdParams {
     float inv_dim, eps;
 };
 
-// TPR threads per row, NV packs of V elements per thread, pack i of thread t at
-// element (i TPR + t) V.
+// Threads of a block (its bound, where the launch chooses).
+__host__ __device__ constexpr int fwd_threads(int tpr) { return tpr < 0 ? -tpr : (tpr < 128 ? 128 : tpr); }
+
+// tpr threads per row, NV packs of V elements per thread, pack i of thread t at
+// element (i tpr + t) V.
 template <class T, class W, int V, int NV, int TPR, bool kGamma, bool kBeta>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(FwdParams<T, W> p)
+__global__ void __launch_bounds__(fwd_threads(TPR)) layer_norm_fwd_kernel(FwdParams<T, W> p)
 {
-    constexpr int BT = TPR < 128 ? 128 : TPR;
-    __shared__ float sh[2][TPR < 32 ? 1 : TPR / 32];
+    constexpr int R = TPR > 0 ? fwd_threads(TPR) / TPR : 1;   // rows of a block
+    __shared__ float sh[2][ln_warps(TPR)];
     griddep_wait();   // X may come from the kernel just before
     griddep_launch_dependents();
-    const int t = threadIdx.x % TPR;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * (BT / TPR) + threadIdx.x / TPR;
+    const int tpr = ln_threads<TPR>();
+    const int t = TPR > 0 ? static_cast<int>(threadIdx.x) % tpr : static_cast<int>(threadIdx.x);
+    int64_t row = static_cast<int64_t>(blockIdx.x) * R + (R > 1 ? static_cast<int>(threadIdx.x) / tpr : 0);
     // Lanes without a row take the last one along, for the sake of the shuffles.
     const bool in = row < p.rows;
     if (!in) row = p.rows - 1;
@@ -44,7 +48,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(F
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int k = (i * TPR + t) * V;
+        const int k = (i * tpr + t) * V;
         if (k < p.dim) px[i].load(x + k);
         else px[i].fill(0.0f);
     }
@@ -56,7 +60,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(F
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((i * TPR + t) * V < p.dim) {
+        if ((i * tpr + t) * V < p.dim) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float d = px[i][j] - mean;
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) layer_norm_fwd_kernel(F
     T *y = p.Y + row * p.dim;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int k = (i * TPR + t) * V;
+        const int k = (i * tpr + t) * V;
         if (k >= p.dim) break;
         LnPack<W, V> g, b;
         if (kGamma) g.load(p.gamma + k);
@@ -119,8 +123,10 @@ __global__ void __launch_bounds__(1024) layer_norm_fwd_long(FwdParams<T, W> p)
 template <class T, class W, int V, int NV, int TPR>
 int launch_one(const FwdParams<T, W> &p, cudaStream_t stream)
 {
-    constexpr int BT = TPR < 128 ? 128 : TPR;
-    constexpr int R = BT / TPR;
+    // Threads: those of the template, or the whole warps that NV packs each need.
+    const int packs = (p.dim + V - 1) / V;
+    const int BT = TPR > 0 ? fwd_threads(TPR) : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    constexpr int R = TPR > 0 ? fwd_threads(TPR) / TPR : 1;
     // The usual case, both weights, has its own kernel: a branch on each pointer
     // at every element is a tenth of the narrow variants' instructions.
     const dim3 grid(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1);
@@ -136,25 +142,25 @@ int launch_packs(const FwdParams<T, W> &p, cudaStream_t stream)
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
     if constexpr (V > 2) {
-        // Short rows (a head's width) share a warp.
+        // Short rows (a head's width) share a warp: 262144 x 128 fp16 66 -> 34 us.
         if (packs <= 8 * N) return launch_one<T, W, V, N, 8>(p, stream);
         if (packs <= 16 * N) return launch_one<T, W, V, N, 16>(p, stream);
     }
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
-    if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
     if constexpr (V > 2) {
+        if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
         if (packs <= 32 * 4 * N) return launch_one<T, W, V, 4 * N, 32>(p, stream);
         if (packs <= 128 * 2 * N) return launch_one<T, W, V, 2 * N, 128>(p, stream);
         if (packs <= 128 * 4 * N) return launch_one<T, W, V, 4 * N, 128>(p, stream);
-        if (packs <= 512 * 2 * N) return launch_one<T, W, V, 2 * N, 512>(p, stream);
+        if (packs <= 256 * 4 * N) return launch_one<T, W, V, 4 * N, 256>(p, stream);
         if (packs <= 512 * 4 * N) return launch_one<T, W, V, 4 * N, 512>(p, stream);
     } else {
-        // Narrow loads: eight elements per thread, as many threads as that takes.
-        if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
-        if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
-        if (packs <= 512 * N) return launch_one<T, W, V, N, 512>(p, stream);
-        if (packs <= 1024 * N) return launch_one<T, W, V, N, 1024>(p, stream);
-        if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
+        // Narrow loads are bound by instructions, so no more threads than eight
+        // elements each take (16384 x 4097 fp16: 147 us with the next power of 2,
+        // 113 us this way).
+        if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
+        if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
+        if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, -1024>(p, stream);
     }
     return ln_launch(layer_norm_fwd_long<T, W>, dim3(static_cast<unsigned>(p.rows), 1, 1), 1024, stream, p);
 }
