@@ -18,7 +18,7 @@
 // of one K block and the next it drains the tensor pipe: the copies of a K
 // block cost about 300 cycles beside 512 of MMAs whether they are two or six
 // (8192^3: 231 us with copies, 165 us with the copies left out), while a
-// store from another warp runs beside the MMAs (185 us).
+// store from another warp runs beside the MMAs (185 us, all else equal).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -54,6 +54,14 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
                 d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
             : "memory");
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ uint4 ld_shared_u32x4(uint32_t addr)
@@ -163,7 +171,7 @@ struct Mx4Cfg {
     // The two accumulators share the columns [ACC1_COL, BN); the epilogue reads
     // the RELEASE chunks that hold those first.
     static constexpr int RELEASE = (BN - ACC1_COL + EPI_COLS - 1) / EPI_COLS;
-    static_assert(ACC1_COL > 0 && RELEASE < EPI_CHUNKS, "part of the epilogue overlaps the next tile's MMAs");
+    static_assert(ACC1_COL > 0 && RELEASE == 2 && EPI_CHUNKS == 4, "the epilogue's order of reads");
     static_assert((4 * STAGES + 4) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
     static_assert(SF_TILES == 2, "the scale warps' stores");
     static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
@@ -243,7 +251,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     volatile uint32_t *tmem_slot_ptr =
         reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (4 * S + 3));
 
-    const int warp = threadIdx.x >> 5;
+    // By shuffle, so that the compiler knows it uniform in the warp.
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();   // 0: the pair leader, which issues the MMAs
     const bool leader = rank == 0;
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     cluster_wait();
     tc_fence_after_sync();
     griddep_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot_ptr, 0);
     const uint64_t limit = p.timeout_cycles;
     const int KB = p.num_k_blocks;
     const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
@@ -355,7 +364,12 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (leader CTA)
-        if (lane == 0 && leader) {
+        // The whole warp walks the loop and one lane issues: what the MMAs take
+        // (descriptors, addresses) is then in uniform registers already.  With a
+        // single lane in the loop each MMA waited for some ten moves there, and
+        // a K block's four MMAs, 512 cycles of work, took some 640 to issue
+        // (8192^3 with this and the epilogue's early reads: 185 us -> 156 us).
+        if (leader) {
             int s = 0;
             uint32_t ph = 0, acc_it = 0;
             bool ok = true, issued_any = false;
@@ -366,44 +380,46 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             for (int t = first; ok && t < p.num_tiles; t += stride, ++acc_it) {
                 // The epilogue has read the columns that this tile's accumulator
                 // shares with the previous one's (and all of the one before).
-                if (acc_it > 0 && !wait_phase(tempty_bar, (acc_it - 1) & 1u, abort, limit, kSiteMmaTmemEmpty)) {
-                    ok = false;
-                    break;
-                }
+                if (acc_it > 0)
+                    ok = __all_sync(0xffffffffu,
+                                    wait_phase(tempty_bar, (acc_it - 1) & 1u, abort, limit, kSiteMmaTmemEmpty));
+                if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t acc = tmem_base + ((acc_it & 1u) ? Cfg::ACC1_COL : 0);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull) ||
-                        !wait_phase(sready_bar(s), ph, abort, limit, kSiteMmaFull)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull) &&
+                                                     wait_phase(sready_bar(s), ph, abort, limit, kSiteMmaFull));
+                    if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
                     const uint64_t a_st = a_desc0 + static_cast<uint64_t>((s * Cfg::A_STAGE_BYTES) >> 4);
                     const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < Cfg::BK / Cfg::UMMA_K; ++ks) {
-                        const uint64_t step = static_cast<uint64_t>((ks * Cfg::STEP_BYTES) >> 4);
-                        const uint32_t id = (ks & 1) * 2;   // bytes 0-1 or 2-3 of the words
-                        mma_mxf4<2>(acc, a_st + step, w_st + step, Cfg::IDESC | (id << 4) | (id << 29),
-                                    sf + 4u * (ks / 2), sf + Cfg::SFW_COL + 8u * (ks / 2),
-                                    (kb != 0 || ks != 0) ? 1u : 0u);
+                        for (int ks = 0; ks < Cfg::BK / Cfg::UMMA_K; ++ks) {
+                            const uint64_t step = static_cast<uint64_t>((ks * Cfg::STEP_BYTES) >> 4);
+                            const uint32_t id = (ks & 1) * 2;   // bytes 0-1 or 2-3 of the words
+                            mma_mxf4<2>(acc, a_st + step, w_st + step, Cfg::IDESC | (id << 4) | (id << 29),
+                                        sf + 4u * (ks / 2), sf + Cfg::SFW_COL + 8u * (ks / 2),
+                                        (kb != 0 || ks != 0) ? 1u : 0u);
+                        }
+                        // Operand slot s is free in both CTAs once these MMAs have read it.
+                        mma_commit_pair_mc(empty_bar(s), kPairMask);
+                        // The tile's accumulator is complete in both CTAs.
+                        if (kb == KB - 1) mma_commit_pair_mc(tfull_bar, kPairMask);
                     }
+                    __syncwarp();
                     issued_any = true;
-                    // Operand slot s is free in both CTAs once these MMAs have read it.
-                    mma_commit_pair_mc(empty_bar(s), kPairMask);
                     if (++s == S) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (!ok) break;
-                mma_commit_pair_mc(tfull_bar, kPairMask);   // the tile's accumulator is complete in both CTAs
             }
             if (!ok && issued_any) {
-                // Wait for this thread's MMAs before the TMEM is freed.
-                mma_commit_pair_mc(drain_bar, static_cast<uint16_t>(1u << rank));
+                // Wait for this warp's MMAs before the TMEM is freed.
+                if (elect_one()) mma_commit_pair_mc(drain_bar, static_cast<uint16_t>(1u << rank));
+                __syncwarp();
                 wait_phase_drain(drain_bar, 0, limit, kSiteDrainMma, p.status);
             }
         }
@@ -468,21 +484,12 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             const uint32_t odd = acc_it & 1u;
             const uint32_t acc_addr =
                 tmem_base + (odd ? Cfg::ACC1_COL : 0) + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-            for (int i = 0; i < Cfg::EPI_CHUNKS; ++i) {
-                // The shared columns lie in the last chunks of accumulator 0 and
-                // the first of accumulator 1.
-                const int c = odd ? i : Cfg::EPI_CHUNKS - 1 - i;
-                uint32_t r[64];
-                tmem_load_32x32b_x64(acc_addr + static_cast<uint32_t>(c * Cfg::EPI_COLS), r);
-                if (i == Cfg::RELEASE - 1) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader) mbar_arrive(tempty_bar);
-                        else mbar_arrive_cluster(tempty_leader);
-                    }
-                }
+            // The shared columns lie in the last chunks of accumulator 0 and the
+            // first of accumulator 1; both are read before anything is packed, so
+            // that the next tile's MMAs wait only for the reads (with one chunk
+            // packed and stored before the next is read, 1700 cycles per tile).
+            auto chunk = [&](int i) { return odd ? i : Cfg::EPI_CHUNKS - 1 - i; };
+            auto store_chunk = [&](const uint32_t (&r)[64], int i) {
                 // The store that used this staging buffer two chunks ago has read it.
                 if (lane == 0) bulk_wait_group_read<1>();
                 __syncwarp();
@@ -499,11 +506,30 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    const int col0 = nb * Cfg::BN + c * Cfg::EPI_COLS;
+                    const int col0 = nb * Cfg::BN + chunk(i) * Cfg::EPI_COLS;
                     if (row0 < p.M && col0 < p.N) tma_store_2d(&tmap_c, cbuf, col0, row0);
                     bulk_commit_group();
                 }
+            };
+            uint32_t ra[64], rb[64];
+            tmem_load_32x32b_x64_async(acc_addr + static_cast<uint32_t>(chunk(0) * Cfg::EPI_COLS), ra);
+            tmem_load_32x32b_x64_async(acc_addr + static_cast<uint32_t>(chunk(1) * Cfg::EPI_COLS), rb);
+            tmem_wait_ld_x64(ra);
+            tmem_wait_ld_x64(rb);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(tempty_bar);
+                else mbar_arrive_cluster(tempty_leader);
             }
+            store_chunk(ra, 0);
+            tmem_load_32x32b_x64_async(acc_addr + static_cast<uint32_t>(chunk(2) * Cfg::EPI_COLS), ra);
+            store_chunk(rb, 1);
+            tmem_wait_ld_x64(ra);
+            tmem_load_32x32b_x64_async(acc_addr + static_cast<uint32_t>(chunk(3) * Cfg::EPI_COLS), rb);
+            store_chunk(ra, 2);
+            tmem_wait_ld_x64(rb);
+            store_chunk(rb, 3);
         }
         if (lane == 0) bulk_wait_group<0>();
     }
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(192, 1)
     volatile uint32_t *tmem_slot_ptr =
         reinterpret_cast<volatile uint32_t *>(base_ptr + Cfg::SMEM_CTL_OFF + 8 * (4 * S + 1));
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // uniform
     const int lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
     const uint32_t ncl = cluster_nctarank();
@@ -743,7 +769,7 @@ __global__ void __launch_bounds__(192, 1)
     if (ncl > 1) cluster_arrive();
     tc_fence_after_sync();
     griddep_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot_ptr, 0);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -775,24 +801,23 @@ __global__ void __launch_bounds__(192, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
-            const uint64_t x_desc0 = smem_desc_sw128(sX, 16, 1024);
-            // Row m0 of A is at word column (m0 % 128) / 32 of its scale tiles.
-            const uint32_t sfx_word = static_cast<uint32_t>((m0 % 128) / 32);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull) ||
-                    !wait_phase(sready_bar(s), ph, abort, limit, kSiteMmaFull)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
-                const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
-                const uint64_t x_st = x_desc0 + static_cast<uint64_t>((s * Cfg::X_STAGE_BYTES) >> 4);
+        // The whole warp walks the loop, one lane issues (see the pair kernel).
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
+        const uint64_t x_desc0 = smem_desc_sw128(sX, 16, 1024);
+        // Row m0 of A is at word column (m0 % 128) / 32 of its scale tiles.
+        const uint32_t sfx_word = static_cast<uint32_t>((m0 % 128) / 32);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = __all_sync(0xffffffffu, wait_phase(full_bar(s), ph, abort, limit, kSiteMmaFull) &&
+                                             wait_phase(sready_bar(s), ph, abort, limit, kSiteMmaFull));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t sf = tmem_base + Cfg::SF_COL0 + static_cast<uint32_t>(s * Cfg::SF_SLOT_COLS);
+            const uint64_t w_st = w_desc0 + static_cast<uint64_t>((s * Cfg::W_STAGE_BYTES) >> 4);
+            const uint64_t x_st = x_desc0 + static_cast<uint64_t>((s * Cfg::X_STAGE_BYTES) >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < Cfg::HALVES * Cfg::STEPS; ++ks) {
                     const int half = ks / Cfg::STEPS, step = (ks % Cfg::STEPS) * Cfg::STEP_BYTES;
@@ -803,16 +828,18 @@ __global__ void __launch_bounds__(192, 1)
                                 sf + 4u * (Cfg::SF_TILES + ks / 2) + sfx_word, (kb != kb0 || ks != 0) ? 1u : 0u);
                 }
                 mma_commit(empty_bar(s));
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1u;
-                }
             }
-            // Also after an abort: the wait below frees the TMEM only once this
-            // thread's MMAs are done.
-            mma_commit(tfull_bar);
-            if (!ok) wait_phase_drain(tfull_bar, 0, limit, kSiteDrainMma, p.status);
+            __syncwarp();
+            if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
+        // Also after an abort: the wait below frees the TMEM only once this warp's
+        // MMAs are done.
+        if (elect_one()) mma_commit(tfull_bar);
+        __syncwarp();
+        if (!ok) wait_phase_drain(tfull_bar, 0, limit, kSiteDrainMma, p.status);
         __syncwarp();
     } else {
         const int q = warp & 3;

@@ -60,7 +60,13 @@ def test_training_lowers_the_loss_and_gradients_match_fp64(ff):
     xd = x.double()
     mean = xd.mean(-1, keepdim=True)
     z = (xd - mean) / torch.sqrt((xd - mean).square().mean(-1, keepdim=True) + layer.eps)
-    y = xd + torch.relu((z * leaves[0] + leaves[1]) @ leaves[2]) @ leaves[3]
+    # The ReLU's gradient is defined by the stored fp16 activation (see
+    # gemm_f16_relu_backward): an element that rounding moved across zero is on
+    # the side where the layer has it.
+    with torch.no_grad():
+        h16, _, _ = ff.g.layer_norm_fwd(x, layer.gamma.detach(), layer.beta.detach(), eps=layer.eps)
+        mask = (ff.g.gemm_f16(h16, layer.w1.detach(), relu=True) > 0).double()
+    y = xd + (((z * leaves[0] + leaves[1]) @ leaves[2]) * mask) @ leaves[3]
     ((y - target.double()).square().mean() * 1024).backward()
     for p, want in zip((layer.gamma, layer.beta, layer.w1, layer.w2), leaves):
         # about six chained roundings to fp16 (2^-11 each) of quantities of the gradient's size
