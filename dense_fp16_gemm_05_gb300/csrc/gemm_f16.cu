@@ -1065,7 +1065,10 @@ extern "C" int layer_norm_bwd(const void *dY, const void *X, const void *gamma, 
     a.xtype = xtype;
     a.wtype = wtype;
     a.sm_count = dev.sm_count;
+    a.device = dev.device;
     a.stream = s;
+    a.status = status_word(dev.device);
+    if (a.status == nullptr) return GEMM_ERR_CUDA;
     return launch_layer_norm_bwd(a);
 }
 

@@ -91,6 +91,7 @@ enum WaitSite : uint32_t {
     kSiteDrainMma = 6,
     kSiteBoxImage = 7,   // the layout diagnostic's wait for its one box (tma_box_image.cu)
     kSiteClusterPartial = 8,   // cluster K split: waiting for the cluster's partial tiles (or their reads)
+    kSiteNormRow = 9,   // layer norm backward: waiting for a row's bytes (layer_norm_bwd.cu)
 };
 
 constexpr int ilog2(int x) { return x <= 1 ? 0 : 1 + ilog2(x / 2); }

@@ -25,8 +25,9 @@ struct LayerNormArgs {
     int64_t dim = 0;
     float eps = 0.0f;
     int xtype = 0, wtype = 0;
-    int sm_count = 0;
+    int sm_count = 0, device = 0;
     cudaStream_t stream = nullptr;
+    unsigned long long *status = nullptr;       // device status word
 };
 
 int launch_layer_norm_fwd(const LayerNormArgs &a);
@@ -80,6 +81,13 @@ struct LnPack {
 #pragma unroll
             for (int i = 0; i < V; ++i) e[i] = __ldg(p + i);
         }
+    }
+    __device__ __forceinline__ void load_shared(const T *p)   // V elements make up 16-byte pieces
+    {
+        uint4 raw[V * sizeof(T) / 16];
+#pragma unroll
+        for (unsigned i = 0; i < V * sizeof(T) / 16; ++i) raw[i] = reinterpret_cast<const uint4 *>(p)[i];
+        memcpy(e, raw, sizeof(e));
     }
     __device__ __forceinline__ void store(T *p) const
     {

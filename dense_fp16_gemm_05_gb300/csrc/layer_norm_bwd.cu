@@ -11,6 +11,10 @@
 // partial sums in a fixed order: no atomics, the same bits every time.
 #include "layer_norm.cuh"
 
+#include <atomic>
+
+#include "gemm_kernel.cuh"
+
 namespace {
 
 using namespace gemm_sm103;
@@ -26,6 +30,8 @@ struct BwdParams {
     int32_t dim;
     int32_t parts;    // blocks
     float inv_dim;
+    int32_t stages;   // rows under way per block (the ring kernel)
+    unsigned long long *status;
 };
 
 // Elements 2m and 2m + 1 of NV packs in order.
@@ -208,6 +214,190 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
     }
 }
 
+// Rows of 16-byte pieces, a block per row at a time: the rows come through a
+// ring of bulk copies in shared memory, `stages` rows of X and dY ahead, so that
+// the bytes under way are not bounded by registers (16384 x 4096 fp16: 83 us with
+// one row prefetched in registers, RINGUS with four in the ring).  A ring slot is
+// free once every thread has its pieces in registers, which the row sum's
+// barrier says; with 16 elements per thread (kReread) z and g are taken from
+// shared memory a second time instead of being kept, and the slot is refilled
+// one row later.  Every wait is bounded: on expiry the site is recorded in the
+// device status word and the block leaves.
+constexpr int kRingStages = 4;
+
+template <class T, class W, int V, int NV, int TPR>
+__global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams<T, W> p)
+{
+    constexpr bool kReread = V * NV > 8;
+    constexpr bool kReload = sizeof(T) == 4 || kReread;   // gamma again for every row, from L1
+    constexpr int P = V * NV / 2;
+    extern __shared__ uint4 ring[];   // (stages, 2, dim) elements
+    __shared__ float2 sh[2][TPR / 32];
+    __shared__ uint64_t full_mem[kRingStages];
+    __shared__ volatile int failed[2];
+    const int t = static_cast<int>(threadIdx.x);
+    const uint32_t row_bytes = static_cast<uint32_t>(p.dim) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t ring_base = smem_addr(ring), full0 = smem_addr(full_mem);
+    constexpr uint64_t kLimit = 1ull << 31;   // about a second
+    if (t == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(full0 + 8u * s, 1);
+        failed[0] = failed[1] = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    auto fetch = [&](int64_t row, int s) {
+        const uint32_t bar = full0 + 8u * static_cast<uint32_t>(s);
+        const uint32_t dst = ring_base + 2u * static_cast<uint32_t>(s) * row_bytes;
+        mbar_arrive_expect_tx(bar, 2u * row_bytes);
+        bulk_load(dst, p.X + row * p.dim, row_bytes, bar);
+        bulk_load(dst + row_bytes, p.dY + row * p.dim, row_bytes, bar);
+    };
+    const int64_t step = gridDim.x;
+    int64_t row = blockIdx.x;
+    if (t == 0)
+        for (int s = 0; s < p.stages && row + s * step < p.rows; ++s) fetch(row + s * step, s);
+
+    float2 dg[P], db[P], gm[P];
+    auto load_gamma = [&]() {
+        LnPack<W, V> pg[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
+            else pg[i].fill(1.0f);
+        }
+#pragma unroll
+        for (int m = 0; m < P; ++m) gm[m] = ln_pair_of(pg, m);
+    };
+    if constexpr (!kReload) load_gamma();
+#pragma unroll
+    for (int m = 0; m < P; ++m) dg[m] = db[m] = make_float2(0.0f, 0.0f);
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (row < p.rows) {
+        next_mean = __ldg(p.mean + row);
+        next_rstd = __ldg(p.rstd + row);
+    }
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (; row < p.rows; row += step, it ^= 1) {
+        const float mean = next_mean, rstd = next_rstd;
+        if (row + step < p.rows) {
+            next_mean = __ldg(p.mean + row + step);
+            next_rstd = __ldg(p.rstd + row + step);
+        }
+        if constexpr (kReload) load_gamma();
+        if (!mbar_try_wait(full0 + 8u * static_cast<uint32_t>(s), ph)) {
+            const long long t0 = clock64();
+            while (!mbar_try_wait(full0 + 8u * static_cast<uint32_t>(s), ph))
+                if (static_cast<uint64_t>(clock64() - t0) > kLimit) {
+                    failed[it] = 1;
+                    break;
+                }
+        }
+        const T *x = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(ring) +
+                                                 2ull * static_cast<uint32_t>(s) * row_bytes);
+        const T *dy = x + p.dim;
+        LnPack<T, V> px[NV], pd[NV];
+        auto pieces = [&]() {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int k = (i * TPR + t) * V;
+                if (k < p.dim) {
+                    px[i].load_shared(x + k);
+                    pd[i].load_shared(dy + k);
+                } else {
+                    px[i].fill(0.0f);
+                    pd[i].fill(0.0f);   // adds nothing to any sum
+                }
+            }
+        };
+        pieces();
+        float2 z[P], g[P];
+        float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+        const float2 neg_mean = make_float2(-mean, -mean), rstd2 = make_float2(rstd, rstd);
+#pragma unroll
+        for (int m = 0; m < P; ++m) {
+            const float2 d = ln_pair_of(pd, m);
+            z[m] = mul_f32x2(add_f32x2(ln_pair_of(px, m), neg_mean), rstd2);
+            g[m] = mul_f32x2(d, gm[m]);
+            s1 = add_f32x2(s1, g[m]);
+            s2 = fma_f32x2(g[m], z[m], s2);
+            dg[m] = fma_f32x2(d, z[m], dg[m]);
+            db[m] = add_f32x2(db[m], d);
+        }
+        const float2 sum = ln_row_sum2<TPR>(s1.x + s1.y, s2.x + s2.y, sh[it]);
+        if (failed[it]) {   // the same answer for every thread: set before the barrier
+            ok = false;
+            break;
+        }
+        if (t == 0) {
+            // This row's slot, or (kReread) the one before's, which every thread
+            // had left when it came to this row's barrier.
+            if constexpr (kReread) {
+                const int64_t next = row + (p.stages - 1) * step;
+                if (row != blockIdx.x && next < p.rows) fetch(next, s == 0 ? p.stages - 1 : s - 1);
+            } else {
+                const int64_t next = row + p.stages * step;
+                if (next < p.rows) fetch(next, s);
+            }
+        }
+        const float rc1 = rstd * (sum.x * p.inv_dim), rc2 = rstd * (sum.y * p.inv_dim);
+        const float2 neg_rc1 = make_float2(-rc1, -rc1), neg_rc2 = make_float2(-rc2, -rc2);
+        if constexpr (kReread) {
+            pieces();
+            load_gamma();
+#pragma unroll
+            for (int m = 0; m < P; ++m) {
+                z[m] = mul_f32x2(add_f32x2(ln_pair_of(px, m), neg_mean), rstd2);
+                g[m] = mul_f32x2(ln_pair_of(pd, m), gm[m]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < P; ++m) z[m] = fma_f32x2(z[m], neg_rc2, fma_f32x2(rstd2, g[m], neg_rc1));
+        T *dx = p.dX + row * p.dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (k >= p.dim) continue;
+            LnPack<T, V> out;
+#pragma unroll
+            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
+            out.store(dx + k);
+        }
+        if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    if (!ok) {
+        if (t == 0) {
+            atomicCAS(p.status, 0ull,
+                      static_cast<unsigned long long>(kSiteNormRow) | (static_cast<unsigned long long>(blockIdx.x) << 8));
+            // Give the copies in flight a bounded time to land before the block exits.
+            const long long t0 = clock64();
+            while (static_cast<uint64_t>(clock64() - t0) < 1000000ull) {
+            }
+        }
+        __syncthreads();
+        return;
+    }
+    if (p.part == nullptr) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float *out = p.part + (static_cast<int64_t>(which) * p.parts + blockIdx.x) * p.dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = (i * TPR + t) * V;
+            if (k >= p.dim) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
+        }
+    }
+}
+
 // Rows longer than a block holds: dX in two passes over the row ...
 template <class T, class W>
 __global__ void __launch_bounds__(1024) layer_norm_bwd_long(BwdParams<T, W> p)
@@ -308,8 +498,46 @@ int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
     return GEMM_OK;
 }
 
+// The ring kernel, where at least two rows fit a block's share of the shared
+// memory, else the register kernel.
+template <class T, class W, int V, int NV, int TPR>
+int launch_ring(BwdParams<T, W> p, int device, cudaStream_t stream)
+{
+    constexpr int kBlocks = 1024 / TPR;
+    constexpr int kBudget = (227 * 1024 - kBlocks * 2048) / kBlocks;
+    const int64_t stage = 2 * static_cast<int64_t>(p.dim) * static_cast<int64_t>(sizeof(T));
+    const int64_t fit = kBudget / stage;
+    if (fit < 2) return launch_one<T, W, V, NV, TPR>(p, stream);
+    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
+    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR>;
+    static std::atomic<int> prepared[kMaxDevices];
+    if (!prepared[device].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        prepared[device].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(p.parts), 1, 1);
+    lc.blockDim = dim3(TPR, 1, 1);
+    lc.dynamicSmemBytes = static_cast<size_t>(p.stages) * static_cast<size_t>(stage);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, kern, p) != cudaSuccess) {
+        cudaGetLastError();
+        prepared[device].store(0, std::memory_order_release);
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
 template <class T, class W, int V>
-int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
+int launch_packs(const BwdParams<T, W> &p, int device, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
@@ -322,11 +550,11 @@ int launch_packs(const BwdParams<T, W> &p, cudaStream_t stream)
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
     if constexpr (V > 2) {
-        if (packs <= 128 * N) return launch_one<T, W, V, N, 128>(p, stream);
-        if (packs <= 256 * N) return launch_one<T, W, V, N, 256>(p, stream);
-        if (packs <= 512 * N) return launch_one<T, W, V, N, 512>(p, stream);
-        if (packs <= 1024 * N) return launch_one<T, W, V, N, 1024>(p, stream);
-        if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, 1024>(p, stream);
+        if (packs <= 128 * N) return launch_ring<T, W, V, N, 128>(p, device, stream);
+        if (packs <= 256 * N) return launch_ring<T, W, V, N, 256>(p, device, stream);
+        if (packs <= 512 * N) return launch_ring<T, W, V, N, 512>(p, device, stream);
+        if (packs <= 1024 * N) return launch_ring<T, W, V, N, 1024>(p, device, stream);
+        if (packs <= 1024 * 2 * N) return launch_ring<T, W, V, 2 * N, 1024>(p, device, stream);
     } else {
         // Narrow loads are bound by instructions, so no more threads than eight
         // elements each take (16384 x 4097 fp16: 347 us with the next power of 2,
@@ -359,13 +587,14 @@ int backward(const LayerNormArgs &a)
     p.dim = static_cast<int32_t>(a.dim);
     p.parts = static_cast<int32_t>(layer_norm_parts(a.rows, a.dim, a.sm_count));
     p.inv_dim = 1.0f / static_cast<float>(a.dim);
+    p.status = a.status;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
                            reinterpret_cast<uintptr_t>(a.Y) | reinterpret_cast<uintptr_t>(a.gamma) |
                            (static_cast<uintptr_t>(a.dim) * sizeof(T));
     constexpr int V = 16 / sizeof(T);
-    int st = (bits & 15u) == 0          ? launch_packs<T, W, V>(p, a.stream)
-             : (bits & 3u) == 0 && V > 4 ? launch_packs<T, W, V / 4>(p, a.stream)
-                                         : launch_packs<T, W, 1>(p, a.stream);
+    int st = (bits & 15u) == 0          ? launch_packs<T, W, V>(p, a.device, a.stream)
+             : (bits & 3u) == 0 && V > 4 ? launch_packs<T, W, V / 4>(p, a.device, a.stream)
+                                         : launch_packs<T, W, 1>(p, a.device, a.stream);
     if (st != GEMM_OK || p.part == nullptr) return st;
     return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 512, a.stream,
                      static_cast<const float *>(p.part), static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta),
