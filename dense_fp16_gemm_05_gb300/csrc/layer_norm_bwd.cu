@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 // device status word and the block leaves.
 constexpr int kRingStages = 4;
 
-template <class T, class W, int V, int NV, int TPR>
+// kFull: the row is exactly the threads' elements, no bounds to check.
+template <class T, class W, int V, int NV, int TPR, bool kFull>
 __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams<T, W> p)
 {
     constexpr bool kReread = V * NV > 8;
@@ -247,17 +248,19 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    auto fetch = [&](int64_t row, int s) {
+    auto fetch = [&](uint32_t row, int s) {
         const uint32_t bar = full0 + 8u * static_cast<uint32_t>(s);
         const uint32_t dst = ring_base + 2u * static_cast<uint32_t>(s) * row_bytes;
         mbar_arrive_expect_tx(bar, 2u * row_bytes);
-        bulk_load(dst, p.X + row * p.dim, row_bytes, bar);
-        bulk_load(dst + row_bytes, p.dY + row * p.dim, row_bytes, bar);
+        bulk_load(dst, p.X + static_cast<int64_t>(row) * p.dim, row_bytes, bar);
+        bulk_load(dst + row_bytes, p.dY + static_cast<int64_t>(row) * p.dim, row_bytes, bar);
     };
-    const int64_t step = gridDim.x;
-    int64_t row = blockIdx.x;
+    // Rows as unsigned 32-bit numbers: the ones past the end may pass 2^31.
+    const uint32_t step = gridDim.x, rows = static_cast<uint32_t>(p.rows);
+    uint32_t row = blockIdx.x;
     if (t == 0)
-        for (int s = 0; s < p.stages && row + s * step < p.rows; ++s) fetch(row + s * step, s);
+        for (int s = 0; s < p.stages && row + static_cast<uint32_t>(s) * step < rows; ++s)
+            fetch(row + static_cast<uint32_t>(s) * step, s);
 
     float2 dg[P], db[P], gm[P];
     auto load_gamma = [&]() {
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
+            if (p.gamma && (kFull || k < p.dim)) pg[i].load(p.gamma + k);
             else pg[i].fill(1.0f);
         }
 #pragma unroll
@@ -275,16 +278,16 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
 #pragma unroll
     for (int m = 0; m < P; ++m) dg[m] = db[m] = make_float2(0.0f, 0.0f);
     float next_mean = 0.0f, next_rstd = 0.0f;
-    if (row < p.rows) {
+    if (row < rows) {
         next_mean = __ldg(p.mean + row);
         next_rstd = __ldg(p.rstd + row);
     }
     int s = 0, it = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (; row < p.rows; row += step, it ^= 1) {
+    for (; row < rows; row += step, it ^= 1) {
         const float mean = next_mean, rstd = next_rstd;
-        if (row + step < p.rows) {
+        if (row + step < rows) {
             next_mean = __ldg(p.mean + row + step);
             next_rstd = __ldg(p.rstd + row + step);
         }
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int k = (i * TPR + t) * V;
-                if (k < p.dim) {
+                if (kFull || k < p.dim) {
                     px[i].load_shared(x + k);
                     pd[i].load_shared(dy + k);
                 } else {
@@ -337,11 +340,11 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
             // This row's slot, or (kReread) the one before's, which every thread
             // had left when it came to this row's barrier.
             if constexpr (kReread) {
-                const int64_t next = row + (p.stages - 1) * step;
-                if (row != blockIdx.x && next < p.rows) fetch(next, s == 0 ? p.stages - 1 : s - 1);
+                const uint32_t next = row + static_cast<uint32_t>(p.stages - 1) * step;
+                if (row != blockIdx.x && next < rows) fetch(next, s == 0 ? p.stages - 1 : s - 1);
             } else {
-                const int64_t next = row + p.stages * step;
-                if (next < p.rows) fetch(next, s);
+                const uint32_t next = row + static_cast<uint32_t>(p.stages) * step;
+                if (next < rows) fetch(next, s);
             }
         }
         const float rc1 = rstd * (sum.x * p.inv_dim), rc2 = rstd * (sum.y * p.inv_dim);
@@ -357,11 +360,11 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
         }
 #pragma unroll
         for (int m = 0; m < P; ++m) z[m] = fma_f32x2(z[m], neg_rc2, fma_f32x2(rstd2, g[m], neg_rc1));
-        T *dx = p.dX + row * p.dim;
+        T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (k >= p.dim) continue;
+            if (!kFull && k >= p.dim) continue;
             LnPack<T, V> out;
 #pragma unroll
             for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * TPR + t) * V;
-            if (k >= p.dim) continue;
+            if (!kFull && k >= p.dim) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
         }
@@ -498,21 +501,13 @@ int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
     return GEMM_OK;
 }
 
-// The ring kernel, where at least two rows fit a block's share of the shared
-// memory, else the register kernel.
-template <class T, class W, int V, int NV, int TPR>
-int launch_ring(BwdParams<T, W> p, int device, cudaStream_t stream)
+template <class T, class W, int V, int NV, int TPR, bool kFull>
+int launch_ring_kernel(const BwdParams<T, W> &p, int device, int budget, int64_t stage, cudaStream_t stream)
 {
-    constexpr int kBlocks = 1024 / TPR;
-    constexpr int kBudget = (227 * 1024 - kBlocks * 2048) / kBlocks;
-    const int64_t stage = 2 * static_cast<int64_t>(p.dim) * static_cast<int64_t>(sizeof(T));
-    const int64_t fit = kBudget / stage;
-    if (fit < 2) return launch_one<T, W, V, NV, TPR>(p, stream);
-    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
-    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR>;
+    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR, kFull>;
     static std::atomic<int> prepared[kMaxDevices];
     if (!prepared[device].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
         }
@@ -534,6 +529,21 @@ int launch_ring(BwdParams<T, W> p, int device, cudaStream_t stream)
         return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
+}
+
+// The ring kernel, where at least two rows fit a block's share of the shared
+// memory, else the register kernel.
+template <class T, class W, int V, int NV, int TPR>
+int launch_ring(BwdParams<T, W> p, int device, cudaStream_t stream)
+{
+    constexpr int kBlocks = 1024 / TPR;
+    constexpr int kBudget = (227 * 1024 - kBlocks * 2048) / kBlocks;
+    const int64_t stage = 2 * static_cast<int64_t>(p.dim) * static_cast<int64_t>(sizeof(T));
+    const int64_t fit = kBudget / stage;
+    if (fit < 2) return launch_one<T, W, V, NV, TPR>(p, stream);
+    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
+    return p.dim == TPR * V * NV ? launch_ring_kernel<T, W, V, NV, TPR, true>(p, device, kBudget, stage, stream)
+                                 : launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, kBudget, stage, stream);
 }
 
 template <class T, class W, int V>

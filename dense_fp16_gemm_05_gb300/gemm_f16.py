@@ -561,13 +561,6 @@ def _check_like(t, name: str, dtype, shape, device):
     return t
 
 
-def _like_or_new(t, name: str, dtype, shape, device):
-    """t after _check_like, or a new tensor where t is None."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _check_like(t, name, dtype, shape, device)
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -590,12 +583,20 @@ def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = Fals
     if code is None or len(shape) != 2 or not X.is_contiguous():
         raise ValueError(f"X must be a contiguous 2-D float16, bfloat16 or float32 tensor, got {dtype} {tuple(shape)}")
     K, rows = shape if transpose else (shape[1], shape[0])
-    q_shape, s_shape = mxfp4_shapes(rows, K)
     dev = X.device
-    Q = _like_or_new(Q, "Q", torch.uint8, q_shape, dev)
-    S = _like_or_new(S, "S", torch.uint8, s_shape, dev)
-    if values or V is not None:
-        V = _like_or_new(V, "V", dtype, (rows, K), dev)
+    q_shape, s_shape = mxfp4_shapes(rows, K)
+    if Q is None:
+        Q = torch.empty(q_shape, dtype=torch.uint8, device=dev)
+    else:
+        _check_like(Q, "Q", torch.uint8, q_shape, dev)
+    if S is None:
+        S = torch.empty(s_shape, dtype=torch.uint8, device=dev)
+    else:
+        _check_like(S, "S", torch.uint8, s_shape, dev)
+    if V is not None:
+        _check_like(V, "V", dtype, (rows, K), dev)
+    elif values:
+        V = torch.empty((rows, K), dtype=dtype, device=dev)
     _call((_lib or lib()).mxfp4_quantize, "mxfp4_quantize", dev, stream, X.data_ptr(), code, Q.data_ptr(),
           S.data_ptr(), _ptr(V), rows, K, 1 if transpose else 0)
     return (Q, S) if V is None else (Q, S, V)
@@ -625,7 +626,10 @@ def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Ten
     q_shape, s_shape = mxfp4_shapes(N, K)
     _check_like(W, "W", u8, q_shape, dev)
     _check_like(SW, "SW", u8, s_shape, dev)
-    C = _like_or_new(C, "C", torch.float16, (M, N), dev)
+    if C is None:
+        C = torch.empty((M, N), dtype=torch.float16, device=dev)
+    else:
+        _check_like(C, "C", torch.float16, (M, N), dev)
     _call((_lib or lib()).gemm_mxfp4, "gemm_mxfp4", dev, stream, A.data_ptr(), SA.data_ptr(), W.data_ptr(),
           SW.data_ptr(), C.data_ptr(), M, N, K, 1 if relu else 0)
     return C
@@ -667,7 +671,10 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
     code, dtype, shape, rows, dim = _norm_input(X)
     dev = X.device
     wt = _norm_weight_type(dtype, dim, dev, gamma, beta)
-    Y = _like_or_new(Y, "Y", dtype, shape, dev)
+    if Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _check_like(Y, "Y", dtype, shape, dev)
     mean = rstd = None
     if stats:
         lead = shape[:-1]
@@ -709,7 +716,10 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
         wt = wtype
         if wt != dtype and wt != torch.float32:
             raise ValueError(f"wtype must be X's type {dtype} or float32, got {wt}")
-    dX = _like_or_new(dX, "dX", dtype, shape, dev)
+    if dX is None:
+        dX = torch.empty_like(X)
+    else:
+        _check_like(dX, "dX", dtype, shape, dev)
     L = _lib or lib()
     dgamma = dbeta = None
     ws_bytes = 0
@@ -717,7 +727,12 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
         dgamma = torch.empty((dim,), dtype=wt, device=dev)
         dbeta = torch.empty((dim,), dtype=wt, device=dev)
         if workspace is None:
-            need = layer_norm_bwd_workspace(rows, dim, dev)
+            if dev.index == _current_device():
+                need = L.layer_norm_bwd_workspace(rows, dim)
+                if need < 0:
+                    raise GemmError(need, "layer_norm_bwd_workspace")
+            else:
+                need = layer_norm_bwd_workspace(rows, dim, dev)
             if stream is None:
                 workspace = torch.empty((need // 4,), dtype=torch.float32, device=dev)
             else:
