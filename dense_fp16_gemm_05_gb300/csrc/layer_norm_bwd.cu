@@ -32,6 +32,7 @@ struct BwdParams {
     float inv_dim;
     int32_t stages;   // rows under way per block (the ring kernel)
     unsigned long long *status;
+    W *dgamma, *dbeta;
 };
 
 // Elements 2m and 2m + 1 of NV packs in order.
@@ -225,18 +226,26 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 // device status word and the block leaves.
 constexpr int kRingStages = 4;
 
-// kFull: the row is exactly the threads' elements, no bounds to check.
-template <class T, class W, int V, int NV, int TPR, bool kFull>
-__global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams<T, W> p)
+// Blocks per SM that the registers are held to.
+__host__ __device__ constexpr int ring_blocks(int tpr, int per)
 {
-    constexpr bool kReread = V * NV > 8;
-    constexpr bool kReload = sizeof(T) == 4 || kReread;   // gamma again for every row, from L1
+    if (tpr > 0) return 1024 / tpr;
+    return per > 8 && tpr != -320 ? 1 : 2;
+}
+
+// TPR > 0: the row is exactly the threads' elements, no bounds to check.
+template <class T, class W, int V, int NV, int TPR>
+__global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) layer_norm_bwd_ring(BwdParams<T, W> p)
+{
+    constexpr bool kFull = TPR > 0;
+    constexpr bool kReread = V * NV > 8 && (TPR == 1024 || TPR == -1024);
+    constexpr bool kReload = sizeof(T) == 4 || V * NV > 8;   // gamma again for every row, from L1
     constexpr int P = V * NV / 2;
     extern __shared__ uint4 ring[];   // (stages, 2, dim) elements
-    __shared__ float2 sh[2][TPR / 32];
+    __shared__ float2 sh[2][ln_warps(TPR)];
     __shared__ uint64_t full_mem[kRingStages];
     __shared__ volatile int failed[2];
-    const int t = static_cast<int>(threadIdx.x);
+    const int t = static_cast<int>(threadIdx.x), tpr = ln_threads<TPR>();
     const uint32_t row_bytes = static_cast<uint32_t>(p.dim) * static_cast<uint32_t>(sizeof(T));
     const uint32_t ring_base = smem_addr(ring), full0 = smem_addr(full_mem);
     constexpr uint64_t kLimit = 1ull << 31;   // about a second
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
         LnPack<W, V> pg[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int k = (i * TPR + t) * V;
+            const int k = (i * tpr + t) * V;
             if (p.gamma && (kFull || k < p.dim)) pg[i].load(p.gamma + k);
             else pg[i].fill(1.0f);
         }
@@ -307,7 +316,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
         auto pieces = [&]() {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int k = (i * TPR + t) * V;
+                const int k = (i * tpr + t) * V;
                 if (kFull || k < p.dim) {
                     px[i].load_shared(x + k);
                     pd[i].load_shared(dy + k);
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
         T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int k = (i * TPR + t) * V;
+            const int k = (i * tpr + t) * V;
             if (!kFull && k >= p.dim) continue;
             LnPack<T, V> out;
 #pragma unroll
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(TPR, 1024 / TPR) layer_norm_bwd_ring(BwdParams
         float *out = p.part + (static_cast<int64_t>(which) * p.parts + blockIdx.x) * p.dim;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int k = (i * TPR + t) * V;
+            const int k = (i * tpr + t) * V;
             if (!kFull && k >= p.dim) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
@@ -477,6 +486,15 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_finish(const float *__rest
     }
 }
 
+// The second kernel, if the weights' gradients are wanted.
+template <class T, class W>
+int finish(const BwdParams<T, W> &p, cudaStream_t stream)
+{
+    if (p.part == nullptr) return GEMM_OK;
+    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((static_cast<int64_t>(p.dim) + 31) / 32), 2, 1),
+                     512, stream, static_cast<const float *>(p.part), p.dgamma, p.dbeta, p.parts, p.dim);
+}
+
 template <class T, class W, int V, int NV, int TPR>
 int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
 {
@@ -498,16 +516,29 @@ int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
-    return GEMM_OK;
+    return finish<T, W>(p, stream);
 }
 
-template <class T, class W, int V, int NV, int TPR, bool kFull>
-int launch_ring_kernel(const BwdParams<T, W> &p, int device, int budget, int64_t stage, cudaStream_t stream)
+// The ring kernel, where at least two rows fit a block's share of the shared
+// memory, else the register kernel.
+template <class T, class W, int V, int NV, int TPR>
+int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream)
 {
-    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR, kFull>;
+    const int packs = p.dim / V;
+    const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    // Blocks per SM: those of the launch bound, or more where they are small.
+    const int fit_blocks = V * NV > 8 ? ring_blocks(TPR, V * NV) : 1024 / threads;
+    const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
+    const int64_t stage = 2 * static_cast<int64_t>(p.dim) * static_cast<int64_t>(sizeof(T));
+    const int64_t fit = budget / stage;
+    if (fit < 2) return launch_one<T, W, V, NV, (TPR > 0 ? TPR : TPR == -320 ? -512 : TPR)>(p, stream);
+    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
+    const int64_t wave = static_cast<int64_t>(fit_blocks) * sm_count;
+    if (p.parts > wave) p.parts = static_cast<int32_t>(wave);
+    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR>;
     static std::atomic<int> prepared[kMaxDevices];
     if (!prepared[device].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
         }
@@ -515,7 +546,7 @@ int launch_ring_kernel(const BwdParams<T, W> &p, int device, int budget, int64_t
     }
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(static_cast<unsigned>(p.parts), 1, 1);
-    lc.blockDim = dim3(TPR, 1, 1);
+    lc.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     lc.dynamicSmemBytes = static_cast<size_t>(p.stages) * static_cast<size_t>(stage);
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -528,26 +559,11 @@ int launch_ring_kernel(const BwdParams<T, W> &p, int device, int budget, int64_t
         prepared[device].store(0, std::memory_order_release);
         return GEMM_ERR_LAUNCH;
     }
-    return GEMM_OK;
-}
-
-// The ring kernel, where at least two rows fit a block's share of the shared
-// memory, else the register kernel.
-template <class T, class W, int V, int NV, int TPR>
-int launch_ring(BwdParams<T, W> p, int device, cudaStream_t stream)
-{
-    constexpr int kBlocks = 1024 / TPR;
-    constexpr int kBudget = (227 * 1024 - kBlocks * 2048) / kBlocks;
-    const int64_t stage = 2 * static_cast<int64_t>(p.dim) * static_cast<int64_t>(sizeof(T));
-    const int64_t fit = kBudget / stage;
-    if (fit < 2) return launch_one<T, W, V, NV, TPR>(p, stream);
-    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
-    return p.dim == TPR * V * NV ? launch_ring_kernel<T, W, V, NV, TPR, true>(p, device, kBudget, stage, stream)
-                                 : launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, kBudget, stage, stream);
+    return finish<T, W>(p, stream);
 }
 
 template <class T, class W, int V>
-int launch_packs(const BwdParams<T, W> &p, int device, cudaStream_t stream)
+int launch_packs(const BwdParams<T, W> &p, int device, int sm_count, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
@@ -560,11 +576,19 @@ int launch_packs(const BwdParams<T, W> &p, int device, cudaStream_t stream)
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
     if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
     if constexpr (V > 2) {
-        if (packs <= 128 * N) return launch_ring<T, W, V, N, 128>(p, device, stream);
-        if (packs <= 256 * N) return launch_ring<T, W, V, N, 256>(p, device, stream);
-        if (packs <= 512 * N) return launch_ring<T, W, V, N, 512>(p, device, stream);
-        if (packs <= 1024 * N) return launch_ring<T, W, V, N, 1024>(p, device, stream);
-        if (packs <= 1024 * 2 * N) return launch_ring<T, W, V, 2 * N, 1024>(p, device, stream);
+        // Rows that fill a power of 2 of threads, eight elements each (16 in the
+        // longest), and then any others: as many warps as the row needs, two blocks
+        // of some 300 threads with 16 elements rather than one of some 600
+        // (16384 x 4104 fp16: 137 us with the next power of 2, 79 us this way).
+        if (packs == 128 * N) return launch_ring<T, W, V, N, 128>(p, device, sm_count, stream);
+        if (packs == 256 * N) return launch_ring<T, W, V, N, 256>(p, device, sm_count, stream);
+        if (packs == 512 * N) return launch_ring<T, W, V, N, 512>(p, device, sm_count, stream);
+        if (packs == 1024 * N) return launch_ring<T, W, V, N, 1024>(p, device, sm_count, stream);
+        if (packs == 1024 * 2 * N) return launch_ring<T, W, V, 2 * N, 1024>(p, device, sm_count, stream);
+        if (packs <= 512 * N) return launch_ring<T, W, V, N, -512>(p, device, sm_count, stream);
+        if (packs <= 320 * 2 * N) return launch_ring<T, W, V, 2 * N, -320>(p, device, sm_count, stream);
+        if (packs <= 512 * 2 * N) return launch_ring<T, W, V, 2 * N, -512>(p, device, sm_count, stream);
+        if (packs <= 1024 * 2 * N) return launch_ring<T, W, V, 2 * N, -1024>(p, device, sm_count, stream);
     } else {
         // Narrow loads are bound by instructions, so no more threads than eight
         // elements each take (16384 x 4097 fp16: 347 us with the next power of 2,
@@ -576,10 +600,11 @@ int launch_packs(const BwdParams<T, W> &p, int device, cudaStream_t stream)
     }
     int st = ln_launch(layer_norm_bwd_long<T, W>, dim3(static_cast<unsigned>(p.parts), 1, 1), 1024, stream, p);
     if (st != GEMM_OK || p.part == nullptr) return st;
-    return ln_launch(layer_norm_bwd_columns<T, W>,
-                     dim3(static_cast<unsigned>((static_cast<int64_t>(p.dim) + 255) / 256),
-                          static_cast<unsigned>(p.parts), 1),
-                     256, stream, p);
+    st = ln_launch(layer_norm_bwd_columns<T, W>,
+                   dim3(static_cast<unsigned>((static_cast<int64_t>(p.dim) + 255) / 256),
+                        static_cast<unsigned>(p.parts), 1),
+                   256, stream, p);
+    return st != GEMM_OK ? st : finish<T, W>(p, stream);
 }
 
 template <class T, class W>
@@ -598,32 +623,30 @@ int backward(const LayerNormArgs &a)
     p.parts = static_cast<int32_t>(layer_norm_parts(a.rows, a.dim, a.sm_count));
     p.inv_dim = 1.0f / static_cast<float>(a.dim);
     p.status = a.status;
+    p.dgamma = static_cast<W *>(a.dgamma);
+    p.dbeta = static_cast<W *>(a.dbeta);
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
                            reinterpret_cast<uintptr_t>(a.Y) | reinterpret_cast<uintptr_t>(a.gamma) |
                            (static_cast<uintptr_t>(a.dim) * sizeof(T));
     constexpr int V = 16 / sizeof(T);
-    int st = (bits & 15u) == 0          ? launch_packs<T, W, V>(p, a.device, a.stream)
-             : (bits & 3u) == 0 && V > 4 ? launch_packs<T, W, V / 4>(p, a.device, a.stream)
-                                         : launch_packs<T, W, 1>(p, a.device, a.stream);
-    if (st != GEMM_OK || p.part == nullptr) return st;
-    return ln_launch(layer_norm_bwd_finish<W>, dim3(static_cast<unsigned>((a.dim + 31) / 32), 2, 1), 512, a.stream,
-                     static_cast<const float *>(p.part), static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta),
-                     p.parts, p.dim);
+    if ((bits & 15u) == 0) return launch_packs<T, W, V>(p, a.device, a.sm_count, a.stream);
+    if ((bits & 3u) == 0 && V > 4) return launch_packs<T, W, V / 4>(p, a.device, a.sm_count, a.stream);
+    return launch_packs<T, W, 1>(p, a.device, a.sm_count, a.stream);
 }
 
 }  // namespace
 
 namespace gemm_sm103 {
 
-// One part per block of the row kernels.  Rows of up to 512 elements go eight
-// at a time (a warp each), longer ones one at a time, with the block's threads
-// taking eight elements each: so many blocks that an SM holds some 1024
-// threads, but no more than two per SM or one per eight rows, whichever is
-// more, for a part costs as much as a row's writes.
+// The most parts, one per block of the row kernels, that a call writes.  Rows
+// of up to 512 elements go eight or more at a time, longer ones one at a time,
+// with the block's threads taking eight elements each: so many blocks that an
+// SM holds some 1024 threads, but no more than two per SM or one per eight
+// rows, whichever is more, for a part costs as much as a row's writes.
 int64_t layer_norm_parts(int64_t rows, int64_t dim, int sm_count)
 {
     const int64_t per = dim <= 512 ? 8 : 1;
-    const int64_t blocks = dim <= 512 ? 4 : (dim <= 1024 ? 8 : (dim <= 2048 ? 4 : (dim <= 4096 ? 2 : 1)));
+    const int64_t blocks = dim <= 512 ? 4 : (dim > 5120 ? 1 : (8192 / dim > 2 ? 8192 / dim : 2));
     const int64_t sms = sm_count;
     int64_t parts = (rows + per - 1) / per;
     if (parts > blocks * sms) parts = blocks * sms;
