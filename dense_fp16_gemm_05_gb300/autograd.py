@@ -62,6 +62,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x, gamma, mean, rstd = ctx.saved_tensors
         dy = dy.contiguous()

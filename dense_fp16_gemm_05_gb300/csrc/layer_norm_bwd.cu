@@ -217,8 +217,11 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 
 // Rows of 16-byte pieces, a block per row at a time: the rows come through a
 // ring of bulk copies in shared memory, `stages` rows of X and dY ahead, so that
-// the bytes under way are not bounded by registers (16384 x 4096 fp16: 83 us with
-// one row prefetched in registers, RINGUS with four in the ring).  A ring slot is
+// the bytes under way are not bounded by registers (16384 x 4096 fp16: 82 us with
+// one row prefetched in registers, 79 us with four in the ring; 75 us, 5.4 TB/s,
+// since both row sums share their shuffles and full rows have no bounds).  What
+// bounds it by counters is issue slots (55-60 % busy) and the two dependent
+// chains of shuffles around the row's barrier, not DRAM.  A ring slot is
 // free once every thread has its pieces in registers, which the row sum's
 // barrier says; with 16 elements per thread (kReread) z and g are taken from
 // shared memory a second time instead of being kept, and the slot is refilled

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256, kQuantBlocks<T, kValues>)
         if (next_g >= p.groups) {
             next_g -= p.groups;
             ++next_row;
-            next_at += p.K - p.groups * G;
+            next_at += p.K - static_cast<int64_t>(p.groups) * G;
         }
         if (next_row < static_cast<uint32_t>(p.rows)) next.load(X + next_at, p.K - next_g * G);
         uint32_t amax = max_magnitude(e);

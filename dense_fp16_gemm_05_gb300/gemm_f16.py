@@ -241,6 +241,16 @@ def _call(fn, what: str, device: torch.device, stream, *args):
         raise GemmError(st, what)
 
 
+def _used_on(stream, device, *tensors):
+    """Tells the allocator that tensors made here on torch's current stream are
+    used on ``stream``: their memory is not reused before that stream is done."""
+    if stream is not None:
+        s = _launch_stream(stream, device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
 def _check_operand(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -599,6 +609,7 @@ def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = Fals
         V = torch.empty((rows, K), dtype=dtype, device=dev)
     _call((_lib or lib()).mxfp4_quantize, "mxfp4_quantize", dev, stream, X.data_ptr(), code, Q.data_ptr(),
           S.data_ptr(), _ptr(V), rows, K, 1 if transpose else 0)
+    _used_on(stream, dev, Q, S, V)
     return (Q, S) if V is None else (Q, S, V)
 
 
@@ -632,6 +643,7 @@ def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Ten
         _check_like(C, "C", torch.float16, (M, N), dev)
     _call((_lib or lib()).gemm_mxfp4, "gemm_mxfp4", dev, stream, A.data_ptr(), SA.data_ptr(), W.data_ptr(),
           SW.data_ptr(), C.data_ptr(), M, N, K, 1 if relu else 0)
+    _used_on(stream, dev, C)
     return C
 
 
@@ -682,6 +694,7 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
         rstd = torch.empty(lead, dtype=torch.float32, device=dev)
     _call((_lib or lib()).layer_norm_fwd, "layer_norm_fwd", dev, stream, X.data_ptr(), _ptr(gamma), _ptr(beta),
           Y.data_ptr(), _ptr(mean), _ptr(rstd), rows, dim, eps, code, TYPES[wt])
+    _used_on(stream, dev, Y, mean, rstd)
     return Y, mean, rstd
 
 
@@ -745,6 +758,7 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
     _call(L.layer_norm_bwd, "layer_norm_bwd", dev, stream, dY.data_ptr(), X.data_ptr(), _ptr(gamma), mean.data_ptr(),
           rstd.data_ptr(), dX.data_ptr(), _ptr(dgamma), _ptr(dbeta), rows, dim, code, TYPES[wt],
           _ptr(workspace) if weights else None, ws_bytes)
+    _used_on(stream, dev, dX, dgamma, dbeta)
     return dX, dgamma, dbeta
 
 

@@ -362,7 +362,10 @@ int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, void *V, int
  *   C[i,j] = R( sum_b 2^(sa[i,b]-127) * 2^(sw[j,b]-127) * sum_{k in block b} A[i,k] * W[j,k] )
  *
  * accumulated in fp32 by the block-scaled 4-bit MMA and rounded once to fp16
- * (R as for gemm_f16; a NaN scale gives NaN without ReLU, +0 with it).
+ * (R as for gemm_f16; a NaN scale gives NaN without ReLU, +0 with it).  The
+ * choice of tiles, and over how many CTAs a tile's K range is divided (few rows
+ * of A: up to 8), depends on the sizes and the GPU alone and every sum has a
+ * fixed order, so equal calls give equal bits.
  * A, SA: the packed form of a (M,K) matrix; W, SW: of a (N,K) matrix (a linear
  * layer's weight, out-features x in-features); C (M,N) row-major.
  *
@@ -376,8 +379,8 @@ int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *S
 
 /*
  * layer_norm_fwd -- layer norm over rows of `dim` elements (the norm in front of
- * a feed-forward or attention block; on the roadmap of the TileLang-MUSA
- * lesson, 7yue.com, section 7, with its backward pass):
+ * a feed-forward or attention block; the TileLang-MUSA lesson, 7yue.com, has
+ * its backward pass on its roadmap):
  *
  *   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
  *   Y = (X - mean) rstd gamma + beta

@@ -252,3 +252,23 @@ def test_product_more_tiles_than_sms(g, M, N, K):
     want = V.double() @ Vw.double().t()
     mag = V.double().abs() @ Vw.double().abs().t()
     assert ((C.double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -25 + (K / 64 + 16) * 2.0 ** -22 * mag).all()
+
+
+def test_calls_on_a_given_stream(g):
+    # outputs made on the current stream, written on another: dropped at once,
+    # their memory may not be handed out before the other stream is done
+    x = draw(64, 4096, torch.float16, 2).to(DEV)
+    (_, _), dev = operands(64, 256, 4096, 8)
+    want_q, want_s = g.mxfp4_quantize(x)
+    want = g.gemm_mxfp4(want_q, want_s, dev[2], dev[3])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kept = []
+    for i in range(20):
+        q, s = g.mxfp4_quantize(x, stream=side)
+        c = g.gemm_mxfp4(q, s, dev[2], dev[3], stream=side)
+        kept.append(c)
+        del q, s
+        torch.full((64, 2048), i, dtype=torch.uint8, device=DEV)   # would land in q's memory
+    side.synchronize()
+    assert all(torch.equal(c, want) for c in kept)
