@@ -139,6 +139,16 @@ struct LnPack {
     }
 };
 
+// Elements 2m and 2m + 1 of NV packs in order.
+template <class T, int V, int NV>
+__device__ __forceinline__ float2 ln_pair_of(const LnPack<T, V> (&p)[NV], int m)
+{
+    if constexpr (V == 1) return make_float2(p[2 * m][0], p[2 * m + 1][0]);
+    else return p[m / (V / 2)].pair(m % (V / 2));
+}
+
+__device__ __forceinline__ float ln_half(float2 v, int j) { return (j & 1) == 0 ? v.x : v.y; }
+
 // Sum over N neighbouring lanes.
 template <int N = 32>
 __device__ __forceinline__ float ln_warp_sum(float v)

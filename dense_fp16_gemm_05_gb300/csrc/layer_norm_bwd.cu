@@ -35,16 +35,6 @@ struct BwdParams {
     W *dgamma, *dbeta;
 };
 
-// Elements 2m and 2m + 1 of NV packs in order.
-template <class T, int V, int NV>
-__device__ __forceinline__ float2 ln_pair_of(const LnPack<T, V> (&p)[NV], int m)
-{
-    if constexpr (V == 1) return make_float2(p[2 * m][0], p[2 * m + 1][0]);
-    else return p[m / (V / 2)].pair(m % (V / 2));
-}
-
-__device__ __forceinline__ float half_of(float2 v, int j) { return (j & 1) == 0 ? v.x : v.y; }
-
 // Threads of a block, and blocks per SM: some 1024 threads, so that the loads of
 // one block run while another waits for its row's sum.
 __host__ __device__ constexpr int bwd_threads(int tpr) { return tpr < 0 ? -tpr : (tpr <= 32 ? 256 : tpr); }
@@ -55,7 +45,8 @@ __host__ __device__ constexpr int bwd_blocks(int tpr, int v, int per)
     return 1024 / tpr;
 }
 
-template <class T, class W, int V, int NV, int TPR>
+// kInner: every pack but a thread's last lies inside the row whatever the thread.
+template <class T, class W, int V, int NV, int TPR, bool kInner>
 __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) layer_norm_bwd_kernel(BwdParams<T, W> p)
 {
     constexpr int R = TPR > 0 ? bwd_threads(TPR) / TPR : 1;   // rows at a time
@@ -80,12 +71,13 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
     constexpr bool kReload = sizeof(T) == 4 || V * NV > 8;
     constexpr bool kLean = (TPR == 1024 || TPR == -1024) && V * NV > 8;
     float2 dg[P], db[P], gm[P];
+    auto inside = [&](int i) { return (kInner && i < NV - 1) || (i * tpr + t) * V < p.dim; };
     auto load_gamma = [&]() {
         LnPack<W, V> pg[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * tpr + t) * V;
-            if (p.gamma && k < p.dim) pg[i].load(p.gamma + k);
+            if (p.gamma && inside(i)) pg[i].load(p.gamma + k);
             else pg[i].fill(1.0f);
         }
 #pragma unroll
@@ -104,7 +96,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * tpr + t) * V;
-            if (in && k < p.dim) {
+            if (in && inside(i)) {
                 nx[i].load(x + k);
                 nd[i].load(dy + k);
             } else {
@@ -174,10 +166,10 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * tpr + t) * V;
-            if (k >= p.dim || (kShared && row >= p.rows)) continue;
+            if (!inside(i) || (kShared && row >= p.rows)) continue;
             LnPack<T, V> out;
 #pragma unroll
-            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
+            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(ln_half(z[(i * V + j) / 2], i * V + j));
             out.store(dx + k);
         }
     }
@@ -192,7 +184,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
                 const int k = (i * tpr + t) * V;
                 if (k >= p.dim) continue;
 #pragma unroll
-                for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
+                for (int j = 0; j < V; ++j) out[k + j] = ln_half(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
             }
         } else {
             __syncthreads();
@@ -202,7 +194,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
                 if (k >= p.dim) continue;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    comb[sub * p.dim + k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
+                    comb[sub * p.dim + k + j] = ln_half(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
             }
             __syncthreads();
             for (int k = threadIdx.x; k < p.dim; k += static_cast<int>(blockDim.x)) {
@@ -379,7 +371,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
             if (!kFull && k >= p.dim) continue;
             LnPack<T, V> out;
 #pragma unroll
-            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(half_of(z[(i * V + j) / 2], i * V + j));
+            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(ln_half(z[(i * V + j) / 2], i * V + j));
             out.store(dx + k);
         }
         if (++s == p.stages) {
@@ -408,7 +400,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
             const int k = (i * tpr + t) * V;
             if (!kFull && k >= p.dim) continue;
 #pragma unroll
-            for (int j = 0; j < V; ++j) out[k + j] = half_of(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
+            for (int j = 0; j < V; ++j) out[k + j] = ln_half(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
         }
     }
 }
@@ -515,7 +507,14 @@ int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&lc, layer_norm_bwd_kernel<T, W, V, NV, TPR>, p) != cudaSuccess) {
+    cudaError_t e;
+    if constexpr (V <= 2 && TPR < 0)
+        e = static_cast<int64_t>(NV - 1) * BT * V <= p.dim
+                ? cudaLaunchKernelEx(&lc, layer_norm_bwd_kernel<T, W, V, NV, TPR, true>, p)
+                : cudaLaunchKernelEx(&lc, layer_norm_bwd_kernel<T, W, V, NV, TPR, false>, p);
+    else
+        e = cudaLaunchKernelEx(&lc, layer_norm_bwd_kernel<T, W, V, NV, TPR, false>, p);
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }

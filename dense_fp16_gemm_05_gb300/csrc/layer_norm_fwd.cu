@@ -9,6 +9,8 @@
 // that a thread holds at most 32 elements; longer rows are read again from L2.
 #include "layer_norm.cuh"
 
+#include <type_traits>
+
 namespace {
 
 using namespace gemm_sm103;
@@ -30,8 +32,9 @@ __host__ __device__ constexpr int fwd_threads(int tpr) { return tpr < 0 ? -tpr :
 
 // tpr threads per row, NV packs of V elements per thread, pack i of thread t at
 // element (i tpr + t) V.
-template <class T, class W, int V, int NV, int TPR, bool kGamma, bool kBeta>
-__global__ void __launch_bounds__(fwd_threads(TPR)) layer_norm_fwd_kernel(FwdParams<T, W> p)
+// kInner: every pack but a thread's last lies inside the row whatever the thread.
+template <class T, class W, int V, int NV, int TPR, bool kInner, bool kGamma, bool kBeta>
+__global__ void __launch_bounds__(fwd_threads(TPR), TPR == -1024 && V * NV == 8 ? 2 : 1) layer_norm_fwd_kernel(FwdParams<T, W> p)
 {
     constexpr int R = TPR > 0 ? fwd_threads(TPR) / TPR : 1;   // rows of a block
     __shared__ float sh[2][ln_warps(TPR)];
@@ -44,49 +47,73 @@ __global__ void __launch_bounds__(fwd_threads(TPR)) layer_norm_fwd_kernel(FwdPar
     const bool in = row < p.rows;
     if (!in) row = p.rows - 1;
     const T *x = p.X + row * p.dim;
-    LnPack<T, V> px[NV];
-    float s = 0.0f;
+    auto inside = [&](int i) { return (kInner && i < NV - 1) || (i * tpr + t) * V < p.dim; };
+    // On pairs, two fp32 operations per instruction: element by element the
+    // narrow variants are bound by instructions.
+    constexpr int P = V * NV / 2;
+    float2 x2[P];
+    {
+        LnPack<T, V> px[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int k = (i * tpr + t) * V;
-        if (k < p.dim) px[i].load(x + k);
-        else px[i].fill(0.0f);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) s += px[i][j];
-    const float mean = ln_row_sum<TPR>(s, sh[0]) * p.inv_dim;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if ((i * tpr + t) * V < p.dim) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = px[i][j] - mean;
-                s = fmaf(d, d, s);
-            }
+        for (int i = 0; i < NV; ++i) {
+            if (inside(i)) px[i].load(x + (i * tpr + t) * V);
+            else px[i].fill(0.0f);
         }
-    const float var = ln_row_sum<TPR>(s, sh[1]) * p.inv_dim;
+#pragma unroll
+        for (int m = 0; m < P; ++m) x2[m] = ln_pair_of(px, m);
+    }
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int m = 0; m < P; ++m) s = add_f32x2(s, x2[m]);
+    const float mean = ln_row_sum<TPR>(s.x + s.y, sh[0]) * p.inv_dim;
+    const float2 neg_mean = make_float2(-mean, -mean);
+    s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+        x2[m] = add_f32x2(x2[m], neg_mean);
+        // A pair of packs one of which may lie outside the row (V = 1), or a pack.
+        const int i0 = 2 * m / V, i1 = (2 * m + 1) / V;
+        float2 d = x2[m];
+        if (!inside(i0)) d.x = 0.0f;
+        if (!inside(i1)) d.y = 0.0f;
+        s = fma_f32x2(d, d, s);
+    }
+    const float var = ln_row_sum<TPR>(s.x + s.y, sh[1]) * p.inv_dim;
     const float rstd = 1.0f / sqrtf(var + p.eps);
     if (!in) return;
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
+    // The weights pack by pack: all of a thread's 32 at once cost 24 registers
+    // more and with them a block per SM (16384 x 4096 fp16: 46 us against 40 us).
     T *y = p.Y + row * p.dim;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        if (!inside(i)) continue;
         const int k = (i * tpr + t) * V;
-        if (k >= p.dim) break;
         LnPack<W, V> g, b;
-        if (kGamma) g.load(p.gamma + k);
-        else g.fill(1.0f);
-        if (kBeta) b.load(p.beta + k);
-        else b.fill(0.0f);
+        if constexpr (kGamma) g.load(p.gamma + k);
+        if constexpr (kBeta) b.load(p.beta + k);
         LnPack<T, V> out;
+        if constexpr (V == 1) {
+            float v = ln_half(x2[i / 2], i) * rstd;
+            if constexpr (kGamma && kBeta) v = fmaf(v, g[0], b[0]);
+            else if constexpr (kGamma) v *= g[0];
+            else if constexpr (kBeta) v += b[0];
+            out.e[0] = ln_round<T>(v);
+        } else {
+            const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
-        for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(fmaf((px[i][j] - mean) * rstd, g[j], b[j]));
+            for (int j = 0; j < V / 2; ++j) {
+                float2 v = mul_f32x2(x2[i * (V / 2) + j], rstd2);
+                if constexpr (kGamma && kBeta) v = fma_f32x2(v, g.pair(j), b.pair(j));
+                else if constexpr (kGamma) v = mul_f32x2(v, g.pair(j));
+                else if constexpr (kBeta) v = add_f32x2(v, b.pair(j));
+                out.e[2 * j] = ln_round<T>(v.x);
+                out.e[2 * j + 1] = ln_round<T>(v.y);
+            }
+        }
         out.store(y + k);
     }
 }
@@ -130,10 +157,16 @@ int launch_one(const FwdParams<T, W> &p, cudaStream_t stream)
     // The usual case, both weights, has its own kernel: a branch on each pointer
     // at every element is a tenth of the narrow variants' instructions.
     const dim3 grid(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1);
-    if (p.gamma && p.beta) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, true, true>, grid, BT, stream, p);
-    if (p.gamma) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, true, false>, grid, BT, stream, p);
-    if (p.beta) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, false, true>, grid, BT, stream, p);
-    return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, false, false>, grid, BT, stream, p);
+    auto launch = [&](auto inner) {
+        constexpr bool I = decltype(inner)::value;
+        if (p.gamma && p.beta) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, I, true, true>, grid, BT, stream, p);
+        if (p.gamma) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, I, true, false>, grid, BT, stream, p);
+        if (p.beta) return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, I, false, true>, grid, BT, stream, p);
+        return ln_launch(layer_norm_fwd_kernel<T, W, V, NV, TPR, I, false, false>, grid, BT, stream, p);
+    };
+    if constexpr (V <= 2 && TPR < 0)
+        if (static_cast<int64_t>(NV - 1) * BT * V <= p.dim) return launch(std::true_type{});
+    return launch(std::false_type{});
 }
 
 template <class T, class W, int V>
@@ -163,7 +196,7 @@ int launch_packs(const FwdParams<T, W> &p, cudaStream_t stream)
     } else {
         // Narrow loads are bound by instructions, so no more threads than eight
         // elements each take (16384 x 4097 fp16: 147 us with the next power of 2,
-        // 113 us this way).
+        // 103 us this way, with two blocks per SM).
         if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
         if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
         if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, -1024>(p, stream);
