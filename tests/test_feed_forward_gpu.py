@@ -102,3 +102,32 @@ def test_decoding_step_in_a_graph(ff):
 def test_command_runs(ff, capsys):
     ff.main(["--rows", "64", "--dim", "128", "--hidden", "256", "--steps", "2"])
     assert '"ms_mxfp4"' in capsys.readouterr().out
+
+
+def test_training_step_in_a_graph(ff):
+    # forward and backward captured together, after warm-up on a side stream and
+    # with no eager graph of the parameters alive
+    layer = ff.FeedForward(128, 256, device=DEV)
+    x, target = data(64, 128, 1), data(64, 128, 2)
+
+    def step():
+        layer.zero_grad(set_to_none=True)
+        loss = (layer(x).float() - target.float()).square().mean() * 1024.0
+        loss.backward()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    want = [p.grad.clone() for p in layer.parameters()]
+    layer.zero_grad(set_to_none=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.grad, w) for p, w in zip(layer.parameters(), want))
