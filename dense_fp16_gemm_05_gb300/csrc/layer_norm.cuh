@@ -82,11 +82,16 @@ struct LnPack {
             for (int i = 0; i < V; ++i) e[i] = __ldg(p + i);
         }
     }
-    __device__ __forceinline__ void load_shared(const T *p)   // V elements make up 16-byte pieces
+    __device__ __forceinline__ void load_shared(const T *p)   // one element, or whole 16-byte pieces
     {
-        uint4 raw[V * sizeof(T) / 16];
+        if constexpr (V == 1) {
+            e[0] = *p;
+            return;
+        }
+        constexpr unsigned N = V * sizeof(T) / 16 > 0 ? V * sizeof(T) / 16 : 1;
+        uint4 raw[N];
 #pragma unroll
-        for (unsigned i = 0; i < V * sizeof(T) / 16; ++i) raw[i] = reinterpret_cast<const uint4 *>(p)[i];
+        for (unsigned i = 0; i < N; ++i) raw[i] = reinterpret_cast<const uint4 *>(p)[i];
         memcpy(e, raw, sizeof(e));
     }
     __device__ __forceinline__ void store(T *p) const

@@ -221,6 +221,32 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 // device status word and the block leaves.
 constexpr int kRingStages = 4;
 
+// Bytes of a row's place in the ring.  Rows of other lengths and alignments
+// (V = 1) are copied with the whole 16-byte pieces that they lie in.
+template <class T, int V>
+__host__ __device__ __forceinline__ uint32_t ring_row_bytes(int dim)
+{
+    const uint32_t bytes = static_cast<uint32_t>(dim) * static_cast<uint32_t>(sizeof(T));
+    return V > 1 ? bytes : (bytes + 15u) / 16u * 16u + 16u;
+}
+
+// The 16-byte pieces of global memory that hold `bytes` bytes at `src`, and what
+// of them lies inside the tensor [lo, hi): the rest is not read.
+struct RingWindow {
+    uint64_t first, begin, end, src, last;
+
+    __device__ __forceinline__ RingWindow(uint64_t src_, uint32_t bytes, uint64_t lo, uint64_t hi)
+    {
+        src = src_;
+        last = src + bytes;
+        first = src & ~15ull;
+        begin = first < lo ? first + 16 : first;
+        end = (last + 15ull) & ~15ull;
+        if (end > hi) end -= 16;
+        if (end < begin) end = begin;
+    }
+};
+
 // Blocks per SM that the registers are held to.
 __host__ __device__ constexpr int ring_blocks(int tpr, int per)
 {
@@ -229,7 +255,8 @@ __host__ __device__ constexpr int ring_blocks(int tpr, int per)
 }
 
 // TPR > 0: the row is exactly the threads' elements, no bounds to check.
-template <class T, class W, int V, int NV, int TPR>
+// kInner: every pack but a thread's last lies inside the row whatever the thread.
+template <class T, class W, int V, int NV, int TPR, bool kInner>
 __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) layer_norm_bwd_ring(BwdParams<T, W> p)
 {
     constexpr bool kFull = TPR > 0;
@@ -241,7 +268,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
     __shared__ uint64_t full_mem[kRingStages];
     __shared__ volatile int failed[2];
     const int t = static_cast<int>(threadIdx.x), tpr = ln_threads<TPR>();
-    const uint32_t row_bytes = static_cast<uint32_t>(p.dim) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t row_bytes = ring_row_bytes<T, V>(p.dim);
     const uint32_t ring_base = smem_addr(ring), full0 = smem_addr(full_mem);
     constexpr uint64_t kLimit = 1ull << 31;   // about a second
     if (t == 0) {
@@ -255,6 +282,32 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
     auto fetch = [&](uint32_t row, int s) {
         const uint32_t bar = full0 + 8u * static_cast<uint32_t>(s);
         const uint32_t dst = ring_base + 2u * static_cast<uint32_t>(s) * row_bytes;
+        if constexpr (V == 1) {
+            const uint32_t bytes = static_cast<uint32_t>(p.dim) * static_cast<uint32_t>(sizeof(T));
+            const uint64_t size = static_cast<uint64_t>(p.rows) * bytes, at = static_cast<uint64_t>(row) * bytes;
+            const uint64_t bx = reinterpret_cast<uint64_t>(p.X), bd = reinterpret_cast<uint64_t>(p.dY);
+            const RingWindow w[2] = {RingWindow(bx + at, bytes, bx, bx + size), RingWindow(bd + at, bytes, bd, bd + size)};
+            uint8_t *to = reinterpret_cast<uint8_t *>(ring) + (dst - ring_base);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // Elements in pieces that reach past the tensor's ends, one by one;
+                // the arrival below releases them to the waiting threads.
+                auto edge = [&](uint64_t a, uint64_t b) {
+                    for (; a < b; a += sizeof(T))
+                        *reinterpret_cast<T *>(to + h * row_bytes + (a - w[h].first)) = *reinterpret_cast<const T *>(a);
+                };
+                if (w[h].begin > w[h].src) edge(w[h].src, w[h].begin < w[h].last ? w[h].begin : w[h].last);
+                if (w[h].end < w[h].last) edge(w[h].end > w[h].src ? w[h].end : w[h].src, w[h].last);
+            }
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(w[0].end - w[0].begin + w[1].end - w[1].begin));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (w[h].end > w[h].begin)
+                    bulk_load(dst + static_cast<uint32_t>(h) * row_bytes + static_cast<uint32_t>(w[h].begin - w[h].first),
+                              reinterpret_cast<const void *>(w[h].begin),
+                              static_cast<uint32_t>(w[h].end - w[h].begin), bar);
+            return;
+        }
         mbar_arrive_expect_tx(bar, 2u * row_bytes);
         bulk_load(dst, p.X + static_cast<int64_t>(row) * p.dim, row_bytes, bar);
         bulk_load(dst + row_bytes, p.dY + static_cast<int64_t>(row) * p.dim, row_bytes, bar);
@@ -266,13 +319,14 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
         for (int s = 0; s < p.stages && row + static_cast<uint32_t>(s) * step < rows; ++s)
             fetch(row + static_cast<uint32_t>(s) * step, s);
 
+    auto inside = [&](int i) { return kFull || (kInner && i < NV - 1) || (i * tpr + t) * V < p.dim; };
     float2 dg[P], db[P], gm[P];
     auto load_gamma = [&]() {
         LnPack<W, V> pg[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * tpr + t) * V;
-            if (p.gamma && (kFull || k < p.dim)) pg[i].load(p.gamma + k);
+            if (p.gamma && inside(i)) pg[i].load(p.gamma + k);
             else pg[i].fill(1.0f);
         }
 #pragma unroll
@@ -306,13 +360,18 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
         }
         const T *x = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(ring) +
                                                  2ull * static_cast<uint32_t>(s) * row_bytes);
-        const T *dy = x + p.dim;
+        const T *dy = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(x) + row_bytes);
+        if constexpr (V == 1) {
+            const int64_t at = static_cast<int64_t>(row) * p.dim;
+            x += (reinterpret_cast<uint64_t>(p.X + at) & 15u) / sizeof(T);
+            dy += (reinterpret_cast<uint64_t>(p.dY + at) & 15u) / sizeof(T);
+        }
         LnPack<T, V> px[NV], pd[NV];
         auto pieces = [&]() {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int k = (i * tpr + t) * V;
-                if (kFull || k < p.dim) {
+                if (inside(i)) {
                     px[i].load_shared(x + k);
                     pd[i].load_shared(dy + k);
                 } else {
@@ -368,7 +427,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * tpr + t) * V;
-            if (!kFull && k >= p.dim) continue;
+            if (!inside(i)) continue;
             LnPack<T, V> out;
 #pragma unroll
             for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(ln_half(z[(i * V + j) / 2], i * V + j));
@@ -398,7 +457,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int k = (i * tpr + t) * V;
-            if (!kFull && k >= p.dim) continue;
+            if (!inside(i)) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) out[k + j] = ln_half(which == 0 ? dg[(i * V + j) / 2] : db[(i * V + j) / 2], i * V + j);
         }
@@ -521,23 +580,10 @@ int launch_one(const BwdParams<T, W> &p, cudaStream_t stream)
     return finish<T, W>(p, stream);
 }
 
-// The ring kernel, where at least two rows fit a block's share of the shared
-// memory, else the register kernel.
-template <class T, class W, int V, int NV, int TPR>
-int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream)
+template <class T, class W, int V, int NV, int TPR, bool kInner>
+int launch_ring_kernel(const BwdParams<T, W> &p, int device, int threads, int64_t stage, cudaStream_t stream)
 {
-    const int packs = p.dim / V;
-    const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
-    // Blocks per SM: those of the launch bound, or more where they are small.
-    const int fit_blocks = V * NV > 8 ? ring_blocks(TPR, V * NV) : 1024 / threads;
-    const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
-    const int64_t stage = 2 * static_cast<int64_t>(p.dim) * static_cast<int64_t>(sizeof(T));
-    const int64_t fit = budget / stage;
-    if (fit < 2) return launch_one<T, W, V, NV, (TPR > 0 ? TPR : TPR == -320 ? -512 : TPR)>(p, stream);
-    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
-    const int64_t wave = static_cast<int64_t>(fit_blocks) * sm_count;
-    if (p.parts > wave) p.parts = static_cast<int32_t>(wave);
-    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR>;
+    auto kern = layer_norm_bwd_ring<T, W, V, NV, TPR, kInner>;
     static std::atomic<int> prepared[kMaxDevices];
     if (!prepared[device].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess) {
@@ -561,7 +607,36 @@ int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream
         prepared[device].store(0, std::memory_order_release);
         return GEMM_ERR_LAUNCH;
     }
-    return finish<T, W>(p, stream);
+    return GEMM_OK;
+}
+
+// The ring kernel, where at least two rows fit a block's share of the shared
+// memory, else the register kernel.
+template <class T, class W, int V, int NV, int TPR>
+int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream)
+{
+    const int packs = p.dim / V;
+    const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    // Blocks per SM: those of the launch bound, or more where they are small.
+    const int fit_blocks = V * NV > 8 ? ring_blocks(TPR, V * NV) : 1024 / threads;
+    const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
+    const int64_t stage = 2 * static_cast<int64_t>(ring_row_bytes<T, V>(p.dim));
+    const int64_t fit = budget / stage;
+    // Two rows always fit but in the longest fp32 rows: a row has at most eight
+    // elements per thread and 1024 threads share the SM, or is at most 8192 long.
+    if constexpr (TPR == 1024 || TPR == -1024)
+        if (fit < 2) return launch_one<T, W, V, NV, TPR>(p, stream);
+    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
+    const int64_t wave = static_cast<int64_t>(fit_blocks) * sm_count;
+    if (p.parts > wave) p.parts = static_cast<int32_t>(wave);
+    int st;
+    if constexpr (V == 1)
+        st = static_cast<int64_t>(NV - 1) * threads <= p.dim
+                 ? launch_ring_kernel<T, W, V, NV, TPR, true>(p, device, threads, stage, stream)
+                 : launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, threads, stage, stream);
+    else
+        st = launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, threads, stage, stream);
+    return st != GEMM_OK ? st : finish<T, W>(p, stream);
 }
 
 template <class T, class W, int V>
@@ -592,12 +667,22 @@ int launch_packs(const BwdParams<T, W> &p, int device, int sm_count, cudaStream_
         if (packs <= 512 * 2 * N) return launch_ring<T, W, V, 2 * N, -512>(p, device, sm_count, stream);
         if (packs <= 1024 * 2 * N) return launch_ring<T, W, V, 2 * N, -1024>(p, device, sm_count, stream);
     } else {
-        // Narrow loads are bound by instructions, so no more threads than eight
-        // elements each take (16384 x 4097 fp16: 347 us with the next power of 2,
-        // 171 us this way).
-        if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
-        if (packs <= 768 * N) return launch_one<T, W, V, N, -768>(p, stream);
-        if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
+        // No more threads than eight elements each take (16384 x 4097 fp16: 347 us
+        // with the next power of 2, 171 us this way).  Single elements go through the
+        // ring, which leaves registers for a second block per SM (16384 x 3001
+        // fp16: 118 us without, 99 us; 16384 x 7001: 311 us, 195 us), unless rows are
+        // short (65536 x 1023: 117 us without, 124 us).
+        if constexpr (V == 1) {
+            if (packs <= 128 * N) return launch_one<T, W, V, N, -512>(p, stream);
+            if (packs <= 512 * N) return launch_ring<T, W, V, N, -512>(p, device, sm_count, stream);
+            if (packs <= 320 * 2 * N) return launch_ring<T, W, V, 2 * N, -320>(p, device, sm_count, stream);
+            if (packs <= 512 * 2 * N) return launch_ring<T, W, V, 2 * N, -512>(p, device, sm_count, stream);
+        }
+        if constexpr (V == 2) {
+            if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
+            if (packs <= 768 * N) return launch_one<T, W, V, N, -768>(p, stream);
+            if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
+        }
         if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, -1024>(p, stream);
     }
     int st = ln_launch(layer_norm_bwd_long<T, W>, dim3(static_cast<unsigned>(p.parts), 1, 1), 1024, stream, p);

@@ -30,11 +30,19 @@ struct FwdParams {
 // Threads of a block (its bound, where the launch chooses).
 __host__ __device__ constexpr int fwd_threads(int tpr) { return tpr < 0 ? -tpr : (tpr < 128 ? 128 : tpr); }
 
+// Blocks per SM that the registers are held to, where the compiler's own choice
+// is one block too few (4096 x 16384 fp32: 108 us, and 80 us so); 0: its choice.
+__host__ __device__ constexpr int fwd_blocks(int tpr, int per)
+{
+    if (tpr == 512 || tpr == -512) return per > 8 ? 2 : 0;
+    return tpr == -1024 && per == 8 ? 2 : 0;
+}
+
 // tpr threads per row, NV packs of V elements per thread, pack i of thread t at
 // element (i tpr + t) V.
 // kInner: every pack but a thread's last lies inside the row whatever the thread.
 template <class T, class W, int V, int NV, int TPR, bool kInner, bool kGamma, bool kBeta>
-__global__ void __launch_bounds__(fwd_threads(TPR), TPR == -1024 && V * NV == 8 ? 2 : 1) layer_norm_fwd_kernel(FwdParams<T, W> p)
+__global__ void __launch_bounds__(fwd_threads(TPR), fwd_blocks(TPR, V * NV)) layer_norm_fwd_kernel(FwdParams<T, W> p)
 {
     constexpr int R = TPR > 0 ? fwd_threads(TPR) / TPR : 1;   // rows of a block
     __shared__ float sh[2][ln_warps(TPR)];

@@ -255,3 +255,23 @@ def test_refusals(g):
     assert st == g.GEMM_ERR_ALIGNMENT
     st = L.layer_norm_fwd(x.data_ptr(), None, None, y.data_ptr(), None, None, 10**6, 64, 0.0, 0, 0, None)
     assert st == g.GEMM_ERR_INVALID_ARG       # past its allocation
+
+
+@pytest.mark.parametrize("xt,wt", TYPES)
+@pytest.mark.parametrize("rows,dim", [(3, 1500), (7, 2049), (2, 4099), (5, 6001)])
+def test_operands_of_different_alignment(g, rows, dim, xt, wt):
+    # X, dY and dX start at different places within 16 bytes, and dY ends with
+    # its allocation
+    x, dy, w, b = draw(rows, dim, DTYPES[xt], DTYPES[wt], rows + dim)
+    moved = []
+    for t, off in ((x, 1), (dy, 2)):
+        flat = torch.empty(t.numel() + off, dtype=t.dtype, device=DEV)
+        flat[off:].copy_(t.reshape(-1))
+        moved.append(flat[off:].reshape(t.shape))
+    guard = torch.full((rows * dim + 8,), 7.0, dtype=x.dtype, device=DEV)
+    dX = guard[3:3 + rows * dim].reshape(rows, dim)
+    mean, rstd = check_forward(g, moved[0], w, b)
+    want, dg, db = check_backward(g, moved[0], moved[1], w, mean, rstd, DTYPES[wt])
+    got, dg2, db2 = g.layer_norm_bwd(moved[1], moved[0], mean, rstd, w, dX=dX)
+    assert got is dX and torch.equal(dX, want) and torch.equal(dg, dg2) and torch.equal(db, db2)
+    assert (guard[:3] == 7.0).all() and (guard[3 + rows * dim:] == 7.0).all()
