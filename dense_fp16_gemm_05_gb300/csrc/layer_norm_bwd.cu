@@ -215,9 +215,9 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 // bounds it by counters is issue slots (55-60 % busy) and the two dependent
 // chains of shuffles around the row's barrier, not DRAM.  A ring slot is
 // free once every thread has its pieces in registers, which the row sum's
-// barrier says; with 16 elements per thread (kReread) z and g are taken from
-// shared memory a second time instead of being kept, and the slot is refilled
-// one row later.  Every wait is bounded: on expiry the site is recorded in the
+// barrier says; with 16 elements in each of 1024 threads (kReread) z and g are
+// taken from shared memory a second time instead of being kept, and the slot is
+// refilled one row later.  Every wait is bounded: on expiry the site is recorded in the
 // device status word and the block leaves.
 constexpr int kRingStages = 4;
 
@@ -291,10 +291,12 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // Elements in pieces that reach past the tensor's ends, one by one;
-                // the arrival below releases them to the waiting threads.
+                // the arrival below releases them to the waiting threads, and the
+                // fence orders them before the copies of the slot's later rows.
                 auto edge = [&](uint64_t a, uint64_t b) {
                     for (; a < b; a += sizeof(T))
                         *reinterpret_cast<T *>(to + h * row_bytes + (a - w[h].first)) = *reinterpret_cast<const T *>(a);
+                    fence_proxy_async_smem();
                 };
                 if (w[h].begin > w[h].src) edge(w[h].src, w[h].begin < w[h].last ? w[h].begin : w[h].last);
                 if (w[h].end < w[h].last) edge(w[h].end > w[h].src ? w[h].end : w[h].src, w[h].last);
