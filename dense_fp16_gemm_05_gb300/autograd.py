@@ -11,7 +11,8 @@ calls the kernel and whose backward returns ``dA = dC @ B.T`` and
 * dB        A^T @ dZ   (A stored (M,K))          gemm_f16_tx with transa = 1 (TN)
 
 and layer norm, for the layer that feeds them, with layer_norm_fwd and
-layer_norm_bwd.
+layer_norm_bwd, and the product of MXFP4-quantised operands with gradients
+passed straight through the quantisation.
 
 The GEMMs' operands and gradients are float16 (the kernels accumulate in fp32).  No step
 falls back to torch arithmetic; a missing library raises LibraryNotBuilt.
@@ -50,6 +51,42 @@ class GemmF16Function(torch.autograd.Function):
         return dA, dB, None
 
 
+class LinearMxfp4Function(torch.autograd.Function):
+    """R(q(A) @ q(B)) with q the MXFP4 quantisation along the summed dimension.
+
+    The gradients are those of the product of the quantised values, passed
+    straight through the quantisation (whose own derivative is zero almost
+    everywhere): dA = dZ @ q(B)^T, dB = q(A)^T @ dZ, in the fp16 GEMMs.
+    """
+
+    @staticmethod
+    def forward(ctx, A: torch.Tensor, B: torch.Tensor, relu: bool):
+        A, B = A.contiguous(), B.contiguous()
+        need_a, need_b = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        qa = _g.mxfp4_quantize(A, values=need_b)
+        qb = _g.mxfp4_quantize(B, transpose=True, values=need_a)
+        C = _g.gemm_mxfp4(qa[0], qa[1], qb[0], qb[1], relu=relu, K=A.shape[1])
+        ctx.relu = relu
+        # q(A) (M,K) and q(B)^T (N,K), as fp16 values.
+        ctx.save_for_backward(qa[2] if need_b else None, qb[2] if need_a else None, C if relu else None)
+        return C
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dC: torch.Tensor):
+        Av, Bv, C = ctx.saved_tensors
+        dC = dC.contiguous()
+        if dC.dtype != torch.float16:
+            dC = dC.half()
+        dZ = _g.relu_backward(dC, C) if ctx.relu else dC
+        dA = dB = None
+        if ctx.needs_input_grad[0]:
+            dA = _g.gemm_f16_t(dZ, Bv, relu=False)                  # (M,N) @ (N,K)
+        if ctx.needs_input_grad[1]:
+            dB = _g.gemm_f16_t(Av, dZ, transa=True, relu=False)     # (K,M) @ (M,N)
+        return dA, dB, None
+
+
 class LayerNormFunction(torch.autograd.Function):
     """Layer norm over the last dimension; its backward is layer_norm_bwd."""
 
@@ -71,6 +108,15 @@ class LayerNormFunction(torch.autograd.Function):
         need_g, need_b = ctx.needs_input_grad[1], ctx.needs_input_grad[2]
         dx, dgamma, dbeta = _g.layer_norm_bwd(dy, x, mean, rstd, gamma, weights=need_g or need_b, wtype=ctx.wtype)
         return (dx if ctx.needs_input_grad[0] else None, dgamma if need_g else None, dbeta if need_b else None, None)
+
+
+def linear_mxfp4(A: torch.Tensor, B: torch.Tensor, relu: bool = False) -> torch.Tensor:
+    """C = A @ B or ReLU(A @ B) with both operands quantised to MXFP4, for training with 4-bit products.
+
+    A (M,K) and B (K,N): float16 CUDA tensors, K and N multiples of 8 (the
+    gradients' GEMMs).  Straight-through gradients, see LinearMxfp4Function.
+    """
+    return LinearMxfp4Function.apply(A, B, bool(relu))
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,

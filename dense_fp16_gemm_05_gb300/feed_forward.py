@@ -1,13 +1,14 @@
 """A pre-norm feed-forward layer on the library's kernels: trained in fp16, served in 4 bits.
 
-    python -m dense_fp16_gemm_05_gb300.feed_forward [--rows 4096 --dim 1024 --hidden 4096 --steps 3]
+    python -m dense_fp16_gemm_05_gb300.feed_forward [--rows 4096 --dim 1024 --hidden 4096 --steps 3] [--four-bit]
 
 :class:`FeedForward` is y = x + ReLU(norm(x) @ W1) @ W2 with layer norm, the
-fp16 GEMMs and their gradients (``autograd``).  :class:`FeedForwardMxfp4` is the
+fp16 GEMMs and their gradients (``autograd``), or, with ``four_bit``, 4-bit
+products trained straight through the quantisation.  :class:`FeedForwardMxfp4` is the
 same layer for inference: its weights are quantised to MXFP4 once, each call
 quantises the activations in front of either product.  The command trains a
 layer for a few steps, converts it and prints both layers' times and how far
-the 4-bit layer's output is from the fp16 one's.
+the served layer's output is from the trained one's (nothing, with --four-bit).
 """
 from __future__ import annotations
 
@@ -23,8 +24,10 @@ from . import gemm_f16 as g
 class FeedForward(torch.nn.Module):
     """x + ReLU(norm(x) @ W1) @ W2 on fp16 CUDA tensors (rows, dim); dim and hidden multiples of 8."""
 
-    def __init__(self, dim: int, hidden: int, eps: float = 1e-5, device="cuda:0", seed: int = 0):
+    def __init__(self, dim: int, hidden: int, eps: float = 1e-5, device="cuda:0", seed: int = 0,
+                 four_bit: bool = False):
         super().__init__()
+        self.four_bit = four_bit
         gen = torch.Generator(device="cpu").manual_seed(seed)
         self.eps = eps
         self.gamma = torch.nn.Parameter(torch.ones(dim, dtype=torch.float16, device=device))
@@ -36,6 +39,8 @@ class FeedForward(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         h = ag.layer_norm(x, self.gamma, self.beta, self.eps)
+        if self.four_bit:
+            return x + ag.linear_mxfp4(ag.linear_mxfp4(h, self.w1, relu=True), self.w2)
         return x + ag.gemm(ag.gemm_relu(h, self.w1), self.w2)
 
 
@@ -94,12 +99,13 @@ def main(argv=None):
     p.add_argument("--dim", type=int, default=1024)
     p.add_argument("--hidden", type=int, default=4096)
     p.add_argument("--steps", type=int, default=3)
+    p.add_argument("--four-bit", action="store_true", help="train with 4-bit products")
     args = p.parse_args(argv)
     dev = torch.device("cuda", 0)
     gen = torch.Generator(device=dev).manual_seed(1)
     x = torch.randn((args.rows, args.dim), generator=gen, device=dev).half()
     target = torch.randn((args.rows, args.dim), generator=gen, device=dev).half()
-    layer = FeedForward(args.dim, args.hidden, device=dev)
+    layer = FeedForward(args.dim, args.hidden, device=dev, four_bit=args.four_bit)
     losses = train(layer, x, target, args.steps)
     served = FeedForwardMxfp4(layer)
     with torch.no_grad():
@@ -109,7 +115,7 @@ def main(argv=None):
     if st != g.GEMM_OK:
         raise SystemExit(f"device status {st}: {g.strerror(st)}")
     update = (want - x.float()).square().mean().sqrt()
-    print(json.dumps({"rows": args.rows, "dim": args.dim, "hidden": args.hidden, "losses": losses, "ms_fp16": ms16,
+    print(json.dumps({"rows": args.rows, "dim": args.dim, "hidden": args.hidden, "losses": losses, "ms_trained": ms16,
                       "ms_mxfp4": ms4, "rms_difference_of_update": float((want - got).square().mean().sqrt() / update)}))
 
 

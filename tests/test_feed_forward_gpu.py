@@ -131,3 +131,41 @@ def test_training_step_in_a_graph(ff):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p.grad, w) for p, w in zip(layer.parameters(), want))
+
+
+@pytest.mark.parametrize("relu", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (40, 24, 72), (130, 264, 136), (257, 128, 320)])
+def test_four_bit_linear_and_its_gradients(ff, M, N, K, relu):
+    ag, g = ff.ag, ff.g
+    gen = torch.Generator().manual_seed(M + N + K)
+    A = torch.randn((M, K), generator=gen).half().to(DEV).requires_grad_()
+    B = torch.randn((K, N), generator=gen).half().to(DEV).requires_grad_()
+    dC = torch.randn((M, N), generator=gen).half().to(DEV)
+    C = ag.linear_mxfp4(A, B, relu)
+    C.backward(dC)
+    a = ref.decode(*ref.quantize(A.detach().cpu().double().numpy()))[:, :K]
+    b = ref.decode(*ref.quantize(B.detach().t().cpu().double().numpy()))[:, :K]      # (N,K)
+    want, mag = ref.product(a, b, relu)
+    assert np.all(np.abs(C.detach().cpu().double().numpy() - want) <= ref.product_tolerance(want, mag, K))
+    # the linear map of the quantised values, with the mask of the stored output
+    dz = dC.cpu().double().numpy() * ((C.detach() > 0).cpu().numpy() if relu else 1.0)
+    for got, x, y in ((A.grad, dz, b), (B.grad, a.T, dz)):
+        want = x @ y
+        # one rounding to fp16, and fp32 sums of up to 320 exact products
+        tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -25 + 330 * 2.0 ** -24 * (np.abs(x) @ np.abs(y))
+        assert np.all(np.abs(got.cpu().double().numpy() - want) <= tol)
+
+
+def test_four_bit_gradients_only_where_wanted(ff):
+    A, B = data(16, 64, 1), data(64, 32, 2).requires_grad_()
+    ff.ag.linear_mxfp4(A, B).sum().backward()
+    assert A.grad is None and B.grad.shape == (64, 32)
+
+
+def test_four_bit_training_matches_the_served_layer(ff):
+    layer = ff.FeedForward(64, 128, device=DEV, four_bit=True)
+    x, target = data(96, 64, 1), data(96, 64, 2)
+    losses = ff.train(layer, x, target, 5)
+    assert losses[-1] < losses[0]
+    with torch.no_grad():
+        assert torch.equal(layer(x), ff.FeedForwardMxfp4(layer)(x))   # the same kernels on the same codes
