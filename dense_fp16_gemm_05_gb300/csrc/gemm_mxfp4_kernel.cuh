@@ -148,6 +148,7 @@ struct Mx4Cfg {
     static constexpr int SFA_STAGE_BYTES = SF_TILES * SF_TILE;          // this CTA's 128 rows
     static constexpr int SFW_STAGE_BYTES = 2 * SF_TILES * SF_TILE;      // all 256 columns, in each CTA
     static constexpr int STAGE_TX_BYTES = A_STAGE_BYTES + W_STAGE_BYTES;
+    static constexpr int HALF_TX_BYTES = A_STAGE_BYTES + W_STAGE_BYTES / 2;   // of a half tile
     static constexpr int SF_TX_BYTES = SFA_STAGE_BYTES + SFW_STAGE_BYTES;
     static constexpr int SF_SLOTS = STAGES;    // scale slots in TMEM, one per ring slot
     static constexpr int SFW_COL = 4 * SF_TILES;                        // W words after A's in a slot
@@ -167,6 +168,7 @@ struct Mx4Cfg {
     static constexpr int SMEM_CTL_BYTES = 256;
     static constexpr int SMEM_BYTES = 1024 + SMEM_CTL_OFF + SMEM_CTL_BYTES;
     static constexpr uint32_t IDESC = idesc_mxf4(TILE_M, BN);
+    static constexpr uint32_t IDESC_HALF = idesc_mxf4(TILE_M, BN / 2);
 
     // The two accumulators share the columns [ACC1_COL, BN); the epilogue reads
     // the RELEASE chunks that hold those first.
@@ -182,14 +184,23 @@ struct Mx4Params {
     int32_t num_m_blocks;   // ceil(M / 256)
     int32_t num_n_blocks;   // ceil(N / 256)
     int32_t num_k_blocks;   // ceil(K / 256)
-    int32_t num_tiles;
+    int32_t num_units;      // whole tiles, then half tiles
+    int32_t split_start;    // tiles from here on are two units of 128 columns each
     int32_t group_m;        // rasterisation panel height, in tiles
     uint64_t timeout_cycles;
     unsigned long long *status;
 };
 
-__device__ __forceinline__ void mx4_tile_coords(int t, const Mx4Params &p, int &mb, int &nb)
+// Work unit u: tile (mb, nb) and, of a split tile, which half of its columns
+// (-1: the whole tile).
+__device__ __forceinline__ void mx4_unit_coords(int u, const Mx4Params &p, int &mb, int &nb, int &half)
 {
+    int t = u;
+    half = -1;
+    if (u >= p.split_start) {
+        t = p.split_start + ((u - p.split_start) >> 1);
+        half = (u - p.split_start) & 1;
+    }
     const int per_group = p.group_m * p.num_n_blocks;
     const int g = t / per_group;
     const int first_m = g * p.group_m;
@@ -216,6 +227,9 @@ __device__ __forceinline__ void mx4_tile_coords(int t, const Mx4Params &p, int &
 // in 120 columns.  The epilogue reads the two chunks that hold those columns first and
 // then lets the next tile's MMAs start, which run while it reads and stores the
 // rest.
+// The tiles of a last wave that fills less than half of the pairs are divided
+// into two units of 128 columns each (M = 256, N = 128 MMAs on half of W's rows);
+// both read the tile's scales whole and take their half's columns.
 // Ragged edges: TMA zero-fills operands and scales outside A and W (a zero
 // scale byte is 2^-127, not NaN); rows and columns outside C are not stored.
 // Every wait is bounded; on expiry the site is recorded in the device status
@@ -223,6 +237,7 @@ __device__ __forceinline__ void mx4_tile_coords(int t, const Mx4Params &p, int &
 template <bool kRelu>
 __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     gemm_mxfp4_sm103a(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                      const __grid_constant__ CUtensorMap tmap_w_half,
                       const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sw,
                       const __grid_constant__ CUtensorMap tmap_c, const Mx4Params p)
 {
@@ -281,6 +296,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&tmap_a);
         prefetch_tensormap(&tmap_w);
+        if (p.split_start < p.num_units) prefetch_tensormap(&tmap_w_half);
         prefetch_tensormap(&tmap_sa);
         prefetch_tensormap(&tmap_sw);
         prefetch_tensormap(&tmap_c);
@@ -311,11 +327,14 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             bool ok = true;
             const uint32_t full_base = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
             griddep_wait();   // A, W and the scales may come from the kernel just before
-            for (int t = first; ok && t < p.num_tiles; t += stride) {
-                int mb, nb;
-                mx4_tile_coords(t, p, mb, nb);
+            for (int u = first; ok && u < p.num_units; u += stride) {
+                int mb, nb, half;
+                mx4_unit_coords(u, p, mb, nb, half);
+                const uint32_t tx = half < 0 ? Cfg::STAGE_TX_BYTES : Cfg::HALF_TX_BYTES;
+                const CUtensorMap *map_w = half < 0 ? &tmap_w : &tmap_w_half;
                 const int m0 = mb * Cfg::TILE_M + static_cast<int>(rank) * Cfg::BM;
-                const int n0 = nb * Cfg::BN + static_cast<int>(rank) * Cfg::BN_CTA;
+                const int n0 = nb * Cfg::BN + (half < 0 ? static_cast<int>(rank) * Cfg::BN_CTA
+                                                        : half * Cfg::BN_CTA + static_cast<int>(rank) * (Cfg::BN_CTA / 2));
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!wait_phase(empty_bar(s), ph ^ 1u, abort, limit, kSiteProducerEmpty)) {
                         ok = false;
@@ -324,10 +343,10 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                     // Both CTAs' bytes are counted on the leader's barrier; each
                     // announces its own.
                     const uint32_t fb = full_base + 8u * s;
-                    if (leader) mbar_arrive_expect_tx(fb, Cfg::STAGE_TX_BYTES);
-                    else mbar_arrive_expect_tx_cluster(fb, Cfg::STAGE_TX_BYTES);
+                    if (leader) mbar_arrive_expect_tx(fb, tx);
+                    else mbar_arrive_expect_tx_cluster(fb, tx);
                     tma_load_2d_pair(sA + s * Cfg::A_STAGE_BYTES, &tmap_a, fb, kb * Cfg::ROW_BYTES, m0);
-                    tma_load_2d_pair(sW + s * Cfg::W_STAGE_BYTES, &tmap_w, fb, kb * Cfg::ROW_BYTES, n0);
+                    tma_load_2d_pair(sW + s * Cfg::W_STAGE_BYTES, map_w, fb, kb * Cfg::ROW_BYTES, n0);
                     // Scale tiles: (word in the tile, tile along K, row block).
                     mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
                     tma_load_3d_cta(sSFA + s * Cfg::SFA_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES,
@@ -377,7 +396,11 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             // elements is +32 B inside the swizzle row.
             const uint64_t a_desc0 = smem_desc_sw128(sA, 16, 1024);
             const uint64_t w_desc0 = smem_desc_sw128(sW, 16, 1024);
-            for (int t = first; ok && t < p.num_tiles; t += stride, ++acc_it) {
+            for (int u = first; ok && u < p.num_units; u += stride, ++acc_it) {
+                int mb, nb, half;
+                mx4_unit_coords(u, p, mb, nb, half);
+                const uint32_t idesc = half < 0 ? Cfg::IDESC : Cfg::IDESC_HALF;
+                const uint32_t sfw_col = Cfg::SFW_COL + (half > 0 ? 4u : 0u);
                 // The epilogue has read the columns that this tile's accumulator
                 // shares with the previous one's (and all of the one before).
                 if (acc_it > 0)
@@ -399,8 +422,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                         for (int ks = 0; ks < Cfg::BK / Cfg::UMMA_K; ++ks) {
                             const uint64_t step = static_cast<uint64_t>((ks * Cfg::STEP_BYTES) >> 4);
                             const uint32_t id = (ks & 1) * 2;   // bytes 0-1 or 2-3 of the words
-                            mma_mxf4<2>(acc, a_st + step, w_st + step, Cfg::IDESC | (id << 4) | (id << 29),
-                                        sf + 4u * (ks / 2), sf + Cfg::SFW_COL + 8u * (ks / 2),
+                            mma_mxf4<2>(acc, a_st + step, w_st + step, idesc | (id << 4) | (id << 29),
+                                        sf + 4u * (ks / 2), sf + sfw_col + 8u * (ks / 2),
                                         (kb != 0 || ks != 0) ? 1u : 0u);
                         }
                         // Operand slot s is free in both CTAs once these MMAs have read it.
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         const int q = warp & 3;        // TMEM lane quarter this warp may access
         const uint32_t sready0 = leader ? sready_bar(0) : mapa_shared(sready_bar(0), 0);
         const uint32_t row = static_cast<uint32_t>(lane) * 16u;
-        const int total = first < p.num_tiles ? (p.num_tiles - first + stride - 1) / stride * KB : 0;
+        const int total = first < p.num_units ? (p.num_units - first + stride - 1) / stride * KB : 0;
         int s = 0;
         uint32_t ph = 0;
         for (int blk = 0; blk < total; ++blk) {
@@ -471,9 +494,9 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         const uint32_t tempty_leader = leader ? tempty_bar : mapa_shared(tempty_bar, 0);
         const uint32_t cbuf0 = sC + static_cast<uint32_t>(ew * 2 * Cfg::C_BUF_BYTES);
         uint32_t acc_it = 0;
-        for (int t = first; t < p.num_tiles; t += stride, ++acc_it) {
-            int mb, nb;
-            mx4_tile_coords(t, p, mb, nb);
+        for (int u = first; u < p.num_units; u += stride, ++acc_it) {
+            int mb, nb, half;
+            mx4_unit_coords(u, p, mb, nb, half);
             int ok = 1;
             if (lane == 0) ok = wait_phase(tfull_bar, acc_it & 1u, abort, limit, kSiteEpilogueTmemFull) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -488,7 +511,9 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             // first of accumulator 1; both are read before anything is packed, so
             // that the next tile's MMAs wait only for the reads (with one chunk
             // packed and stored before the next is read, 1700 cycles per tile).
-            auto chunk = [&](int i) { return odd ? i : Cfg::EPI_CHUNKS - 1 - i; };
+            // A half tile has the first two chunks only.
+            const bool reversed = !odd && half < 0;
+            auto chunk = [&](int i) { return reversed ? Cfg::EPI_CHUNKS - 1 - i : i; };
             auto store_chunk = [&](const uint32_t (&r)[64], int i) {
                 // The store that used this staging buffer two chunks ago has read it.
                 if (lane == 0) bulk_wait_group_read<1>();
@@ -506,7 +531,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    const int col0 = nb * Cfg::BN + chunk(i) * Cfg::EPI_COLS;
+                    const int col0 = nb * Cfg::BN + (half > 0 ? Cfg::BN_CTA : 0) + chunk(i) * Cfg::EPI_COLS;
                     if (row0 < p.M && col0 < p.N) tma_store_2d(&tmap_c, cbuf, col0, row0);
                     bulk_commit_group();
                 }
@@ -523,6 +548,10 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                 else mbar_arrive_cluster(tempty_leader);
             }
             store_chunk(ra, 0);
+            if (half >= 0) {
+                store_chunk(rb, 1);
+                continue;
+            }
             tmem_load_32x32b_x64_async(acc_addr + static_cast<uint32_t>(chunk(2) * Cfg::EPI_COLS), ra);
             store_chunk(rb, 1);
             tmem_wait_ld_x64(ra);

@@ -237,7 +237,9 @@ def test_other_stream_and_graph_give_the_same_bits(g):
         assert torch.equal(c, want)
 
 
-@pytest.mark.parametrize("M,N,K", [(4096, 5128, 512), (3000, 6000, 260), (8200, 2056, 1100)])
+# 336, 288, 297, 256, 80 and 156 tiles: with and without half tiles at the end
+@pytest.mark.parametrize("M,N,K", [(4096, 5128, 512), (3000, 6000, 260), (8200, 2056, 1100), (4096, 4096, 768),
+                                   (2560, 2000, 512), (3012, 3304, 250)])
 def test_product_more_tiles_than_sms(g, M, N, K):
     # several tiles per CTA pair: both accumulators and every ring slot in turn
     gen = torch.Generator(device=DEV).manual_seed(M)
