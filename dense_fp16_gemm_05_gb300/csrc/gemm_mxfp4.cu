@@ -73,7 +73,10 @@ int launch_pairs(const Mx4LaunchArgs &a)
     p.num_k_blocks = static_cast<int32_t>((a.K + Cfg::BK - 1) / Cfg::BK);
     const int64_t tiles = static_cast<int64_t>(p.num_m_blocks) * p.num_n_blocks;
     if (tiles > INT32_MAX - 1024) return GEMM_ERR_INVALID_ARG;
-    p.group_m = 8;   // 2048-row panels, as the fp16 kernels
+    // 2048-row panels, as the fp16 kernels.  Panels of 16 tiles gain 0.7 % at 8192^3
+    // (152.0 against 153.1 us) and lose 2-5 % on smaller outputs (4096 x 8192 x
+    // 1024: 19.4 against 18.4 us).
+    p.group_m = 8;
     p.timeout_cycles = timeout_cycles_for(a.K);
     p.status = a.status;
 
