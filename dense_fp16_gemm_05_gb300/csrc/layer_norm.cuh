@@ -82,10 +82,14 @@ struct LnPack {
             for (int i = 0; i < V; ++i) e[i] = __ldg(p + i);
         }
     }
-    __device__ __forceinline__ void load_shared(const T *p)   // one element, or whole 16-byte pieces
+    __device__ __forceinline__ void load_shared(const T *p)   // an element, four bytes or whole 16-byte pieces
     {
         if constexpr (V == 1) {
             e[0] = *p;
+            return;
+        } else if constexpr (V * sizeof(T) == 4) {
+            const uint32_t raw = *reinterpret_cast<const uint32_t *>(p);
+            memcpy(e, &raw, sizeof(e));
             return;
         }
         constexpr unsigned N = V * sizeof(T) / 16 > 0 ? V * sizeof(T) / 16 : 1;

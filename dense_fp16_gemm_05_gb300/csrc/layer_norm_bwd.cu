@@ -221,13 +221,17 @@ __global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks(TPR, V, V * NV)) 
 // device status word and the block leaves.
 constexpr int kRingStages = 4;
 
-// Bytes of a row's place in the ring.  Rows of other lengths and alignments
-// (V = 1) are copied with the whole 16-byte pieces that they lie in.
+// Packs that do not make up 16-byte pieces: rows of other lengths and
+// alignments, copied with the whole 16-byte pieces that they lie in.
+template <class T, int V>
+constexpr bool kRingAny = V * sizeof(T) < 16;
+
+// Bytes of a row's place in the ring.
 template <class T, int V>
 __host__ __device__ __forceinline__ uint32_t ring_row_bytes(int dim)
 {
     const uint32_t bytes = static_cast<uint32_t>(dim) * static_cast<uint32_t>(sizeof(T));
-    return V > 1 ? bytes : (bytes + 15u) / 16u * 16u + 16u;
+    return kRingAny<T, V> ? (bytes + 15u) / 16u * 16u + 16u : bytes;
 }
 
 // The 16-byte pieces of global memory that hold `bytes` bytes at `src`, and what
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
     auto fetch = [&](uint32_t row, int s) {
         const uint32_t bar = full0 + 8u * static_cast<uint32_t>(s);
         const uint32_t dst = ring_base + 2u * static_cast<uint32_t>(s) * row_bytes;
-        if constexpr (V == 1) {
+        if constexpr (kRingAny<T, V>) {
             const uint32_t bytes = static_cast<uint32_t>(p.dim) * static_cast<uint32_t>(sizeof(T));
             const uint64_t size = static_cast<uint64_t>(p.rows) * bytes, at = static_cast<uint64_t>(row) * bytes;
             const uint64_t bx = reinterpret_cast<uint64_t>(p.X), bd = reinterpret_cast<uint64_t>(p.dY);
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
         const T *x = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(ring) +
                                                  2ull * static_cast<uint32_t>(s) * row_bytes);
         const T *dy = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(x) + row_bytes);
-        if constexpr (V == 1) {
+        if constexpr (kRingAny<T, V>) {
             const int64_t at = static_cast<int64_t>(row) * p.dim;
             x += (reinterpret_cast<uint64_t>(p.X + at) & 15u) / sizeof(T);
             dy += (reinterpret_cast<uint64_t>(p.dY + at) & 15u) / sizeof(T);
@@ -617,7 +621,7 @@ int launch_ring_kernel(const BwdParams<T, W> &p, int device, int threads, int64_
 template <class T, class W, int V, int NV, int TPR>
 int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream)
 {
-    const int packs = p.dim / V;
+    const int packs = (p.dim + V - 1) / V;
     const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
     // Blocks per SM: those of the launch bound, or more where they are small.
     const int fit_blocks = V * NV > 8 ? ring_blocks(TPR, V * NV) : 1024 / threads;
@@ -632,8 +636,8 @@ int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream
     const int64_t wave = static_cast<int64_t>(fit_blocks) * sm_count;
     if (p.parts > wave) p.parts = static_cast<int32_t>(wave);
     int st;
-    if constexpr (V == 1)
-        st = static_cast<int64_t>(NV - 1) * threads <= p.dim
+    if constexpr (kRingAny<T, V>)
+        st = static_cast<int64_t>(NV - 1) * threads * V <= p.dim
                  ? launch_ring_kernel<T, W, V, NV, TPR, true>(p, device, threads, stage, stream)
                  : launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, threads, stage, stream);
     else
@@ -670,21 +674,14 @@ int launch_packs(const BwdParams<T, W> &p, int device, int sm_count, cudaStream_
         if (packs <= 1024 * 2 * N) return launch_ring<T, W, V, 2 * N, -1024>(p, device, sm_count, stream);
     } else {
         // No more threads than eight elements each take (16384 x 4097 fp16: 347 us
-        // with the next power of 2, 171 us this way).  Single elements go through the
+        // with the next power of 2, 171 us this way).  Such rows too go through the
         // ring, which leaves registers for a second block per SM (16384 x 3001
         // fp16: 118 us without, 99 us; 16384 x 7001: 311 us, 195 us), unless rows are
         // short (65536 x 1023: 117 us without, 124 us).
-        if constexpr (V == 1) {
-            if (packs <= 128 * N) return launch_one<T, W, V, N, -512>(p, stream);
-            if (packs <= 512 * N) return launch_ring<T, W, V, N, -512>(p, device, sm_count, stream);
-            if (packs <= 320 * 2 * N) return launch_ring<T, W, V, 2 * N, -320>(p, device, sm_count, stream);
-            if (packs <= 512 * 2 * N) return launch_ring<T, W, V, 2 * N, -512>(p, device, sm_count, stream);
-        }
-        if constexpr (V == 2) {
-            if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
-            if (packs <= 768 * N) return launch_one<T, W, V, N, -768>(p, stream);
-            if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
-        }
+        if (packs <= 128 * N) return launch_one<T, W, V, N, -512>(p, stream);
+        if (packs <= 512 * N) return launch_ring<T, W, V, N, -512>(p, device, sm_count, stream);
+        if (packs <= 320 * 2 * N) return launch_ring<T, W, V, 2 * N, -320>(p, device, sm_count, stream);
+        if (packs <= 512 * 2 * N) return launch_ring<T, W, V, 2 * N, -512>(p, device, sm_count, stream);
         if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, -1024>(p, stream);
     }
     int st = ln_launch(layer_norm_bwd_long<T, W>, dim3(static_cast<unsigned>(p.parts), 1, 1), 1024, stream, p);

@@ -1,13 +1,14 @@
 """Runs one named workload through the C ABI a few times and prints the timings.
 
     python -m dense_fp16_gemm_05_gb300.run --workload relu_8192 --reps 4 [--config ID]
-        [--op gemm|dA_nt|dB_tn|relu_backward|fp8|attn]
+        [--op gemm|dA_nt|dB_tn|relu_backward|fp8|mxfp8|mxfp4|attn]
 
 --op picks the kernel: the forward GEMM (default), the two backward GEMMs of
 the workload (dA = dZ @ B^T in the NT layout, dB = A^T @ dZ in the TN layout)
 or the ReLU-gradient mask over an (M,N) gradient; --op fp8 runs the FP8
 block-scaled GEMM on the workload's sizes (E4M3 operands quantized per
-128-block, fp32 scales), --op mxfp8 the same with power-of-two scales; --op attn runs the attention forward on an attention
+128-block, fp32 scales), --op mxfp8 the same with power-of-two scales, --op mxfp4
+the 4-bit GEMM on the workload's operands quantized on the GPU; --op attn runs the attention forward on an attention
 workload (--workload attn_4096_d128, ...); causal attention takes work items
 from one work queue made before the first launch (--attn-queue fixed: the
 fixed shares instead).
@@ -34,7 +35,8 @@ def main(argv=None):
     p.add_argument("--reps", type=int, default=4)
     p.add_argument("--config", type=int, default=0)
     p.add_argument("--relu", type=int, default=None, help="override the workload's ReLU flag")
-    p.add_argument("--op", default="gemm", choices=["gemm", "dA_nt", "dB_tn", "relu_backward", "fp8", "mxfp8", "attn"])
+    p.add_argument("--op", default="gemm", choices=["gemm", "dA_nt", "dB_tn", "relu_backward", "fp8", "mxfp8", "mxfp4",
+                                                 "attn"])
     p.add_argument("--attn-queue", default="reuse", choices=["reuse", "fixed"])
     args = p.parse_args(argv)
     if args.op == "attn":
@@ -50,6 +52,8 @@ def main(argv=None):
         return run_fp8(w, relu, args.reps, dev, pow2=args.op == "mxfp8")
     A_cpu, B_cpu = draw_workload(w)
     A, B = A_cpu.to(dev), B_cpu.to(dev)
+    if args.op == "mxfp4":
+        return run_mxfp4(w, relu, args.reps, A, B)
     C = torch.empty((w.M, w.N), dtype=torch.float16, device=dev)
     cfg = args.config or g.auto_config(w.M, w.N, w.K)
     dZ = dA = dB = None
@@ -107,6 +111,24 @@ def run_fp8(w, relu, reps, dev, pow2=False):
     if st != g.GEMM_OK:
         raise SystemExit(f"device status {st}: {g.strerror(st)}")
     print(json.dumps({"workload": w.name, "op": "mxfp8" if pow2 else "fp8", "M": w.M, "N": w.N, "K": w.K, "relu": relu, "ms": times,
+                      "best_tflops": w.flops / (min(times) * 1e-3) / 1e12}))
+
+
+def run_mxfp4(w, relu, reps, A, B):
+    qa, qb = g.mxfp4_quantize(A), g.mxfp4_quantize(B, transpose=True)
+    C = torch.empty((w.M, w.N), dtype=torch.float16, device=A.device)
+    times = []
+    for _ in range(reps):
+        s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        s.record()
+        g.gemm_mxfp4(*qa, *qb, C=C, relu=relu, K=w.K)
+        e.record()
+        e.synchronize()
+        times.append(s.elapsed_time(e))
+    st = g.check()
+    if st != g.GEMM_OK:
+        raise SystemExit(f"device status {st}: {g.strerror(st)}")
+    print(json.dumps({"workload": w.name, "op": "mxfp4", "M": w.M, "N": w.N, "K": w.K, "relu": relu, "ms": times,
                       "best_tflops": w.flops / (min(times) * 1e-3) / 1e12}))
 
 
