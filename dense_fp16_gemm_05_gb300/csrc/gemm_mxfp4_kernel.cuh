@@ -216,7 +216,7 @@ __device__ __forceinline__ void mx4_unit_coords(int u, const Mx4Params &p, int &
 //                      barrier, and the scale tiles of A's 128 rows and of the
 //                      tile's 256 columns, completing on this CTA's "scales
 //                      full" barrier
-//   warp 1, one lane   (leader CTA only) issues the MMAs, M = 256, N = 256, K = 64
+//   warp 1             (leader CTA only) issues the MMAs, M = 256, N = 256, K = 64
 //   warps 2..5         epilogue: accumulator -> R -> fp16 -> shared memory ->
 //                      TMA store
 //   warps 6..9         scale warps: tiles from shared memory to TMEM, then an
@@ -224,9 +224,9 @@ __device__ __forceinline__ void mx4_unit_coords(int u, const Mx4Params &p, int &
 // TMEM (512 columns): each ring slot has its own scale slot of 24 columns, free
 // again when the ring slot is: the scale warps need no barrier of their own for
 // it.  Two accumulators of 256 columns do not fit beside them, so these overlap
-// in 120 columns.  The epilogue reads the two chunks that hold those columns first and
-// then lets the next tile's MMAs start, which run while it reads and stores the
-// rest.
+// in 120 columns.  The epilogue reads the two chunks that hold those columns
+// first and then lets the next tile's MMAs start, which run while it reads and
+// stores the rest.
 // The tiles of a last wave that fills less than half of the pairs are divided
 // into two units of 128 columns each (M = 256, N = 128 MMAs on half of W's rows);
 // both read the tile's scales whole and take their half's columns.
@@ -609,7 +609,6 @@ struct Mx4NarrowCfg {
     static constexpr int SF_TILES = BK / 128;
     static constexpr int STAGES = kStages;
     static constexpr int THREADS = 192;
-    static constexpr int MAX_CLUSTER = 8;
     static constexpr int W_HALF_BYTES = BM * ROW_BYTES;
     static constexpr int X_HALF_BYTES = BN * ROW_BYTES;
     static constexpr int W_STAGE_BYTES = HALVES * W_HALF_BYTES;
@@ -662,8 +661,8 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
 // Adds CTA crank's share of the tile over the S partial tiles in rank order.
 // Item i: row i / 16 of A and rows 8 (i % 16) .. + 7 of W, consecutive items to
 // a CTA.  All S pairs of loads are issued before the first is used: one after
-// another they cost S round trips through the cluster (23 us against 12 for
-// 128 x 4096 x 4096).
+// another they cost S round trips through the cluster (23 us against 16 for
+// 128 x 4096 x 4096 in 128-row tiles over 8 CTAs).
 template <int S, bool kRelu, int kBN>
 __device__ __forceinline__ void mx4_reduce(const Mx4NarrowParams &p, uint32_t part, uint32_t crank, int m0, int n0,
                                            int t)
