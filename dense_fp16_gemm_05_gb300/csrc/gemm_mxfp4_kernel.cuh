@@ -660,9 +660,10 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
 
 // Adds CTA crank's share of the tile over the S partial tiles in rank order.
 // Item i: row i / 16 of A and rows 8 (i % 16) .. + 7 of W, consecutive items to
-// a CTA.  All S pairs of loads are issued before the first is used: one after
-// another they cost S round trips through the cluster (23 us against 16 for
-// 128 x 4096 x 4096 in 128-row tiles over 8 CTAs).
+// a CTA.  All S pairs of loads are issued before the first is used, so that
+// their round trips through the cluster overlap: with N = K = 4096, 1 row
+// 5.1 us against 5.3 and 16 rows 5.5 against 6.0 for one pair after another,
+// and no difference beyond 1.5 % at 64 and 128 rows.
 template <int S, bool kRelu, int kBN>
 __device__ __forceinline__ void mx4_reduce(const Mx4NarrowParams &p, uint32_t part, uint32_t crank, int m0, int n0,
                                            int t)
