@@ -148,6 +148,19 @@ struct LnPack {
     }
 };
 
+// Elements per pack that a call's alignments allow: 16 bytes of X's type, four
+// bytes (two 16-bit elements), or one element.  x_bits: the rows' addresses and
+// bytes per row, w_bits: the weights' addresses, each or-ed together.  A pack of
+// weights has as many elements as one of X, so the same pieces ask for twice the
+// alignment where fp32 weights stand beside 16-bit rows.
+template <class T, class W>
+int ln_pack_elements(uintptr_t x_bits, uintptr_t w_bits)
+{
+    if (((x_bits | w_bits) & 15u) == 0) return 16 / static_cast<int>(sizeof(T));
+    if (sizeof(T) == 2 && (x_bits & 3u) == 0 && (w_bits & (2 * sizeof(W) - 1)) == 0) return 2;
+    return 1;
+}
+
 // Elements 2m and 2m + 1 of NV packs in order.
 template <class T, int V, int NV>
 __device__ __forceinline__ float2 ln_pair_of(const LnPack<T, V> (&p)[NV], int m)

@@ -717,12 +717,15 @@ int backward(const LayerNormArgs &a)
     p.status = a.status;
     p.dgamma = static_cast<W *>(a.dgamma);
     p.dbeta = static_cast<W *>(a.dbeta);
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
-                           reinterpret_cast<uintptr_t>(a.Y) | reinterpret_cast<uintptr_t>(a.gamma) |
-                           (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    const uintptr_t x_bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
+                             reinterpret_cast<uintptr_t>(a.Y) |
+                             (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    const uintptr_t w_bits = reinterpret_cast<uintptr_t>(a.gamma);
     constexpr int V = 16 / sizeof(T);
-    if ((bits & 15u) == 0) return launch_packs<T, W, V>(p, a.device, a.sm_count, a.stream);
-    if ((bits & 3u) == 0 && V > 4) return launch_packs<T, W, V / 4>(p, a.device, a.sm_count, a.stream);
+    const int pack = ln_pack_elements<T, W>(x_bits, w_bits);
+    if (pack == V) return launch_packs<T, W, V>(p, a.device, a.sm_count, a.stream);
+    if constexpr (V > 4)
+        if (pack == V / 4) return launch_packs<T, W, V / 4>(p, a.device, a.sm_count, a.stream);
     return launch_packs<T, W, 1>(p, a.device, a.sm_count, a.stream);
 }
 

@@ -226,12 +226,14 @@ int forward(const LayerNormArgs &a)
     p.dim = static_cast<int32_t>(a.dim);
     p.inv_dim = 1.0f / static_cast<float>(a.dim);
     p.eps = a.eps;
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.Y) |
-                           reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.beta) |
-                           (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    const uintptr_t x_bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.Y) |
+                             (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    const uintptr_t w_bits = reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.beta);
     constexpr int V = 16 / sizeof(T);
-    if ((bits & 15u) == 0) return launch_packs<T, W, V>(p, a.stream);
-    if ((bits & 3u) == 0 && V > 4) return launch_packs<T, W, V / 4>(p, a.stream);
+    const int pack = ln_pack_elements<T, W>(x_bits, w_bits);
+    if (pack == V) return launch_packs<T, W, V>(p, a.stream);
+    if constexpr (V > 4)
+        if (pack == V / 4) return launch_packs<T, W, V / 4>(p, a.stream);
     return launch_packs<T, W, 1>(p, a.stream);
 }
 
