@@ -251,8 +251,10 @@ except AttributeError:
     _empty_strided_cuda = None
 
 
-def _new(shape, dtype, device) -> torch.Tensor:
-    """torch.empty(shape) for one to three sizes."""
+def _new(shape, dtype, device, stream=None) -> torch.Tensor:
+    """torch.empty(shape) for one to three sizes, an output of a launch on ``stream``."""
+    if stream is not None:
+        return _new_on(stream, shape, dtype, device)
     if _empty_strided_cuda is None or device.index is None or device.index != _current_device():
         return torch.empty(shape, dtype=dtype, device=device)
     n = len(shape)   # plain tuples below: the function takes no torch.Size
@@ -267,9 +269,29 @@ def _new(shape, dtype, device) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _on_gpu(device) -> bool:
+    return device.type == "cuda"
+
+
+def _new_on(stream, shape, dtype, device) -> torch.Tensor:
+    """torch.empty(shape) for a launch on ``stream`` (None: torch's current stream).
+
+    Made on the stream that writes it: a block of the current stream's pool may
+    still be in use by work queued there, which the launch does not wait for.
+    The current stream, on which the caller gets the tensor, is recorded, so
+    that the memory is not reused before what is queued there is done.
+    """
+    if stream is None or not _on_gpu(device):   # the library refuses host memory
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_launch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _used_on(stream, device, *tensors):
-    """Tells the allocator that tensors made here on torch's current stream are
-    used on ``stream``: their memory is not reused before that stream is done."""
+    """Tells the allocator that the caller's tensors are used on ``stream``: their
+    memory is not reused before that stream is done."""
     if stream is not None:
         s = _launch_stream(stream, device)
         for t in tensors:
@@ -300,7 +322,7 @@ def gemm_f16(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None, re
     if K != K2:
         raise ValueError(f"inner sizes differ: A {tuple(A.shape)}, B {tuple(B.shape)}")
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        C = _new_on(stream, (M, N), torch.float16, A.device)
     _check_operand(C, "C")
     if tuple(C.shape) != (M, N):
         raise ValueError(f"C must be {(M, N)}, got {tuple(C.shape)}")
@@ -350,7 +372,7 @@ def gemm_f16_t(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None, 
     if K != K2:
         raise ValueError(f"inner sizes differ: op(A) {M}x{K}, op(B) {K2}x{N}")
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        C = _new_on(stream, (M, N), torch.float16, A.device)
     _check_operand(C, "C")
     if tuple(C.shape) != (M, N):
         raise ValueError(f"C must be {(M, N)}, got {tuple(C.shape)}")
@@ -370,7 +392,7 @@ def relu_backward(dC: torch.Tensor, C: torch.Tensor, dZ: torch.Tensor | None = N
     if dC.shape != C.shape:
         raise ValueError(f"dC {tuple(dC.shape)} and C {tuple(C.shape)} differ")
     if dZ is None:
-        dZ = torch.empty_like(dC)
+        dZ = _new_on(stream, dC.shape, torch.float16, dC.device)
     with _device_scope(dC.device):
         st = lib().gemm_f16_relu_backward(dC.data_ptr(), C.data_ptr(), dZ.data_ptr(), dC.numel(),
                                           _stream_handle(stream, dC.device))
@@ -385,7 +407,7 @@ def tma_box_image(X: torch.Tensor, box_rows: int, x: int, y: int, stream=None) -
     by TMA with the GEMM's operand encoding (gemm_f16_tma_box_image)."""
     _check_operand(X, "X")
     rows, cols = X.shape
-    out = torch.empty(int(box_rows) * 128, dtype=torch.uint8, device=X.device)
+    out = _new_on(stream, (int(box_rows) * 128,), torch.uint8, X.device)
     L = lib()
     with _device_scope(X.device):
         st = L.gemm_f16_tma_box_image(X.data_ptr(), rows, cols, int(box_rows), int(x), int(y), out.data_ptr(),
@@ -513,7 +535,7 @@ def gemm_fp8_block_scaled(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW
     _check_scales(SA, "SA", (M, KB))
     _check_scales(SW, "SW", (NB, KB))
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        C = _new_on(stream, (M, N), torch.float16, A.device)
     _check_operand(C, "C")
     if tuple(C.shape) != (M, N):
         raise ValueError(f"C must be {(M, N)}, got {tuple(C.shape)}")
@@ -542,7 +564,7 @@ def gemm_mxfp8_block_scaled(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, 
         if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        C = _new_on(stream, (M, N), torch.float16, A.device)
     _check_operand(C, "C")
     if tuple(C.shape) != (M, N):
         raise ValueError(f"C must be {(M, N)}, got {tuple(C.shape)}")
@@ -622,17 +644,17 @@ def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = Fals
     dev = X.device
     q_shape, s_shape = mxfp4_shapes(rows, K)
     if Q is None:
-        Q = _new(q_shape, torch.uint8, dev)
+        Q = _new(q_shape, torch.uint8, dev, stream)
     else:
         _check_like(Q, "Q", torch.uint8, q_shape, dev)
     if S is None:
-        S = _new(s_shape, torch.uint8, dev)
+        S = _new(s_shape, torch.uint8, dev, stream)
     else:
         _check_like(S, "S", torch.uint8, s_shape, dev)
     if V is not None:
         _check_like(V, "V", dtype, (rows, K), dev)
     elif values:
-        V = _new((rows, K), dtype, dev)
+        V = _new((rows, K), dtype, dev, stream)
     _call((_lib or lib()).mxfp4_quantize, "mxfp4_quantize", dev, stream, X.data_ptr(), code, Q.data_ptr(),
           S.data_ptr(), _ptr(V), rows, K, 1 if transpose else 0)
     _used_on(stream, dev, Q, S, V)
@@ -664,7 +686,7 @@ def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Ten
     _check_like(W, "W", u8, q_shape, dev)
     _check_like(SW, "SW", u8, s_shape, dev)
     if C is None:
-        C = _new((M, N), torch.float16, dev)
+        C = _new((M, N), torch.float16, dev, stream)
     else:
         _check_like(C, "C", torch.float16, (M, N), dev)
     _call((_lib or lib()).gemm_mxfp4, "gemm_mxfp4", dev, stream, A.data_ptr(), SA.data_ptr(), W.data_ptr(),
@@ -710,14 +732,14 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
     dev = X.device
     wt = _norm_weight_type(dtype, dim, dev, gamma, beta)
     if Y is None:
-        Y = _new(shape, dtype, dev)
+        Y = _new(shape, dtype, dev, stream)
     else:
         _check_like(Y, "Y", dtype, shape, dev)
     mean = rstd = None
     if stats:
         lead = shape[:-1]
-        mean = _new(lead, torch.float32, dev)
-        rstd = _new(lead, torch.float32, dev)
+        mean = _new(lead, torch.float32, dev, stream)
+        rstd = _new(lead, torch.float32, dev, stream)
     _call((_lib or lib()).layer_norm_fwd, "layer_norm_fwd", dev, stream, X.data_ptr(), _ptr(gamma), _ptr(beta),
           Y.data_ptr(), _ptr(mean), _ptr(rstd), rows, dim, eps, code, TYPES[wt])
     _used_on(stream, dev, Y, mean, rstd)
@@ -756,15 +778,15 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
         if wt != dtype and wt != torch.float32:
             raise ValueError(f"wtype must be X's type {dtype} or float32, got {wt}")
     if dX is None:
-        dX = _new(shape, dtype, dev)
+        dX = _new(shape, dtype, dev, stream)
     else:
         _check_like(dX, "dX", dtype, shape, dev)
     L = _lib or lib()
     dgamma = dbeta = None
     ws_bytes = 0
     if weights:
-        dgamma = _new((dim,), wt, dev)
-        dbeta = _new((dim,), wt, dev)
+        dgamma = _new((dim,), wt, dev, stream)
+        dbeta = _new((dim,), wt, dev, stream)
         if workspace is None:
             if dev.index == _current_device():
                 need = L.layer_norm_bwd_workspace(rows, dim)
@@ -829,7 +851,7 @@ def attention_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Te
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
     if O is None:
-        O = torch.empty_like(Q)
+        O = _new_on(stream, Q.shape, torch.float16, Q.device)
     if O.dtype != torch.float16 or O.shape != Q.shape or not O.is_contiguous():
         raise ValueError("O must be a contiguous float16 tensor shaped like Q")
     q_ptr = None
