@@ -290,8 +290,9 @@ def _new_on(stream, shape, dtype, device) -> torch.Tensor:
 
 
 def _used_on(stream, device, *tensors):
-    """Tells the allocator that the caller's tensors are used on ``stream``: their
-    memory is not reused before that stream is done."""
+    """Tells the allocator that a call's tensors, inputs too, are used on ``stream``:
+    a caller may drop them at once and their memory is not reused before that
+    stream is done."""
     if stream is not None:
         s = _launch_stream(stream, device)
         for t in tensors:
@@ -657,7 +658,7 @@ def mxfp4_quantize(X: torch.Tensor, transpose: bool = False, values: bool = Fals
         V = _new((rows, K), dtype, dev, stream)
     _call((_lib or lib()).mxfp4_quantize, "mxfp4_quantize", dev, stream, X.data_ptr(), code, Q.data_ptr(),
           S.data_ptr(), _ptr(V), rows, K, 1 if transpose else 0)
-    _used_on(stream, dev, Q, S, V)
+    _used_on(stream, dev, X, Q, S, V)
     return (Q, S) if V is None else (Q, S, V)
 
 
@@ -691,7 +692,7 @@ def gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, W: torch.Tensor, SW: torch.Ten
         _check_like(C, "C", torch.float16, (M, N), dev)
     _call((_lib or lib()).gemm_mxfp4, "gemm_mxfp4", dev, stream, A.data_ptr(), SA.data_ptr(), W.data_ptr(),
           SW.data_ptr(), C.data_ptr(), M, N, K, 1 if relu else 0)
-    _used_on(stream, dev, C)
+    _used_on(stream, dev, A, SA, W, SW, C)
     return C
 
 
@@ -742,7 +743,7 @@ def layer_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, beta: tor
         rstd = _new(lead, torch.float32, dev, stream)
     _call((_lib or lib()).layer_norm_fwd, "layer_norm_fwd", dev, stream, X.data_ptr(), _ptr(gamma), _ptr(beta),
           Y.data_ptr(), _ptr(mean), _ptr(rstd), rows, dim, eps, code, TYPES[wt])
-    _used_on(stream, dev, Y, mean, rstd)
+    _used_on(stream, dev, X, gamma, beta, Y, mean, rstd)
     return Y, mean, rstd
 
 
@@ -806,7 +807,7 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
     _call(L.layer_norm_bwd, "layer_norm_bwd", dev, stream, dY.data_ptr(), X.data_ptr(), _ptr(gamma), mean.data_ptr(),
           rstd.data_ptr(), dX.data_ptr(), _ptr(dgamma), _ptr(dbeta), rows, dim, code, TYPES[wt],
           _ptr(workspace) if weights else None, ws_bytes)
-    _used_on(stream, dev, dX, dgamma, dbeta)
+    _used_on(stream, dev, dY, X, mean, rstd, gamma, dX, dgamma, dbeta, workspace if weights else None)
     return dX, dgamma, dbeta
 
 

@@ -83,3 +83,32 @@ def test_host_tensors_are_refused_on_a_given_stream(g):
     with pytest.raises(Exception):
         g.gemm_f16(a, a, stream=side)
     assert g.check() == g.GEMM_OK
+
+
+def test_inputs_dropped_right_after_the_call(g):
+    # the next allocations on the current stream would land in their memory
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    base = [torch.randn((64, 512), generator=gen, device=DEV).half() for _ in range(2)]
+    _, mean, rstd = g.layer_norm_fwd(base[1])
+    want = (*g.mxfp4_quantize(base[0], values=True)[::2], g.layer_norm_fwd(base[0])[0],
+            *g.layer_norm_bwd(*base, mean, rstd))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+
+    def fresh(t):
+        return torch.empty_like(t).copy_(t)
+
+    got = []
+    inputs = [[fresh(base[0])], [fresh(base[0])], [fresh(t) for t in (*base, mean, rstd)]]
+    torch.cuda.current_stream().synchronize()
+    got += g.mxfp4_quantize(*inputs.pop(0), values=True, stream=side)[::2]
+    got.append(g.layer_norm_fwd(*inputs.pop(0), stream=side)[0])
+    got += g.layer_norm_bwd(*inputs.pop(0), stream=side)
+    for _ in range(6):
+        for t in (base[0], mean):
+            torch.full_like(t, 7.0)
+    torch.cuda.synchronize()
+    assert g.check() == g.GEMM_OK and all(torch.equal(a, b) for a, b in zip(got, want))

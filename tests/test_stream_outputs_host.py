@@ -63,9 +63,9 @@ def codes(rows, K):
 CALLS = {
     "mxfp4_quantize": lambda s: g.mxfp4_quantize(zeros((4, 64), H), values=True, stream=s),
     "gemm_mxfp4": lambda s: g.gemm_mxfp4(*codes(4, 64), *codes(8, 64), stream=s),
-    "layer_norm_fwd": lambda s: g.layer_norm_fwd(zeros((4, 64), H), stream=s),
+    "layer_norm_fwd": lambda s: g.layer_norm_fwd(zeros((4, 64), H), zeros(64, H), zeros(64, H), stream=s),
     "layer_norm_bwd": lambda s: g.layer_norm_bwd(zeros((4, 64), H), zeros((4, 64), H), zeros(4, F), zeros(4, F),
-                                                 workspace=zeros(16, F), stream=s),
+                                                 zeros(64, H), workspace=zeros(16, F), stream=s),
     "gemm_f16": lambda s: g.gemm_f16(zeros((4, 8), H), zeros((8, 8), H), stream=s),
     "gemm_f16_t": lambda s: g.gemm_f16_t(zeros((4, 8), H), zeros((8, 8), H), transb=True, stream=s),
     "relu_backward": lambda s: g.relu_backward(zeros((4, 8), H), zeros((4, 8), H), stream=s),
@@ -93,3 +93,27 @@ def test_outputs_come_from_the_launch_streams_pool(made, name):
 def test_without_a_stream_nothing_is_recorded(made, name):
     CALLS[name](None)
     assert made.allocated and all(s is CURRENT for _, s in made.allocated) and not made.recorded
+
+
+def _inputs(monkeypatch):
+    """Every tensor that zeros() makes for a call."""
+    kept = []
+    plain = zeros
+
+    def keep(shape, dtype):
+        t = plain(shape, dtype)
+        kept.append(t)
+        return t
+
+    monkeypatch.setitem(globals(), "zeros", keep)
+    return kept
+
+
+@pytest.mark.parametrize("name", ["mxfp4_quantize", "gemm_mxfp4", "layer_norm_fwd", "layer_norm_bwd"])
+def test_inputs_are_recorded_on_the_launch_stream(made, monkeypatch, name):
+    # a temporary passed to the call is dropped before the launch stream has read it
+    kept = _inputs(monkeypatch)
+    CALLS[name](LAUNCH)
+    assert kept
+    for t in kept:
+        assert any(u is t and s is LAUNCH for u, s in made.recorded)
