@@ -116,6 +116,9 @@ def linear_mxfp4(A: torch.Tensor, B: torch.Tensor, relu: bool = False) -> torch.
     A (M,K) and B (K,N): float16 CUDA tensors, K and N multiples of 8 (the
     gradients' GEMMs).  Straight-through gradients, see LinearMxfp4Function.
     """
+    if A.dim() == 2 and B.dim() == 2 and A.shape[1] != B.shape[0]:
+        # Their packed forms would not tell: K is rounded up to whole blocks there.
+        raise ValueError(f"inner sizes differ: A {tuple(A.shape)}, B {tuple(B.shape)}")
     return LinearMxfp4Function.apply(A, B, bool(relu))
 
 
