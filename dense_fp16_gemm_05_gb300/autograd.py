@@ -114,11 +114,20 @@ def linear_mxfp4(A: torch.Tensor, B: torch.Tensor, relu: bool = False) -> torch.
     """C = A @ B or ReLU(A @ B) with both operands quantised to MXFP4, for training with 4-bit products.
 
     A (M,K) and B (K,N): float16 CUDA tensors, K and N multiples of 8 (the
-    gradients' GEMMs).  Straight-through gradients, see LinearMxfp4Function.
+    gradients' GEMMs); where no gradient is recorded any K and the quantiser's
+    other types serve too.  Straight-through gradients, see LinearMxfp4Function.
     """
     if A.dim() == 2 and B.dim() == 2 and A.shape[1] != B.shape[0]:
         # Their packed forms would not tell: K is rounded up to whole blocks there.
         raise ValueError(f"inner sizes differ: A {tuple(A.shape)}, B {tuple(B.shape)}")
+    if torch.is_grad_enabled() and (A.requires_grad or B.requires_grad):
+        # Here and not in the backward pass, whose fp16 GEMMs would refuse: either
+        # gradient is a product with the other operand's values.
+        for t, other, name in ((A, B, "A"), (B, A, "B")):
+            if other.requires_grad and t.dtype != torch.float16:
+                raise ValueError(f"{name} must be float16 for the gradients, got {t.dtype}")
+        if A.dim() == 2 and A.shape[1] % 8:
+            raise ValueError(f"K must be a multiple of 8 for the gradients, got {A.shape[1]}")
     return LinearMxfp4Function.apply(A, B, bool(relu))
 
 

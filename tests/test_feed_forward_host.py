@@ -20,3 +20,16 @@ def test_four_bit_linear_refuses_inner_sizes_that_differ(ag, a, b):
     # also those that fill the same number of blocks of 32
     with pytest.raises(ValueError, match="inner sizes differ"):
         ag.linear_mxfp4(torch.zeros(a, dtype=torch.float16), torch.zeros(b, dtype=torch.float16))
+
+
+H, BF, F = torch.float16, torch.bfloat16, torch.float32
+
+
+# dA is a product with B's values, dB one with A's, both over rows of K
+@pytest.mark.parametrize("K,ta,tb,which", [(64, BF, BF, "A"), (64, F, F, "B"), (64, H, BF, "A"), (64, BF, H, "B"),
+                                           (64, H, F, "AB"), (36, H, H, "A"), (36, H, H, "B"), (4, H, H, "AB")])
+def test_four_bit_linear_refuses_at_the_call_what_its_gradients_do_not_take(ag, K, ta, tb, which):
+    A = torch.zeros((4, K), dtype=ta, requires_grad="A" in which)
+    B = torch.zeros((K, 8), dtype=tb, requires_grad="B" in which)
+    with pytest.raises(ValueError, match="for the gradients"):
+        ag.linear_mxfp4(A, B)
