@@ -49,7 +49,8 @@ class FeedForwardMxfp4:
 
     The weights are stored in-features x out-features, so their columns are
     quantised (``transpose=True``): blocks of 32 along the dimension that the
-    product sums over.
+    product sums over.  No gradient is recorded: the output of an input that
+    requires one is detached from it.
     """
 
     def __init__(self, layer: FeedForward):
@@ -62,7 +63,8 @@ class FeedForwardMxfp4:
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         h, _, _ = g.layer_norm_fwd(x, self.gamma, self.beta, eps=self.eps, stats=False)
         a = g.gemm_mxfp4(*g.mxfp4_quantize(h), *self.w1, relu=True, K=self.dim)
-        return x + g.gemm_mxfp4(*g.mxfp4_quantize(a), *self.w2, K=self.hidden)
+        # Through the residual alone a gradient would be wrong.
+        return x.detach() + g.gemm_mxfp4(*g.mxfp4_quantize(a), *self.w2, K=self.hidden)
 
 
 def train(layer: FeedForward, x: torch.Tensor, target: torch.Tensor, steps: int, lr: float = 0.05) -> list[float]:

@@ -1,6 +1,8 @@
 """Refusals of the feed-forward layer's functions that need no GPU."""
 from __future__ import annotations
 
+import types
+
 import pytest
 import torch
 
@@ -33,3 +35,22 @@ def test_four_bit_linear_refuses_at_the_call_what_its_gradients_do_not_take(ag, 
     B = torch.zeros((K, 8), dtype=tb, requires_grad="B" in which)
     with pytest.raises(ValueError, match="for the gradients"):
         ag.linear_mxfp4(A, B)
+
+
+@pytest.fixture
+def ff(ag, monkeypatch):
+    """The example with the operators' results replaced by zeros of their shapes."""
+    from dense_fp16_gemm_05_gb300 import feed_forward
+    shapes = {"mxfp4_quantize": lambda x, transpose=False: (x.detach().t() if transpose else x.detach(), None),
+              "gemm_mxfp4": lambda a, sa, w, sw, **kw: torch.zeros((a.shape[0], w.shape[0]), dtype=H),
+              "layer_norm_fwd": lambda x, gamma, beta, eps, stats: (x.detach() * gamma + beta, None, None)}
+    monkeypatch.setattr(feed_forward, "g", types.SimpleNamespace(**shapes))
+    return feed_forward
+
+
+def test_served_layer_gives_no_gradient(ff):
+    # the residual's gradient alone would be a wrong one
+    served = ff.FeedForwardMxfp4(ff.FeedForward(64, 128, device="cpu"))
+    x = torch.ones((4, 64), dtype=H, requires_grad=True)
+    y = served(x)
+    assert not y.requires_grad and torch.equal(y, x.detach()) and x.grad is None
