@@ -55,7 +55,8 @@ class FeedForwardMxfp4:
 
     def __init__(self, layer: FeedForward):
         self.eps = layer.eps
-        self.gamma, self.beta = layer.gamma.detach(), layer.beta.detach()
+        # Copies, as the packed weights are: training the layer further changes neither.
+        self.gamma, self.beta = layer.gamma.detach().clone(), layer.beta.detach().clone()
         self.dim, self.hidden = layer.w1.shape
         self.w1 = g.mxfp4_quantize(layer.w1.detach(), transpose=True)
         self.w2 = g.mxfp4_quantize(layer.w2.detach(), transpose=True)

@@ -54,3 +54,12 @@ def test_served_layer_gives_no_gradient(ff):
     x = torch.ones((4, 64), dtype=H, requires_grad=True)
     y = served(x)
     assert not y.requires_grad and torch.equal(y, x.detach()) and x.grad is None
+
+
+def test_served_layer_is_the_layer_as_it_was_converted(ff):
+    layer = ff.FeedForward(64, 128, device="cpu")
+    served = ff.FeedForwardMxfp4(layer)
+    with torch.no_grad():
+        layer.gamma += 1.0
+        layer.beta -= 1.0
+    assert (served.gamma == 1.0).all() and (served.beta == 0.0).all()
