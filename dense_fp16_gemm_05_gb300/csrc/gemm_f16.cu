@@ -877,8 +877,10 @@ extern "C" int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, v
     return launch_mxfp4_quantize(a);
 }
 
-extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C, int64_t M,
-                          int64_t N, int64_t K, int relu, void *stream)
+namespace {
+
+int run_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C, int64_t M, int64_t N,
+              int64_t K, int relu, void *stream, int withhold, uint64_t timeout_cycles)
 {
     int st = check_sizes(M, N, K, relu);
     if (st != GEMM_OK) return st;
@@ -920,7 +922,28 @@ extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const
     a.stream = s;
     a.status = status_word(dev.device);
     if (a.status == nullptr) return GEMM_ERR_CUDA;
+    a.withhold = withhold;
+    a.timeout_cycles = timeout_cycles;
     return launch_mxfp4(a);
+}
+
+}  // namespace
+
+extern "C" int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C, int64_t M,
+                          int64_t N, int64_t K, int relu, void *stream)
+{
+    return run_mxfp4(A, SA, W, SW, C, M, N, K, relu, stream, 0, 0);
+}
+
+extern "C" int gemm_mxfp4_selftest_timeout(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C,
+                                           int64_t M, int64_t N, int64_t K, int withhold, uint64_t timeout_cycles,
+                                           void *stream)
+{
+    if (K == 0 || M == 0 || N == 0) return reject(GEMM_ERR_INVALID_ARG, "an empty problem launches no kernel");
+    if (withhold != 1 && withhold != 2) return reject(GEMM_ERR_INVALID_ARG, "withhold is not 1 or 2");
+    if (timeout_cycles < (1ull << 16) || timeout_cycles > (1ull << 32))
+        return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
+    return run_mxfp4(A, SA, W, SW, C, M, N, K, 0, stream, withhold, timeout_cycles);
 }
 
 namespace {

@@ -77,7 +77,8 @@ int launch_pairs(const Mx4LaunchArgs &a)
     // (152.0 against 153.1 us) and lose 2-5 % on smaller outputs (4096 x 8192 x
     // 1024: 19.4 against 18.4 us).
     p.group_m = 8;
-    p.timeout_cycles = timeout_cycles_for(a.K);
+    p.withhold = a.withhold;
+    p.timeout_cycles = a.timeout_cycles ? a.timeout_cycles : timeout_cycles_for(a.K);
     p.status = a.status;
 
     using Prep = Mx4Prepared<kRelu>;
@@ -135,7 +136,8 @@ int launch_narrow(const Mx4LaunchArgs &a, int splits)
     p.num_m_tiles = static_cast<int32_t>((a.M + Cfg::BN - 1) / Cfg::BN);
     p.num_k_blocks = static_cast<int32_t>((a.K + Cfg::BK - 1) / Cfg::BK);
     p.k_per_cta = (p.num_k_blocks + splits - 1) / splits;
-    p.timeout_cycles = timeout_cycles_for(a.K);
+    p.withhold = a.withhold;
+    p.timeout_cycles = a.timeout_cycles ? a.timeout_cycles : timeout_cycles_for(a.K);
     p.C = static_cast<__half *>(a.C);
     p.status = a.status;
     const int64_t ctas = static_cast<int64_t>(p.num_m_tiles) * ((a.N + Cfg::BM - 1) / Cfg::BM) * splits;

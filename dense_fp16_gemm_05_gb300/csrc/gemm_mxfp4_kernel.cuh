@@ -174,7 +174,7 @@ struct Mx4Cfg {
     // the RELEASE chunks that hold those first.
     static constexpr int RELEASE = (BN - ACC1_COL + EPI_COLS - 1) / EPI_COLS;
     static_assert(ACC1_COL > 0 && RELEASE == 2 && EPI_CHUNKS == 4, "the epilogue's order of reads");
-    static_assert((4 * STAGES + 4) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert((4 * STAGES + 5) * 8 <= SMEM_CTL_BYTES, "control block");
     static_assert(SF_TILES == 2, "the scale warps' stores");
     static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
 };
@@ -187,6 +187,8 @@ struct Mx4Params {
     int32_t num_units;      // whole tiles, then half tiles
     int32_t split_start;    // tiles from here on are two units of 128 columns each
     int32_t group_m;        // rasterisation panel height, in tiles
+    int32_t withhold;       // test hook (gemm_mxfp4_selftest_timeout): loads not issued,
+                            // 1 all of them, 2 the scale tiles'; 0 in every normal call
     uint64_t timeout_cycles;
     unsigned long long *status;
 };
@@ -317,6 +319,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     const uint64_t limit = p.timeout_cycles;
     const int KB = p.num_k_blocks;
     const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
+    // The producer's ring slots in use, and the parity of their last load.
+    volatile uint32_t *issued_ptr = tmem_slot_ptr + 2;
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             bool ok = true;
             const uint32_t full_base = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
             griddep_wait();   // A, W and the scales may come from the kernel just before
-            for (int u = first; ok && u < p.num_units; u += stride) {
+            for (int u = first; ok && u < p.num_units && p.withhold != 1; u += stride) {
                 int mb, nb, half;
                 mx4_unit_coords(u, p, mb, nb, half);
                 const uint32_t tx = half < 0 ? Cfg::STAGE_TX_BYTES : Cfg::HALF_TX_BYTES;
@@ -348,11 +352,13 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                     tma_load_2d_pair(sA + s * Cfg::A_STAGE_BYTES, &tmap_a, fb, kb * Cfg::ROW_BYTES, m0);
                     tma_load_2d_pair(sW + s * Cfg::W_STAGE_BYTES, map_w, fb, kb * Cfg::ROW_BYTES, n0);
                     // Scale tiles: (word in the tile, tile along K, row block).
-                    mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
-                    tma_load_3d_cta(sSFA + s * Cfg::SFA_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES,
-                                    mb * 2 + static_cast<int>(rank));
-                    tma_load_3d_cta(sSFW + s * Cfg::SFW_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0, kb * Cfg::SF_TILES,
-                                    nb * 2);
+                    if (p.withhold == 0) {
+                        mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
+                        tma_load_3d_cta(sSFA + s * Cfg::SFA_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0,
+                                        kb * Cfg::SF_TILES, mb * 2 + static_cast<int>(rank));
+                        tma_load_3d_cta(sSFW + s * Cfg::SFW_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0,
+                                        kb * Cfg::SF_TILES, nb * 2);
+                    }
                     issued_mask |= 1u << s;
                     issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
                     if (++s == S) {
@@ -361,24 +367,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                // Let the loads in flight land before the CTA exits.
-                for (int i = 0; i < S; ++i)
-                    if (issued_mask & (1u << i))
-                        wait_phase_drain(sfull_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
-                if (leader) {
-                    for (int i = 0; i < S; ++i)
-                        if (issued_mask & (1u << i))
-                            wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads,
-                                             p.status);
-                } else {
-                    // This CTA's operand loads complete on the leader's barrier, which it
-                    // cannot probe: give them a bounded time (~1e6 cycles) to land.
-                    const long long t0 = clock64();
-                    while (clock64() - t0 < 1000000) {
-                    }
-                }
-            }
+            issued_ptr[0] = issued_mask;
+            issued_ptr[1] = issued_parity;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -565,6 +555,28 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
 
     tc_fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && abort.raised()) {
+        // Let the loads in flight land before the CTA exits.  Here, where the roles
+        // have met, and not in the producer: it may have issued its last load before
+        // another role gave up.  Without an abort every load has been waited for.
+        const uint32_t issued_mask = issued_ptr[0], issued_parity = issued_ptr[1];
+        for (int i = 0; i < S; ++i)
+            if (issued_mask & (1u << i))
+                wait_phase_drain(sfull_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+        if (leader) {
+            for (int i = 0; i < S; ++i)
+                if (issued_mask & (1u << i))
+                    wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+        } else {
+            // This CTA's operand loads complete on the leader's barrier, which it
+            // cannot probe: give them a bounded time (~1e6 cycles) to land.
+            const long long t0 = clock64();
+            while (clock64() - t0 < 1000000) {
+            }
+        }
+    }
+    // A warp's lanes meet again for the aligned barrier.
+    __syncwarp();
     // Neither CTA exits while the other may still signal its barriers or its
     // MMAs may still use this CTA's shared or tensor memory.
     cluster_arrive();
@@ -634,7 +646,7 @@ struct Mx4NarrowCfg {
     static_assert(SF_TILES == 2 * HALVES && X_HALF_BYTES % 1024 == 0, "tiles of a half; swizzle atoms");
     static_assert(BN % 16 == 0 && BN <= 128, "N of the MMA; scale words of one row block");
     static_assert(PART_BYTES <= STAGES * (W_STAGE_BYTES + X_STAGE_BYTES), "the partial tile fits in the ring");
-    static_assert((4 * STAGES + 2) * 8 + 8 <= SMEM_CTL_BYTES, "control block");
+    static_assert((4 * STAGES + 3) * 8 <= SMEM_CTL_BYTES, "control block");
     static_assert(SMEM_BYTES <= 232448, "shared memory per block on sm_103");
 };
 
@@ -643,6 +655,7 @@ struct Mx4NarrowParams {
     int32_t num_m_tiles;    // ceil(M / BN)
     int32_t num_k_blocks;   // ceil(K / 512)
     int32_t k_per_cta;      // K blocks of each CTA of a cluster
+    int32_t withhold;       // test hook, as above
     uint64_t timeout_cycles;
     __half *C;
     unsigned long long *status;
@@ -776,13 +789,16 @@ __global__ void __launch_bounds__(192, 1)
             tma_load_2d(sW + s * Cfg::W_STAGE_BYTES + h * Cfg::W_HALF_BYTES, &tmap_w, full_bar(s), x, n0);
             tma_load_2d(sX + s * Cfg::X_STAGE_BYTES + h * Cfg::X_HALF_BYTES, &tmap_a, full_bar(s), x, m0);
         }
+        if (p.withhold != 0) return;
         mbar_arrive_expect_tx(sfull_bar(s), Cfg::SF_TX_BYTES);
         tma_load_3d_cta(sSFW + s * Cfg::SF_STAGE_BYTES, &tmap_sw, sfull_bar(s), 0, kb * Cfg::SF_TILES, wb);
         tma_load_3d_cta(sSFX + s * Cfg::SF_STAGE_BYTES, &tmap_sa, sfull_bar(s), 0, kb * Cfg::SF_TILES, m0 / 128);
     };
     // The thread that initialised the barriers fills the ring before it joins
     // the others, whose set-up runs while the first loads are on their way.
-    const int filled = min(S, kb1 - kb0);
+    const int filled = p.withhold != 1 ? min(S, kb1 - kb0) : 0;
+    // The producer's ring slots in use, and the parity of their last load.
+    volatile uint32_t *issued_ptr = tmem_slot_ptr + 2;
     if (threadIdx.x == 0) {
         griddep_wait();   // A, W and the scales may come from the kernel just before
         for (int s = 0; s < filled; ++s) load(kb0 + s, s);
@@ -802,16 +818,12 @@ __global__ void __launch_bounds__(192, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            // Ring slots in use, and the parity of their last load.
-            uint32_t issued_mask = (1u << filled) - 1u, issued_parity = 0;
-            bool ok = true;
+            const uint32_t issued_mask = (1u << filled) - 1u;
+            uint32_t issued_parity = 0;
             int s = 0;
             uint32_t ph = 1;
-            for (int kb = kb0 + filled; kb < kb1; ++kb) {
-                if (!wait_phase(empty_bar(s), ph ^ 1u, abort, limit, kSiteProducerEmpty)) {
-                    ok = false;
-                    break;
-                }
+            for (int kb = kb0 + filled; kb < kb1 && p.withhold != 1; ++kb) {
+                if (!wait_phase(empty_bar(s), ph ^ 1u, abort, limit, kSiteProducerEmpty)) break;
                 load(kb, s);
                 issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
                 if (++s == S) {
@@ -819,14 +831,8 @@ __global__ void __launch_bounds__(192, 1)
                     ph ^= 1u;
                 }
             }
-            if (!ok) {
-                // Let the loads in flight land before the CTA exits.
-                for (int i = 0; i < S; ++i)
-                    if (issued_mask & (1u << i)) {
-                        wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
-                        wait_phase_drain(sfull_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
-                    }
-            }
+            issued_ptr[0] = issued_mask;
+            issued_ptr[1] = issued_parity;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -941,6 +947,15 @@ __global__ void __launch_bounds__(192, 1)
         case 4: mx4_reduce<4, kRelu, Cfg::BN>(p, sW, crank, m0, n0, t); break;
         default: mx4_reduce<8, kRelu, Cfg::BN>(p, sW, crank, m0, n0, t); break;
         }
+    }
+    if (threadIdx.x == 0 && abort.raised()) {
+        // Let the loads in flight land before the CTA exits (see the pair kernel).
+        const uint32_t issued_mask = issued_ptr[0], issued_parity = issued_ptr[1];
+        for (int i = 0; i < S; ++i)
+            if (issued_mask & (1u << i)) {
+                wait_phase_drain(full_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+                wait_phase_drain(sfull_bar(i), (issued_parity >> i) & 1u, limit, kSiteDrainLoads, p.status);
+            }
     }
     __syncwarp();
     if (ncl > 1) {

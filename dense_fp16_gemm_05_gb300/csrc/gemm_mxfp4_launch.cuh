@@ -43,6 +43,8 @@ struct Mx4LaunchArgs {
     DeviceInfo dev;
     cudaStream_t stream = nullptr;
     unsigned long long *status = nullptr;
+    int withhold = 0;              // test hook: loads that are not issued (Mx4Params)
+    uint64_t timeout_cycles = 0;   // 0: the normal budget
 };
 
 int launch_mxfp4(const Mx4LaunchArgs &a);

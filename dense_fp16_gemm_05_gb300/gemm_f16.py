@@ -116,6 +116,8 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_quantize.restype = ci
     L.gemm_mxfp4.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
     L.gemm_mxfp4.restype = ci
+    L.gemm_mxfp4_selftest_timeout.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, ctypes.c_uint64, vp]
+    L.gemm_mxfp4_selftest_timeout.restype = ci
     cf = ctypes.c_float
     L.layer_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, cf, ci, ci, vp]
     L.layer_norm_fwd.restype = ci

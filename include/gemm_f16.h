@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define GEMM_F16_VERSION 8
+#define GEMM_F16_VERSION 9
 
 /* Return codes.  0 is success; every error is negative. */
 enum gemm_f16_status {
@@ -376,6 +376,20 @@ int mxfp4_quantize(const void *X, int type, uint8_t *Q, uint8_t *S, void *V, int
  */
 int gemm_mxfp4(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C,
                int64_t M, int64_t N, int64_t K, int relu, void *stream);
+
+/*
+ * gemm_mxfp4_selftest_timeout -- exercises the bounded waits of gemm_mxfp4's
+ * kernels (a test hook as gemm_f16_selftest_timeout; it computes nothing).  The
+ * kernel of the problem is launched with a wait budget of `timeout_cycles` SM
+ * clocks (2^16 .. 2^32) and its producer issues no load (withhold = 1), or the
+ * operands' loads and not the scale tiles' (withhold = 2): the waits for them run
+ * out, every role leaves its loop, the loads in flight land, the tensor memory
+ * is freed and the kernel exits without writing C.  The next gemm_f16_check
+ * returns GEMM_ERR_TIMEOUT.  Buffers and sizes are validated as for gemm_mxfp4.
+ */
+int gemm_mxfp4_selftest_timeout(const void *A, const uint8_t *SA, const void *W, const uint8_t *SW, void *C,
+                                int64_t M, int64_t N, int64_t K, int withhold, uint64_t timeout_cycles,
+                                void *stream);
 
 /*
  * layer_norm_fwd -- layer norm over rows of `dim` elements (the norm in front of
