@@ -1029,9 +1029,11 @@ extern "C" int64_t layer_norm_bwd_workspace(int64_t rows, int64_t dim)
     return 2 * layer_norm_parts(rows, dim, dev.sm_count) * dim * static_cast<int64_t>(sizeof(float));
 }
 
-extern "C" int layer_norm_bwd(const void *dY, const void *X, const void *gamma, const float *mean, const float *rstd,
-                              void *dX, void *dgamma, void *dbeta, int64_t rows, int64_t dim, int xtype, int wtype,
-                              void *workspace, int64_t workspace_bytes, void *stream)
+namespace {
+
+int run_layer_norm_bwd(const void *dY, const void *X, const void *gamma, const float *mean, const float *rstd, void *dX,
+                       void *dgamma, void *dbeta, int64_t rows, int64_t dim, int xtype, int wtype, void *workspace,
+                       int64_t workspace_bytes, void *stream, int withhold, uint64_t timeout_cycles)
 {
     int st = check_norm_args(rows, dim, xtype, wtype);
     if (st != GEMM_OK) return st;
@@ -1092,7 +1094,30 @@ extern "C" int layer_norm_bwd(const void *dY, const void *X, const void *gamma, 
     a.stream = s;
     a.status = status_word(dev.device);
     if (a.status == nullptr) return GEMM_ERR_CUDA;
+    a.withhold = withhold;
+    a.timeout_cycles = timeout_cycles;
     return launch_layer_norm_bwd(a);
+}
+
+}  // namespace
+
+extern "C" int layer_norm_bwd(const void *dY, const void *X, const void *gamma, const float *mean, const float *rstd,
+                              void *dX, void *dgamma, void *dbeta, int64_t rows, int64_t dim, int xtype, int wtype,
+                              void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return run_layer_norm_bwd(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, rows, dim, xtype, wtype, workspace,
+                              workspace_bytes, stream, 0, 0);
+}
+
+extern "C" int layer_norm_bwd_selftest_timeout(const void *dY, const void *X, const float *mean, const float *rstd,
+                                               void *dX, int64_t rows, int64_t dim, int xtype,
+                                               uint64_t timeout_cycles, void *stream)
+{
+    if (rows == 0 || dim == 0) return reject(GEMM_ERR_INVALID_ARG, "an empty problem launches no kernel");
+    if (timeout_cycles < (1ull << 16) || timeout_cycles > (1ull << 32))
+        return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
+    return run_layer_norm_bwd(dY, X, nullptr, mean, rstd, dX, nullptr, nullptr, rows, dim, xtype, xtype, nullptr, 0,
+                              stream, 1, timeout_cycles);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

@@ -28,6 +28,8 @@ struct LayerNormArgs {
     int sm_count = 0, device = 0;
     cudaStream_t stream = nullptr;
     unsigned long long *status = nullptr;       // device status word
+    int withhold = 0;                           // test hook (layer_norm_bwd_selftest_timeout)
+    uint64_t timeout_cycles = 0;                // 0: the normal budget
 };
 
 int launch_layer_norm_fwd(const LayerNormArgs &a);

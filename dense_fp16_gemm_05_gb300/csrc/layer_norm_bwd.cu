@@ -31,6 +31,8 @@ struct BwdParams {
     int32_t parts;    // blocks
     float inv_dim;
     int32_t stages;   // rows under way per block (the ring kernel)
+    int32_t withhold; // test hook: 1 = the ring's rows are not loaded; 0 in every normal call
+    uint64_t limit;   // SM clocks of a wait (the ring kernel)
     unsigned long long *status;
     W *dgamma, *dbeta;
 };
@@ -274,7 +276,6 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
     const int t = static_cast<int>(threadIdx.x), tpr = ln_threads<TPR>();
     const uint32_t row_bytes = ring_row_bytes<T, V>(p.dim);
     const uint32_t ring_base = smem_addr(ring), full0 = smem_addr(full_mem);
-    constexpr uint64_t kLimit = 1ull << 31;   // about a second
     if (t == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(full0 + 8u * s, 1);
         failed[0] = failed[1] = 0;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
     // Rows as unsigned 32-bit numbers: the ones past the end may pass 2^31.
     const uint32_t step = gridDim.x, rows = static_cast<uint32_t>(p.rows);
     uint32_t row = blockIdx.x;
-    if (t == 0)
+    if (t == 0 && p.withhold == 0)
         for (int s = 0; s < p.stages && row + static_cast<uint32_t>(s) * step < rows; ++s)
             fetch(row + static_cast<uint32_t>(s) * step, s);
 
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), ring_blocks(TPR, V * NV)) la
         if (!mbar_try_wait(full0 + 8u * static_cast<uint32_t>(s), ph)) {
             const long long t0 = clock64();
             while (!mbar_try_wait(full0 + 8u * static_cast<uint32_t>(s), ph))
-                if (static_cast<uint64_t>(clock64() - t0) > kLimit) {
+                if (static_cast<uint64_t>(clock64() - t0) > p.limit) {
                     failed[it] = 1;
                     break;
                 }
@@ -752,6 +753,8 @@ int backward(const LayerNormArgs &a)
     p.dim = static_cast<int32_t>(a.dim);
     p.parts = static_cast<int32_t>(layer_norm_parts(a.rows, a.dim, a.sm_count));
     p.inv_dim = 1.0f / static_cast<float>(a.dim);
+    p.withhold = a.withhold;
+    p.limit = a.timeout_cycles ? a.timeout_cycles : 1ull << 31;   // about a second
     p.status = a.status;
     p.dgamma = static_cast<W *>(a.dgamma);
     p.dbeta = static_cast<W *>(a.dbeta);

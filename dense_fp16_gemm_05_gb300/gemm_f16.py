@@ -123,6 +123,8 @@ def lib() -> ctypes.CDLL:
     L.layer_norm_fwd.restype = ci
     L.layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]
     L.layer_norm_bwd.restype = ci
+    L.layer_norm_bwd_selftest_timeout.argtypes = [vp, vp, vp, vp, vp, i64, i64, ci, ctypes.c_uint64, vp]
+    L.layer_norm_bwd_selftest_timeout.restype = ci
     L.layer_norm_bwd_workspace.argtypes = [i64, i64]
     L.layer_norm_bwd_workspace.restype = i64
     pi = ctypes.POINTER(ctypes.c_int)

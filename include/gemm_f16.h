@@ -442,6 +442,19 @@ int layer_norm_bwd(const void *dY, const void *X, const void *gamma, const float
  * device, or a negative status. */
 int64_t layer_norm_bwd_workspace(int64_t rows, int64_t dim);
 
+/*
+ * layer_norm_bwd_selftest_timeout -- exercises the bounded wait of the kernel
+ * that takes rows through a ring of bulk copies, rows of more than 512 elements
+ * (1024 where they are not on the 16-byte grid) up to about 16384 (a test hook as
+ * gemm_f16_selftest_timeout).  No row is loaded and a wait may take
+ * `timeout_cycles` SM clocks (2^16 .. 2^32): every block records the site (9) and
+ * leaves without writing dX.  The next gemm_f16_check returns GEMM_ERR_TIMEOUT.
+ * Other rows wait for nothing: there the call computes dX.  Arguments are
+ * validated as for layer_norm_bwd without weights.
+ */
+int layer_norm_bwd_selftest_timeout(const void *dY, const void *X, const float *mean, const float *rstd, void *dX,
+                                    int64_t rows, int64_t dim, int xtype, uint64_t timeout_cycles, void *stream);
+
 /* Launch geometry of gemm_fp8_block_scaled for this problem on the current
  * device: persistent grid in CTAs (CTA pairs over 256 x 256 output tiles) and
  * the number of tiles.  Either pointer may be NULL.  Launches nothing. */
