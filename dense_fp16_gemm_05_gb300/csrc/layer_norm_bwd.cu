@@ -35,6 +35,7 @@ struct BwdParams {
     uint64_t limit;   // SM clocks of a wait (the ring kernel)
     unsigned long long *status;
     W *dgamma, *dbeta;
+    int32_t sm_count;
 };
 
 // Threads of a block, and blocks per SM: some 1024 threads, so that the loads of
@@ -595,7 +596,7 @@ int finish(const BwdParams<T, W> &p, cudaStream_t stream)
     if (p.part == nullptr) return GEMM_OK;
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.dim) + 31) / 32), 2, 1);
     const float *part = p.part;
-    if (p.parts > 320)
+    if (p.parts > 2 * p.sm_count)
         return ln_launch(layer_norm_bwd_finish<W, 32>, grid, 1024, stream, part, p.dgamma, p.dbeta, p.parts, p.dim);
     return ln_launch(layer_norm_bwd_finish<W, 16>, grid, 512, stream, part, p.dgamma, p.dbeta, p.parts, p.dim);
 }
@@ -758,6 +759,7 @@ int backward(const LayerNormArgs &a)
     p.status = a.status;
     p.dgamma = static_cast<W *>(a.dgamma);
     p.dbeta = static_cast<W *>(a.dbeta);
+    p.sm_count = a.sm_count;
     const uintptr_t x_bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
                              reinterpret_cast<uintptr_t>(a.Y) |
                              (static_cast<uintptr_t>(a.dim) * sizeof(T));

@@ -44,6 +44,19 @@ def test_parts_of_one_row_are_added_exactly(g, rows, dim):
     check(db, dy.double())
 
 
+@pytest.mark.parametrize("over", [0, 1, 9])
+def test_either_side_of_two_parts_per_sm(g, over):
+    # a part per eight rows: where the second kernel's blocks change from 16 to 32 warps
+    parts = 2 * torch.cuda.get_device_properties(DEV).multi_processor_count + over
+    gen = torch.Generator(device=DEV).manual_seed(over)
+    dy = torch.randint(-1000, 1001, (8 * parts, 768), generator=gen, device=DEV).float()   # sums exact in fp32
+    x = torch.ones_like(dy)
+    mean, rstd = torch.zeros(8 * parts, device=DEV), torch.ones(8 * parts, device=DEV)
+    assert g.layer_norm_bwd_workspace(8 * parts, 768) == 8 * parts * 768
+    _, dg, db = g.layer_norm_bwd(dy, x, mean, rstd)
+    assert torch.equal(dg.double(), dy.double().sum(0)) and torch.equal(dg, db)
+
+
 def test_sums_that_cancel(g):
     # 2^24 and its negative around small terms, which plain fp32 sums lose
     gen = torch.Generator().manual_seed(3)
