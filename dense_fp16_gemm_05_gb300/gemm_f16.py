@@ -248,18 +248,36 @@ def _call(fn, what: str, device: torch.device, stream, *args):
 # torch's allocation of a strided CUDA tensor on the current device without the
 # argument parser and dispatcher of torch.empty: 1.4 us instead of 3 us between
 # launches, for calls that are bound by the host.  The same allocator, so stream
-# order and graph pools are the same.
-try:
-    _empty_strided_cuda = torch._C._dynamo.guards._empty_strided_cuda
-except AttributeError:
-    _empty_strided_cuda = None
+# order and graph pools are the same; dispatch modes and the deterministic fill of
+# new memory do not see these tensors, which the launch that follows writes.  The
+# name is not a public one: it is tried once before it is relied on.
+def _find_empty_strided():
+    """The function, or None where it is missing or does not do what _new needs."""
+    try:
+        f = torch._C._dynamo.guards._empty_strided_cuda
+        t = f((2, 3), (3, 1), torch.float16)
+        if (tuple(t.shape) == (2, 3) and t.stride() == (3, 1) and t.dtype == torch.float16
+                and t.device == torch.device("cuda", _current_device())):
+            return f
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return None
+
+
+_empty_strided_cuda = False   # not looked for yet
 
 
 def _new(shape, dtype, device, stream=None) -> torch.Tensor:
     """torch.empty(shape) for one to three sizes, an output of a launch on ``stream``."""
     if stream is not None:
         return _new_on(stream, shape, dtype, device)
-    if _empty_strided_cuda is None or device.index is None or device.index != _current_device():
+    if device.index is None or device.index != _current_device():
+        return torch.empty(shape, dtype=dtype, device=device)
+    global _empty_strided_cuda
+    if not _empty_strided_cuda:
+        if _empty_strided_cuda is False:
+            _empty_strided_cuda = _find_empty_strided()
+            return _new(shape, dtype, device)
         return torch.empty(shape, dtype=dtype, device=device)
     n = len(shape)   # plain tuples below: the function takes no torch.Size
     if n == 2:
