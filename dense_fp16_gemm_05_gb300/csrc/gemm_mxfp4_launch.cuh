@@ -1,6 +1,5 @@
 // gemm_mxfp4_launch.cuh -- internal interface between the C ABI (gemm_f16.cu)
-// and the 4-bit microscaled kernels (gemm_mxfp4.cu, mxfp4_quantize.cu) and the
-// layer norm kernels (layer_norm.cu).
+// and the 4-bit microscaled kernels (gemm_mxfp4.cu, mxfp4_quantize.cu).
 #pragma once
 
 #include "gemm_launch.cuh"
