@@ -674,9 +674,10 @@ int launch_ring(BwdParams<T, W> p, int device, int sm_count, cudaStream_t stream
     const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
     const int64_t stage = 2 * static_cast<int64_t>(ring_row_bytes<T, V>(p.dim));
     const int64_t fit = budget / stage;
-    // Two rows always fit but in the longest fp32 rows: a row has at most eight
-    // elements per thread and 1024 threads share the SM, or is at most 8192 long.
-    if constexpr (TPR == 1024 || TPR == -1024)
+    // Two rows always fit but in fp32 rows of 16 elements in each of 1024 threads:
+    // others have eight elements per thread and 1024 threads share the SM, or are
+    // at most 8192 long, or of 16-bit elements.
+    if constexpr (sizeof(T) == 4 && V * NV > 8 && (TPR == 1024 || TPR == -1024))
         if (fit < 2) return launch_one<T, W, V, NV, TPR>(p, stream);
     p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
     const int64_t wave = static_cast<int64_t>(fit_blocks) * sm_count;
