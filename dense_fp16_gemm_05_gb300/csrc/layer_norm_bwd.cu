@@ -8,7 +8,8 @@
 // rows; a thread always has the same columns, so the columns' sums stay in its
 // registers (fp32) until the block's last row, and only then one partial sum
 // per block and column goes to the workspace.  A second kernel adds the blocks'
-// partial sums in a fixed order: no atomics, the same bits every time.
+// partial sums in a fixed order and keeps what the additions lose: no atomics, the
+// same bits every time.
 #include "layer_norm.cuh"
 
 #include <atomic>
@@ -588,8 +589,8 @@ __global__ void __launch_bounds__(NW * 32) layer_norm_bwd_finish(const float *__
 
 // The second kernel, if the weights' gradients are wanted.  More than two parts
 // per SM come with short rows, so few columns for the SMs to share: 32 warps each
-// (8192 x 768 fp16, both kernels: 21.2 us with 16 warps, 19.7 us); with fewer parts
-// the smaller blocks start sooner (64 x 4096: 8.2 us, 13.4 us with 32 warps).
+// (8192 x 768 fp16, both kernels: 21.4 us with 16 warps, 19.8 us); with fewer parts
+// the smaller blocks start sooner (64 x 4096: 8.0 us, 12.5 us with 32 warps).
 template <class T, class W>
 int finish(const BwdParams<T, W> &p, cudaStream_t stream)
 {

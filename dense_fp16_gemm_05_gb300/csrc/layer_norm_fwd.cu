@@ -207,7 +207,7 @@ int launch_packs(const FwdParams<T, W> &p, cudaStream_t stream)
     } else {
         // Narrow loads are bound by instructions, so no more threads than eight
         // elements each take (16384 x 4097 fp16: 148 us with the next power of 2,
-        // 103 us this way, with two blocks per SM).
+        // 104 us this way, with two blocks per SM).
         if (packs <= 512 * N) return launch_one<T, W, V, N, -512>(p, stream);
         if (packs <= 1024 * N) return launch_one<T, W, V, N, -1024>(p, stream);
         if (packs <= 1024 * 2 * N) return launch_one<T, W, V, 2 * N, -1024>(p, stream);

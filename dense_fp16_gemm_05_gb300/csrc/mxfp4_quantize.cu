@@ -8,7 +8,8 @@
 //
 // A block of zeros gets scale byte 0; a block that holds an infinity or a NaN,
 // which E2M1 lacks, gets the NaN scale byte 0xFF and zero codes, so that it
-// does not vanish from a product.  floor(log2) is read from the exponent bits
+// does not vanish from a product (with the fused ReLU it does: R(NaN) is +0 in
+// every GEMM of the library).  floor(log2) is read from the exponent bits
 // of the block's largest magnitude and 2^-e is a power of two in fp32, so the
 // only rounding is the conversion to E2M1.
 #include <cuda_bf16.h>

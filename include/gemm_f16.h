@@ -408,8 +408,10 @@ int gemm_mxfp4_selftest_timeout(const void *A, const uint8_t *SA, const void *W,
  *   mean, rstd   NULL (not kept) or rows floats, written, for layer_norm_bwd
  *   eps          finite, >= 0
  *
- * Buffers are aligned to their element (16-byte alignment and rows of a
- * multiple of 16 bytes select the vectorised path); outputs overlap neither
+ * Buffers are aligned to their element (16-byte alignment of all of them, the
+ * weights too, and rows of a multiple of 16 bytes select the vectorised path;
+ * 16-bit rows and weights on the grid of two elements go by pairs, anything
+ * else element by element); outputs overlap neither
  * inputs nor each other.  rows == 0 or dim == 0: no-op.  Only enqueues on `stream`.
  */
 int layer_norm_fwd(const void *X, const void *gamma, const void *beta, void *Y, float *mean, float *rstd,
@@ -422,7 +424,8 @@ int layer_norm_fwd(const void *X, const void *gamma, const void *beta, void *Y, 
  *   dX = rstd (g - mean_row(g) - z mean_row(g z)),  dgamma = sum_rows dY z,  dbeta = sum_rows dY
  *
  * in fp32, each output rounded once; the sums over rows are taken in a fixed
- * order (equal calls give equal bits on one GPU model).
+ * order (equal calls give equal bits on one GPU model): a block's rows in fp32,
+ * then the blocks' sums without loss, rounded once.
  *
  *   dY, X, gamma, mean, rstd  as given to and kept by layer_norm_fwd
  *   dX             (rows, dim) of type xtype
