@@ -846,6 +846,8 @@ def _launch_stream(stream, device) -> torch.cuda.Stream:
         return torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream
+    if int(stream) == 0:   # the default stream; of a null handle ExternalStream makes a new one
+        return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 

@@ -112,3 +112,22 @@ def test_inputs_dropped_right_after_the_call(g):
             torch.full_like(t, 7.0)
     torch.cuda.synchronize()
     assert g.check() == g.GEMM_OK and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("name", ["mxfp4_quantize", "layer_norm_bwd", "gemm_f16", "attention_fwd"])
+@pytest.mark.parametrize("kind", ["null", "raw"])
+def test_raw_handles(g, name, kind):
+    call = calls(g)[name]
+    want = call(None)
+    want = want if isinstance(want, tuple) else (want,)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(0 if kind == "null" else side.cuda_stream)
+    got = got if isinstance(got, tuple) else (got,)
+    if name == "layer_norm_bwd":
+        assert g._launch_stream(0, DEV) == torch.cuda.default_stream(DEV)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        if name == "mxfp4_quantize" and a.dim() == 3:
+            a, b = g.mxfp4_row_scales(a, 64, 512), g.mxfp4_row_scales(b, 64, 512)
+        assert torch.equal(a, b)

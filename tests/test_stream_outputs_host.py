@@ -117,3 +117,10 @@ def test_inputs_are_recorded_on_the_launch_stream(made, monkeypatch, name):
     assert kept
     for t in kept:
         assert any(u is t and s is LAUNCH for u, s in made.recorded)
+
+
+def test_a_null_handle_is_the_default_stream(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: LAUNCH)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: (handle, device))
+    assert g._launch_stream(0, "cuda:0") is LAUNCH
+    assert g._launch_stream(ctypes.c_void_p(8).value, "cuda:0") == (8, "cuda:0")
