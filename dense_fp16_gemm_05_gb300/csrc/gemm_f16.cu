@@ -19,10 +19,12 @@
 
 #include "gemm_f16.h"
 #include "attention_launch.cuh"
+#include "feed_forward_launch.cuh"
 #include "gemm_fp8_launch.cuh"
 #include "gemm_launch.cuh"
 #include "gemm_mxfp4_launch.cuh"
 #include "layer_norm.cuh"
+#include "rms_norm.cuh"
 
 using namespace gemm_sm103;
 
@@ -1118,6 +1120,337 @@ extern "C" int layer_norm_bwd_selftest_timeout(const void *dY, const void *X, co
         return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
     return run_layer_norm_bwd(dY, X, nullptr, mean, rstd, dX, nullptr, nullptr, rows, dim, xtype, xtype, nullptr, 0,
                               stream, 1, timeout_cycles);
+}
+
+namespace {
+
+// An output that may take the place of one of the call's inputs: the same
+// address, or no overlap.
+bool in_place_or_apart(const void *out, uint64_t out_bytes, const void *in, uint64_t in_bytes)
+{
+    return in == nullptr || out == in || !ranges_overlap(out, out_bytes, in, in_bytes);
+}
+
+// What rms_norm_fwd and rms_norm_fp8 share: with Q the output is FP8.
+int run_rms_norm_fwd(const void *X, const void *R, const void *gamma, void *H, void *Y, void *Q, void *S, float *rstd,
+                     int64_t rows, int64_t dim, float eps, int xtype, int wtype, int pow2, void *stream)
+{
+    int st = check_norm_args(rows, dim, xtype, wtype);
+    if (st != GEMM_OK) return st;
+    if (!std::isfinite(eps) || eps < 0.0f) return reject(GEMM_ERR_INVALID_ARG, "eps is negative or not finite");
+    if (pow2 != 0 && pow2 != 1) return reject(GEMM_ERR_INVALID_ARG, "pow2 is not 0 or 1");
+    if ((R == nullptr) != (H == nullptr))
+        return reject(GEMM_ERR_INVALID_ARG, "one of R and H is NULL and the other is not");
+    if (rows == 0 || dim == 0) return GEMM_OK;
+    if (X == nullptr || (Y == nullptr && Q == nullptr) || (Q != nullptr && S == nullptr))
+        return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint32_t el = type_bytes(xtype);
+    const uint64_t n = static_cast<uint64_t>(rows) * static_cast<uint64_t>(dim), x_bytes = n * el;
+    const uint64_t s_bytes = static_cast<uint64_t>(rows) * static_cast<uint64_t>((dim + 127) / 128) * (pow2 ? 1u : 4u);
+    // H takes the place of X or R, or overlaps nothing: left out here where it does.
+    const bool in_place = H != nullptr && (H == X || H == R);
+    const NormBuffer b[] = {{X, x_bytes, el, in_place && H == X},
+                            {R, x_bytes, el, in_place && H == R},
+                            {gamma, static_cast<uint64_t>(dim) * type_bytes(wtype), type_bytes(wtype), false},
+                            {in_place ? nullptr : H, x_bytes, el, true},
+                            {Y, x_bytes, el, true},
+                            {Q, n, 1, true},
+                            {S, s_bytes, pow2 ? 1u : 4u, true},
+                            {rstd, static_cast<uint64_t>(rows) * sizeof(float), 4, true}};
+    if (in_place && X == R) {
+        // The stream doubled in place: X and R are one buffer, written.
+        const NormBuffer one[] = {{X, x_bytes, el, true}, b[2], b[4], b[5], b[6], b[7]};
+        if ((st = check_norm_buffers(one, 6, dev.device)) != GEMM_OK) return st;
+    } else if ((st = check_norm_buffers(b, 8, dev.device)) != GEMM_OK) {
+        return st;
+    }
+    RmsNormArgs a;
+    a.X = X;
+    a.R = R;
+    a.gamma = gamma;
+    a.H = H;
+    a.Y = Y;
+    a.Q = Q;
+    a.S = S;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.dim = dim;
+    a.eps = eps;
+    a.xtype = xtype;
+    a.wtype = wtype;
+    a.pow2 = pow2;
+    a.sm_count = dev.sm_count;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_rms_norm_fwd(a);
+}
+
+uint64_t rms_norm_bwd_bytes(int64_t rows, int64_t dim, int sm_count)
+{
+    return static_cast<uint64_t>(layer_norm_parts(rows, dim, sm_count)) * static_cast<uint64_t>(dim) * sizeof(float);
+}
+
+int run_rms_norm_bwd(const void *dY, const void *H, const void *gamma, const float *rstd, const void *dH, void *dX,
+                     void *dgamma, int64_t rows, int64_t dim, int xtype, int wtype, void *workspace,
+                     int64_t workspace_bytes, void *stream, int withhold, uint64_t timeout_cycles)
+{
+    int st = check_norm_args(rows, dim, xtype, wtype);
+    if (st != GEMM_OK) return st;
+    if (dim == 0) return GEMM_OK;
+    if (rows > 0 && (dY == nullptr || H == nullptr || rstd == nullptr || dX == nullptr))
+        return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    if (rows == 0 && dgamma == nullptr) return GEMM_OK;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint32_t el = type_bytes(xtype), wel = type_bytes(wtype);
+    const uint64_t x_bytes = static_cast<uint64_t>(rows) * static_cast<uint64_t>(dim) * el;
+    const uint64_t w_bytes = static_cast<uint64_t>(dim) * wel;
+    if (rows == 0) {
+        // Empty sums.
+        const NormBuffer b[] = {{dgamma, w_bytes, wel, true}};
+        if ((st = check_norm_buffers(b, 1, dev.device)) != GEMM_OK) return st;
+        if (cudaMemsetAsync(dgamma, 0, w_bytes, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        return GEMM_OK;
+    }
+    const uint64_t need = dgamma ? rms_norm_bwd_bytes(rows, dim, dev.sm_count) : 0u;
+    if (dgamma && (workspace == nullptr || workspace_bytes < 0 || static_cast<uint64_t>(workspace_bytes) < need))
+        return reject(GEMM_ERR_INVALID_ARG, "the workspace is smaller than rms_norm_bwd_workspace says");
+    const NormBuffer b[] = {{dY, x_bytes, el, false},
+                            {H, x_bytes, el, false},
+                            {gamma, w_bytes, wel, false},
+                            {rstd, static_cast<uint64_t>(rows) * sizeof(float), 4, false},
+                            {dH, x_bytes, el, false},
+                            {dX, x_bytes, el, true},
+                            {dgamma, w_bytes, wel, true},
+                            {dgamma ? workspace : nullptr, need, 16, true}};
+    if ((st = check_norm_buffers(b, 8, dev.device)) != GEMM_OK) return st;
+    RmsNormArgs a;
+    a.dY = dY;
+    a.X = H;
+    a.gamma = gamma;
+    a.rstd = const_cast<float *>(rstd);
+    a.dH = dH;
+    a.dX = dX;
+    a.dgamma = dgamma;
+    a.workspace = static_cast<float *>(workspace);
+    a.rows = rows;
+    a.dim = dim;
+    a.xtype = xtype;
+    a.wtype = wtype;
+    a.sm_count = dev.sm_count;
+    a.device = dev.device;
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.status = status_word(dev.device);
+    if (a.status == nullptr) return GEMM_ERR_CUDA;
+    a.withhold = withhold;
+    a.timeout_cycles = timeout_cycles;
+    return launch_rms_norm_bwd(a);
+}
+
+}  // namespace
+
+extern "C" int rms_norm_fwd(const void *X, const void *R, const void *gamma, void *H, void *Y, float *rstd,
+                            int64_t rows, int64_t dim, float eps, int xtype, int wtype, void *stream)
+{
+    if (Y == nullptr && rows > 0 && dim > 0) return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    return run_rms_norm_fwd(X, R, gamma, H, Y, nullptr, nullptr, rstd, rows, dim, eps, xtype, wtype, 0, stream);
+}
+
+extern "C" int rms_norm_fp8(const void *X, const void *R, const void *gamma, void *H, void *Q, void *S, float *rstd,
+                            int64_t rows, int64_t dim, float eps, int xtype, int wtype, int pow2, void *stream)
+{
+    if (Q == nullptr && rows > 0 && dim > 0) return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    return run_rms_norm_fwd(X, R, gamma, H, nullptr, Q, S, rstd, rows, dim, eps, xtype, wtype, pow2, stream);
+}
+
+extern "C" int64_t rms_norm_bwd_workspace(int64_t rows, int64_t dim)
+{
+    int st = check_sizes(rows, dim, 0, 0);
+    if (st != GEMM_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    return static_cast<int64_t>(rms_norm_bwd_bytes(rows, dim, dev.sm_count));
+}
+
+extern "C" int rms_norm_bwd(const void *dY, const void *H, const void *gamma, const float *rstd, const void *dH,
+                            void *dX, void *dgamma, int64_t rows, int64_t dim, int xtype, int wtype, void *workspace,
+                            int64_t workspace_bytes, void *stream)
+{
+    return run_rms_norm_bwd(dY, H, gamma, rstd, dH, dX, dgamma, rows, dim, xtype, wtype, workspace, workspace_bytes,
+                            stream, 0, 0);
+}
+
+extern "C" int rms_norm_bwd_selftest_timeout(const void *dY, const void *H, const float *rstd, void *dX, int64_t rows,
+                                             int64_t dim, int xtype, uint64_t timeout_cycles, void *stream)
+{
+    if (rows == 0 || dim == 0) return reject(GEMM_ERR_INVALID_ARG, "an empty problem launches no kernel");
+    if (timeout_cycles < (1ull << 16) || timeout_cycles > (1ull << 32))
+        return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
+    return run_rms_norm_bwd(dY, H, nullptr, rstd, nullptr, dX, nullptr, rows, dim, xtype, xtype, nullptr, 0, stream, 1,
+                            timeout_cycles);
+}
+
+extern "C" int fp8_quantize(const void *X, int type, void *Q, void *S, int64_t rows, int64_t K, int block_rows,
+                            int pow2, void *stream)
+{
+    int st = check_sizes(rows, 0, K, 0);
+    if (st != GEMM_OK) return st;
+    const uint32_t el = type_bytes(type);
+    if (el == 0) return reject(GEMM_ERR_INVALID_ARG, "type is not a gemm_f16_type");
+    if (block_rows != 1 && block_rows != 128) return reject(GEMM_ERR_INVALID_ARG, "block_rows is not 1 or 128");
+    if (pow2 != 0 && pow2 != 1) return reject(GEMM_ERR_INVALID_ARG, "pow2 is not 0 or 1");
+    if (rows == 0 || K == 0) return GEMM_OK;
+    const int64_t blocks = (rows + block_rows - 1) / block_rows * ((K + 127) / 128);
+    if (blocks > INT32_MAX) return reject(GEMM_ERR_INVALID_ARG, "more than INT32_MAX blocks");
+    if (X == nullptr || Q == nullptr || S == nullptr) return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint64_t n = static_cast<uint64_t>(rows) * static_cast<uint64_t>(K);
+    const uint32_t sel = pow2 ? 1u : 4u;
+    const NormBuffer b[] = {{X, n * el, el, false}, {Q, n, 1, true}, {S, static_cast<uint64_t>(blocks) * sel, sel, true}};
+    if ((st = check_norm_buffers(b, 3, dev.device)) != GEMM_OK) return st;
+    Fp8QuantArgs a;
+    a.X = X;
+    a.Q = Q;
+    a.S = S;
+    a.rows = rows;
+    a.K = K;
+    a.type = type;
+    a.block_rows = block_rows;
+    a.pow2 = pow2;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_fp8_quantize(a);
+}
+
+extern "C" int dropout_philox(const void *X, const void *R, void *Y, int64_t n, int type, double p, uint64_t seed,
+                              uint64_t offset, const void *offset_ptr, void *stream)
+{
+    const uint32_t el = type_bytes(type);
+    if (n < 0) return reject(GEMM_ERR_INVALID_ARG, "a size is negative");
+    if (el == 0) return reject(GEMM_ERR_INVALID_ARG, "type is not a gemm_f16_type");
+    if (!(p >= 0.0 && p < 1.0)) return reject(GEMM_ERR_INVALID_ARG, "p is not in [0, 1)");
+    if (n == 0) return GEMM_OK;
+    if (n > INT64_MAX / 8) return reject(GEMM_ERR_INVALID_ARG, "n is beyond any memory");
+    if (X == nullptr || Y == nullptr) return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    DeviceInfo dev;
+    int st = current_device_info(&dev);
+    if (st != GEMM_OK) return st;
+    const uint64_t bytes = static_cast<uint64_t>(n) * el;
+    const NormBuffer b[] = {{X, bytes, el, false}, {R, bytes, el, false}, {Y, bytes, el, false}, {offset_ptr, 8, 8, false}};
+    if ((st = check_norm_buffers(b, 4, dev.device)) != GEMM_OK) return st;
+    if (!in_place_or_apart(Y, bytes, X, bytes) || !in_place_or_apart(Y, bytes, R, bytes) ||
+        (offset_ptr != nullptr && ranges_overlap(Y, bytes, offset_ptr, 8)))
+        return reject(GEMM_ERR_INVALID_ARG, "Y overlaps another buffer without being X or R");
+    DropoutArgs a;
+    a.X = X;
+    a.R = R;
+    a.Y = Y;
+    a.n = n;
+    a.type = type;
+    a.p = p;
+    a.seed = seed;
+    a.offset = offset;
+    a.offset_ptr = static_cast<const uint64_t *>(offset_ptr);
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_dropout(a);
+}
+
+namespace {
+
+int check_w4_args(int64_t N, int64_t K, int group, int stype)
+{
+    const int st = check_sizes(N, 0, K, 0);
+    if (st != GEMM_OK) return st;
+    if (group != 32 && group != 64 && group != 128) return reject(GEMM_ERR_INVALID_ARG, "group is not 32, 64 or 128");
+    if (stype != GEMM_TYPE_F16 && stype != GEMM_TYPE_BF16)
+        return reject(GEMM_ERR_INVALID_ARG, "the scales' type is not a 16-bit gemm_f16_type");
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z, int64_t N, int64_t K, int group,
+                           int stype, int trans, void *stream)
+{
+    int st = check_w4_args(N, K, group, stype);
+    if (st != GEMM_OK) return st;
+    const uint32_t el = type_bytes(type);
+    if (el == 0) return reject(GEMM_ERR_INVALID_ARG, "type is not a gemm_f16_type");
+    if (trans != 0 && trans != 1) return reject(GEMM_ERR_INVALID_ARG, "trans is not 0 or 1");
+    if (N == 0 || K == 0) return GEMM_OK;
+    if (W == nullptr || Q == nullptr || S == nullptr) return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint64_t values = static_cast<uint64_t>(w4_group_values(N, K, group));
+    const NormBuffer b[] = {{W, static_cast<uint64_t>(N) * static_cast<uint64_t>(K) * el, el, false},
+                            {Q, static_cast<uint64_t>(w4_code_bytes(N, K)), 16, true},
+                            {S, values * 2u, 2, true},
+                            {Z, values, 1, true}};
+    if ((st = check_norm_buffers(b, 4, dev.device)) != GEMM_OK) return st;
+    W4QuantArgs a;
+    a.W = W;
+    a.Q = Q;
+    a.S = S;
+    a.Z = Z;
+    a.N = N;
+    a.K = K;
+    a.type = type;
+    a.stype = stype;
+    a.group = group;
+    a.trans = trans;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_w4_quantize(a);
+}
+
+extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M,
+                         int64_t N, int64_t K, int group, int relu, void *stream)
+{
+    int st = check_w4_args(N, K, group, type);
+    if (st != GEMM_OK) return st;
+    if ((st = check_sizes(M, N, K, relu)) != GEMM_OK) return st;
+    if (M > GEMM_W4_MAX_ROWS) return reject(GEMM_ERR_INVALID_ARG, "M is above GEMM_W4_MAX_ROWS");
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (C == nullptr || (K > 0 && (X == nullptr || Q == nullptr || S == nullptr)))
+        return reject(GEMM_ERR_INVALID_ARG, "a buffer pointer is NULL");
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != GEMM_OK) return st;
+    const uint64_t c_bytes = static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * 2u;
+    if (K == 0) {
+        // Empty sum: every output is R(+0) = +0.
+        if ((st = check_device_buffer_fast(C, c_bytes, dev.device, 2)) != GEMM_OK) return st;
+        if (cudaMemsetAsync(C, 0, c_bytes, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        return GEMM_OK;
+    }
+    const uint64_t values = static_cast<uint64_t>(w4_group_values(N, K, group));
+    const NormBuffer b[] = {{X, static_cast<uint64_t>(M) * static_cast<uint64_t>(K) * 2u, 2, false},
+                            {Q, static_cast<uint64_t>(w4_code_bytes(N, K)), 16, false},
+                            {S, values * 2u, 2, false},
+                            {Z, values, 1, false},
+                            {C, c_bytes, 2, true}};
+    if ((st = check_norm_buffers(b, 5, dev.device)) != GEMM_OK) return st;
+    W4LinearArgs a;
+    a.X = X;
+    a.Q = Q;
+    a.S = S;
+    a.Z = Z;
+    a.C = C;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.type = type;
+    a.group = group;
+    a.relu = relu;
+    a.sm_count = dev.sm_count;
+    a.device = dev.device;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_linear_w4(a);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

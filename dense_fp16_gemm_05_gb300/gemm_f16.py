@@ -127,6 +127,25 @@ def lib() -> ctypes.CDLL:
     L.layer_norm_bwd_selftest_timeout.restype = ci
     L.layer_norm_bwd_workspace.argtypes = [i64, i64]
     L.layer_norm_bwd_workspace.restype = i64
+    u64 = ctypes.c_uint64
+    L.rms_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, cf, ci, ci, vp]
+    L.rms_norm_fwd.restype = ci
+    L.rms_norm_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, cf, ci, ci, ci, vp]
+    L.rms_norm_fp8.restype = ci
+    L.rms_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]
+    L.rms_norm_bwd.restype = ci
+    L.rms_norm_bwd_selftest_timeout.argtypes = [vp, vp, vp, vp, i64, i64, ci, u64, vp]
+    L.rms_norm_bwd_selftest_timeout.restype = ci
+    L.rms_norm_bwd_workspace.argtypes = [i64, i64]
+    L.rms_norm_bwd_workspace.restype = i64
+    L.fp8_quantize.argtypes = [vp, ci, vp, vp, i64, i64, ci, ci, vp]
+    L.fp8_quantize.restype = ci
+    L.dropout_philox.argtypes = [vp, vp, vp, i64, ci, ctypes.c_double, u64, u64, vp, vp]
+    L.dropout_philox.restype = ci
+    L.w4_quantize.argtypes = [vp, ci, vp, vp, vp, i64, i64, ci, ci, ci, vp]
+    L.w4_quantize.restype = ci
+    L.linear_w4.argtypes = [vp, ci, vp, vp, vp, vp, i64, i64, i64, ci, ci, vp]
+    L.linear_w4.restype = ci
     pi = ctypes.POINTER(ctypes.c_int)
     L.gemm_fp8_launch_info.argtypes = [i64, i64, i64, pi, pi]
     L.gemm_fp8_launch_info.restype = ci
@@ -831,6 +850,322 @@ def layer_norm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: 
           _ptr(workspace) if weights else None, ws_bytes)
     _used_on(stream, dev, dY, X, mean, rstd, gamma, dX, dgamma, dbeta, workspace if weights else None)
     return dX, dgamma, dbeta
+
+
+def _fp8_outputs(shape, block_rows: int, pow2: bool, Q, S, dev, stream):
+    """Codes of `shape` (made or checked) and their scales, one per block_rows x 128 elements."""
+    lead = tuple(shape[:-1])
+    if block_rows != 1:
+        lead = (-(-lead[0] // block_rows),)
+    s_shape = (*lead, -(-shape[-1] // FP8_BLOCK))
+    s_type = torch.uint8 if pow2 else torch.float32
+    if Q is None:
+        Q = _new(shape, torch.float8_e4m3fn, dev, stream)
+    else:
+        _check_like(Q, "Q", torch.float8_e4m3fn, shape, dev)
+    if S is None:
+        S = _new(s_shape, s_type, dev, stream)
+    else:
+        _check_like(S, "S", s_type, s_shape, dev)
+    return Q, S
+
+
+def fp8_quantize(X: torch.Tensor, block_rows: int = 1, pow2: bool = False, Q: torch.Tensor | None = None,
+                 S: torch.Tensor | None = None, stream=None):
+    """E4M3 codes and scales (Q, S) of the (rows, K) matrix X for the block-scaled FP8 products.
+
+    X: contiguous 2-D float16, bfloat16 or float32 CUDA tensor.  One scale per
+    ``block_rows`` x 128 elements: 1 for activations (the products' A, SA), 128
+    for a weight (W, SW).  S is float32 (gemm_fp8_block_scaled) or, with
+    ``pow2``, E8M0 bytes (gemm_mxfp8_block_scaled).  Q is float8_e4m3fn.  Q and S
+    are allocated when not given; rounding as in gemm_f16.h.  Asynchronous on
+    ``stream``.
+    """
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    dtype, shape = X.dtype, X.shape
+    code = TYPES.get(dtype)
+    if code is None or len(shape) != 2 or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous 2-D float16, bfloat16 or float32 tensor, got {dtype} {tuple(shape)}")
+    if block_rows != 1 and block_rows != FP8_BLOCK:
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
+    rows, K = shape
+    dev = X.device
+    Q, S = _fp8_outputs((rows, K), block_rows, pow2, Q, S, dev, stream)
+    _call((_lib or lib()).fp8_quantize, "fp8_quantize", dev, stream, X.data_ptr(), code, Q.data_ptr(), S.data_ptr(),
+          rows, K, block_rows, 1 if pow2 else 0)
+    _used_on(stream, dev, X, Q, S)
+    return Q, S
+
+
+def _rms_input(X, gamma, residual, H, stream):
+    """What rms_norm_fwd and rms_norm_fp8 check alike; H is made where it is needed."""
+    code, dtype, shape, rows, dim = _norm_input(X)
+    dev = X.device
+    wt = _norm_weight_type(dtype, dim, dev, gamma)
+    if residual is None:
+        if H is not None:
+            raise ValueError("H is the sum of X and a residual: without one it is X itself")
+    else:
+        _check_like(residual, "residual", dtype, shape, dev)
+        if H is None:
+            H = _new(shape, dtype, dev, stream)
+        else:
+            _check_like(H, "H", dtype, shape, dev)
+    return code, dtype, shape, rows, dim, dev, wt, H
+
+
+def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                 eps: float = 1e-6, Y: torch.Tensor | None = None, H: torch.Tensor | None = None, stats: bool = True,
+                 stream=None):
+    """(Y, H, rstd) of the RMS norm of H = X + residual over the last dimension (see gemm_f16.h).
+
+    X and residual: contiguous float16, bfloat16 or float32 CUDA tensors of one
+    shape; without a residual H is X itself.  gamma: None (ones) or a vector of
+    X's type or float32.  ``H`` may be given, X or residual among them (the
+    residual stream updated in place).  rstd is float32 of X's leading shape, or
+    None without ``stats``.  Asynchronous on ``stream``.
+    """
+    code, dtype, shape, rows, dim, dev, wt, H = _rms_input(X, gamma, residual, H, stream)
+    if Y is None:
+        Y = _new(shape, dtype, dev, stream)
+    else:
+        _check_like(Y, "Y", dtype, shape, dev)
+    rstd = _new(shape[:-1], torch.float32, dev, stream) if stats else None
+    _call((_lib or lib()).rms_norm_fwd, "rms_norm_fwd", dev, stream, X.data_ptr(), _ptr(residual), _ptr(gamma),
+          _ptr(H), Y.data_ptr(), _ptr(rstd), rows, dim, eps, code, TYPES[wt])
+    _used_on(stream, dev, X, residual, gamma, H, Y, rstd)
+    return Y, X if H is None else H, rstd
+
+
+def rms_norm_fp8(X: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                 eps: float = 1e-6, pow2: bool = False, Q: torch.Tensor | None = None, S: torch.Tensor | None = None,
+                 H: torch.Tensor | None = None, stream=None):
+    """(Q, S, H): rms_norm_fwd's output in FP8, as the block-scaled products take it.
+
+    Q: float8_e4m3fn of X's shape; S: one scale per row and 128 columns, float32
+    (gemm_fp8_block_scaled) or, with ``pow2``, E8M0 bytes
+    (gemm_mxfp8_block_scaled).  Everything else as for rms_norm_fwd.
+    """
+    code, dtype, shape, rows, dim, dev, wt, H = _rms_input(X, gamma, residual, H, stream)
+    Q, S = _fp8_outputs(shape, 1, pow2, Q, S, dev, stream)
+    _call((_lib or lib()).rms_norm_fp8, "rms_norm_fp8", dev, stream, X.data_ptr(), _ptr(residual), _ptr(gamma),
+          _ptr(H), Q.data_ptr(), S.data_ptr(), None, rows, dim, eps, code, TYPES[wt], 1 if pow2 else 0)
+    _used_on(stream, dev, X, residual, gamma, H, Q, S)
+    return Q, S, X if H is None else H
+
+
+def rms_norm_bwd_workspace(rows: int, dim: int, device=None) -> int:
+    """Bytes of workspace rms_norm_bwd needs."""
+    with _device_scope(torch.cuda.current_device() if device is None else device):
+        n = int(lib().rms_norm_bwd_workspace(rows, dim))
+    if n < 0:
+        raise GemmError(n, "rms_norm_bwd_workspace")
+    return n
+
+
+def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor | None = None,
+                 dH: torch.Tensor | None = None, dX: torch.Tensor | None = None, weights: bool = True,
+                 wtype: torch.dtype | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(dX, dgamma) of rms_norm_fwd; dgamma None without ``weights``.
+
+    dY like H; H, rstd and gamma as given to and returned by rms_norm_fwd; dH the
+    gradient that reaches H past the norm (the residual stream's), or None.  dX
+    is the gradient of X and of the residual alike.  dgamma has gamma's type
+    (``wtype`` without a gamma, H's type by default).  ``workspace``: a float32
+    vector of rms_norm_bwd_workspace bytes for callers that keep one; made on the
+    launch stream when not given.  Asynchronous on ``stream``.
+    """
+    code, dtype, shape, rows, dim = _norm_input(H, "H")
+    dev = H.device
+    _check_like(dY, "dY", dtype, shape, dev)
+    _check_like(rstd, "rstd", torch.float32, shape[:-1], dev)
+    if dH is not None:
+        _check_like(dH, "dH", dtype, shape, dev)
+    wt = _norm_weight_type(dtype, dim, dev, gamma)
+    if gamma is None and wtype is not None:
+        wt = wtype
+        if wt != dtype and wt != torch.float32:
+            raise ValueError(f"wtype must be H's type {dtype} or float32, got {wt}")
+    if dX is None:
+        dX = _new(shape, dtype, dev, stream)
+    else:
+        _check_like(dX, "dX", dtype, shape, dev)
+    L = _lib or lib()
+    dgamma = None
+    ws_bytes = 0
+    if weights:
+        dgamma = _new((dim,), wt, dev, stream)
+        if workspace is None:
+            if dev.index == _current_device():
+                need = L.rms_norm_bwd_workspace(rows, dim)
+                if need < 0:
+                    raise GemmError(need, "rms_norm_bwd_workspace")
+            else:
+                need = rms_norm_bwd_workspace(rows, dim, dev)
+            if stream is None:
+                workspace = _new((need // 4,), torch.float32, dev)
+            else:
+                with torch.cuda.stream(_launch_stream(stream, dev)):
+                    workspace = torch.empty((need // 4,), dtype=torch.float32, device=dev)
+        elif (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.float32
+              or not workspace.is_contiguous() or workspace.device != dev):
+            raise ValueError("workspace must be a contiguous float32 tensor on H's device")
+        ws_bytes = 4 * workspace.numel()
+    _call(L.rms_norm_bwd, "rms_norm_bwd", dev, stream, dY.data_ptr(), H.data_ptr(), _ptr(gamma), rstd.data_ptr(),
+          _ptr(dH), dX.data_ptr(), _ptr(dgamma), rows, dim, code, TYPES[wt], _ptr(workspace) if weights else None,
+          ws_bytes)
+    _used_on(stream, dev, dY, H, rstd, gamma, dH, dX, dgamma, workspace if weights else None)
+    return dX, dgamma
+
+
+def dropout(X: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0,
+            residual: torch.Tensor | None = None, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = residual + X / (1 - p) where an element is kept, residual (0 without one) where not.
+
+    The mask is a function of ``seed``, ``offset`` (whole numbers below 2^64) and
+    the element's place, and is not stored (see gemm_f16.h): the gradient is
+    this call on dY with the same p, seed and offset and no residual.  ``offset``
+    may be an int64 CUDA tensor of one element, read by the kernel when it runs:
+    a captured graph that advances it draws another mask at every replay.  X and
+    residual: contiguous float16, bfloat16 or float32 CUDA tensors of one shape;
+    ``Y`` may be either of them.  Asynchronous on ``stream``.
+    """
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    dtype, shape, dev = X.dtype, X.shape, X.device
+    code = TYPES.get(dtype)
+    if code is None or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous float16, bfloat16 or float32 tensor, got {dtype} {tuple(shape)}")
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p must be in [0, 1), got {p}")
+    off = None
+    if isinstance(offset, torch.Tensor):
+        off = offset
+        offset = 0
+        if off.dtype != torch.int64 or off.numel() != 1 or off.device != dev:
+            raise ValueError(f"offset must be a number or an int64 tensor of one element on {dev}")
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("seed and offset must be in [0, 2^64)")
+    if residual is not None:
+        _check_like(residual, "residual", dtype, shape, dev)
+    if Y is None:
+        Y = _new(shape, dtype, dev, stream)
+    else:
+        _check_like(Y, "Y", dtype, shape, dev)
+    _call((_lib or lib()).dropout_philox, "dropout", dev, stream, X.data_ptr(), _ptr(residual), Y.data_ptr(),
+          X.numel(), code, p, seed, offset, _ptr(off))
+    _used_on(stream, dev, X, residual, Y, off)
+    return Y
+
+
+W4_GROUPS = (32, 64, 128)
+W4_MAX_ROWS = 64   # GEMM_W4_MAX_ROWS
+
+
+def w4_shapes(N: int, K: int, group: int = 128) -> tuple[tuple[int, int, int], tuple[int, int, int]]:
+    """Shapes of the codes and of the scales (zero points) of a (N, K) 4-bit weight (see gemm_f16.h)."""
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    return (-(-N // 16), -(-K // 64), 512), (-(-N // 16), -(-K // group), 16)
+
+
+def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, group: int = 128):
+    """(Q, S, Z) of linear_w4 from row-major codes (N, K), a byte each, and scales and zero points (N, groups).
+
+    A layout change in torch, on the tensors' device: for weights that come
+    quantised.  Z is None without zero points (W = s (q - 8) then).  Codes and zero
+    points are in 0 .. 15; scales are float16 or bfloat16, the activations' type.
+    """
+    if not isinstance(codes, torch.Tensor) or codes.dtype != torch.uint8 or codes.dim() != 2:
+        raise ValueError("codes must be a 2-D uint8 tensor")
+    N, K = codes.shape
+    (nt, kt, _), (_, groups, _) = w4_shapes(N, K, group)
+    if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("scales must be a float16 or bfloat16 tensor")
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t is not None and tuple(t.shape) != (N, groups):
+            raise ValueError(f"{name} must be of shape {(N, groups)}, got {tuple(t.shape)}")
+    if zeros is not None and zeros.dtype != torch.uint8:
+        raise ValueError("zeros must be a uint8 tensor")
+    full = torch.zeros((nt * 16, kt * 64), dtype=torch.uint8, device=codes.device)
+    full[:N, :K] = codes & 15
+    # row 8 b + g; column 32 h + 8 t + 4 i + 2 d + e; nibble 4 e + 2 d + b of word 4 (4 g + t) + 2 h + i
+    full = full.reshape(nt, 2, 8, kt, 2, 4, 2, 2, 2).permute(0, 3, 2, 5, 4, 6, 8, 7, 1).reshape(nt, kt, 512, 2)
+    Q = (full[..., 0] | full[..., 1] << 4).contiguous()
+
+    def side_by_side(t):
+        out = torch.zeros((nt * 16, groups), dtype=t.dtype, device=t.device)
+        out[:N] = t
+        return out.reshape(nt, 16, groups).transpose(1, 2).contiguous()
+
+    return Q, side_by_side(scales), None if zeros is None else side_by_side(zeros & 15)
+
+
+def w4_quantize(W: torch.Tensor, group: int = 128, zeros: bool = False, transpose: bool = False,
+                stype: torch.dtype = torch.float16, stream=None):
+    """4-bit codes, scales and zero points (Q, S, Z) of the weight W (N, K) for linear_w4.
+
+    W: contiguous 2-D float16, bfloat16 or float32 CUDA tensor; with
+    ``transpose`` it is (K, N), a weight stored in-features x out-features.  One
+    scale of ``stype`` (the activations' type, float16 or bfloat16) per row and
+    ``group`` (32, 64, 128) columns; with ``zeros`` a zero point beside it,
+    without them Z is None and codes are symmetric.  Rounding as in gemm_f16.h.
+    Asynchronous on ``stream``.
+    """
+    if not isinstance(W, torch.Tensor):
+        raise TypeError("W must be a torch.Tensor")
+    code = TYPES.get(W.dtype)
+    if code is None or W.dim() != 2 or not W.is_contiguous():
+        raise ValueError(f"W must be a contiguous 2-D float16, bfloat16 or float32 tensor, got {W.dtype} {tuple(W.shape)}")
+    if stype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"stype must be float16 or bfloat16, got {stype}")
+    K, N = W.shape if transpose else (W.shape[1], W.shape[0])
+    q_shape, s_shape = w4_shapes(N, K, group)
+    dev = W.device
+    Q = _new(q_shape, torch.uint8, dev, stream)
+    S = _new(s_shape, stype, dev, stream)
+    Z = _new(s_shape, torch.uint8, dev, stream) if zeros else None
+    _call((_lib or lib()).w4_quantize, "w4_quantize", dev, stream, W.data_ptr(), code, Q.data_ptr(), S.data_ptr(),
+          _ptr(Z), N, K, group, TYPES[stype], 1 if transpose else 0)
+    _used_on(stream, dev, W, Q, S, Z)
+    return Q, S, Z
+
+
+def linear_w4(X: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, Z: torch.Tensor | None = None, N: int | None = None,
+              group: int = 128, relu: bool = False, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """C = R(X @ W^T) for a few rows of X and a 4-bit weight (Q, S, Z) of w4_quantize or w4_pack.
+
+    X (M, K): contiguous float16 or bfloat16 CUDA tensor of at most W4_MAX_ROWS
+    rows, of the scales' type; ``N``, W's rows, is 16 Q.shape[0] by default (give it
+    when N is not a multiple of 16).  C (M, N) of X's type is allocated when not
+    given.  Asynchronous on ``stream``.
+    """
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    if not isinstance(Q, torch.Tensor):
+        raise TypeError("Q must be a torch.Tensor")
+    dtype, shape, dev = X.dtype, X.shape, X.device
+    if dtype != torch.float16 and dtype != torch.bfloat16 or len(shape) != 2 or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous 2-D float16 or bfloat16 tensor, got {dtype} {tuple(shape)}")
+    M, K = shape
+    if M > W4_MAX_ROWS:
+        raise ValueError(f"X must have at most {W4_MAX_ROWS} rows, got {M}")
+    if N is None:
+        N = 16 * Q.shape[0]
+    q_shape, s_shape = w4_shapes(N, K, group)
+    _check_like(Q, "Q", torch.uint8, q_shape, dev)
+    _check_like(S, "S", dtype, s_shape, dev)
+    if Z is not None:
+        _check_like(Z, "Z", torch.uint8, s_shape, dev)
+    if C is None:
+        C = _new((M, N), dtype, dev, stream)
+    else:
+        _check_like(C, "C", dtype, (M, N), dev)
+    _call((_lib or lib()).linear_w4, "linear_w4", dev, stream, X.data_ptr(), TYPES[dtype], Q.data_ptr(), S.data_ptr(),
+          _ptr(Z), C.data_ptr(), M, N, K, group, 1 if relu else 0)
+    _used_on(stream, dev, X, Q, S, Z, C)
+    return C
 
 
 def fp8_launch_info(M: int, N: int, K: int) -> dict:

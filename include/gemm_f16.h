@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define GEMM_F16_VERSION 9
+#define GEMM_F16_VERSION 10
 
 /* Return codes.  0 is success; every error is negative. */
 enum gemm_f16_status {
@@ -457,6 +457,180 @@ int64_t layer_norm_bwd_workspace(int64_t rows, int64_t dim);
  */
 int layer_norm_bwd_selftest_timeout(const void *dY, const void *X, const float *mean, const float *rstd, void *dX,
                                     int64_t rows, int64_t dim, int xtype, uint64_t timeout_cycles, void *stream);
+
+/*
+ * rms_norm_fwd -- root-mean-square norm over rows of `dim` elements, after the
+ * residual's addition (the norm in front of a feed-forward or attention block;
+ * "Writing High-Performance Kernels in TileLang, from GEMM to MLA" has an RMS
+ * norm among its kernels):
+ *
+ *   H = X + R (X itself without a residual),  rstd = 1 / sqrt(sum H^2 / dim + eps),  Y = H rstd gamma
+ *
+ * in fp32.  H is rounded to X's type, the norm is taken of the rounded H, and Y
+ * is rounded once to X's type.
+ *
+ *   X, R, H, Y  device pointers, (rows, dim) row-major, type xtype (enum
+ *               gemm_f16_type).  R and H are both given or both NULL; H may be
+ *               X or R itself (the residual stream updated in place)
+ *   gamma       NULL (ones) or dim elements of type wtype: xtype, or
+ *               GEMM_TYPE_F32
+ *   rstd        NULL (not kept) or rows floats, written, for rms_norm_bwd
+ *   eps         finite, >= 0
+ *
+ * Alignment, overlap and sizes as for layer_norm_fwd.  Only enqueues on `stream`.
+ */
+int rms_norm_fwd(const void *X, const void *R, const void *gamma, void *H, void *Y, float *rstd,
+                 int64_t rows, int64_t dim, float eps, int xtype, int wtype, void *stream);
+
+/*
+ * rms_norm_fp8 -- rms_norm_fwd with Y quantised to E4M3 straight from fp32, as
+ * the A operand of gemm_fp8_block_scaled or gemm_mxfp8_block_scaled:
+ *
+ *   Q  device pointer, (rows, dim) E4M3 codes, row-major
+ *   S  (rows, ceil(dim/128)) scales: floats (pow2 = 0) or E8M0 bytes (pow2 = 1);
+ *      see fp8_quantize
+ *
+ * dim may be any number (the products take multiples of 16).  Q and S overlap
+ * nothing else.  Everything else as for rms_norm_fwd.
+ */
+int rms_norm_fp8(const void *X, const void *R, const void *gamma, void *H, void *Q, void *S, float *rstd,
+                 int64_t rows, int64_t dim, float eps, int xtype, int wtype, int pow2, void *stream);
+
+/*
+ * rms_norm_bwd -- gradients of rms_norm_fwd.  With z = H rstd and g = dY gamma:
+ *
+ *   dX = dH + rstd (g - z mean_row(g z)),  dgamma = sum_rows dY z
+ *
+ * in fp32, each output rounded once; dX is the gradient of X and of R alike.
+ * Sums over rows are taken in a fixed order (equal calls give equal bits on one
+ * GPU model): a block's rows in fp32, then the blocks' sums without loss, rounded
+ * once.
+ *
+ *   dY, H, gamma, rstd  as given to and kept by rms_norm_fwd (H: X itself where
+ *                  there was no residual)
+ *   dH             NULL (0) or the gradient that reaches H past the norm, like H
+ *   dX             (rows, dim) of type xtype
+ *   dgamma         dim elements of type wtype, or NULL (not wanted)
+ *   workspace      rms_norm_bwd_workspace(rows, dim) bytes, 16-byte aligned,
+ *                  written before it is read; may be NULL if dgamma is.  Calls
+ *                  that may run at the same time need one each.
+ *
+ * Outputs and the workspace overlap neither inputs nor each other.  rows == 0:
+ * dgamma is filled with zeros; dim == 0: no-op.
+ */
+int rms_norm_bwd(const void *dY, const void *H, const void *gamma, const float *rstd, const void *dH, void *dX,
+                 void *dgamma, int64_t rows, int64_t dim, int xtype, int wtype, void *workspace,
+                 int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace rms_norm_bwd needs for these sizes on the current device,
+ * or a negative status. */
+int64_t rms_norm_bwd_workspace(int64_t rows, int64_t dim);
+
+/*
+ * rms_norm_bwd_selftest_timeout -- exercises the bounded wait of rms_norm_bwd's
+ * ring of bulk copies, as layer_norm_bwd_selftest_timeout does (a test hook; the
+ * same site, 9).
+ */
+int rms_norm_bwd_selftest_timeout(const void *dY, const void *H, const float *rstd, void *dX, int64_t rows,
+                                  int64_t dim, int xtype, uint64_t timeout_cycles, void *stream);
+
+/*
+ * fp8_quantize -- X -> (Q, S) for the block-scaled FP8 products: E4M3 codes with
+ * one scale per block of block_rows x 128 elements (block_rows = 1: the A operand;
+ * 128: a weight).  With a = max |x| over a block:
+ *
+ *   pow2 = 0  S = a / 448, fp32;  Q = 448 x / a to the nearest E4M3, ties to even
+ *   pow2 = 1  S = 2^e with the least e >= -127 for which a <= 448 2^e, stored as
+ *             the E8M0 byte e + 127;  Q = x 2^-e to the nearest E4M3
+ *
+ * and S = 1 for a block of zeros.  A block that holds an infinity or a NaN gets
+ * a NaN scale (E8M0 0xFF) and NaN codes.
+ *
+ *   X  device pointer, (rows, K) row-major, type `type` (enum gemm_f16_type)
+ *   Q  (rows, K) codes;  S  (ceil(rows/block_rows), ceil(K/128)), row-major
+ *
+ * Buffers are aligned to their element (16-byte aligned rows of X take the
+ * vectorised path) and do not overlap.  At most INT32_MAX blocks.  rows == 0 or
+ * K == 0: no-op.  Only enqueues on `stream`.
+ */
+int fp8_quantize(const void *X, int type, void *Q, void *S, int64_t rows, int64_t K, int block_rows, int pow2,
+                 void *stream);
+
+/*
+ * dropout_philox -- dropout: Y = R + X / (1 - p) where an element is kept, R where not (R NULL:
+ * 0), rounded once to the type.  Element e of n is kept if word e % 4 of
+ * Philox4x32-10 with the 64-bit counter halves (e / 4, offset) and the key `seed`
+ * is at least floor(p 2^32): the mask is a function of seed, offset and e, and is
+ * not stored.  Its gradient with respect to X is the same call on dY without R.
+ *
+ *   X, R, Y     device pointers, n elements of type `type` (enum gemm_f16_type);
+ *               Y may be X or R itself, and overlaps nothing else
+ *   p           0 <= p < 1
+ *   offset_ptr  NULL, or a device pointer to a 64-bit offset, 8-byte aligned, read
+ *               by the kernel in place of `offset`: a captured graph that advances
+ *               it draws another mask at every replay
+ *
+ * A dropped element's value does not matter (an infinity or NaN of X is dropped
+ * too).  n == 0: no-op.  Only enqueues on `stream`.
+ */
+int dropout_philox(const void *X, const void *R, void *Y, int64_t n, int type, double p, uint64_t seed,
+                   uint64_t offset, const void *offset_ptr, void *stream);
+
+/*
+ * Weights in 4 bits with group scales, for products with a few rows of 16-bit
+ * activations.  The packed form of a weight W (N, K), W[n, k] = s (q - z) with
+ * a 16-bit scale s and optionally a zero point z (else 8) per row and `group`
+ * (32, 64 or 128) columns:
+ *
+ *   Q  (ceil(N/16), ceil(K/64), 512) bytes, 16-byte aligned.  In the 512 bytes of
+ *      16 rows and 64 columns the little-endian word 4 (4 g + t) + j holds rows g
+ *      and g + 8 (g < 8) and columns 32 (j / 2) + 8 t + 4 (j % 2) + c, c = 0 .. 3
+ *      (t < 4, j < 4): nibbles 0 .. 3 are (g, c = 0), (g + 8, 0), (g, 2), (g + 8, 2),
+ *      nibbles 4 .. 7 the same with c = 1 and 3
+ *   S  (ceil(N/16), ceil(K/group), 16) scales, one per group and row
+ *   Z  NULL, or as S in bytes, of which the low four bits count
+ *
+ * Codes, scales and zero points of rows and columns that W does not have may be
+ * anything finite; w4_quantize writes zeros.
+ *
+ * w4_quantize -- W -> (Q, S, Z).  Without Z: s = max|w| / 7 over the group rounded
+ * to the scales' type, q = 8 + w / s; with Z: s = (max(w, 0) - min(w, 0)) / 15,
+ * z = -min(w, 0) / s, q = z + w / s; z and q rounded to nearest even and kept in
+ * 0 .. 15.  s is at most the type's largest number; a group whose scale rounds to
+ * zero has s = 0; one that holds an infinity or a NaN has a NaN scale.
+ *
+ *   W      device pointer, elements of type `type`, (N, K) row-major for trans = 0,
+ *          (K, N) for trans = 1 (a weight stored in-features x out-features)
+ *   stype  the scales' type, GEMM_TYPE_F16 or GEMM_TYPE_BF16: the activations'
+ *
+ * Buffers are aligned to their element (Q to 16 bytes) and do not overlap.
+ * N == 0 or K == 0: no-op.  Only enqueues on `stream`.
+ */
+int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z, int64_t N, int64_t K, int group, int stype,
+                int trans, void *stream);
+
+/* Most rows of X that linear_w4 takes: it is made for tokens being generated. */
+#define GEMM_W4_MAX_ROWS 64
+
+/*
+ * linear_w4 -- C = R(X @ W^T) from a packed 4-bit weight (R as for gemm_f16):
+ *
+ *   C[m,n] = R( sum_groups s[n] * sum_{k in group} X[m,k] (q[n,k] - z[n]) )
+ *
+ * q - z is exact, sums are fp32, the result is rounded once to X's type.
+ *
+ *   X  device pointer, (M, K) row-major, GEMM_TYPE_F16 or GEMM_TYPE_BF16, M up to
+ *      GEMM_W4_MAX_ROWS; the scales have its type
+ *   C  (M, N) row-major of X's type, overlapping no input
+ *
+ * Any N and K.  Buffers are aligned to their element (Q to 16 bytes); rows of X on
+ * the 16-byte grid take the vectorised path.  The division of K among
+ * blocks depends on the sizes and the GPU alone and every sum has a fixed
+ * order, so equal calls give equal bits.  M == 0 or N == 0: no-op; K == 0: C = +0.
+ * Only enqueues on `stream`, allocates nothing.
+ */
+int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M, int64_t N,
+              int64_t K, int group, int relu, void *stream);
 
 /* Launch geometry of gemm_fp8_block_scaled for this problem on the current
  * device: persistent grid in CTAs (CTA pairs over 256 x 256 output tiles) and
