@@ -62,6 +62,9 @@ struct W4LinearArgs {
     int sm_count = 0, device = 0;
     cudaStream_t stream = nullptr;
 };
-int launch_linear_w4(const W4LinearArgs &a);
+// One scale group width each.
+int launch_linear_w4_g32(const W4LinearArgs &a);
+int launch_linear_w4_g64(const W4LinearArgs &a);
+int launch_linear_w4_g128(const W4LinearArgs &a);
 
 }  // namespace gemm_sm103

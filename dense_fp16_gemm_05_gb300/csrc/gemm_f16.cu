@@ -1388,8 +1388,8 @@ extern "C" int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z
     const uint64_t values = static_cast<uint64_t>(w4_group_values(N, K, group));
     const NormBuffer b[] = {{W, static_cast<uint64_t>(N) * static_cast<uint64_t>(K) * el, el, false},
                             {Q, static_cast<uint64_t>(w4_code_bytes(N, K)), 16, true},
-                            {S, values * 2u, 2, true},
-                            {Z, values, 1, true}};
+                            {S, values * 2u, 16, true},
+                            {Z, values, 16, true}};
     if ((st = check_norm_buffers(b, 4, dev.device)) != GEMM_OK) return st;
     W4QuantArgs a;
     a.W = W;
@@ -1431,8 +1431,8 @@ extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, 
     const uint64_t values = static_cast<uint64_t>(w4_group_values(N, K, group));
     const NormBuffer b[] = {{X, static_cast<uint64_t>(M) * static_cast<uint64_t>(K) * 2u, 2, false},
                             {Q, static_cast<uint64_t>(w4_code_bytes(N, K)), 16, false},
-                            {S, values * 2u, 2, false},
-                            {Z, values, 1, false},
+                            {S, values * 2u, 16, false},
+                            {Z, values, 16, false},
                             {C, c_bytes, 2, true}};
     if ((st = check_norm_buffers(b, 5, dev.device)) != GEMM_OK) return st;
     W4LinearArgs a;
@@ -1450,7 +1450,8 @@ extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, 
     a.sm_count = dev.sm_count;
     a.device = dev.device;
     a.stream = static_cast<cudaStream_t>(stream);
-    return launch_linear_w4(a);
+    if (group == 32) return launch_linear_w4_g32(a);
+    return group == 64 ? launch_linear_w4_g64(a) : launch_linear_w4_g128(a);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

@@ -582,16 +582,16 @@ int dropout_philox(const void *X, const void *R, void *Y, int64_t n, int type, d
  * a 16-bit scale s and optionally a zero point z (else 8) per row and `group`
  * (32, 64 or 128) columns:
  *
- *   Q  (ceil(N/16), ceil(K/64), 512) bytes, 16-byte aligned.  In the 512 bytes of
- *      16 rows and 64 columns the little-endian word 4 (4 g + t) + j holds rows g
- *      and g + 8 (g < 8) and columns 32 (j / 2) + 8 t + 4 (j % 2) + c, c = 0 .. 3
+ *   Q  (ceil(N/16), ceil(K/64), 512) bytes.  In the 512 bytes of 16 rows and 64
+ *      columns the little-endian word 4 (4 g + t) + j holds rows g and g + 8
+ *      (g < 8) and columns 32 (j / 2) + 8 t + 4 (j % 2) + c, c = 0 .. 3
  *      (t < 4, j < 4): nibbles 0 .. 3 are (g, c = 0), (g + 8, 0), (g, 2), (g + 8, 2),
  *      nibbles 4 .. 7 the same with c = 1 and 3
  *   S  (ceil(N/16), ceil(K/group), 16) scales, one per group and row
  *   Z  NULL, or as S in bytes, of which the low four bits count
  *
- * Codes, scales and zero points of rows and columns that W does not have may be
- * anything finite; w4_quantize writes zeros.
+ * All three are 16-byte aligned.  Codes, scales and zero points of rows and columns
+ * that W does not have may be anything; w4_quantize writes zeros.
  *
  * w4_quantize -- W -> (Q, S, Z).  Without Z: s = max|w| / 7 over the group rounded
  * to the scales' type, q = 8 + w / s; with Z: s = (max(w, 0) - min(w, 0)) / 15,
@@ -603,7 +603,7 @@ int dropout_philox(const void *X, const void *R, void *Y, int64_t n, int type, d
  *          (K, N) for trans = 1 (a weight stored in-features x out-features)
  *   stype  the scales' type, GEMM_TYPE_F16 or GEMM_TYPE_BF16: the activations'
  *
- * Buffers are aligned to their element (Q to 16 bytes) and do not overlap.
+ * W is aligned to its element; buffers do not overlap.
  * N == 0 or K == 0: no-op.  Only enqueues on `stream`.
  */
 int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z, int64_t N, int64_t K, int group, int stype,
@@ -623,8 +623,8 @@ int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z, int64_t N
  *      GEMM_W4_MAX_ROWS; the scales have its type
  *   C  (M, N) row-major of X's type, overlapping no input
  *
- * Any N and K.  Buffers are aligned to their element (Q to 16 bytes); rows of X on
- * the 16-byte grid take the vectorised path.  The division of K among
+ * Any N and K.  X and C are aligned to their element; rows of X on the 16-byte
+ * grid take the vectorised path.  The division of K among
  * blocks depends on the sizes and the GPU alone and every sum has a fixed
  * order, so equal calls give equal bits.  M == 0 or N == 0: no-op; K == 0: C = +0.
  * Only enqueues on `stream`, allocates nothing.
