@@ -29,7 +29,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 __device__ __forceinline__ uint32_t fp8_magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // Scale of a block whose largest |x| has the bit pattern `amax` (NaN above
-// infinity), and what its elements are converted with.
+// infinity), and what its elements are converted with.  kTies: see codes().
+template <bool kTies>
 struct Fp8Block {
     float a, inv;
     bool pow2, near_limits;
@@ -48,7 +49,7 @@ struct Fp8Block {
         } else {
             // 1 / a and 448 x stay clear of fp32's limits.
             near_limits = a < 0x1p-100f || a > 0x1p100f;
-            inv = 1.0f / a;
+            inv = (kTies ? 1.0f : 448.0f) / a;
         }
     }
 
@@ -72,14 +73,15 @@ struct Fp8Block {
         }
     }
 
-    // Two elements' codes.  448 x / a is the product with 1 / a put right by its
-    // remainder (P. Markstein, IBM J. Res. Dev. 34, 1990): a quotient half way
-    // between two codes, which 16-bit elements often give, stays there.
+    // Two elements' codes.  With kTies 448 x / a is the product with 1 / a put right by
+    // its remainder (P. Markstein, IBM J. Res. Dev. 34, 1990): a quotient half way
+    // between two codes, which 16-bit elements often give, stays there.  Elements that
+    // are results in fp32 are multiplied with 448 / a.
     __device__ __forceinline__ uint32_t codes(float2 x) const
     {
         float2 q;
         const float2 inv2 = make_float2(inv, inv);
-        if (pow2) {
+        if (pow2 || (!kTies && !near_limits)) {
             q = mul_f32x2(x, inv2);
         } else if (!near_limits) {
             const float2 t = mul_f32x2(x, make_float2(448.0f, 448.0f));

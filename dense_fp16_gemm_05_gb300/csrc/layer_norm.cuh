@@ -60,6 +60,21 @@ __device__ __forceinline__ float2 ln_pair(uint32_t raw, __nv_bfloat16)
     return make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xFFFF0000u));
 }
 
+__device__ __forceinline__ uint32_t ln_raw_pair(float2 v, __half)
+{
+    const __half2 h = __float22half2_rn(v);
+    uint32_t raw;
+    memcpy(&raw, &h, 4);
+    return raw;
+}
+__device__ __forceinline__ uint32_t ln_raw_pair(float2 v, __nv_bfloat16)
+{
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    uint32_t raw;
+    memcpy(&raw, &h, 4);
+    return raw;
+}
+
 // V adjacent elements, loaded and stored in pieces of 16, 8 or 4 bytes where V
 // elements make them up (the caller vouches for the alignment), else one by one.
 template <class T, int V>
@@ -135,6 +150,17 @@ struct LnPack {
 #pragma unroll
             for (unsigned i = 0; i < V * sizeof(T) / 4; ++i) asm volatile("" : "+r"(raw[i]));
             memcpy(e, raw, sizeof(e));
+        }
+    }
+    // Elements 2i and 2i + 1, rounded to T: 16-bit ones by one instruction.
+    __device__ __forceinline__ void set_pair(int i, float2 v)
+    {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t raw = ln_raw_pair(v, T{});
+            memcpy(e + 2 * i, &raw, 4);
+        } else {
+            e[2 * i] = v.x;
+            e[2 * i + 1] = v.y;
         }
     }
     // Elements 2i and 2i + 1.

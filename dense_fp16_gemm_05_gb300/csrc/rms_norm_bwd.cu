@@ -342,8 +342,12 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
             const int k = (i * tpr + t) * V;
             if (!inside(i)) continue;
             LnPack<T, V> out;
+            if constexpr (V == 1) {
+                out.e[0] = ln_round<T>(ln_half(z[i / 2], i));
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) out.e[j] = ln_round<T>(ln_half(z[(i * V + j) / 2], i * V + j));
+                for (int j = 0; j < V / 2; ++j) out.set_pair(j, z[i * (V / 2) + j]);
+            }
             out.store(dx + k);
         }
         if (++s == p.stages) {
