@@ -10,9 +10,10 @@ calls the kernel and whose backward returns ``dA = dC @ B.T`` and
 * dA        dZ @ B^T   (B stored (K,N))          gemm_f16_tx with transb = 1 (NT)
 * dB        A^T @ dZ   (A stored (M,K))          gemm_f16_tx with transa = 1 (TN)
 
-and layer norm, for the layer that feeds them, with layer_norm_fwd and
-layer_norm_bwd, and the product of MXFP4-quantised operands with gradients
-passed straight through the quantisation.
+and, for the block around them, layer norm (layer_norm_fwd, layer_norm_bwd), RMS
+norm with the residual's addition (rms_norm_fwd, rms_norm_bwd), dropout whose mask
+is never stored, and the product of MXFP4-quantised operands with gradients passed
+straight through the quantisation.
 
 The GEMMs' operands and gradients are float16 (the kernels accumulate in fp32).  No step
 falls back to torch arithmetic; a missing library raises LibraryNotBuilt.
@@ -110,6 +111,52 @@ class LayerNormFunction(torch.autograd.Function):
         return (dx if ctx.needs_input_grad[0] else None, dgamma if need_g else None, dbeta if need_b else None, None)
 
 
+class RmsNormFunction(torch.autograd.Function):
+    """(Y, H): RMS norm of H = x + residual over the last dimension; Y alone without a residual."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, gamma: torch.Tensor | None, residual: torch.Tensor | None, eps: float):
+        x = x.contiguous()
+        y, h, rstd = _g.rms_norm_fwd(x, gamma, None if residual is None else residual.contiguous(), eps=eps)
+        ctx.save_for_backward(h, gamma, rstd)
+        ctx.set_materialize_grads(False)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy: torch.Tensor | None, dh: torch.Tensor | None = None):
+        h, gamma, rstd = ctx.saved_tensors
+        need_x, need_g, need_r, _ = ctx.needs_input_grad
+        if dh is not None:
+            dh = dh.contiguous().to(h.dtype)
+        if dy is None:   # only the stream was used
+            return (dh if need_x else None, torch.zeros_like(gamma) if need_g else None, dh if need_r else None, None)
+        dx, dgamma = _g.rms_norm_bwd(dy.contiguous().to(h.dtype), h, rstd, gamma, dH=dh, weights=need_g)
+        return dx if need_x else None, dgamma, dx if need_r else None, None
+
+
+class DropoutFunction(torch.autograd.Function):
+    """residual + x / (1 - p) where an element is kept; the backward pass makes the mask again."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, p: float, seed: int, offset, residual: torch.Tensor | None):
+        y = _g.dropout(x.contiguous(), p, seed, offset, residual=None if residual is None else residual.contiguous())
+        ctx.p, ctx.seed = p, seed
+        # Saved, so that a change of it in between is an error and not another mask.
+        ctx.save_for_backward(offset if isinstance(offset, torch.Tensor) else None)
+        ctx.offset = None if isinstance(offset, torch.Tensor) else offset
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy: torch.Tensor):
+        (offset,) = ctx.saved_tensors
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = _g.dropout(dy.contiguous(), ctx.p, ctx.seed, ctx.offset if offset is None else offset)
+        return dx, None, None, None, dy if ctx.needs_input_grad[4] else None
+
+
 def linear_mxfp4(A: torch.Tensor, B: torch.Tensor, relu: bool = False) -> torch.Tensor:
     """C = A @ B or ReLU(A @ B) with both operands quantised to MXFP4, for training with 4-bit products.
 
@@ -140,6 +187,30 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     eager graph of the same leaves alive.
     """
     return LayerNormFunction.apply(x, gamma, beta, eps)
+
+
+def rms_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, eps: float = 1e-6,
+             residual: torch.Tensor | None = None):
+    """Differentiable RMS norm over x's last dimension on CUDA tensors.
+
+    With ``residual`` (x's shape and type) it returns (Y, H): H = x + residual, the
+    residual stream, and Y its norm; the gradients that reach H past the norm are
+    added in the backward kernel.  Without one it returns Y, the norm of x.
+    Capturing a backward pass: as for layer_norm.
+    """
+    return RmsNormFunction.apply(x, gamma, residual, eps)
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0,
+            residual: torch.Tensor | None = None) -> torch.Tensor:
+    """Differentiable residual + x / (1 - p) where an element is kept, residual (0 without one) where not.
+
+    The mask is a function of ``seed``, ``offset`` and the element's place (see
+    gemm_f16.dropout) and is not stored.  ``offset`` may be an int64 CUDA tensor of
+    one element, for captured steps that advance it; it must not change between the
+    forward and the backward pass.
+    """
+    return DropoutFunction.apply(x, p, seed, offset, residual)
 
 
 def gemm_relu(A: torch.Tensor, B: torch.Tensor) -> torch.Tensor:
