@@ -349,6 +349,64 @@ def test_pending_work_on_the_current_stream_does_not_reach_the_outputs(ff, name)
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+@pytest.mark.parametrize("name", [n for n in NAMES if n != "w4_quantize"])
+def test_short_and_long_way_give_the_same(ff, monkeypatch, name):
+    g = ff.g
+    call = calls(ff)[name]
+    g._short()
+    with monkeypatch.context() as m:
+        m.setattr(g, "_call", None)   # the long way's last step
+        got = call(None)
+    with monkeypatch.context() as m:
+        import types
+        never = {n: lambda *a: None for n in ("rms_norm_fwd", "rms_norm_fp8", "rms_norm_bwd", "fp8_quantize", "dropout",
+                                              "linear_w4")}
+        m.setattr(g, "_binding", types.SimpleNamespace(**never))
+        want = call(None)
+    assert len(got) == len(want)
+    for a, b in zip(got, want):
+        assert a.dtype == b.dtype and a.stride() == b.stride() and a.device == b.device
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_short_way_leaves_anything_else_to_the_long_way(ff):
+    g = ff.g
+    b = g._short()
+    assert b.torch_version == torch.__version__
+    x, w = data(4, 128), data(1, 128)[0]
+    r = torch.ones(4, device=DEV)
+    Q, S, Z = g.w4_quantize(data(32, 128), zeros=True)
+    off = torch.zeros(1, dtype=torch.int64, device=DEV)
+    plain = {"rms_norm_fwd": (x, w, x, 1e-6, True), "rms_norm_fp8": (x, w, x, 1e-6, False),
+             "rms_norm_bwd": (x, x, r, w, x, True), "fp8_quantize": (x, 1, False), "dropout": (x, 0.5, 1, off, x),
+             "linear_w4": (x, Q, S, Z, 32, 128, False)}
+    for name, args in plain.items():
+        assert getattr(b, name)(*args) is not None
+        for i, a in enumerate(args):
+            if isinstance(a, torch.Tensor):
+                others = [a.cpu(), a.double() if a.is_floating_point() else a.int(), a[:0], [1], torch.stack([a, a])]
+                if a.dim() > 1:
+                    others += [a.transpose(0, 1), a[:1] if name != "linear_w4" or i else a[:, :64]]
+                if i == 0 or (name == "rms_norm_bwd" and i == 1):
+                    # another type, size or shape of the input alone is another call's plain one
+                    others = others[:2] + others[3:4] + ([a.transpose(0, 1)] if a.dim() > 1 else [])
+            elif isinstance(a, float):
+                others = ["a"] if name != "dropout" else ["a", 1.0, -0.1, float("nan")]
+            elif isinstance(a, bool):
+                continue
+            else:
+                others = ["a", -1]
+            for o in others:
+                got = getattr(b, name)(*args[:i], o, *args[i + 1:])
+                assert got is None, (name, i, o)
+    assert b.linear_w4(x, Q, S, Z, 33, 128, False) is None and b.linear_w4(x, Q, S, Z, 32, 64, False) is None
+    assert b.fp8_quantize(x, 64, False) is None
+    assert b.dropout(x, 0.5, 1 << 64, 0, None) is None and b.dropout(x, 0.5, 1, -1, None) is None
+    with pytest.raises(ValueError):
+        g.dropout(x, 0.5, 1 << 64)
+    assert g.check() == g.GEMM_OK
+
+
 @pytest.mark.parametrize("name", NAMES)
 def test_calls_on_two_streams_at_once(ff, name):
     call = calls(ff)[name]
