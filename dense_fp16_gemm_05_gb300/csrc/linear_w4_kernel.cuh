@@ -15,16 +15,16 @@
 // Every warp streams its own units -- 16 rows x 128 columns of codes with their
 // scales and zero points -- through its own ring of asynchronous copies in shared
 // memory: nothing but its own copies makes a warp wait, and the bytes under way are
-// not bounded by registers.  Few rows of X stay in shared memory for the whole call
-// and a block's sixteen warps divide the columns of 16 rows of W (KW = 16), one
-// block per SM walking such strips; their sums are added through shared memory in a
-// fixed order.  More rows of X come in chunks for the block's 256 rows of W (KW = 1),
-// so that X is read less often than W.  Where W has few rows, K is also divided over
-// the blocks of a cluster, whose sums are added through distributed shared memory.
+// not bounded by registers.  A block's sixteen warps are RW strips of 16 rows times
+// KW = 16 / RW ways that the strips' columns are divided, whose sums are added
+// through shared memory in a fixed order.  X stays in shared memory for the whole
+// call where it fits, while blocks walk over the strips; else it comes in chunks for
+// 16 strips at a time, so that it is read less often than W.  K may also be divided
+// over the blocks of a cluster, whose sums are added through distributed shared
+// memory: so that X fits, or to have blocks enough.
 #pragma once
 
 #include <atomic>
-#include <type_traits>
 
 #include "feed_forward_launch.cuh"
 #include "gemm_launch.cuh"
@@ -42,23 +42,57 @@ struct W4Params {
     int32_t M;
     int32_t strips, k_tiles, groups, units;   // 16 rows; 64 columns; scale groups; 128 columns
     int32_t relu;
+    int32_t rw, kw;             // strips of a block, ways of a strip
     int32_t x_row, x_bytes;     // X in shared memory: bytes between rows, bytes of a buffer
+    int32_t keep_x;             // one buffer for the block's columns; else two chunks
+    int32_t vec;                // X's rows are on the 16-byte grid
 };
 
 constexpr int kW4Warps = 16, kW4Threads = kW4Warps * 32;
 
-// Asynchronous copies of 16 and of 8 bytes to shared memory.
-__device__ __forceinline__ void w4_copy16(uint32_t dst, const void *src)
+// Asynchronous copies to shared memory of 16 bytes, of which the first `bytes` are read
+// and the others zero, and of 8 bytes, all or none.
+__device__ __forceinline__ void w4_copy16(uint32_t dst, const void *src, uint32_t bytes = 16)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes)
+                 : "memory");
 }
-__device__ __forceinline__ void w4_copy8(uint32_t dst, const void *src)
+__device__ __forceinline__ void w4_copy8(uint32_t dst, const void *src, bool read)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
+                 "r"(read ? 8u : 0u)
+                 : "memory");
 }
 __device__ __forceinline__ void w4_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void w4_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Eight elements at `src`, of which `left` lie in the row, the others zero; [lo, hi) is
+// the tensor.  From the two 16-byte pieces that hold them where those lie in it.
+template <class T>
+__device__ __forceinline__ uint4 w4_eight(const T *src, int64_t left, uint64_t lo, uint64_t hi)
+{
+    const uint64_t at = reinterpret_cast<uint64_t>(src), first = at & ~15ull;
+    T e[8];
+    if (left >= 8 && first >= lo && first + 32 <= hi) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(first)), b = __ldg(reinterpret_cast<const uint4 *>(first) + 1);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t shift = static_cast<uint32_t>(at & 15u) / 2u;   // elements
+        uint32_t t[6], u[5], v[4];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) t[i] = shift & 4u ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) u[i] = shift & 2u ? t[i + 1] : t[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(u[i], u[i + 1], (shift & 1u) * 16u);
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < left ? __ldg(src + i) : ln_round<T>(0.0f);
+    uint4 r;
+    memcpy(&r, e, 16);
+    return r;
+}
 
 // (v & mask) | bits in one instruction: of two constants the compiler makes two.
 __device__ __forceinline__ uint32_t w4_and_or(uint32_t v, uint32_t mask, uint32_t bits)
@@ -127,52 +161,54 @@ struct W4Codes<__nv_bfloat16> {
     }
 };
 
-// Sizes of one kernel: NT groups of 8 rows of X; KW ways (16 or 1) that a strip's
-// columns are divided among the warps.  G: columns of a scale group.
-template <int NT, int KW, int G>
+// Sizes of one kernel: NT groups of 8 rows of X; G columns of a scale group.
+template <int NT, int G>
 struct W4Shape {
-    static constexpr int STRIPS = kW4Warps / KW, ROWS = STRIPS * kW4Rows, COLS = NT * 8;
-    static constexpr int U = 128 / G;                       // scale groups of a unit
-    static constexpr int SLOT = 1024 + U * 48;              // bytes: codes, scales, zero points
-    static constexpr int DEPTH = KW > 1 || NT <= 2 ? 6 : 4; // units under way per warp
+    static constexpr int COLS = NT * 8;
+    static constexpr int U = 128 / G;                     // scale groups of a unit
+    static constexpr int SLOT = 1024 + U * 48;            // bytes: codes, scales, zero points
+    static constexpr int DEPTH = NT <= 2 ? 6 : 4;         // units under way per warp
     static constexpr int RING = kW4Warps * DEPTH * SLOT;
-    static constexpr int X_UNITS = NT <= 2 ? 8 : 4;         // of a chunk of X, at least DEPTH (KW = 1)
-    static constexpr int SUMS = KW * ROWS * (COLS + 1) * 4; // KW = 1: in place of X and the ring
+    static constexpr int X_UNITS = NT <= 2 ? 8 : 4;       // of a chunk of X, at least DEPTH
+    static constexpr int SUMS = kW4Warps * 16 * (COLS + 1) * 4;
 };
 
 // Rows of X half a 128-byte line apart, so that eight lanes' 16-byte loads from two
 // rows meet no bank twice.
-constexpr int w4_x_row(int64_t units) { return static_cast<int>(units * 256 + 64); }
+constexpr int64_t w4_x_row(int64_t units) { return units * 256 + 64; }
 
-// kVec: X's rows are on the 16-byte grid and come through shared memory; else their
-// elements are read one by one.
-template <class T, int NT, int KW, int G, bool kVec>
+template <class T, int NT, int G>
 __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
 {
     using Codes = W4Codes<T>;
-    using Shape = W4Shape<NT, KW, G>;
-    constexpr int U = Shape::U, ROWS = Shape::ROWS, COLS = Shape::COLS, D = Shape::DEPTH;
-    extern __shared__ uint4 smem[];   // the rings; X (KW = 1: two chunks); KW = 16: two buffers of sums
-    typedef float Sums[KW][ROWS][COLS + 1];
+    using Shape = W4Shape<NT, G>;
+    constexpr int U = Shape::U, COLS = Shape::COLS, D = Shape::DEPTH;
+    extern __shared__ uint4 smem[];   // the rings; X; sums (behind a kept X, else in the place of all)
+    typedef float Sums[kW4Warps][16][COLS + 1];   // of a warp's strip
     griddep_wait();
     griddep_launch_dependents();
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int kw = KW > 1 ? warp : 0, rw = KW > 1 ? 0 : warp;
+    const int kw = warp / p.rw, rw = warp - kw * p.rw;
     const int slices = static_cast<int>(gridDim.y), slice = static_cast<int>(blockIdx.y);
     const int u_begin = static_cast<int>(static_cast<int64_t>(p.units) * slice / slices);
     const int u_end = static_cast<int>(static_cast<int64_t>(p.units) * (slice + 1) / slices);
+    uint8_t *x_mem = reinterpret_cast<uint8_t *>(smem) + Shape::RING;
     const uint8_t *ring = reinterpret_cast<const uint8_t *>(smem) + warp * (D * Shape::SLOT);
-    const uint8_t *x_mem = reinterpret_cast<const uint8_t *>(smem) + Shape::RING;
-    const uint32_t ring_at = smem_addr(ring), x_at = smem_addr(x_mem);
+    const uint32_t ring_at = smem_addr(ring);
 
-    // Copies of X: `units` units from unit u on, all threads together.
-    auto copy_x = [&](uint32_t dst, int u, int units) {
+    // X's columns of `units` units from unit u on, all threads together, zeros past K.
+    auto copy_x = [&](uint8_t *dst, int u, int units) {
         const int per_row = units * 16;   // 16-byte pieces
         const int64_t k0 = static_cast<int64_t>(u) * 128;
+        const uint64_t lo = reinterpret_cast<uint64_t>(p.X), hi = lo + static_cast<uint64_t>(p.M) * p.K * sizeof(T);
         for (int i = threadIdx.x; i < p.M * per_row; i += kW4Threads) {
             const int m = i / per_row, c = i - m * per_row;
-            if (k0 + c * 8 < p.K) w4_copy16(dst + static_cast<uint32_t>(m * p.x_row + c * 16), p.X + m * p.K + k0 + c * 8);
+            const int64_t left = p.K - (k0 + c * 8);
+            const T *src = p.X + m * p.K + k0 + c * 8;
+            uint8_t *to = dst + m * p.x_row + c * 16;
+            if (p.vec) w4_copy16(smem_addr(to), left > 0 ? src : p.X, left > 0 ? 16u : 0u);
+            else *reinterpret_cast<uint4 *>(to) = w4_eight(src, left, lo, hi);
         }
     };
     // This lane's piece of a unit's scales (the first 4 U lanes) or zero points (2 U).
@@ -181,40 +217,34 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
     const uint8_t *side_base = (side_s ? p.S : p.Z) + side_j * 8;
     const uint32_t side_bytes = side_s ? 32u : 16u;   // of a group
     const uint32_t side_to = 1024u + static_cast<uint32_t>(side_s ? lane * 8 : U * 32 + side_j * 8);
+    const uint32_t q_step = p.kw * 1024u, side_step = p.kw * U * side_bytes;
     const uint8_t *q_src = nullptr, *side_src = nullptr;
     auto seek = [&](int strip, int u) {
         strip = min(strip, p.strips - 1);   // one past the last is read as the last and not stored
         q_src = p.Q + (static_cast<int64_t>(strip) * p.k_tiles + 2 * u) * kW4TileBytes + lane * 16;
         side_src = side_base + (static_cast<int64_t>(strip) * p.groups + static_cast<int64_t>(u) * U) * side_bytes;
     };
+    // Unit u, the last of which may have one tile, and scales of fewer groups: zeros
+    // stand for the others.
     auto fetch = [&](int slot, int u) {
         const uint32_t dst = ring_at + static_cast<uint32_t>(slot * Shape::SLOT);
-        const bool tail = u == p.units - 1;
+        const bool tile2 = 2 * u + 1 < p.k_tiles, in = u * U + side_group < p.groups;
         w4_copy16(dst + lane * 16, q_src);
-        if (!tail || 2 * u + 1 < p.k_tiles) w4_copy16(dst + 512 + lane * 16, q_src + 512);
-        if (side && (!tail || u * U + side_group < p.groups)) w4_copy8(dst + side_to, side_src);
-        q_src += KW * 1024;
-        side_src += KW * U * side_bytes;
+        w4_copy16(dst + 512 + lane * 16, tile2 ? q_src + 512 : q_src, tile2 ? 16u : 0u);
+        if (side) w4_copy8(dst + side_to, in ? side_src : p.Q, in);
+        q_src += q_step;
+        side_src += side_step;
     };
 
     // A row past X's last is read as the last one: it reaches nothing but its own
     // column of the result, which is not stored.
     uint32_t x_off[NT];
-    const T *x_src[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int m = min(n * 8 + g, p.M - 1);
-        x_off[n] = static_cast<uint32_t>(m * p.x_row + t * 16);
-        x_src[n] = p.X + m * p.K + t * 8;
-    }
+    for (int n = 0; n < NT; ++n) x_off[n] = static_cast<uint32_t>(min(n * 8 + g, p.M - 1) * p.x_row + t * 16);
     float sum[NT][4];
-    // Adds unit u's products.  kTail: the last unit, which may reach past K.
-    auto unit = [&](const uint8_t *slot, const uint8_t *x_unit, int u, auto tail_) {
-        constexpr bool kTail = decltype(tail_)::value;
-        const int left = kTail ? static_cast<int>(p.K - static_cast<int64_t>(u) * 128) - t * 8 : 0;
+    // Adds a unit's products: codes, scales and zero points in `slot`, X's columns at `x_unit`.
+    auto unit = [&](const uint8_t *slot, const uint8_t *x_unit) {
         const uint4 *q = reinterpret_cast<const uint4 *>(slot) + lane;
-        // In a last unit of one tile the second one's codes are those of an earlier
-        // unit, times zeros.
         const uint4 tile[2] = {q[0], q[32]};
         const uint8_t *scales = slot + 1024 + g * 2, *zeros = slot + 1024 + U * 32 + g;
 #pragma unroll
@@ -232,19 +262,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
             for (int h = j * (G / 32); h < (j + 1) * (G / 32); ++h) {
                 uint4 x[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (kVec) {
-                        x[n] = *reinterpret_cast<const uint4 *>(x_unit + x_off[n] + h * 64);
-                        if (kTail && h * 32 >= left) x[n] = make_uint4(0, 0, 0, 0);
-                    } else {
-                        T e[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            e[k] = !kTail || h * 32 + k < left ? __ldg(x_src[n] + static_cast<int64_t>(u) * 128 + h * 32 + k)
-                                                               : ln_round<T>(0.0f);
-                        memcpy(&x[n], e, 16);
-                    }
-                }
+                for (int n = 0; n < NT; ++n) x[n] = *reinterpret_cast<const uint4 *>(x_unit + x_off[n] + h * 64);
                 const uint4 &v = tile[h / 2];
                 const uint32_t w[2] = {h % 2 ? v.z : v.x, h % 2 ? v.w : v.y};
 #pragma unroll
@@ -261,8 +279,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
                 }
             }
             const T *sc = reinterpret_cast<const T *>(scales + j * 32);
-            float s0 = ln_float(sc[0]), s1 = ln_float(sc[8]);
-            if (kTail && u * U + j >= p.groups) s0 = s1 = 0.0f;
+            const float s0 = ln_float(sc[0]), s1 = ln_float(sc[8]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -271,11 +288,6 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
                     sum[n][e] = fmaf(e < 2 ? s0 : s1, v, sum[n][e]);
                 }
         }
-    };
-    auto step = [&](int slot, const uint8_t *x_unit, int u) {
-        const uint8_t *at = ring + slot * Shape::SLOT;
-        if (u < p.units - 1) unit(at, x_unit, u, std::false_type{});
-        else unit(at, x_unit, u, std::true_type{});
     };
     auto clear = [&]() {
 #pragma unroll
@@ -288,62 +300,78 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sums[kw][rw * 16 + g + 8 * (e >> 1)][n * 8 + 2 * t + (e & 1)] = sum[n][e];
+            for (int e = 0; e < 4; ++e) sums[warp][g + 8 * (e >> 1)][n * 8 + 2 * t + (e & 1)] = sum[n][e];
     };
-    constexpr int OUT = ROWS * COLS;
-    auto ways = [&](const Sums &sums, int r, int m) {
-        float v = sums[0][r][m];
-#pragma unroll
-        for (int i = 1; i < KW; ++i) v += sums[i][r][m];
-        return v;
-    };
-    auto store = [&](int64_t n, int m, float v) {
-        if (n >= p.N || m >= p.M) return;
-        if (p.relu) v = v > 0.0f ? v : 0.0f;
-        p.C[m * p.N + n] = ln_round<T>(v);
-    };
-    auto finish = [&](Sums &sums, int64_t n0) {
+    // The block's outputs, of strips strip0 .. strip0 + rw - 1: o is a row of them and of X.
+    const int rows = p.rw * 16, out = rows * p.M;
+    // `ordered`: room for them, among the blocks of a cluster.
+    auto finish = [&](Sums &sums, float *ordered, int strip0) {
+        const int64_t n0 = static_cast<int64_t>(strip0) * 16;
+        auto ways = [&](int r, int m) {
+            float v = sums[r >> 4][r & 15][m];
+            for (int i = 1; i < p.kw; ++i) v += sums[i * p.rw + (r >> 4)][r & 15][m];
+            return v;
+        };
+        auto store = [&](int r, int m, float v) {
+            if (n0 + r >= p.N) return;
+            if (p.relu) v = v > 0.0f ? v : 0.0f;
+            p.C[m * p.N + n0 + r] = ln_round<T>(v);
+        };
         if (slices == 1) {
-            for (int o = threadIdx.x; o < OUT; o += kW4Threads) store(n0 + o % ROWS, o / ROWS, ways(sums, o % ROWS, o / ROWS));
+            for (int o = threadIdx.x; o < out; o += kW4Threads) {
+                const int m = o / rows, r = o - m * rows;
+                store(r, m, ways(r, m));
+            }
             return;
         }
-        // The block's sums in place of the first way's, then every block of the cluster
-        // adds and stores a share.
-        if constexpr (KW > 1)
-            for (int o = threadIdx.x; o < OUT; o += kW4Threads) sums[0][o % ROWS][o / ROWS] = ways(sums, o % ROWS, o / ROWS);
+        // The block's sums in the outputs' order, then every block of the cluster adds and
+        // stores a share: loads from another block are worth it in whole 16-byte pieces
+        // (64 x 8192 x 1024 over 8 blocks: 98 us element by element).
+        for (int o = threadIdx.x; o < out; o += kW4Threads) {
+            const int m = o / rows, r = o - m * rows;
+            ordered[o] = ways(r, m);
+        }
         cluster_arrive();
         cluster_wait();
-        for (int o = threadIdx.x + slice * kW4Threads; o < OUT; o += slices * kW4Threads) {
-            const int r = o % ROWS, m = o / ROWS;
-            float v = 0.0f;
-            for (int i = 0; i < slices; ++i) {
-                const uint32_t at = mapa_shared(smem_addr(&sums[0][r][m]), static_cast<uint32_t>(i));
-                float other;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(at));
-                v += other;
+        for (int o = 4 * (threadIdx.x + slice * kW4Threads); o < out; o += 4 * slices * kW4Threads) {
+            const uint32_t at = smem_addr(ordered + o);
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, part[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < slices)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(part[i][0]), "=f"(part[i][1]), "=f"(part[i][2]), "=f"(part[i][3])
+                                 : "r"(mapa_shared(at, static_cast<uint32_t>(i))));
+            const int m = o / rows, r = o - m * rows;   // rows are a multiple of 16
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < slices) v[e] += part[i][e];
+                store(r + e, m, v[e]);
             }
-            store(n0 + r, m, v);
         }
-        cluster_arrive();   // nobody leaves while its sums are read
+        cluster_arrive();   // nobody goes on while its sums are read
         cluster_wait();
     };
 
-    if constexpr (KW > 1) {
-        // Strips blockIdx.x, blockIdx.x + gridDim.x, ...; this warp has units u_begin + kw,
-        // u_begin + kw + KW, ... of each, `mine` of them.
-        Sums *part = reinterpret_cast<Sums *>(const_cast<uint8_t *>(x_mem) + p.x_bytes);
-        const int first = u_begin + kw, mine = first < u_end ? (u_end - first + KW - 1) / KW : 0;
-        if (kVec) copy_x(x_at, u_begin, u_end - u_begin);
+    if (p.keep_x) {
+        // Groups of rw strips blockIdx.x, blockIdx.x + gridDim.x, ...; this warp has units
+        // u_begin + kw, u_begin + kw + KW, ... of its strip of each, `mine` of them.
+        Sums *part = reinterpret_cast<Sums *>(x_mem + p.x_bytes);
+        const int first = u_begin + kw, mine = first < u_end ? (u_end - first + p.kw - 1) / p.kw : 0;
+        copy_x(x_mem, u_begin, u_end - u_begin);
         w4_commit();
         // The copies run ahead of the products by D units, over the strips' ends.
-        int ahead_strip = blockIdx.x, ahead = 0;
+        const int strip_step = static_cast<int>(gridDim.x) * p.rw, strip_first = static_cast<int>(blockIdx.x) * p.rw;
+        int ahead_strip = strip_first, ahead = 0;
         auto next = [&](int slot) {
             if (mine > 0 && ahead_strip < p.strips) {
-                if (ahead == 0) seek(ahead_strip, first);
-                fetch(slot, first + ahead * KW);
+                if (ahead == 0) seek(ahead_strip + rw, first);
+                fetch(slot, first + ahead * p.kw);
                 if (++ahead == mine) {
                     ahead = 0;
-                    ahead_strip += static_cast<int>(gridDim.x);
+                    ahead_strip += strip_step;
                 }
             }
             w4_commit();
@@ -352,32 +380,36 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         for (int i = 0; i < D; ++i) next(i);
         w4_wait<D>();
         __syncthreads();   // X is there
+        const uint8_t *x_first = x_mem + kw * 256;
         int slot = 0, buffer = 0;
-        for (int strip = blockIdx.x; strip < p.strips; strip += static_cast<int>(gridDim.x)) {
+        for (int strip0 = strip_first; strip0 < p.strips; strip0 += strip_step) {
             clear();
+            const uint8_t *x_unit = x_first;
             for (int i = 0; i < mine; ++i) {
                 w4_wait<D - 1>();
                 __syncwarp();
-                const int u = first + i * KW;
-                step(slot, x_mem + (u - u_begin) * 256, u);
+                unit(ring + slot * Shape::SLOT, x_unit);
+                x_unit += p.kw * 256;
                 __syncwarp();
                 next(slot);
                 if (++slot == D) slot = 0;
             }
             keep(part[buffer]);
             __syncthreads();
-            finish(part[buffer], static_cast<int64_t>(strip) * ROWS);
-            // Sums of the strip after the next are written behind the next one's barrier.
-            buffer ^= 1;
+            finish(part[buffer], reinterpret_cast<float *>(part + 1), strip0);
+            // Sums of the group after the next are written behind the next one's barrier
+            // (among the blocks of a cluster, all of a group behind the last one's).
+            if (slices == 1) buffer ^= 1;
         }
     } else {
-        // One strip per warp, units u_begin .. u_end - 1; X in chunks that the block shares.
+        // One strip per warp (kw = 0), units u_begin .. u_end - 1; X in chunks that the
+        // block shares.
         constexpr int XU = Shape::X_UNITS;
         static_assert(XU >= D, "a chunk of X is there when the units copied with it are");
         const int n = u_end - u_begin;
-        seek(static_cast<int>(blockIdx.x) * Shape::STRIPS + warp, u_begin);
+        seek(static_cast<int>(blockIdx.x) * kW4Warps + warp, u_begin);
         clear();
-        if (kVec) copy_x(x_at, u_begin, XU);
+        copy_x(x_mem, u_begin, min(XU, n));
 #pragma unroll
         for (int i = 0; i < D; ++i) {
             if (i < n) fetch(i, u_begin + i);
@@ -386,13 +418,13 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         int slot = 0, x_unit = 0, x_buffer = 0;
         for (int i = 0; i < n; ++i) {
             w4_wait<D - 1>();
-            if (kVec && x_unit == 0) {
+            if (x_unit == 0) {
                 __syncthreads();   // this chunk is there, and the one before is done with
-                if (i + XU < n) copy_x(x_at + static_cast<uint32_t>((x_buffer ^ 1) * p.x_bytes), u_begin + i + XU, XU);
+                if (i + XU < n) copy_x(x_mem + (x_buffer ^ 1) * p.x_bytes, u_begin + i + XU, min(XU, n - i - XU));
             } else {
                 __syncwarp();
             }
-            step(slot, x_mem + x_buffer * p.x_bytes + x_unit * 256, u_begin + i);
+            unit(ring + slot * Shape::SLOT, x_mem + x_buffer * p.x_bytes + x_unit * 256);
             __syncwarp();
             if (i + D < n) fetch(slot, u_begin + i + D);
             w4_commit();
@@ -407,40 +439,60 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         Sums &sums = *reinterpret_cast<Sums *>(smem);
         keep(sums);
         __syncthreads();
-        finish(sums, static_cast<int64_t>(blockIdx.x) * ROWS);
+        finish(sums, reinterpret_cast<float *>(&sums + 1), static_cast<int>(blockIdx.x) * kW4Warps);
     }
 }
 
 constexpr int kW4Budget = 225 * 1024;   // dynamic shared memory of a block
 
-// Rows of X that stay in shared memory beside the rings and the sums (KW = 16).
-template <int G>
-constexpr int kW4KeepBytes = kW4Budget - W4Shape<1, 16, G>::RING - 2 * W4Shape<1, 16, G>::SUMS;
-
-// Blocks of a cluster that divide K: while the GPU has room for them and every warp
-// keeps two of its units.
-inline int w4_slices(int64_t row_groups, int64_t units_per_warp, int sm_count)
-{
-    int slices = 1;
-    while (slices < 8 && 2 * slices * row_groups <= sm_count && 4 * slices <= units_per_warp) slices *= 2;
-    return slices;
-}
-
-template <class T, int NT, int KW, int G, bool kVec>
+template <class T, int NT, int G>
 int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
 {
-    using Shape = W4Shape<NT, KW, G>;
-    auto kern = linear_w4_kernel<T, NT, KW, G, kVec>;
-    const int64_t row_groups = (p.strips + Shape::STRIPS - 1) / Shape::STRIPS;
-    const int slices = w4_slices(row_groups, (p.units + KW - 1) / KW, a.sm_count);
-    int smem = Shape::RING;
-    if (kVec) {
-        p.x_row = w4_x_row(KW > 1 ? (p.units + slices - 1) / slices : Shape::X_UNITS);
-        p.x_bytes = p.M * p.x_row;
-        smem += KW > 1 ? p.x_bytes : 2 * p.x_bytes;
+    using Shape = W4Shape<NT, G>;
+    auto kern = linear_w4_kernel<T, NT, G>;
+    // The division of the work that costs least by this count of nanoseconds, fitted to
+    // whole calls of 16 shapes (1 x 64 x 64 to 64 x 16384 x 8192) under every division: a
+    // unit of each of a block's warps takes 450 with 8 rows of X, 1850 with 64; a group
+    // of strips ends with 500, more among the blocks of a cluster, and a quarter for each
+    // output; X comes with 60 bytes each, 20 where its rows are off the 16-byte grid, and
+    // in chunks half hidden.  The count's choice is within 10 % of the best of all but
+    // the smallest calls.
+    const int64_t sms = a.sm_count, strips = p.strips;
+    const int64_t room = kW4Budget - Shape::RING - 2 * Shape::SUMS;   // for a kept X
+    const int64_t unit_cost = NT == 1 ? 450 : (NT == 2 ? 650 : (NT == 4 ? 1030 : 1850));
+    int64_t least = INT64_MAX;
+    int slices = 1;
+    for (int sl = 1; sl <= 8 && sl <= p.units; sl *= 2) {
+        const int64_t units = (p.units + sl - 1) / sl, x_bytes = p.M * w4_x_row(units);
+        const int64_t x_cost = x_bytes / (p.vec ? 60 : 20), end = sl == 1 ? 500 : (sl == 2 ? 1500 : (sl == 4 ? 3000 : 4000));
+        const int64_t most = sms / sl;   // clusters at a time
+        auto consider = [&](int keep, int kw) {
+            const int64_t rw = kW4Warps / kw, rounds = ((strips + rw - 1) / rw + most - 1) / most;
+            const int64_t group = (units + kw - 1) / kw * unit_cost + end + rw * 4 * p.M;
+            const int64_t cost = keep ? rounds * group + x_cost : rounds * (group + x_cost / 2);
+            if (cost >= least) return;
+            least = cost;
+            slices = sl;
+            p.keep_x = keep;
+            p.kw = kw;
+        };
+        consider(0, 1);
+        if (NT <= 4 && x_bytes <= room)
+            for (int kw = 1; kw <= kW4Warps && kw <= units; kw *= 2) consider(1, kw);
     }
-    if (KW > 1) smem += 2 * Shape::SUMS;
-    else if (smem < Shape::SUMS) smem = Shape::SUMS;
+    p.rw = kW4Warps / p.kw;
+    const int64_t groups = (strips + p.rw - 1) / p.rw, most = sms / slices;
+    int64_t smem = Shape::RING;
+    if (p.keep_x) {
+        p.x_row = static_cast<int32_t>(w4_x_row((p.units + slices - 1) / slices));
+        p.x_bytes = p.M * p.x_row;
+        smem += p.x_bytes + 2 * Shape::SUMS;
+    } else {
+        p.x_row = static_cast<int32_t>(w4_x_row(Shape::X_UNITS));
+        p.x_bytes = p.M * p.x_row;
+        smem += 2 * p.x_bytes;
+        if (smem < 2 * Shape::SUMS) smem = 2 * Shape::SUMS;
+    }
     static std::atomic<int> prepared[kMaxDevices];
     if (!prepared[a.device].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4Budget) != cudaSuccess) {
@@ -450,8 +502,7 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
         prepared[a.device].store(1, std::memory_order_release);
     }
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>(KW > 1 && slices == 1 && row_groups > a.sm_count ? a.sm_count : row_groups),
-                      static_cast<unsigned>(slices), 1);
+    lc.gridDim = dim3(static_cast<unsigned>(p.keep_x && groups > most ? most : groups), static_cast<unsigned>(slices), 1);
     lc.blockDim = dim3(kW4Threads, 1, 1);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = a.stream;
@@ -473,20 +524,6 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
 }
 
 // Calls of one scale group width (linear_w4_g32.cu, ...: a translation unit each).
-template <class T, int G, bool kVec>
-int launch_w4_shape(const W4Params<T> &p, const W4LinearArgs &a)
-{
-    // Few rows of X that fit beside the rings, and enough columns for half of the
-    // warps: M = 1, 16384 x 8192 fp16 17.8 us, 25 us by KW = 1; M = 8 there, whose X
-    // does not fit, 21.2 us.
-    const bool fits = !kVec || p.M * static_cast<int64_t>(w4_x_row(p.units)) <= kW4KeepBytes<G>;
-    if (p.M <= 8 && fits && p.units >= 8) return launch_w4_kernel<T, 1, 16, G, kVec>(p, a);
-    if (p.M <= 8) return launch_w4_kernel<T, 1, 1, G, kVec>(p, a);
-    if (p.M <= 16) return launch_w4_kernel<T, 2, 1, G, kVec>(p, a);
-    if (p.M <= 32) return launch_w4_kernel<T, 4, 1, G, kVec>(p, a);
-    return launch_w4_kernel<T, 8, 1, G, kVec>(p, a);
-}
-
 template <class T, int G>
 int launch_w4(const W4LinearArgs &a)
 {
@@ -504,8 +541,11 @@ int launch_w4(const W4LinearArgs &a)
     p.groups = static_cast<int32_t>((a.K + G - 1) / G);
     p.units = (p.k_tiles + 1) / 2;
     p.relu = a.relu;
-    const bool vec = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.K % 8 == 0;
-    return vec ? launch_w4_shape<T, G, true>(p, a) : launch_w4_shape<T, G, false>(p, a);
+    p.vec = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.K % 8 == 0;
+    if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
+    if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);
+    if (p.M <= 32) return launch_w4_kernel<T, 4, G>(p, a);
+    return launch_w4_kernel<T, 8, G>(p, a);
 }
 
 }  // namespace gemm_sm103
