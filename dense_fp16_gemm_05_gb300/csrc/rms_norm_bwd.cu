@@ -170,7 +170,9 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR)) rms_norm_bwd_kernel(RmsB
 
 // Rows through a ring of bulk copies in shared memory, `stages` rows ahead, a
 // block per row at a time.  A slot is free once every thread has its pieces in
-// registers, which the row sum's barrier says.  Every wait is bounded: on expiry
+// registers, which the row sum's barrier says; with 16 elements in each of 1024
+// threads (kReread) they are read a second time instead of being kept, and the slot is
+// refilled one row later.  Every wait is bounded: on expiry
 // the site is recorded in the device status word and the block leaves.
 // Blocks per SM that the registers are held to.
 __host__ __device__ constexpr int rms_ring_blocks(int tpr, int per)
@@ -186,6 +188,8 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
 {
     constexpr bool kFull = TPR > 0;
     constexpr bool kReload = sizeof(T) == 4 || V * NV > 8;   // gamma again for every row, from L1
+    // 16 elements in each of 1024 threads, which have 64 registers each.
+    constexpr bool kReread = V * NV > 8 && (TPR == 1024 || TPR == -1024);
     constexpr int P = V * NV / 2;
     extern __shared__ uint4 ring[];   // (stages, arrays, dim) elements: H, dY, dH
     __shared__ float sh[2][ln_warps(TPR)];
@@ -261,6 +265,19 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
 #pragma unroll
         for (int m = 0; m < P; ++m) gm[m] = ln_pair_of(pg, m);
     };
+    // gamma of elements j and j + 1 of pack i, from L1 (V = 1: of the one element).
+    auto gamma_of = [&](int i, int j) {
+        const int k = (i * tpr + t) * V + j;
+        if (!p.gamma || !inside(i)) return make_float2(1.0f, 1.0f);
+        LnPack<W, (V > 1 ? 2 : 1)> w;
+        if constexpr (V > 1) {
+            w.load(p.gamma + k);
+            return w.pair(0);
+        } else {
+            w.load(p.gamma + k);
+            return make_float2(w[0], 0.0f);
+        }
+    };
     if constexpr (!kReload) load_gamma();
 #pragma unroll
     for (int m = 0; m < P; ++m) dg[m] = make_float2(0.0f, 0.0f);
@@ -271,7 +288,6 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
     for (; row < rows; row += step, it ^= 1) {
         const float rstd = next_rstd;
         if (row + step < rows) next_rstd = __ldg(p.rstd + row + step);
-        if constexpr (kReload) load_gamma();
         if (!mbar_try_wait(full0 + 8u * static_cast<uint32_t>(s), ph)) {
             const long long t0 = clock64();
             while (!mbar_try_wait(full0 + 8u * static_cast<uint32_t>(s), ph))
@@ -287,34 +303,92 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
                 e += (reinterpret_cast<uint64_t>(source(h) + static_cast<int64_t>(row) * p.dim) & 15u) / sizeof(T);
             return e;
         };
-        LnPack<T, V> px[NV], pd[NV], ps[NV];
-        {
-            const T *x = place(0), *dy = place(1);
+        // Pack i of array h of the row; zeros past its end, which add nothing to any sum.
+        auto piece = [&](LnPack<T, V> &pack, int h, int i) {
+            if (inside(i)) pack.load_shared(place(h) + (i * tpr + t) * V);
+            else pack.fill(0.0f);
+        };
+        float2 z[P];   // in the end dX
+        float2 sum2 = make_float2(0.0f, 0.0f);
+        const float2 rstd2 = make_float2(rstd, rstd);
+        if constexpr (kReread) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int k = (i * tpr + t) * V;
-                if (inside(i)) {
-                    px[i].load_shared(x + k);
-                    pd[i].load_shared(dy + k);
-                } else {
-                    px[i].fill(0.0f);
-                    pd[i].fill(0.0f);   // adds nothing to any sum
+                LnPack<T, V> ph, pd;
+                piece(ph, 0, i);
+                piece(pd, 1, i);
+#pragma unroll
+                for (int j = 0; j < V; j += 2) {
+                    // With V = 1 a pair is two packs: left to the single elements below.
+                    const float2 d = V > 1 ? pd.pair(j / 2) : make_float2(pd[0], 0.0f);
+                    const float2 x = V > 1 ? ph.pair(j / 2) : make_float2(ph[0], 0.0f);
+                    float2 &acc = dg[(i * V + j) / 2];
+                    const float2 zz = mul_f32x2(x, rstd2), ga = gamma_of(i, j);
+                    if constexpr (V > 1) {
+                        acc = fma_f32x2(d, zz, acc);
+                    } else {
+                        float &one = i & 1 ? acc.y : acc.x;
+                        one = fmaf(d.x, zz.x, one);
+                    }
+                    sum2 = fma_f32x2(mul_f32x2(d, ga), zz, sum2);
                 }
             }
+            const float c = ln_row_sum<TPR>(sum2.x + sum2.y, sh[it]) * p.inv_dim;
+            if (failed[it]) {   // the same answer for every thread: set before the barrier
+                ok = false;
+                break;
+            }
+            // The slot of the row before, which every thread has left.
+            if (t == 0 && p.stages > 1) {
+                const uint32_t next = row + static_cast<uint32_t>(p.stages - 1) * step;
+                if (row != blockIdx.x && next < rows) fetch(next, s == 0 ? p.stages - 1 : s - 1);
+            }
+            T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!inside(i)) continue;
+                LnPack<T, V> ph, pd, ps, out;
+                piece(ph, 0, i);
+                piece(pd, 1, i);
+                if (p.dH) piece(ps, 2, i);
+                else ps.fill(0.0f);
+                if constexpr (V == 1) {
+                    const float v = fmaf(ph[0] * rstd, -c, pd[0] * gamma_of(i, 0).x);
+                    out.e[0] = ln_round<T>(fmaf(v, rstd, ps[0]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) {
+                        const float2 zz = mul_f32x2(ph.pair(j), rstd2), gz = mul_f32x2(pd.pair(j), gamma_of(i, 2 * j));
+                        out.set_pair(j, fma_f32x2(fma_f32x2(zz, make_float2(-c, -c), gz), rstd2, ps.pair(j)));
+                    }
+                }
+                out.store(dx + (i * tpr + t) * V);
+            }
+            if (p.stages == 1) {
+                __syncthreads();   // the one slot is read
+                if (t == 0 && row + step < rows) fetch(row + step, 0);
+            }
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+            continue;
+        }
+        if constexpr (kReload && !kReread) load_gamma();
+        LnPack<T, V> px[NV], pd[NV], ps[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            piece(px[i], 0, i);
+            piece(pd[i], 1, i);
         }
         if (p.dH) {
-            const T *dh = place(2);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (inside(i)) ps[i].load_shared(dh + (i * tpr + t) * V);
-                else ps[i].fill(0.0f);
+            for (int i = 0; i < NV; ++i) piece(ps[i], 2, i);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) ps[i].fill(0.0f);
         }
-        float2 z[P], g[P];
-        float2 sum2 = make_float2(0.0f, 0.0f);
-        const float2 rstd2 = make_float2(rstd, rstd);
+        float2 g[P];
 #pragma unroll
         for (int m = 0; m < P; ++m) {
             const float2 d = ln_pair_of(pd, m);
