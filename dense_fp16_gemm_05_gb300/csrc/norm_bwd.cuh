@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "gemm_kernel.cuh"
 #include "layer_norm.cuh"
@@ -71,17 +72,21 @@ __global__ void __launch_bounds__(NW * 32) norm_bwd_finish(const float *__restri
     float s = 0.0f, c = 0.0f;
     if (k < dim) {
         auto at = [&](int r) { return src[static_cast<int64_t>(r) * dim + k]; };
-        constexpr int B = 8;   // loads under way
-        int r = w;
-        for (; r + (B - 1) * NW < parts; r += B * NW) {
+        // Ten loads under way at a time, or four for the last few: a few hundred parts
+        // come at once.  Zeros in the place of parts that are not there change no sum.
+        // (RMS norm, both kernels, with eight and the rest by fours: 1000 x 1024 fp16
+        // 7.5 us, 6.2 us so; 64 x 4096 5.5 and 5.4.)
+        auto batch = [&](auto count, int r0) {
+            constexpr int B = decltype(count)::value;
             float x[B];
 #pragma unroll
-            for (int i = 0; i < B; ++i) x[i] = at(r + i * NW);
+            for (int i = 0; i < B; ++i) x[i] = r0 + i * NW < parts ? at(r0 + i * NW) : 0.0f;
 #pragma unroll
             for (int i = 0; i < B; ++i) ln_add_exact(s, c, x[i]);
-        }
-#pragma unroll 4
-        for (; r < parts; r += NW) ln_add_exact(s, c, at(r));
+        };
+        int r = w;
+        for (; r + 4 * NW < parts; r += 10 * NW) batch(std::integral_constant<int, 10>{}, r);
+        if (r < parts) batch(std::integral_constant<int, 4>{}, r);
     }
     // NW neighbouring lanes take a column's sums.  One array for both: with two
     // these blocks started later (1000 x 1023 fp32: 11.3 us, 8.7 us so), likely for

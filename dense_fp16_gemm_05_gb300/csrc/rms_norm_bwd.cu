@@ -447,8 +447,16 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
     for (int i = 0; i < NV; ++i) {
         const int k = (i * tpr + t) * V;
         if (!inside(i)) continue;
+        if constexpr (V >= 4) {   // dim is a multiple of V, the workspace on the 16-byte grid
 #pragma unroll
-        for (int j = 0; j < V; ++j) out[k + j] = ln_half(dg[(i * V + j) / 2], i * V + j);
+            for (int j = 0; j < V; j += 4) {
+                const float2 a = dg[(i * V + j) / 2], b = dg[(i * V + j) / 2 + 1];
+                *reinterpret_cast<float4 *>(out + k + j) = make_float4(a.x, a.y, b.x, b.y);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[k + j] = ln_half(dg[(i * V + j) / 2], i * V + j);
+        }
     }
 }
 
@@ -494,14 +502,15 @@ __global__ void __launch_bounds__(256) rms_norm_bwd_columns(RmsBwdParams<T, W> p
     }
 }
 
-// The second kernel, if dgamma is wanted; block sizes as for layer norm.
+// The second kernel, if dgamma is wanted: 32 warps per block for short rows, whose few
+// columns few blocks share, and for many parts.
 template <class T, class W>
 int finish(const RmsBwdParams<T, W> &p, cudaStream_t stream)
 {
     if (p.part == nullptr) return GEMM_OK;
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.dim) + 31) / 32), 1, 1);
     const float *part = p.part;
-    if (p.parts > 2 * p.sm_count)
+    if (p.parts > 2 * p.sm_count || (p.parts > p.sm_count && p.dim <= 32 * p.sm_count))
         return ln_launch(norm_bwd_finish<W, 32>, grid, 1024, stream, part, p.dgamma, p.dgamma, p.parts, p.dim);
     return ln_launch(norm_bwd_finish<W, 16>, grid, 512, stream, part, p.dgamma, p.dgamma, p.parts, p.dim);
 }
