@@ -7,9 +7,9 @@
 // with counter (e / 4, offset), 64 bits each, and key seed is at least
 // floor(p 2^32).  The gradient is the same call on dY without a residual: the
 // mask is made again from seed and offset and never stored.  Ten rounds for four
-// elements are some 15 instructions for each beside 4 to 6 bytes: with a residual the
-// pass is bound by memory (16384 x 4096 fp16 59 us, 6.8 TB/s), without one by
-// instructions (61 us, 4.4 TB/s).
+// elements are some 19 instructions for each beside 4 to 6 bytes: with a residual the
+// pass is bound by memory (16384 x 4096 fp16 58 us, 6.9 TB/s), without one by the pipe
+// that multiplies whole numbers (54 us, 4.9 TB/s).
 #include "feed_forward_launch.cuh"
 #include "layer_norm.cuh"
 
@@ -50,12 +50,13 @@ __device__ __forceinline__ Words philox(uint64_t index, uint64_t offset, const u
 }
 
 // Packs of a thread, a block's threads apart: the keys and the offset's products are
-// the same for all of them (with one pack per thread 77 us and 68 us).
-constexpr int kPacks = 4;
+// the same for all of them.  Two, in registers that let eight blocks run on an SM: one
+// pack 73 us and 65 us (with and without a residual), four on five blocks 57 and 58.
+constexpr int kPacks = 2;
 
 // V elements at a time: 16 bytes, or the four of one counter one by one.
 template <class T, int V, bool kPacked>
-__global__ void __launch_bounds__(256) dropout_kernel(DropoutParams<T> p)
+__global__ void __launch_bounds__(256, 8) dropout_kernel(DropoutParams<T> p)
 {
     griddep_wait();
     griddep_launch_dependents();
