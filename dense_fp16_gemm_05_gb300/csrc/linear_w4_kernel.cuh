@@ -224,14 +224,20 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         q_src = p.Q + (static_cast<int64_t>(strip) * p.k_tiles + 2 * u) * kW4TileBytes + lane * 16;
         side_src = side_base + (static_cast<int64_t>(strip) * p.groups + static_cast<int64_t>(u) * U) * side_bytes;
     };
-    // Unit u, the last of which may have one tile, and scales of fewer groups: zeros
-    // stand for the others.
-    auto fetch = [&](int slot, int u) {
-        const uint32_t dst = ring_at + static_cast<uint32_t>(slot * Shape::SLOT);
-        const bool tile2 = 2 * u + 1 < p.k_tiles, in = u * U + side_group < p.groups;
-        w4_copy16(dst + lane * 16, q_src);
-        w4_copy16(dst + 512 + lane * 16, tile2 ? q_src + 512 : q_src, tile2 ? 16u : 0u);
-        if (side) w4_copy8(dst + side_to, in ? side_src : p.Q, in);
+    // Unit u into the slot at `dst` bytes.  The last unit may have one tile, and scales of
+    // fewer groups: zeros stand for the others.
+    const uint32_t q_to = ring_at + lane * 16, s_to = ring_at + side_to;
+    auto fetch = [&](uint32_t dst, int u) {
+        if (u + 1 < p.units) {
+            w4_copy16(q_to + dst, q_src);
+            w4_copy16(q_to + dst + 512, q_src + 512);
+            if (side) w4_copy8(s_to + dst, side_src, true);
+        } else {
+            const bool tile2 = 2 * u + 1 < p.k_tiles, in = u * U + side_group < p.groups;
+            w4_copy16(q_to + dst, q_src);
+            w4_copy16(q_to + dst + 512, tile2 ? q_src + 512 : q_src, tile2 ? 16u : 0u);
+            if (side) w4_copy8(s_to + dst, in ? side_src : p.Q, in);
+        }
         q_src += q_step;
         side_src += side_step;
     };
@@ -364,35 +370,41 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         w4_commit();
         // The copies run ahead of the products by D units, over the strips' ends.
         const int strip_step = static_cast<int>(gridDim.x) * p.rw, strip_first = static_cast<int>(blockIdx.x) * p.rw;
-        int ahead_strip = strip_first, ahead = 0;
-        auto next = [&](int slot) {
-            if (mine > 0 && ahead_strip < p.strips) {
-                if (ahead == 0) seek(ahead_strip + rw, first);
-                fetch(slot, first + ahead * p.kw);
-                if (++ahead == mine) {
-                    ahead = 0;
+        // Of the strip under way there, the next unit to fetch; of the last, none.
+        int ahead_strip = strip_first, ahead = mine > 0 && strip_first < p.strips ? first : u_end;
+        seek(ahead_strip + rw, first);
+        auto next = [&](uint32_t dst) {
+            if (ahead < u_end) {
+                fetch(dst, ahead);
+                ahead += p.kw;
+                if (ahead >= u_end) {
                     ahead_strip += strip_step;
+                    if (ahead_strip < p.strips) {
+                        ahead = first;
+                        seek(ahead_strip + rw, first);
+                    }
                 }
             }
             w4_commit();
         };
 #pragma unroll
-        for (int i = 0; i < D; ++i) next(i);
+        for (int i = 0; i < D; ++i) next(i * Shape::SLOT);
         w4_wait<D>();
         __syncthreads();   // X is there
         const uint8_t *x_first = x_mem + kw * 256;
-        int slot = 0, buffer = 0;
+        uint32_t slot = 0;   // bytes
+        int buffer = 0;
         for (int strip0 = strip_first; strip0 < p.strips; strip0 += strip_step) {
             clear();
             const uint8_t *x_unit = x_first;
             for (int i = 0; i < mine; ++i) {
                 w4_wait<D - 1>();
                 __syncwarp();
-                unit(ring + slot * Shape::SLOT, x_unit);
+                unit(ring + slot, x_unit);
                 x_unit += p.kw * 256;
                 __syncwarp();
                 next(slot);
-                if (++slot == D) slot = 0;
+                slot = slot == (D - 1) * Shape::SLOT ? 0u : slot + Shape::SLOT;
             }
             keep(part[buffer]);
             __syncthreads();
@@ -412,10 +424,11 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         copy_x(x_mem, u_begin, min(XU, n));
 #pragma unroll
         for (int i = 0; i < D; ++i) {
-            if (i < n) fetch(i, u_begin + i);
+            if (i < n) fetch(i * Shape::SLOT, u_begin + i);
             w4_commit();
         }
-        int slot = 0, x_unit = 0, x_buffer = 0;
+        uint32_t slot = 0;   // bytes
+        int x_unit = 0, x_buffer = 0;
         for (int i = 0; i < n; ++i) {
             w4_wait<D - 1>();
             if (x_unit == 0) {
@@ -424,11 +437,11 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
             } else {
                 __syncwarp();
             }
-            unit(ring + slot * Shape::SLOT, x_mem + x_buffer * p.x_bytes + x_unit * 256);
+            unit(ring + slot, x_mem + x_buffer * p.x_bytes + x_unit * 256);
             __syncwarp();
             if (i + D < n) fetch(slot, u_begin + i + D);
             w4_commit();
-            if (++slot == D) slot = 0;
+            slot = slot == (D - 1) * Shape::SLOT ? 0u : slot + Shape::SLOT;
             if (++x_unit == XU) {
                 x_unit = 0;
                 x_buffer ^= 1;
