@@ -16,7 +16,7 @@
 // scales and zero points -- through its own ring of asynchronous copies in shared
 // memory: nothing but its own copies makes a warp wait, and the bytes under way are
 // not bounded by registers.  A block's sixteen warps are RW strips of 16 rows times
-// KW = 16 / RW ways that the strips' columns are divided, whose sums are added
+// KW ways that the strips' columns are divided, whose sums are added
 // through shared memory in a fixed order.  X stays in shared memory for the whole
 // call where it fits, while blocks walk over the strips; else it comes in chunks for
 // 16 strips at a time, so that it is read less often than W.  K may also be divided
@@ -363,9 +363,10 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
 
     if (p.keep_x) {
         // Groups of rw strips blockIdx.x, blockIdx.x + gridDim.x, ...; this warp has units
-        // u_begin + kw, u_begin + kw + KW, ... of its strip of each, `mine` of them.
+        // u_begin + kw, u_begin + kw + KW, ... of its strip of each, `mine` of them (none, if
+        // it is beyond the rw kw warps that there is work for).
         Sums *part = reinterpret_cast<Sums *>(x_mem + p.x_bytes);
-        const int first = u_begin + kw, mine = first < u_end ? (u_end - first + p.kw - 1) / p.kw : 0;
+        const int first = u_begin + kw, mine = kw < p.kw && first < u_end ? (u_end - first + p.kw - 1) / p.kw : 0;
         copy_x(x_mem, u_begin, u_end - u_begin);
         w4_commit();
         // The copies run ahead of the products by D units, over the strips' ends.
@@ -414,12 +415,12 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
             if (slices == 1) buffer ^= 1;
         }
     } else {
-        // One strip per warp (kw = 0), units u_begin .. u_end - 1; X in chunks that the
+        // One strip per warp (rw = 16), units u_begin .. u_end - 1; X in chunks that the
         // block shares.
         constexpr int XU = Shape::X_UNITS;
         static_assert(XU >= D, "a chunk of X is there when the units copied with it are");
         const int n = u_end - u_begin;
-        seek(static_cast<int>(blockIdx.x) * kW4Warps + warp, u_begin);
+        seek(static_cast<int>(blockIdx.x) * p.rw + rw, u_begin);
         clear();
         copy_x(x_mem, u_begin, min(XU, n));
 #pragma unroll
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         Sums &sums = *reinterpret_cast<Sums *>(smem);
         keep(sums);
         __syncthreads();
-        finish(sums, reinterpret_cast<float *>(&sums + 1), static_cast<int>(blockIdx.x) * kW4Warps);
+        finish(sums, reinterpret_cast<float *>(&sums + 1), static_cast<int>(blockIdx.x) * p.rw);
     }
 }
 
@@ -464,37 +465,46 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
     using Shape = W4Shape<NT, G>;
     auto kern = linear_w4_kernel<T, NT, G>;
     // The division of the work that costs least by this count of nanoseconds, fitted to
-    // whole calls of 16 shapes (1 x 64 x 64 to 64 x 16384 x 8192) under every division: a
-    // unit of each of a block's warps takes 450 with 8 rows of X, 1850 with 64; a group
-    // of strips ends with 500, more among the blocks of a cluster, and a quarter for each
-    // output; X comes with 60 bytes each, 20 where its rows are off the 16-byte grid, and
-    // in chunks half hidden.  The count's choice is within 10 % of the best of all but
-    // the smallest calls.
-    const int64_t sms = a.sm_count, strips = p.strips;
+    // whole calls of 18 shapes (1 x 64 x 64 to 64 x 16384 x 8192) under every division (its
+    // choice was within a tenth of the best of each, but one of the smallest): a
+    // unit of each of a block's sixteen warps takes 450 with 8 rows of X, 1850 with 64,
+    // and with fewer warps as much less, down to eleven; a group of strips ends with 500,
+    // more among the blocks of a cluster, and a quarter for each output; X comes with 60
+    // bytes each, 20 where its rows are off the 16-byte grid, and in chunks half hidden.
     const int64_t room = kW4Budget - Shape::RING - 2 * Shape::SUMS;   // for a kept X
-    const int64_t unit_cost = NT == 1 ? 450 : (NT == 2 ? 650 : (NT == 4 ? 1030 : 1850));
-    int64_t least = INT64_MAX;
+    const float unit_cost = NT == 1 ? 450.0f : (NT == 2 ? 650.0f : (NT == 4 ? 1030.0f : 1850.0f));
+    static constexpr uint8_t kDivisions[][2] = {{16, 1}, {15, 1}, {14, 1}, {8, 2}, {7, 2}, {6, 2},
+                                                {5, 3},  {4, 4},  {3, 5},  {2, 8}, {2, 7}, {1, 16}};
+    float least = 1e30f;
     int slices = 1;
     for (int sl = 1; sl <= 8 && sl <= p.units; sl *= 2) {
-        const int64_t units = (p.units + sl - 1) / sl, x_bytes = p.M * w4_x_row(units);
-        const int64_t x_cost = x_bytes / (p.vec ? 60 : 20), end = sl == 1 ? 500 : (sl == 2 ? 1500 : (sl == 4 ? 3000 : 4000));
-        const int64_t most = sms / sl;   // clusters at a time
-        auto consider = [&](int keep, int kw) {
-            const int64_t rw = kW4Warps / kw, rounds = ((strips + rw - 1) / rw + most - 1) / most;
-            const int64_t group = (units + kw - 1) / kw * unit_cost + end + rw * 4 * p.M;
-            const int64_t cost = keep ? rounds * group + x_cost : rounds * (group + x_cost / 2);
-            if (cost >= least) return;
-            least = cost;
-            slices = sl;
-            p.keep_x = keep;
-            p.kw = kw;
-        };
-        consider(0, 1);
-        if (NT <= 4 && x_bytes <= room)
-            for (int kw = 1; kw <= kW4Warps && kw <= units; kw *= 2) consider(1, kw);
+        // Clusters at a time: of blocks that fill an SM a cluster lies within a part of the
+        // GPU, whose SMs larger clusters do not divide evenly (37 of four took as long as
+        // two rounds, 35 one).
+        const int units = (p.units + sl - 1) / sl, most = (a.sm_count - (sl > 2 ? 3 * sl : 0)) / sl;
+        const int64_t x_bytes = p.M * w4_x_row(units);
+        const float x_cost = static_cast<float>(x_bytes) / (p.vec ? 60.0f : 20.0f);
+        const float end = sl == 1 ? 500.0f : (sl == 2 ? 1500.0f : (sl == 4 ? 3000.0f : 4000.0f));
+        const bool fits = NT <= 4 && x_bytes <= room;
+        for (const auto &d : kDivisions) {
+            const int rw = d[0], kw = d[1];
+            if (kw > units) break;
+            const int rounds = ((p.strips + rw - 1) / rw + most - 1) / most, warps = rw * kw > 11 ? rw * kw : 11;
+            const float group = static_cast<float>((units + kw - 1) / kw * warps) * (unit_cost / 16.0f) + end +
+                                static_cast<float>(rw * 4 * p.M);
+            auto consider = [&](float cost, int keep) {
+                if (cost >= least) return;
+                least = cost;
+                slices = sl;
+                p.keep_x = keep;
+                p.rw = rw;
+                p.kw = kw;
+            };
+            if (rw == kW4Warps) consider(static_cast<float>(rounds) * (group + 0.5f * x_cost), 0);
+            if (fits) consider(static_cast<float>(rounds) * group + x_cost, 1);
+        }
     }
-    p.rw = kW4Warps / p.kw;
-    const int64_t groups = (strips + p.rw - 1) / p.rw, most = sms / slices;
+    const int groups = (p.strips + p.rw - 1) / p.rw, most = a.sm_count / slices;
     int64_t smem = Shape::RING;
     if (p.keep_x) {
         p.x_row = static_cast<int32_t>(w4_x_row((p.units + slices - 1) / slices));

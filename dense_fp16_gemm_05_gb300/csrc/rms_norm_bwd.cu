@@ -368,61 +368,57 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
                 __syncthreads();   // the one slot is read
                 if (t == 0 && row + step < rows) fetch(row + step, 0);
             }
-            if (++s == p.stages) {
-                s = 0;
-                ph ^= 1u;
-            }
-            continue;
-        }
-        if constexpr (kReload && !kReread) load_gamma();
-        LnPack<T, V> px[NV], pd[NV], ps[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            piece(px[i], 0, i);
-            piece(pd[i], 1, i);
-        }
-        if (p.dH) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) piece(ps[i], 2, i);
         } else {
+            if constexpr (kReload) load_gamma();
+            LnPack<T, V> px[NV], pd[NV], ps[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) ps[i].fill(0.0f);
-        }
-        float2 g[P];
+            for (int i = 0; i < NV; ++i) {
+                piece(px[i], 0, i);
+                piece(pd[i], 1, i);
+            }
+            if (p.dH) {
 #pragma unroll
-        for (int m = 0; m < P; ++m) {
-            const float2 d = ln_pair_of(pd, m);
-            z[m] = mul_f32x2(ln_pair_of(px, m), rstd2);
-            g[m] = mul_f32x2(d, gm[m]);
-            sum2 = fma_f32x2(g[m], z[m], sum2);
-            dg[m] = fma_f32x2(d, z[m], dg[m]);
-        }
-        const float c = ln_row_sum<TPR>(sum2.x + sum2.y, sh[it]) * p.inv_dim;
-        if (failed[it]) {   // the same answer for every thread: set before the barrier
-            ok = false;
-            break;
-        }
-        if (t == 0) {
-            const uint32_t next = row + static_cast<uint32_t>(p.stages) * step;
-            if (next < rows) fetch(next, s);
-        }
-        const float2 neg_c2 = make_float2(-c, -c);
-#pragma unroll
-        for (int m = 0; m < P; ++m)
-            z[m] = fma_f32x2(fma_f32x2(z[m], neg_c2, g[m]), rstd2, ln_pair_of(ps, m));
-        T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int k = (i * tpr + t) * V;
-            if (!inside(i)) continue;
-            LnPack<T, V> out;
-            if constexpr (V == 1) {
-                out.e[0] = ln_round<T>(ln_half(z[i / 2], i));
+                for (int i = 0; i < NV; ++i) piece(ps[i], 2, i);
             } else {
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) out.set_pair(j, z[i * (V / 2) + j]);
+                for (int i = 0; i < NV; ++i) ps[i].fill(0.0f);
             }
-            out.store(dx + k);
+            float2 g[P];
+#pragma unroll
+            for (int m = 0; m < P; ++m) {
+                const float2 d = ln_pair_of(pd, m);
+                z[m] = mul_f32x2(ln_pair_of(px, m), rstd2);
+                g[m] = mul_f32x2(d, gm[m]);
+                sum2 = fma_f32x2(g[m], z[m], sum2);
+                dg[m] = fma_f32x2(d, z[m], dg[m]);
+            }
+            const float c = ln_row_sum<TPR>(sum2.x + sum2.y, sh[it]) * p.inv_dim;
+            if (failed[it]) {   // the same answer for every thread: set before the barrier
+                ok = false;
+                break;
+            }
+            if (t == 0) {
+                const uint32_t next = row + static_cast<uint32_t>(p.stages) * step;
+                if (next < rows) fetch(next, s);
+            }
+            const float2 neg_c2 = make_float2(-c, -c);
+#pragma unroll
+            for (int m = 0; m < P; ++m)
+                z[m] = fma_f32x2(fma_f32x2(z[m], neg_c2, g[m]), rstd2, ln_pair_of(ps, m));
+            T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int k = (i * tpr + t) * V;
+                if (!inside(i)) continue;
+                LnPack<T, V> out;
+                if constexpr (V == 1) {
+                    out.e[0] = ln_round<T>(ln_half(z[i / 2], i));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) out.set_pair(j, z[i * (V / 2) + j]);
+                }
+                out.store(dx + k);
+            }
         }
         if (++s == p.stages) {
             s = 0;
