@@ -174,6 +174,12 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR)) rms_norm_bwd_kernel(RmsB
 // threads (kReread) they are read a second time instead of being kept, and the slot is
 // refilled one row later.  Every wait is bounded: on expiry
 // the site is recorded in the device status word and the block leaves.
+//
+// Rows that are not whole 16-byte pieces (kShift) are taken with the whole pieces that
+// they lie in, from the first one on: a block's rows lie a multiple of a piece's elements
+// apart, so that all of them begin at the same place in their first piece, a thread's
+// columns are the same in each and only the first and the last piece of a row have
+// elements that are not its own (16384 x 4097 fp16 88 us; 262 us element by element).
 // Blocks per SM that the registers are held to.
 __host__ __device__ constexpr int rms_ring_blocks(int tpr, int per)
 {
@@ -181,13 +187,24 @@ __host__ __device__ constexpr int rms_ring_blocks(int tpr, int per)
     return per > 8 && tpr != -320 ? 1 : 2;
 }
 
-// TPR > 0: the row is exactly the threads' elements, no bounds to check.
-// kInner: every pack but a thread's last lies inside the row whatever the thread.
-template <class T, class W, int V, int NV, int TPR, bool kInner>
-__global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V * NV)) rms_norm_bwd_ring(RmsBwdParams<T, W> p)
+template <class T>
+constexpr int kPiece = 16 / static_cast<int>(sizeof(T));   // elements
+
+// Bytes of a row's place in the ring.
+template <class T, bool kShift>
+__host__ __device__ __forceinline__ uint32_t rms_row_bytes(int dim)
 {
+    const uint32_t bytes = static_cast<uint32_t>(dim) * static_cast<uint32_t>(sizeof(T));
+    return kShift ? (bytes + 15u) / 16u * 16u + 16u : bytes;
+}
+
+// TPR > 0: the row is exactly the threads' elements, no bounds to check.
+template <class T, class W, int NV, int TPR, bool kShift>
+__global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, kPiece<T> * NV)) rms_norm_bwd_ring(RmsBwdParams<T, W> p)
+{
+    constexpr int V = kPiece<T>;
     constexpr bool kFull = TPR > 0;
-    constexpr bool kReload = sizeof(T) == 4 || V * NV > 8;   // gamma again for every row, from L1
+    constexpr bool kReload = kShift || sizeof(T) == 4 || V * NV > 8;   // gamma again for every row, from L1
     // 16 elements in each of 1024 threads, which have 64 registers each.
     constexpr bool kReread = V * NV > 8 && (TPR == 1024 || TPR == -1024);
     constexpr int P = V * NV / 2;
@@ -195,13 +212,33 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
     __shared__ float sh[2][ln_warps(TPR)];
     __shared__ uint64_t full_mem[kRingStages];
     __shared__ volatile int failed[2];
+    __shared__ uint4 edge_mask[2];   // kShift: of the row's first and last piece
+    // kShift: the first and the last warp have the edges to see to.
+    constexpr int kIssuer = kShift ? 32 : 0;
     const int t = static_cast<int>(threadIdx.x), tpr = ln_threads<TPR>();
-    const uint32_t row_bytes = ring_row_bytes<T, V>(p.dim), slot_bytes = static_cast<uint32_t>(p.arrays) * row_bytes;
+    // Elements in front of the row in its first piece: the same number for all rows of
+    // the block.
+    const int shift = kShift ? static_cast<int>((reinterpret_cast<uint64_t>(p.H + static_cast<int64_t>(blockIdx.x) * p.dim) & 15u) / sizeof(T)) : 0;
+    auto column = [&](int i) { return (i * tpr + t) * V - shift; };   // of pack i's first element
+    auto inside = [&](int i) { return kFull || column(i) < p.dim; };
+    auto whole = [&](int i) { return !kShift || (column(i) >= 0 && column(i) + V <= p.dim); };
+    auto own = [&](int k) { return k >= 0 && k < p.dim; };
+    const uint32_t row_bytes = rms_row_bytes<T, kShift>(p.dim), slot_bytes = static_cast<uint32_t>(p.arrays) * row_bytes;
     const uint32_t ring_base = smem_addr(ring), full0 = smem_addr(full_mem);
     if (t == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(full0 + 8u * s, 1);
         failed[0] = failed[1] = 0;
         fence_mbar_init();
+    }
+    if (kShift && t < 2) {
+        const int tail = (p.dim + shift) % V;   // elements in the last piece, 0: all
+        T keep[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool in = t == 0 ? j >= shift : (tail == 0 || j < tail);
+            memset(&keep[j], in ? 0xFF : 0, sizeof(T));
+        }
+        memcpy(&edge_mask[t], keep, 16);
     }
     __syncthreads();
     griddep_wait();
@@ -210,34 +247,33 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
     auto fetch = [&](uint32_t row, int s) {
         const uint32_t bar = full0 + 8u * static_cast<uint32_t>(s);
         const uint32_t dst = ring_base + static_cast<uint32_t>(s) * slot_bytes;
-        if constexpr (kRingAny<T, V>) {
+        if constexpr (kShift) {
+            // The arrays' rows begin alike: one window for all.
             const uint32_t bytes = static_cast<uint32_t>(p.dim) * static_cast<uint32_t>(sizeof(T));
             const uint64_t size = static_cast<uint64_t>(p.rows) * bytes, at = static_cast<uint64_t>(row) * bytes;
-            uint8_t *to = reinterpret_cast<uint8_t *>(ring) + (dst - ring_base);
-            uint32_t total = 0;
-            for (int h = 0; h < p.arrays; ++h) {
-                const uint64_t base = reinterpret_cast<uint64_t>(source(h));
-                const RingWindow w(base + at, bytes, base, base + size);
-                // Elements in pieces that reach past the tensor's ends, one by one;
-                // the arrival below releases them to the waiting threads, and the
-                // fence orders them before the copies of the slot's later rows.
-                auto edge = [&](uint64_t a, uint64_t b) {
-                    for (; a < b; a += sizeof(T))
-                        *reinterpret_cast<T *>(to + h * row_bytes + (a - w.first)) = *reinterpret_cast<const T *>(a);
-                    fence_proxy_async_smem();
-                };
-                if (w.begin > w.src) edge(w.src, w.begin < w.last ? w.begin : w.last);
-                if (w.end < w.last) edge(w.end > w.src ? w.end : w.src, w.last);
-                total += static_cast<uint32_t>(w.end - w.begin);
+            const uint64_t base = reinterpret_cast<uint64_t>(p.H);
+            const RingWindow w(base + at, bytes, base, base + size);
+            const uint32_t n = static_cast<uint32_t>(w.end - w.begin);
+            // Elements in pieces that reach past the tensor's ends, one by one; the
+            // arrival below releases them to the waiting threads, and the fence orders
+            // them before the copies of the slot's later rows.
+            if (w.begin > w.src || w.end < w.last) {
+                uint8_t *to = reinterpret_cast<uint8_t *>(ring) + (dst - ring_base);
+                for (int h = 0; h < p.arrays; ++h) {
+                    const uint64_t from = reinterpret_cast<uint64_t>(source(h)) - base;
+                    auto edge = [&](uint64_t a, uint64_t b) {
+                        for (; a < b; a += sizeof(T))
+                            *reinterpret_cast<T *>(to + h * row_bytes + (a - w.first)) = *reinterpret_cast<const T *>(from + a);
+                    };
+                    if (w.begin > w.src) edge(w.src, w.begin);
+                    if (w.end < w.last) edge(w.end, w.last);
+                }
+                fence_proxy_async_smem();
             }
-            mbar_arrive_expect_tx(bar, total);
-            for (int h = 0; h < p.arrays; ++h) {
-                const uint64_t base = reinterpret_cast<uint64_t>(source(h));
-                const RingWindow w(base + at, bytes, base, base + size);
-                if (w.end > w.begin)
-                    bulk_load(dst + static_cast<uint32_t>(h) * row_bytes + static_cast<uint32_t>(w.begin - w.first),
-                              reinterpret_cast<const void *>(w.begin), static_cast<uint32_t>(w.end - w.begin), bar);
-            }
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.arrays) * n);
+            for (int h = 0; h < p.arrays; ++h)
+                bulk_load(dst + static_cast<uint32_t>(h) * row_bytes + static_cast<uint32_t>(w.begin - w.first),
+                          reinterpret_cast<const uint8_t *>(source(h)) + (w.begin - base), n, bar);
             return;
         }
         mbar_arrive_expect_tx(bar, slot_bytes);
@@ -249,33 +285,57 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
     // Rows as unsigned 32-bit numbers: the ones past the end may pass 2^31.
     const uint32_t step = gridDim.x, rows = static_cast<uint32_t>(p.rows);
     uint32_t row = blockIdx.x;
-    if (t == 0 && p.withhold == 0)
+    if (t == kIssuer && p.withhold == 0)
         for (int s = 0; s < p.stages && row + static_cast<uint32_t>(s) * step < rows; ++s)
             fetch(row + static_cast<uint32_t>(s) * step, s);
+    // kShift: gamma behind the ring, with the rows' columns.
+    constexpr bool kGammaShared = kShift && sizeof(T) == 2 && !kReread;
+    W *gamma_row = reinterpret_cast<W *>(reinterpret_cast<uint8_t *>(ring) + static_cast<size_t>(p.stages) * slot_bytes);
+    if constexpr (kGammaShared) {
+        W w[V * NV];   // all loads under way at once
+#pragma unroll
+        for (int u = 0; u < V * NV; ++u) {
+            const int k = u * tpr + t - shift;
+            w[u] = p.gamma && own(k) ? __ldg(p.gamma + k) : ln_round<W>(1.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < V * NV; ++u) {
+            const int k = u * tpr + t;
+            if (k < (p.dim + 2 * V - 1) / V * V) gamma_row[k] = w[u];
+        }
+        __syncthreads();
+    }
 
-    auto inside = [&](int i) { return kFull || (kInner && i < NV - 1) || (i * tpr + t) * V < p.dim; };
     float2 dg[P], gm[P];
     auto load_gamma = [&]() {
         LnPack<W, V> pg[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (p.gamma && inside(i)) pg[i].load(p.gamma + (i * tpr + t) * V);
-            else pg[i].fill(1.0f);
+            pg[i].fill(1.0f);
+            if ((!kGammaShared && !p.gamma) || !inside(i)) continue;
+            if constexpr (kGammaShared) {
+                pg[i].load_shared(gamma_row + (i * tpr + t) * V);
+            } else if constexpr (kShift) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (own(column(i) + j)) pg[i].e[j] = __ldg(p.gamma + column(i) + j);
+            } else {
+                pg[i].load(p.gamma + column(i));
+            }
         }
 #pragma unroll
         for (int m = 0; m < P; ++m) gm[m] = ln_pair_of(pg, m);
     };
-    // gamma of elements j and j + 1 of pack i, from L1 (V = 1: of the one element).
+    // gamma of elements j and j + 1 of pack i, from L1.
     auto gamma_of = [&](int i, int j) {
-        const int k = (i * tpr + t) * V + j;
+        const int k = column(i) + j;
         if (!p.gamma || !inside(i)) return make_float2(1.0f, 1.0f);
-        LnPack<W, (V > 1 ? 2 : 1)> w;
-        if constexpr (V > 1) {
+        if constexpr (kShift) {
+            return make_float2(own(k) ? ln_float(__ldg(p.gamma + k)) : 0.0f, own(k + 1) ? ln_float(__ldg(p.gamma + k + 1)) : 0.0f);
+        } else {
+            LnPack<W, 2> w;
             w.load(p.gamma + k);
             return w.pair(0);
-        } else {
-            w.load(p.gamma + k);
-            return make_float2(w[0], 0.0f);
         }
     };
     if constexpr (!kReload) load_gamma();
@@ -297,16 +357,31 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
                 }
         }
         const uint8_t *slot = reinterpret_cast<const uint8_t *>(ring) + static_cast<size_t>(s) * slot_bytes;
-        auto place = [&](int h) {
-            const T *e = reinterpret_cast<const T *>(slot + static_cast<size_t>(h) * row_bytes);
-            if constexpr (kRingAny<T, V>)
-                e += (reinterpret_cast<uint64_t>(source(h) + static_cast<int64_t>(row) * p.dim) & 15u) / sizeof(T);
-            return e;
-        };
-        // Pack i of array h of the row; zeros past its end, which add nothing to any sum.
+        // Pack i of array h of the row; of H and dY zeros for what is not the row's own,
+        // which add nothing to any sum.
         auto piece = [&](LnPack<T, V> &pack, int h, int i) {
-            if (inside(i)) pack.load_shared(place(h) + (i * tpr + t) * V);
-            else pack.fill(0.0f);
+            if (!inside(i)) {
+                pack.fill(0.0f);
+                return;
+            }
+            pack.load_shared(reinterpret_cast<const T *>(slot + static_cast<size_t>(h) * row_bytes) + (i * tpr + t) * V);
+            if (kShift && h < 2 && !whole(i)) {
+                const uint4 mask = edge_mask[column(i) < 0 ? 0 : 1];
+                uint4 raw;
+                memcpy(&raw, pack.e, 16);
+                raw = make_uint4(raw.x & mask.x, raw.y & mask.y, raw.z & mask.z, raw.w & mask.w);
+                memcpy(pack.e, &raw, 16);
+            }
+        };
+        T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
+        auto put = [&](const LnPack<T, V> &pack, int i) {
+            if (whole(i)) {
+                pack.store(dx + column(i));
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (own(column(i) + j)) dx[column(i) + j] = pack.e[j];
+            }
         };
         float2 z[P];   // in the end dX
         float2 sum2 = make_float2(0.0f, 0.0f);
@@ -314,23 +389,15 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
         if constexpr (kReread) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                LnPack<T, V> ph, pd;
-                piece(ph, 0, i);
+                LnPack<T, V> px, pd;
+                piece(px, 0, i);
                 piece(pd, 1, i);
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    // With V = 1 a pair is two packs: left to the single elements below.
-                    const float2 d = V > 1 ? pd.pair(j / 2) : make_float2(pd[0], 0.0f);
-                    const float2 x = V > 1 ? ph.pair(j / 2) : make_float2(ph[0], 0.0f);
-                    float2 &acc = dg[(i * V + j) / 2];
-                    const float2 zz = mul_f32x2(x, rstd2), ga = gamma_of(i, j);
-                    if constexpr (V > 1) {
-                        acc = fma_f32x2(d, zz, acc);
-                    } else {
-                        float &one = i & 1 ? acc.y : acc.x;
-                        one = fmaf(d.x, zz.x, one);
-                    }
-                    sum2 = fma_f32x2(mul_f32x2(d, ga), zz, sum2);
+                for (int j = 0; j < V / 2; ++j) {
+                    const float2 d = pd.pair(j), zz = mul_f32x2(px.pair(j), rstd2);
+                    float2 &acc = dg[i * (V / 2) + j];
+                    acc = fma_f32x2(d, zz, acc);
+                    sum2 = fma_f32x2(mul_f32x2(d, gamma_of(i, 2 * j)), zz, sum2);
                 }
             }
             const float c = ln_row_sum<TPR>(sum2.x + sum2.y, sh[it]) * p.inv_dim;
@@ -339,34 +406,28 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
                 break;
             }
             // The slot of the row before, which every thread has left.
-            if (t == 0 && p.stages > 1) {
+            if (t == kIssuer && p.stages > 1) {
                 const uint32_t next = row + static_cast<uint32_t>(p.stages - 1) * step;
                 if (row != blockIdx.x && next < rows) fetch(next, s == 0 ? p.stages - 1 : s - 1);
             }
-            T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!inside(i)) continue;
-                LnPack<T, V> ph, pd, ps, out;
-                piece(ph, 0, i);
+                LnPack<T, V> px, pd, ps, out;
+                piece(px, 0, i);
                 piece(pd, 1, i);
                 if (p.dH) piece(ps, 2, i);
                 else ps.fill(0.0f);
-                if constexpr (V == 1) {
-                    const float v = fmaf(ph[0] * rstd, -c, pd[0] * gamma_of(i, 0).x);
-                    out.e[0] = ln_round<T>(fmaf(v, rstd, ps[0]));
-                } else {
 #pragma unroll
-                    for (int j = 0; j < V / 2; ++j) {
-                        const float2 zz = mul_f32x2(ph.pair(j), rstd2), gz = mul_f32x2(pd.pair(j), gamma_of(i, 2 * j));
-                        out.set_pair(j, fma_f32x2(fma_f32x2(zz, make_float2(-c, -c), gz), rstd2, ps.pair(j)));
-                    }
+                for (int j = 0; j < V / 2; ++j) {
+                    const float2 zz = mul_f32x2(px.pair(j), rstd2), gz = mul_f32x2(pd.pair(j), gamma_of(i, 2 * j));
+                    out.set_pair(j, fma_f32x2(fma_f32x2(zz, make_float2(-c, -c), gz), rstd2, ps.pair(j)));
                 }
-                out.store(dx + (i * tpr + t) * V);
+                put(out, i);
             }
             if (p.stages == 1) {
                 __syncthreads();   // the one slot is read
-                if (t == 0 && row + step < rows) fetch(row + step, 0);
+                if (t == kIssuer && row + step < rows) fetch(row + step, 0);
             }
         } else {
             if constexpr (kReload) load_gamma();
@@ -397,7 +458,7 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
                 ok = false;
                 break;
             }
-            if (t == 0) {
+            if (t == kIssuer) {
                 const uint32_t next = row + static_cast<uint32_t>(p.stages) * step;
                 if (next < rows) fetch(next, s);
             }
@@ -405,19 +466,13 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
 #pragma unroll
             for (int m = 0; m < P; ++m)
                 z[m] = fma_f32x2(fma_f32x2(z[m], neg_c2, g[m]), rstd2, ln_pair_of(ps, m));
-            T *dx = p.dX + static_cast<int64_t>(row) * p.dim;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int k = (i * tpr + t) * V;
                 if (!inside(i)) continue;
                 LnPack<T, V> out;
-                if constexpr (V == 1) {
-                    out.e[0] = ln_round<T>(ln_half(z[i / 2], i));
-                } else {
 #pragma unroll
-                    for (int j = 0; j < V / 2; ++j) out.set_pair(j, z[i * (V / 2) + j]);
-                }
-                out.store(dx + k);
+                for (int j = 0; j < V / 2; ++j) out.set_pair(j, z[i * (V / 2) + j]);
+                put(out, i);
             }
         }
         if (++s == p.stages) {
@@ -441,9 +496,9 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
     float *out = p.part + static_cast<int64_t>(blockIdx.x) * p.dim;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int k = (i * tpr + t) * V;
+        const int k = column(i);
         if (!inside(i)) continue;
-        if constexpr (V >= 4) {   // dim is a multiple of V, the workspace on the 16-byte grid
+        if constexpr (!kShift) {   // dim is a multiple of V, the workspace on the 16-byte grid
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
                 const float2 a = dg[(i * V + j) / 2], b = dg[(i * V + j) / 2 + 1];
@@ -451,7 +506,8 @@ __global__ void __launch_bounds__(rms_bwd_threads(TPR), rms_ring_blocks(TPR, V *
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) out[k + j] = ln_half(dg[(i * V + j) / 2], i * V + j);
+            for (int j = 0; j < V; ++j)
+                if (own(k + j)) out[k + j] = ln_half(dg[(i * V + j) / 2], i * V + j);
         }
     }
 }
@@ -543,10 +599,32 @@ int launch_one(const RmsBwdParams<T, W> &p, cudaStream_t stream)
     return st != GEMM_OK ? st : finish<T, W>(p, stream);
 }
 
-template <class T, class W, int V, int NV, int TPR, bool kInner>
-int launch_ring_kernel(const RmsBwdParams<T, W> &p, int device, int threads, int64_t stage, cudaStream_t stream)
+// The ring kernel, where one row fits a block's share of the shared memory.
+template <class T, class W, int NV, int TPR, bool kShift>
+int launch_ring(RmsBwdParams<T, W> p, int device, cudaStream_t stream, bool *done)
 {
-    auto kern = rms_norm_bwd_ring<T, W, V, NV, TPR, kInner>;
+    constexpr int V = kPiece<T>;
+    const int packs = (p.dim + (kShift ? 2 * V - 2 : V - 1)) / V;
+    const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    // Blocks per SM: those of the launch bound, or more where they are small.
+    const int fit_blocks = V * NV > 8 ? rms_ring_blocks(TPR, V * NV) : 1024 / threads;
+    const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
+    p.arrays = p.dH ? 3 : 2;
+    const int64_t stage = p.arrays * static_cast<int64_t>(rms_row_bytes<T, kShift>(p.dim));
+    constexpr bool kGammaShared = kShift && sizeof(T) == 2 && TPR != -1024;
+    const int64_t gamma_bytes = kGammaShared ? (p.dim + 2 * V - 1) / V * V * static_cast<int64_t>(sizeof(W)) : 0;
+    const int64_t fit = (budget - gamma_bytes) / stage;
+    *done = fit >= 1;
+    if (fit < 1) return GEMM_OK;
+    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
+    const int64_t wave = static_cast<int64_t>(fit_blocks) * p.sm_count;
+    if (p.parts > wave) p.parts = static_cast<int32_t>(wave);
+    if (kShift && p.parts < p.rows) {   // a block's rows begin alike
+        p.parts = p.parts / V * V;
+        *done = p.parts > 0;
+        if (p.parts == 0) return GEMM_OK;
+    }
+    auto kern = rms_norm_bwd_ring<T, W, NV, TPR, kShift>;
     static std::atomic<int> prepared[kMaxDevices];
     if (!prepared[device].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess) {
@@ -555,37 +633,12 @@ int launch_ring_kernel(const RmsBwdParams<T, W> &p, int device, int threads, int
         }
         prepared[device].store(1, std::memory_order_release);
     }
-    const int st = launch(kern, p, threads, static_cast<size_t>(p.stages) * static_cast<size_t>(stage), stream);
-    if (st != GEMM_OK) prepared[device].store(0, std::memory_order_release);
-    return st;
-}
-
-// The ring kernel, where at least two rows fit a block's share of the shared
-// memory, else the long rows' kernels.
-template <class T, class W, int V, int NV, int TPR>
-int launch_ring(RmsBwdParams<T, W> p, int device, cudaStream_t stream, bool *done)
-{
-    const int packs = (p.dim + V - 1) / V;
-    const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
-    // Blocks per SM: those of the launch bound, or more where they are small.
-    const int fit_blocks = V * NV > 8 ? rms_ring_blocks(TPR, V * NV) : 1024 / threads;
-    const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
-    p.arrays = p.dH ? 3 : 2;
-    const int64_t stage = p.arrays * static_cast<int64_t>(ring_row_bytes<T, V>(p.dim));
-    const int64_t fit = budget / stage;
-    *done = fit >= 1;
-    if (fit < 1) return GEMM_OK;
-    p.stages = static_cast<int32_t>(fit < kRingStages ? fit : kRingStages);
-    const int64_t wave = static_cast<int64_t>(fit_blocks) * p.sm_count;
-    if (p.parts > wave) p.parts = static_cast<int32_t>(wave);
-    int st;
-    if constexpr (kRingAny<T, V>)
-        st = static_cast<int64_t>(NV - 1) * threads * V <= p.dim
-                 ? launch_ring_kernel<T, W, V, NV, TPR, true>(p, device, threads, stage, stream)
-                 : launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, threads, stage, stream);
-    else
-        st = launch_ring_kernel<T, W, V, NV, TPR, false>(p, device, threads, stage, stream);
-    return st != GEMM_OK ? st : finish<T, W>(p, stream);
+    const int st = launch(kern, p, threads, static_cast<size_t>(p.stages * stage + gamma_bytes), stream);
+    if (st != GEMM_OK) {
+        prepared[device].store(0, std::memory_order_release);
+        return st;
+    }
+    return finish<T, W>(p, stream);
 }
 
 template <class T, class W>
@@ -600,8 +653,34 @@ int launch_long(const RmsBwdParams<T, W> &p, cudaStream_t stream)
     return st != GEMM_OK ? st : finish<T, W>(p, stream);
 }
 
+// Rows of more than 512 elements through the ring.
+template <class T, class W, bool kShift>
+int launch_rows(const RmsBwdParams<T, W> &p, int device, cudaStream_t stream)
+{
+    constexpr int V = kPiece<T>, N = 8 / V;   // packs of 8 elements
+    const int packs = (p.dim + (kShift ? 2 * V - 2 : V - 1)) / V;
+    bool done = false;
+    int st = GEMM_OK;
+    // Thread counts as for layer norm: rows that fill a power of 2 of threads, then
+    // any others, with as many warps as the row needs.
+    if constexpr (!kShift) {
+        if (packs == 128 * N) st = launch_ring<T, W, N, 128, false>(p, device, stream, &done);
+        else if (packs == 256 * N) st = launch_ring<T, W, N, 256, false>(p, device, stream, &done);
+        else if (packs == 512 * N) st = launch_ring<T, W, N, 512, false>(p, device, stream, &done);
+        else if (packs == 1024 * N) st = launch_ring<T, W, N, 1024, false>(p, device, stream, &done);
+        if (done || st != GEMM_OK) return st;
+    }
+    if (packs <= 512 * N) st = launch_ring<T, W, N, -512, kShift>(p, device, stream, &done);
+    else if (packs <= 320 * 2 * N) st = launch_ring<T, W, 2 * N, -320, kShift>(p, device, stream, &done);
+    else if (packs <= 512 * 2 * N) st = launch_ring<T, W, 2 * N, -512, kShift>(p, device, stream, &done);
+    else if (packs <= 1024 * 2 * N) st = launch_ring<T, W, 2 * N, -1024, kShift>(p, device, stream, &done);
+    return done || st != GEMM_OK ? st : launch_long<T, W>(p, stream);
+}
+
+// Rows of up to 512 elements by lanes of a warp, V elements at a time; layer_norm_parts
+// counts on it.
 template <class T, class W, int V>
-int launch_packs(const RmsBwdParams<T, W> &p, int device, cudaStream_t stream)
+int launch_short(const RmsBwdParams<T, W> &p, cudaStream_t stream)
 {
     const int packs = (p.dim + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
@@ -610,30 +689,8 @@ int launch_packs(const RmsBwdParams<T, W> &p, int device, cudaStream_t stream)
         if (packs <= 8 * N) return launch_one<T, W, V, N, 8>(p, stream);
         if (packs <= 16 * N) return launch_one<T, W, V, N, 16>(p, stream);
     }
-    // Up to 512 elements a warp per row; layer_norm_parts counts on it.
     if (packs <= 32 * N) return launch_one<T, W, V, N, 32>(p, stream);
-    if (packs <= 32 * 2 * N) return launch_one<T, W, V, 2 * N, 32>(p, stream);
-    bool done = false;
-    int st = GEMM_OK;
-    // Thread counts as for layer norm: rows that fill a power of 2 of threads, then
-    // any others, with as many warps as the row needs.
-    if constexpr (V > 2) {
-        if (packs == 128 * N) st = launch_ring<T, W, V, N, 128>(p, device, stream, &done);
-        else if (packs == 256 * N) st = launch_ring<T, W, V, N, 256>(p, device, stream, &done);
-        else if (packs == 512 * N) st = launch_ring<T, W, V, N, 512>(p, device, stream, &done);
-        else if (packs == 1024 * N) st = launch_ring<T, W, V, N, 1024>(p, device, stream, &done);
-        else if (packs <= 512 * N) st = launch_ring<T, W, V, N, -512>(p, device, stream, &done);
-        else if (packs <= 320 * 2 * N) st = launch_ring<T, W, V, 2 * N, -320>(p, device, stream, &done);
-        else if (packs <= 512 * 2 * N) st = launch_ring<T, W, V, 2 * N, -512>(p, device, stream, &done);
-        else if (packs <= 1024 * 2 * N) st = launch_ring<T, W, V, 2 * N, -1024>(p, device, stream, &done);
-    } else {
-        if (packs <= 128 * N) return launch_one<T, W, V, N, -512>(p, stream);
-        if (packs <= 512 * N) st = launch_ring<T, W, V, N, -512>(p, device, stream, &done);
-        else if (packs <= 320 * 2 * N) st = launch_ring<T, W, V, 2 * N, -320>(p, device, stream, &done);
-        else if (packs <= 512 * 2 * N) st = launch_ring<T, W, V, 2 * N, -512>(p, device, stream, &done);
-        else if (packs <= 1024 * 2 * N) st = launch_ring<T, W, V, 2 * N, -1024>(p, device, stream, &done);
-    }
-    return done || st != GEMM_OK ? st : launch_long<T, W>(p, stream);
+    return launch_one<T, W, V, 2 * N, 32>(p, stream);
 }
 
 template <class T, class W>
@@ -656,16 +713,29 @@ int backward(const RmsNormArgs &a)
     p.status = a.status;
     p.dgamma = static_cast<W *>(a.dgamma);
     p.sm_count = a.sm_count;
-    const uintptr_t x_bits = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.dY) |
-                             reinterpret_cast<uintptr_t>(a.dH) | reinterpret_cast<uintptr_t>(a.dX) |
-                             (static_cast<uintptr_t>(a.dim) * sizeof(T));
+    const uintptr_t all[] = {reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.dY),
+                             reinterpret_cast<uintptr_t>(a.dX), reinterpret_cast<uintptr_t>(a.dH ? a.dH : a.X)};
+    const uintptr_t x_bits = all[0] | all[1] | all[2] | all[3] | (static_cast<uintptr_t>(a.dim) * sizeof(T));
     const uintptr_t w_bits = reinterpret_cast<uintptr_t>(a.gamma);
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = kPiece<T>;
     const int pack = ln_pack_elements<T, W>(x_bits, w_bits);
-    if (pack == V) return launch_packs<T, W, V>(p, a.device, a.stream);
-    if constexpr (V > 4)
-        if (pack == V / 4) return launch_packs<T, W, V / 4>(p, a.device, a.stream);
-    return launch_packs<T, W, 1>(p, a.device, a.stream);
+    if (a.dim <= 512) {
+        if (pack == V) return launch_short<T, W, V>(p, a.stream);
+        if constexpr (V > 4)
+            if (pack == V / 4) return launch_short<T, W, V / 4>(p, a.stream);
+        return launch_short<T, W, 1>(p, a.stream);
+    }
+    if (pack == V) return launch_rows<T, W, false>(p, a.device, a.stream);
+    // All arrays' rows begin at the same place of a 16-byte piece, or their elements are
+    // taken one by one, as are a few short rows, for which the ring is not worth its
+    // setting up (300 x 2047 bf16 9.6 us with it, 7.5 us without; 1000 x 1023 fp32 8.5 and
+    // 8.1; 4000 x 2047 fp16 22 and 33).
+    const bool few = a.dim * static_cast<int64_t>(sizeof(T)) <= 4096 && a.rows <= 4 * static_cast<int64_t>(p.parts);
+    if (!few && (((all[0] ^ all[1]) | (all[0] ^ all[2]) | (all[0] ^ all[3])) & 15u) == 0)
+        return launch_rows<T, W, true>(p, a.device, a.stream);
+    if (a.dim <= 512 * 8) return launch_one<T, W, 1, 8, -512>(p, a.stream);
+    if (a.dim <= 512 * 16) return launch_one<T, W, 1, 16, -512>(p, a.stream);
+    return launch_long<T, W>(p, a.stream);
 }
 
 }  // namespace

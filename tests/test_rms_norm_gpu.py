@@ -333,3 +333,68 @@ def test_rows_whose_squares_are_beyond_fp32(g, dim, xt):
     v = Q.float().double() * ref.spread(S.double(), 1, 5, dim)
     a = ref.spread(ref.blocks(y, 1).abs().amax(dim=(1, 3)), 1, 5, dim)
     assert ((v - y).abs() <= 2.0 ** -4 * 1.001 * y.abs() + a * 2.0 ** -17).all()
+
+
+def check_many_rows(g, H, dy, w, rstd, dh, dX=None):
+    """Gradients of more rows than a block has: a block adds at most rows / 152 + 8 of them one by one."""
+    rows = H.shape[0]
+    r, d = rstd.double()[:, None], dy.double()
+    z = H.double() * r
+    dX, dg = g.rms_norm_bwd(dy, H, rstd, w, dH=dh, dX=dX)
+    assert g.check() == g.GEMM_OK
+    terms = d * z
+    rel, tiny = half_step(w.dtype)
+    tol = (rows / 152 + 24) * U * terms.abs().sum(0) + rel * terms.sum(0).abs() + tiny
+    assert ((dg.double() - terms.sum(0)).abs() <= 1.01 * tol).all()
+    gr = d * w.double()
+    c = (gr * z).mean(-1, keepdim=True)
+    want = r * (gr - z * c) + (0.0 if dh is None else dh.double())
+    rel, tiny = half_step(H.dtype)
+    d_c = (ADDS + 5) * U * (gr * z).abs().mean(-1, keepdim=True)
+    tol = r * (z.abs() * d_c + 6 * U * (gr.abs() + (z * c).abs())) + 2 * U * want.abs()
+    assert ((dX.double() - want).abs() <= 1.01 * (tol + rel * want.abs() + tiny)).all()
+    return dX, dg
+
+
+@pytest.mark.parametrize("xt,wt,rows,dim", [
+    ("fp16", "fp16", 400, 16384), ("fp32", "fp32", 400, 16384), ("bf16", "fp32", 700, 12000), ("fp32", "fp32", 333, 16377),
+    ("bf16", "bf16", 500, 16370), ("bf16", "bf16", 200, 16371), ("fp16", "fp32", 700, 9001), ("fp16", "fp16", 1300, 4097),
+    ("bf16", "fp32", 1300, 4999), ("fp32", "fp32", 900, 3001), ("bf16", "bf16", 4000, 1023), ("fp32", "fp32", 2000, 513),
+    ("fp16", "fp16", 2001, 514), ("fp32", "fp32", 305, 2), ("fp16", "fp16", 153, 1025), ("fp16", "fp16", 305, 1025)])
+def test_rows_of_any_width_more_than_blocks(g, xt, wt, rows, dim):
+    x, _, dy, dh, w = draw(rows, dim, DTYPES[xt], DTYPES[wt], rows + dim)
+    _, H, rstd = g.rms_norm_fwd(x, w, eps=EPS)
+    first = check_many_rows(g, H, dy, w, rstd, dh)
+    check_many_rows(g, H, dy, w, rstd, None)
+    # all four off the 16-byte grid by the same element, then by different ones
+    off = torch.empty(rows * dim + 1, dtype=x.dtype, device=DEV)[1:].reshape(rows, dim)
+    same = check_many_rows(g, moved(H), moved(dy), moved(w), rstd, moved(dh), dX=off)
+    other = check_many_rows(g, moved(H), dy, w, rstd, dh, dX=off.clone())
+    for got in (same, other):   # the same sums, divided among threads another way
+        assert got[0].shape == first[0].shape and got[1].dtype == first[1].dtype
+
+
+@pytest.mark.parametrize("xt,dim", [("fp16", 1025), ("bf16", 4099), ("fp32", 2047), ("fp16", 16369)])
+def test_nothing_beside_the_rows_is_read_or_written(g, xt, dim):
+    """NaN in front of the first and behind the last row, and in the 16-byte pieces that they share."""
+    rows = 7
+    x, _, dy, dh, w = draw(rows, dim, DTYPES[xt], DTYPES[xt], dim)
+    _, H, rstd = g.rms_norm_fwd(x, w, eps=EPS)
+    want = g.rms_norm_bwd(dy, H, rstd, w, dH=dh)
+
+    def inside(t, by):
+        flat = torch.full((t.numel() + 64,), float("nan"), dtype=t.dtype, device=DEV)
+        part = flat[by:by + t.numel()].reshape(t.shape)
+        part.copy_(t)
+        return flat, part
+
+    for by in (0, 1, 3, 8):
+        flat, out = inside(torch.zeros_like(H), by)
+        got = g.rms_norm_bwd(inside(dy, by)[1], inside(H, by)[1], rstd, w, dH=inside(dh, by)[1], dX=out)
+        assert g.check() == g.GEMM_OK
+        assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+        assert torch.isnan(flat[:by]).all() and torch.isnan(flat[by + H.numel():]).all()
+        rel, tiny = half_step(H.dtype)
+        # another division of the row's sum among threads may turn a rounding
+        assert ((got[0].double() - want[0].double()).abs()
+                <= 2 * rel * want[0].double().abs() + 2.0 ** -18 * want[0].double().abs().max()).all()
