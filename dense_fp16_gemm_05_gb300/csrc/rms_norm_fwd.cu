@@ -58,9 +58,13 @@ constexpr float kDown = 0x1p-100f;
 __device__ __forceinline__ bool rms_beyond(float sum) { return !(sum <= 3.4028235e38f); }
 __device__ __forceinline__ float rms_rstd(float sum, float inv_dim, float eps) { return 1.0f / sqrtf(sum * inv_dim + eps); }
 
-template <class T, class W, int V, int NV, int TPR, bool kFp8>
+// kShift: a row that is not whole 16-byte pieces is taken with the pieces that it lies
+// in, from the first one on; of the first and the last the neighbours' elements count
+// as zeros and the row's own are stored one by one.
+template <class T, class W, int V, int NV, int TPR, bool kFp8, bool kShift>
 __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParams<T, W> p)
 {
+    static_assert(!kShift || (TPR > 32 || TPR < 0), "a block's rows begin at one place");
     constexpr int R = TPR > 0 ? rms_threads(TPR) / TPR : 1;   // rows of a block
     constexpr int C = rms_run(TPR, V, kFp8), RL = rms_lanes(TPR, V, kFp8);
     static_assert(NV % C == 0 || !kFp8, "whole blocks of columns");
@@ -73,25 +77,49 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
     // Lanes without a row take the last one along, for the sake of the shuffles.
     const bool in = row < p.rows;
     if (!in) row = p.rows - 1;
+    const int64_t at = row * p.dim;
+    // Elements in front of the row in its first piece.
+    const int shift = kShift ? static_cast<int>((reinterpret_cast<uint64_t>(p.X + at) & 15u) / sizeof(T)) : 0;
     auto column = [&](int i) {
-        if constexpr (C == 1) return (i * tpr + t) * V;
+        if constexpr (C == 1) return (i * tpr + t) * V - shift;
         else return (((i / C) * (tpr / RL) + t / RL) * (RL * C) + (i % C) * RL + t % RL) * V;
     };
-    const int64_t at = row * p.dim;
+    auto whole = [&](int k) { return !kShift || (k >= 0 && k + V <= p.dim); };
+    auto own = [&](int k) { return k >= 0 && k < p.dim; };
+    // A pack of a row at column k < dim, with the neighbours' elements that its piece
+    // holds; one by one where the piece reaches past the tensor's ends.
+    const int64_t total = p.rows * p.dim;
+    auto load = [&](LnPack<T, V> &pack, const T *src, int k) {
+        if (!kShift || (at + k >= 0 && at + k + V <= total)) {
+            rms_load(pack, src + at + k);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) pack.e[j] = own(k + j) ? src[at + k + j] : ln_round<T>(0.0f);
+        }
+    };
+    auto store = [&](const LnPack<T, V> &pack, T *dst, int k) {
+        if (whole(k)) {
+            pack.store(dst + k);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (own(k + j)) dst[k + j] = pack.e[j];
+        }
+    };
     constexpr int P = V * NV / 2;
     float2 h[P];
     {
         LnPack<T, V> px[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (column(i) < p.dim) rms_load(px[i], p.X + at + column(i));
+            if (column(i) < p.dim) load(px[i], p.X, column(i));
             else px[i].fill(0.0f);
         }
         if (p.R) {
             LnPack<T, V> pr[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (column(i) < p.dim) rms_load(pr[i], p.R + at + column(i));
+                if (column(i) < p.dim) load(pr[i], p.R, column(i));
                 else pr[i].fill(0.0f);
             }
 #pragma unroll
@@ -102,7 +130,16 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
 #pragma unroll
                     for (int j = 0; j < V / 2; ++j) px[i].set_pair(j, add_f32x2(px[i].pair(j), pr[i].pair(j)));
                 }
-                if (in && column(i) < p.dim) px[i].store(p.H + at + column(i));
+                if (in && column(i) < p.dim) store(px[i], p.H + at, column(i));
+            }
+        }
+        if constexpr (kShift) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (whole(column(i))) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (!own(column(i) + j)) px[i].e[j] = ln_round<T>(0.0f);
             }
         }
 #pragma unroll
@@ -133,8 +170,14 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
             const int k = column(i);
             if (k >= p.dim) continue;
             LnPack<W, V> g;
-            if (p.gamma) g.load(p.gamma + k);
-            else g.fill(1.0f);
+            g.fill(1.0f);
+            if constexpr (kShift) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (p.gamma && own(k + j)) g.e[j] = __ldg(p.gamma + k + j);
+            } else if (p.gamma) {
+                g.load(p.gamma + k);
+            }
             LnPack<T, V> out;
             if constexpr (V == 1) {
                 out.e[0] = ln_round<T>(ln_half(h[i / 2], i) * rstd * g[0]);
@@ -143,7 +186,7 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
                 for (int j = 0; j < V / 2; ++j)
                     out.set_pair(j, mul_f32x2(mul_f32x2(h[i * (V / 2) + j], rstd2), g.pair(j)));
             }
-            out.store(p.Y + at + k);
+            store(out, p.Y + at, k);
         }
     } else {
         // h becomes y; what lies past the row's end is zero.
@@ -263,15 +306,15 @@ __global__ void __launch_bounds__(1024) rms_norm_fwd_long(RmsParams<T, W> p)
     }
 }
 
-template <class T, class W, bool kFp8, int V, int NV, int TPR>
+template <class T, class W, bool kFp8, int V, int NV, int TPR, bool kShift = false>
 int launch_one(const RmsParams<T, W> &p, cudaStream_t stream)
 {
     // Threads: those of the template, or the whole warps that NV packs each need.
     constexpr int C = rms_run(TPR, V, kFp8);
-    const int runs = (p.dim + V * C - 1) / (V * C);   // C packs each
+    const int runs = (p.dim + (kShift ? V - 1 : 0) + V * C - 1) / (V * C);   // C packs each
     const int BT = TPR > 0 ? rms_threads(TPR) : ((runs + NV / C - 1) / (NV / C) + 31) / 32 * 32;
     constexpr int R = TPR > 0 ? rms_threads(TPR) / TPR : 1;
-    return ln_launch(rms_norm_fwd_kernel<T, W, V, NV, TPR, kFp8>,
+    return ln_launch(rms_norm_fwd_kernel<T, W, V, NV, TPR, kFp8, kShift>,
                      dim3(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1), BT, stream, p);
 }
 
@@ -327,6 +370,22 @@ int forward(const RmsNormArgs &a)
     // Q is stored a pack at a time, a byte per element.
     if (kFp8 && (reinterpret_cast<uintptr_t>(a.Q) & static_cast<uintptr_t>(pack - 1)) != 0) pack = 1;
     if (pack == V) return launch_packs<T, W, kFp8, V>(p, a.stream);
+    if constexpr (!kFp8) {
+        // All arrays' rows begin at the same place of a 16-byte piece and fit a block, and
+        // there is enough to stream to pay for the edges: 16384 x 4097 fp16 88 us, 150 us
+        // by elements; 65536 x 1023 93 and 104; but 65536 x 513 75 and 71, 1 x 4097 3.4
+        // and 2.2, 2000 x 3001 fp32 21.1 and 18.9.  Pairs: 16384 x 4098 87 and 99, but
+        // 16384 x 2050 49 and 47.
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.X), y = reinterpret_cast<uintptr_t>(a.Y);
+        const uintptr_t r = a.R ? reinterpret_cast<uintptr_t>(a.R) : x, h = a.R ? reinterpret_cast<uintptr_t>(a.H) : x;
+        constexpr int N = 8 / V;   // packs of 8 elements
+        const int packs = (p.dim + 2 * V - 2) / V;
+        if ((((x ^ y) | (x ^ r) | (x ^ h)) & 15u) == 0 && p.dim >= (pack == 1 ? 768 : 2560) &&
+            p.rows * p.dim >= (sizeof(T) == 2 ? 1 << 22 : 1 << 23)) {
+            if (packs <= 128 * 2 * N) return launch_one<T, W, false, V, 2 * N, -128, true>(p, a.stream);
+            if (packs <= 512 * 4 * N) return launch_one<T, W, false, V, 4 * N, -512, true>(p, a.stream);
+        }
+    }
     if constexpr (V > 4)
         if (pack == V / 4) return launch_packs<T, W, kFp8, V / 4>(p, a.stream);
     return launch_packs<T, W, kFp8, 1>(p, a.stream);

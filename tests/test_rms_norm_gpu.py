@@ -398,3 +398,54 @@ def test_nothing_beside_the_rows_is_read_or_written(g, xt, dim):
         # another division of the row's sum among threads may turn a rounding
         assert ((got[0].double() - want[0].double()).abs()
                 <= 2 * rel * want[0].double().abs() + 2.0 ** -18 * want[0].double().abs().max()).all()
+
+
+@pytest.mark.parametrize("xt,wt,rows,dim", [
+    ("fp16", "fp16", 1300, 4097), ("bf16", "fp32", 1300, 4098), ("bf16", "bf16", 300, 16371), ("bf16", "bf16", 300, 16369),
+    ("fp16", "fp32", 5600, 769), ("fp32", "fp32", 2100, 4095), ("fp32", "fp32", 1000, 8389), ("fp16", "fp16", 2100, 2048),
+    ("fp16", "fp16", 2098, 2047)])
+def test_many_rows_of_any_width_forward(g, xt, wt, rows, dim):
+    x, r, _, _, w = draw(rows, dim, DTYPES[xt], DTYPES[wt], rows + dim)
+    check_forward(g, x, w, None)
+    check_forward(g, x, None, r)
+    want = g.rms_norm_fwd(x, w, residual=r, eps=EPS)
+    total = rows * dim
+
+    def beside(t, by):
+        """t's values among NaNs, `by` elements off the 16-byte grid."""
+        flat = torch.full((total + 64,), float("nan"), dtype=t.dtype, device=DEV)
+        flat[by:by + total].copy_(t.reshape(-1))
+        return flat, flat[by:by + total].reshape(rows, dim)
+
+    check_forward(g, moved(x), moved(w), moved(r))
+    for by in (0, 3):
+        for which in (0, 1):   # the stream in the place of either summand
+            fx, px = beside(x, by)
+            fr, pr = beside(r, by)
+            fy, py = beside(torch.zeros_like(x), by)
+            Y, H, _ = g.rms_norm_fwd(px, w, residual=pr, eps=EPS, Y=py, H=(px, pr)[which])
+            assert g.check() == g.GEMM_OK
+            rel, tiny = half_step(x.dtype)
+            # another division of the row's sum among threads may turn a rounding
+            step = (2 * rel + 2 * D_R) * want[0].double().abs() + tiny
+            assert torch.equal(H, want[1]) and ((Y.double() - want[0].double()).abs() <= step).all()
+            for flat in (fx, fr, fy):
+                assert torch.isnan(flat[:by]).all() and torch.isnan(flat[by + total:]).all()
+            assert torch.equal((pr, px)[which], (r, x)[which])
+
+
+@pytest.mark.parametrize("dim", [4097, 8191])
+def test_many_rows_beyond_fp32_squares(g, dim):
+    gen = torch.Generator().manual_seed(dim)
+    scale = torch.tensor([1.0, 1e19, 1e30, 1e-30, 1.0]).repeat(260).reshape(-1, 1)
+    x = (torch.randn((1300, dim), generator=gen).clamp(-4, 4) * scale).to(torch.bfloat16).to(DEV)
+    x[4, 7], x[9, dim - 1] = float("inf"), float("nan")
+    Y, _, rstd = g.rms_norm_fwd(x, eps=EPS)
+    assert g.check() == g.GEMM_OK
+    good = torch.ones(1300, dtype=torch.bool, device=DEV)
+    good[4] = good[9] = False
+    h = x[good].double()
+    want_r = 1 / torch.sqrt((h * h).mean(-1) + EPS)
+    assert ((rstd[good].double() - want_r).abs() <= D_R * want_r + 2.0 ** -149).all()
+    assert rstd[4] == 0 and torch.isnan(rstd[9])
+    assert torch.isnan(Y[4, 7]) and (Y[4, 8:] == 0).all() and torch.isnan(Y[9]).all()
