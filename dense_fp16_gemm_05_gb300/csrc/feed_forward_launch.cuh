@@ -61,6 +61,9 @@ struct W4LinearArgs {
     int type = 0, group = 0, relu = 0;
     int sm_count = 0, device = 0;
     cudaStream_t stream = nullptr;
+    unsigned long long *status = nullptr;       // device status word
+    int withhold = 0;                           // test hook (linear_w4_selftest_timeout)
+    uint64_t timeout_cycles = 0;                // 0: the normal budget
 };
 // One scale group width each.
 int launch_linear_w4_g32(const W4LinearArgs &a);

@@ -1406,8 +1406,8 @@ extern "C" int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z
     return launch_w4_quantize(a);
 }
 
-extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M,
-                         int64_t N, int64_t K, int group, int relu, void *stream)
+static int run_linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M,
+                         int64_t N, int64_t K, int group, int relu, void *stream, int withhold, uint64_t timeout_cycles)
 {
     int st = check_w4_args(N, K, group, type);
     if (st != GEMM_OK) return st;
@@ -1449,9 +1449,29 @@ extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, 
     a.relu = relu;
     a.sm_count = dev.sm_count;
     a.device = dev.device;
+    a.status = status_word(dev.device);
+    if (a.status == nullptr) return GEMM_ERR_CUDA;
+    a.withhold = withhold;
+    a.timeout_cycles = timeout_cycles;
     a.stream = static_cast<cudaStream_t>(stream);
     if (group == 32) return launch_linear_w4_g32(a);
     return group == 64 ? launch_linear_w4_g64(a) : launch_linear_w4_g128(a);
+}
+
+extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M,
+                         int64_t N, int64_t K, int group, int relu, void *stream)
+{
+    return run_linear_w4(X, type, Q, S, Z, C, M, N, K, group, relu, stream, 0, 0);
+}
+
+extern "C" int linear_w4_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z,
+                                          void *C, int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles,
+                                          void *stream)
+{
+    if (M <= 32 || N == 0 || K == 0) return reject(GEMM_ERR_INVALID_ARG, "the kernel with waits takes more than 32 rows of X");
+    if (timeout_cycles < (1ull << 16) || timeout_cycles > (1ull << 32))
+        return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
+    return run_linear_w4(X, type, Q, S, Z, C, M, N, K, group, 0, stream, 1, timeout_cycles);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

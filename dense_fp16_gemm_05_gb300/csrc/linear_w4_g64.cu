@@ -1,5 +1,5 @@
 // linear_w4_g64.cu -- linear_w4's kernels for scale groups of 64 columns.
-#include "linear_w4_kernel.cuh"
+#include "linear_w4_launch.cuh"
 
 namespace gemm_sm103 {
 

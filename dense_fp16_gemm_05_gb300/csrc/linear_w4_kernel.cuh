@@ -8,9 +8,13 @@
 // as the 16-row operand and up to 8 rows of X as the 8-column one: the codes are
 // laid out so that one 16-byte load per lane is the operand of four such products,
 // and q - z is exact in 16 bits, so what is rounded is the fp32 sum alone; a
-// group's sum is scaled in fp32.  (The tensor memory path wants 128 rows of
-// operands in shared memory, four times the codes' bytes written there first, for
-// an arithmetic that a matrix-vector product does not need.)
+// group's sum is scaled in fp32.  (For more than 32 rows of X: linear_w4_tmem.cuh.)
+//
+// 1 x 4096 x 4096 takes 4.5 us, 1 x 16384 x 8192 16.9 us (4.1 TB/s), 8 x 16384 x 8192 bf16
+// with zero points 22 us, 16 x 16384 x 8192 29.4 us, 32 x 16384 x 8192 44 us; with
+// the products left out the copies alone take 13 to 17 us at that size.  With one row of
+// X the copies and the conversion of the codes share the time, with more it is the
+// instructions: for eight codes of a lane some 11 of conversion, and the mma.sync.
 //
 // Every warp streams its own units -- 16 rows x 128 columns of codes with their
 // scales and zero points -- through its own ring of asynchronous copies in shared
@@ -110,6 +114,7 @@ struct W4Codes;
 
 template <>
 struct W4Codes<__half> {
+    static constexpr bool kBf16 = false;
     // -(1024 + z) for rows g, -(64 + z) for rows g + 8, twice.
     static __device__ __forceinline__ uint32_t bias(uint32_t z, int odd)
     {
@@ -139,6 +144,7 @@ struct W4Codes<__half> {
 
 template <>
 struct W4Codes<__nv_bfloat16> {
+    static constexpr bool kBf16 = true;
     // -(128 + z), twice.
     static __device__ __forceinline__ uint32_t bias(uint32_t z, int) { return 0xC300C300u + z * 0x00010001u; }
     // 128 + q: with seven bits behind the point no second nibble fits.
@@ -459,33 +465,85 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
 
 constexpr int kW4Budget = 225 * 1024;   // dynamic shared memory of a block
 
+// Clusters of 1, 2, 4 and 8 blocks that the GPU holds at a time, 0: none.  Of blocks that
+// fill an SM a cluster lies within a part of the GPU, whose SMs larger clusters do not
+// divide evenly: clusters that are a few too many take as long as twice as many.
+struct W4Clusters {
+    std::atomic<int> most[4];
+};
+
+inline cudaLaunchConfig_t w4_launch_config(int groups, int slices, int threads, int64_t smem, cudaStream_t stream,
+                                           cudaLaunchAttribute (&attr)[2])
+{
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(groups), static_cast<unsigned>(slices), 1);
+    lc.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = static_cast<unsigned>(slices);
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = slices > 1 ? 2 : 1;
+    return lc;
+}
+
+// Once per kernel and device: its shared memory, and the clusters that fit.
+template <class Kernel>
+bool w4_prepare(Kernel kern, int threads, int64_t smem, const W4LinearArgs &a, std::atomic<int> (&prepared)[kMaxDevices],
+                W4Clusters (&clusters)[kMaxDevices])
+{
+    if (prepared[a.device].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    clusters[a.device].most[0].store(a.sm_count, std::memory_order_relaxed);
+    for (int l = 1; l < 4; ++l) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t lc = w4_launch_config(a.sm_count, 1 << l, threads, smem, a.stream, attr);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        clusters[a.device].most[l].store(n, std::memory_order_relaxed);
+    }
+    prepared[a.device].store(1, std::memory_order_release);
+    return true;
+}
+
 template <class T, int NT, int G>
 int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
 {
     using Shape = W4Shape<NT, G>;
     auto kern = linear_w4_kernel<T, NT, G>;
+    static std::atomic<int> prepared[kMaxDevices];
+    static W4Clusters clusters[kMaxDevices];
+    if (!w4_prepare(kern, kW4Threads, kW4Budget, a, prepared, clusters)) return GEMM_ERR_LAUNCH;
     // The division of the work that costs least by this count of nanoseconds, fitted to
-    // whole calls of 18 shapes (1 x 64 x 64 to 64 x 16384 x 8192) under every division (its
+    // whole calls of 18 shapes (up to 32 x 16384 x 8192) under every division (its
     // choice was within a tenth of the best of each, but one of the smallest): a
-    // unit of each of a block's sixteen warps takes 450 with 8 rows of X, 1850 with 64,
+    // unit of each of a block's sixteen warps takes 450 with 8 rows of X, 1030 with 32,
     // and with fewer warps as much less, down to eleven; a group of strips ends with 500,
     // more among the blocks of a cluster, and a quarter for each output; X comes with 60
     // bytes each, 20 where its rows are off the 16-byte grid, and in chunks half hidden.
     const int64_t room = kW4Budget - Shape::RING - 2 * Shape::SUMS;   // for a kept X
-    const float unit_cost = NT == 1 ? 450.0f : (NT == 2 ? 650.0f : (NT == 4 ? 1030.0f : 1850.0f));
+    const float unit_cost = NT == 1 ? 450.0f : (NT == 2 ? 650.0f : 1030.0f);
     static constexpr uint8_t kDivisions[][2] = {{16, 1}, {15, 1}, {14, 1}, {8, 2}, {7, 2}, {6, 2},
                                                 {5, 3},  {4, 4},  {3, 5},  {2, 8}, {2, 7}, {1, 16}};
     float least = 1e30f;
     int slices = 1;
-    for (int sl = 1; sl <= 8 && sl <= p.units; sl *= 2) {
-        // Clusters at a time: of blocks that fill an SM a cluster lies within a part of the
-        // GPU, whose SMs larger clusters do not divide evenly (37 of four took as long as
-        // two rounds, 35 one).
-        const int units = (p.units + sl - 1) / sl, most = (a.sm_count - (sl > 2 ? 3 * sl : 0)) / sl;
+    for (int l = 0; l < 4 && (1 << l) <= p.units; ++l) {
+        const int sl = 1 << l, units = (p.units + sl - 1) / sl, most = clusters[a.device].most[l].load(std::memory_order_relaxed);
+        if (most == 0) continue;
         const int64_t x_bytes = p.M * w4_x_row(units);
         const float x_cost = static_cast<float>(x_bytes) / (p.vec ? 60.0f : 20.0f);
         const float end = sl == 1 ? 500.0f : (sl == 2 ? 1500.0f : (sl == 4 ? 3000.0f : 4000.0f));
-        const bool fits = NT <= 4 && x_bytes <= room;
+        const bool fits = x_bytes <= room;
         for (const auto &d : kDivisions) {
             const int rw = d[0], kw = d[1];
             if (kw > units) break;
@@ -504,7 +562,8 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
             if (fits) consider(static_cast<float>(rounds) * group + x_cost, 1);
         }
     }
-    const int groups = (p.strips + p.rw - 1) / p.rw, most = a.sm_count / slices;
+    const int groups = (p.strips + p.rw - 1) / p.rw;
+    const int most = slices == 1 ? a.sm_count : clusters[a.device].most[slices == 2 ? 1 : (slices == 4 ? 2 : 3)].load(std::memory_order_relaxed);
     int64_t smem = Shape::RING;
     if (p.keep_x) {
         p.x_row = static_cast<int32_t>(w4_x_row((p.units + slices - 1) / slices));
@@ -516,59 +575,14 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
         smem += 2 * p.x_bytes;
         if (smem < 2 * Shape::SUMS) smem = 2 * Shape::SUMS;
     }
-    static std::atomic<int> prepared[kMaxDevices];
-    if (!prepared[a.device].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4Budget) != cudaSuccess) {
-            cudaGetLastError();
-            return GEMM_ERR_LAUNCH;
-        }
-        prepared[a.device].store(1, std::memory_order_release);
-    }
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>(p.keep_x && groups > most ? most : groups), static_cast<unsigned>(slices), 1);
-    lc.blockDim = dim3(kW4Threads, 1, 1);
-    lc.dynamicSmemBytes = static_cast<size_t>(smem);
-    lc.stream = a.stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = static_cast<unsigned>(slices);
-    attr[1].val.clusterDim.z = 1;
-    lc.attrs = attr;
-    lc.numAttrs = slices > 1 ? 2 : 1;
+    const cudaLaunchConfig_t lc = w4_launch_config(p.keep_x && groups > most ? most : groups, slices, kW4Threads, smem, a.stream, attr);
     if (cudaLaunchKernelEx(&lc, kern, p) != cudaSuccess) {
         cudaGetLastError();
         prepared[a.device].store(0, std::memory_order_release);
         return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
-}
-
-// Calls of one scale group width (linear_w4_g32.cu, ...: a translation unit each).
-template <class T, int G>
-int launch_w4(const W4LinearArgs &a)
-{
-    W4Params<T> p{};
-    p.X = static_cast<const T *>(a.X);
-    p.Q = static_cast<const uint8_t *>(a.Q);
-    p.S = static_cast<const uint8_t *>(a.S);
-    p.Z = a.Z;
-    p.C = static_cast<T *>(a.C);
-    p.M = static_cast<int32_t>(a.M);
-    p.N = a.N;
-    p.K = a.K;
-    p.strips = static_cast<int32_t>(w4_strips(a.N));
-    p.k_tiles = static_cast<int32_t>((a.K + kW4Cols - 1) / kW4Cols);
-    p.groups = static_cast<int32_t>((a.K + G - 1) / G);
-    p.units = (p.k_tiles + 1) / 2;
-    p.relu = a.relu;
-    p.vec = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.K % 8 == 0;
-    if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
-    if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);
-    if (p.M <= 32) return launch_w4_kernel<T, 4, G>(p, a);
-    return launch_w4_kernel<T, 8, G>(p, a);
 }
 
 }  // namespace gemm_sm103

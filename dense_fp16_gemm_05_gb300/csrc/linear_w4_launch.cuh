@@ -1,0 +1,37 @@
+// linear_w4_launch.cuh -- which kernel takes a product with 4-bit weights.
+#pragma once
+
+#include "linear_w4_kernel.cuh"
+#include "linear_w4_tmem.cuh"
+
+namespace gemm_sm103 {
+
+// Calls of one scale group width (linear_w4_g32.cu, ...: a translation unit each).
+template <class T, int G>
+int launch_w4(const W4LinearArgs &a)
+{
+    W4Params<T> p{};
+    p.X = static_cast<const T *>(a.X);
+    p.Q = static_cast<const uint8_t *>(a.Q);
+    p.S = static_cast<const uint8_t *>(a.S);
+    p.Z = a.Z;
+    p.C = static_cast<T *>(a.C);
+    p.M = static_cast<int32_t>(a.M);
+    p.N = a.N;
+    p.K = a.K;
+    p.strips = static_cast<int32_t>(w4_strips(a.N));
+    p.k_tiles = static_cast<int32_t>((a.K + kW4Cols - 1) / kW4Cols);
+    p.groups = static_cast<int32_t>((a.K + G - 1) / G);
+    p.units = (p.k_tiles + 1) / 2;
+    p.relu = a.relu;
+    p.vec = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.K % 8 == 0;
+    // By mma.sync, 8 rows of X to an instruction, or from tensor memory, whose MMAs take 64
+    // in the time of 8: 64 x 8192 x 8192 39 and 30 us, 40 x 4096 x 4096 28 and 12, but
+    // 32 x 8192 x 8192 22.3 and 23.1 (and that with 32), 16 x 8192 x 8192 14.5 and 20.2.
+    if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
+    if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);
+    if (p.M <= 32) return launch_w4_kernel<T, 4, G>(p, a);
+    return launch_w4_tmem<T, G>(p, a);
+}
+
+}  // namespace gemm_sm103

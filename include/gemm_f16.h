@@ -632,6 +632,15 @@ int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z, int64_t N
 int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M, int64_t N,
               int64_t K, int group, int relu, void *stream);
 
+/*
+ * linear_w4_selftest_timeout -- exercises the bounded waits of linear_w4's kernel for
+ * more than 32 rows of X (a test hook as gemm_f16_selftest_timeout; C is left alone).
+ * W's operands are not handed to the tensor core and a wait may take timeout_cycles
+ * (2^16 .. 2^32) SM clocks; gemm_f16_check then returns GEMM_ERR_TIMEOUT (site 3).
+ */
+int linear_w4_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C,
+                               int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles, void *stream);
+
 /* Launch geometry of gemm_fp8_block_scaled for this problem on the current
  * device: persistent grid in CTAs (CTA pairs over 256 x 256 output tiles) and
  * the number of tiles.  Either pointer may be NULL.  Launches nothing. */

@@ -200,3 +200,108 @@ def test_empty_and_refused(g):
     with pytest.raises(g.GemmError):
         g.linear_w4(X, *W, group=64, C=X.reshape(-1)[:64].reshape(2, 32))
     assert g.check() == g.GEMM_OK
+
+
+# More than 32 rows of X go to the tensor memory kernel: blocks of 128 rows of W, walked
+# by the GPU's 152 blocks or one to a block or a cluster; units of 128 columns.
+MANY = [(33, 1, 1), (33, 20000, 100), (64, 19600, 130), (40, 128, 128), (50, 129, 300), (48, 1000, 2184), (64, 2048, 6000),
+        (37, 260, 8191), (64, 4100, 1024), (64, 9728, 520), (35, 38912, 64), (63, 640, 16384)]
+
+
+@pytest.mark.parametrize("xt", ["fp16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,N,K", MANY)
+def test_many_rows_of_activations(g, M, N, K, group, zeros, xt):
+    W = packed(g, N, K, group, zeros, DTYPES[xt], M + N + K)
+    gen = torch.Generator().manual_seed(K)
+    X = torch.randn((M, K), generator=gen).to(DTYPES[xt]).to(DEV)
+    C = check(g, X, W, N, group, relu=(M + N) % 2 == 0)
+    # off the 16-byte grid, between other tensors' bytes: the same products and sums
+    flat = torch.full((M * K + 2,), float("nan"), dtype=X.dtype, device=DEV)
+    flat[1:-1].copy_(X.reshape(-1))
+    buf = torch.full((M * N + 64,), 7.0, dtype=X.dtype, device=DEV)
+    out = buf[32:32 + M * N].reshape(M, N)
+    assert torch.equal(g.linear_w4(flat[1:-1].reshape(M, K), *W, N=N, group=group, relu=(M + N) % 2 == 0, C=out), C)
+    assert (buf[:32] == 7).all() and (buf[32 + M * N:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [33, 64])
+def test_columns_reach_their_own_products(g, M):
+    """One activation at a time: every column of W, in its own place, with its own sign and group."""
+    K, N, group = 256, 144, 64
+    gen = torch.Generator().manual_seed(M)
+    q = torch.randint(0, 16, (N, K), generator=gen, dtype=torch.uint8)
+    s = torch.exp2(torch.randint(-3, 4, (N, K // group), generator=gen).float()).half()
+    z = torch.randint(0, 16, s.shape, generator=gen, dtype=torch.uint8)
+    W = g.w4_pack(q.to(DEV), s.to(DEV), z.to(DEV), group)
+    w = (q.double() - z.double().repeat_interleave(group, 1)) * s.double().repeat_interleave(group, 1)
+    for k0 in range(0, K, M):
+        n = min(M, K - k0)
+        X = torch.zeros((M, K), dtype=torch.float16)
+        X[torch.arange(n), k0 + torch.arange(n)] = 1.0
+        C = g.linear_w4(X.to(DEV), *W, N=N, group=group)
+        assert torch.equal(C[:n].double().cpu(), w[:, k0:k0 + n].t()) and (C[n:] == 0).all()
+    assert g.check() == g.GEMM_OK
+
+
+def test_rows_of_many_do_not_reach_one_another(g):
+    W = packed(g, 96, 512, 64, True, torch.float16, 1)
+    X = torch.randn((40, 512), device=DEV).half()
+    want = g.linear_w4(X, *W, group=64)
+    X[5, 100], X[37, 0] = float("inf"), float("nan")
+    got = g.linear_w4(X, *W, group=64)
+    rows = [i for i in range(40) if i not in (5, 37)]
+    assert torch.equal(got[rows], want[rows])
+    assert not torch.isfinite(got[5]).any() and torch.isnan(got[37]).all()
+
+
+@pytest.mark.parametrize("M", [8, 32, 64])
+def test_two_streams_and_replays(g, M):
+    """Calls on two streams at once and replayed from two graphs give what one call gives."""
+    W = [packed(g, 4096, 1024, 128, False, torch.bfloat16, i) for i in range(2)]
+    X = torch.randn((M, 1024), device=DEV).bfloat16()
+    want = [g.linear_w4(X, *w, group=128) for w in W]
+    streams = [torch.cuda.Stream() for _ in W]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, w in zip(streams, W):
+            with torch.cuda.stream(s):
+                got.append([g.linear_w4(X, *w, group=128) for _ in range(4)])
+        torch.cuda.synchronize()
+        assert all(torch.equal(c, want[i]) for i in range(2) for c in got[i])
+    graphs, outs = [], []
+    for s, w in zip(streams, W):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(g.linear_w4(X, *w, group=128))
+        graphs.append(graph)
+    for _ in range(3):
+        for c in outs:
+            c.zero_()
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(c, w) for c, w in zip(outs, want))
+    assert g.check() == g.GEMM_OK
+
+
+@pytest.mark.parametrize("N,K", [(256, 1024), (4096, 4096), (33, 64)])
+def test_wait_runs_out_and_context_survives(g, N, K):
+    W = packed(g, N, K, 64, True, torch.float16, 2)
+    X = torch.randn((40, K), device=DEV).half()
+    C = torch.full((40, N), 5.0, device=DEV).half()
+    assert g.check() == g.GEMM_OK
+    args = (X.data_ptr(), g.TYPES[X.dtype], W[0].data_ptr(), W[1].data_ptr(), W[2].data_ptr(), C.data_ptr(), 40, N, K, 64)
+    st = g.lib().linear_w4_selftest_timeout(*args, 1 << 20, torch.cuda.current_stream().cuda_stream)
+    assert st == g.GEMM_OK
+    assert g.check() == g.GEMM_ERR_TIMEOUT
+    assert (g.last_timeout_record() & 0xFF) == 3, hex(g.last_timeout_record())
+    assert (C == 5.0).all()
+    check(g, X, W, N, 64, False)
+    assert g.lib().linear_w4_selftest_timeout(*args, 1, None) == g.GEMM_ERR_INVALID_ARG
+    few = args[:6] + (32,) + args[7:]
+    assert g.lib().linear_w4_selftest_timeout(*few, 1 << 20, None) == g.GEMM_ERR_INVALID_ARG
