@@ -108,7 +108,7 @@ struct W4TmemShape {
     static constexpr int STRIPS = 8, WAYS = 2;          // warps of W: a strip, every other unit
     static constexpr int THREADS = 32 * (8 + STRIPS * WAYS + 1);
     static constexpr int COLS = NX / 2;                 // of a warp that sums
-    static constexpr int DEPTH = 16;                    // units of W under way
+    static constexpr int DEPTH = 8;                    // units of W under way
     static constexpr int SLOT = 1024 + U * 16;          // bytes: codes, zero points
     static constexpr int S_DEPTH = 8, S_SLOT = 64 * U;  // scales of two strips
     static constexpr int X_ATOM = NX * 128;             // bytes: 64 columns
@@ -191,16 +191,24 @@ __global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm1
         const uint8_t *ring = mem + Shape::S_OFF + warp * (Shape::S_DEPTH * Shape::S_SLOT);
         const uint32_t ring_at = smem_addr(ring) + lane * 8;
         int group = static_cast<int>(blockIdx.x), u = u_begin;   // the next to copy
+        const uint8_t *s_src = nullptr;
+        auto seek = [&]() {
+            const int strip = min(group * Shape::STRIPS + 2 * quarter + half, p.strips - 1);
+            s_src = p.S + (static_cast<int64_t>(strip) * p.groups + static_cast<int64_t>(u) * U) * 32 + piece * 8;
+        };
+        seek();
         auto next = [&](int i) {
-            if (i < total && copies) {
-                const int strip = min(group * Shape::STRIPS + 2 * quarter + half, p.strips - 1);
-                const bool in = u * U + piece_group < p.groups;
-                const uint8_t *src = p.S + (static_cast<int64_t>(strip) * p.groups + static_cast<int64_t>(u) * U) * 32 + piece * 8;
-                w4_copy8(ring_at + (i % Shape::S_DEPTH) * Shape::S_SLOT, in ? src : p.S, in);
-            }
-            if (++u == u_end) {
-                u = u_begin;
-                group += static_cast<int>(gridDim.x);
+            if (i < total) {
+                if (copies) {
+                    const bool in = u + 1 < p.units || u * U + piece_group < p.groups;
+                    w4_copy8(ring_at + (i % Shape::S_DEPTH) * Shape::S_SLOT, in ? s_src : p.S, in);
+                }
+                s_src += U * 32;
+                if (++u == u_end) {
+                    u = u_begin;
+                    group += static_cast<int>(gridDim.x);
+                    seek();
+                }
             }
             w4_commit();
         };
@@ -350,31 +358,37 @@ __global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm1
             i_w += WAYS;
             seek(WAYS);
         };
-        // Two of every 16 rows of X: this lane's 16 bytes of a row's 256, whose halves go to
-        // different places.  The rows differ by two, so that the swizzle puts what a warp
-        // stores into different banks.
+        // Rows j and j + 8 of every 16 of X: this lane's 16 bytes of a row's 256, whose
+        // halves go to different places.
         constexpr int XL = NX / 16;
-        const int x_row = (j >> 2) * 8 + (j & 1) + (j & 2) * 2 + (lane >> 4) * 2, x_piece = lane & 15, x_swap = x_row & 7;
+        const int x_row = j + (lane >> 4) * 8, x_piece = lane & 15;
         const int first = (x_piece >> 2) * 64 + (x_piece & 3) * 8, second = first + 32;
         uint8_t *x_to = mem + Shape::X_OFF + (first >> 7) * Shape::X_ATOM + x_row * 128;
-        const int x_first = ((((first & 127) >> 4) ^ x_swap) << 4) + (first & 8), x_second = ((((second & 127) >> 4) ^ x_swap) << 4) + (second & 8);
-        const uint64_t x_lo = reinterpret_cast<uint64_t>(p.X), x_hi = x_lo + static_cast<uint64_t>(p.M) * p.K * sizeof(T);
-        const T *x_mine = p.X + x_row * p.K + x_piece * 8;
+        const int x_first = ((((first & 127) >> 4) ^ j) << 4) + (first & 8), x_second = ((((second & 127) >> 4) ^ j) << 4) + (second & 8);
+        const int x_loads = x_row < p.M ? (p.M - x_row + 15) / 16 : 0;   // of this lane
+        const int64_t x_step = 16 * p.K;
         int x_u = u_begin + way;   // the next to load
         while (x_u >= u_end) x_u -= mine;
+        const T *x_src = p.X + x_row * p.K + static_cast<int64_t>(x_u) * 128 + x_piece * 8;
         uint4 xv[XL];
         auto load_x = [&]() {
-            const int64_t k0 = static_cast<int64_t>(x_u) * 128, left = p.K - (k0 + x_piece * 8);
-            const T *src = x_mine + k0;
+            const T *src = x_src;
+            if (p.vec) {
+                const int loads = x_u + 1 < p.units || x_u * 128 + x_piece * 8 < p.K ? x_loads : 0;
 #pragma unroll
-            for (int m = 0; m < XL; ++m) {
-                xv[m] = make_uint4(0u, 0u, 0u, 0u);
-                if (x_row + m * 16 < p.M && left > 0) {
-                    if (p.vec) xv[m] = __ldg(reinterpret_cast<const uint4 *>(src + m * 16 * p.K));
-                    else xv[m] = w4_eight(src + m * 16 * p.K, left, x_lo, x_hi);
+                for (int m = 0; m < XL; ++m, src += x_step)
+                    xv[m] = m < loads ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                const uint64_t lo = reinterpret_cast<uint64_t>(p.X), hi = lo + static_cast<uint64_t>(p.M) * p.K * sizeof(T);
+                const int64_t left = p.K - (static_cast<int64_t>(x_u) * 128 + x_piece * 8);
+#pragma unroll
+                for (int m = 0; m < XL; ++m, src += x_step) {
+                    xv[m] = make_uint4(0u, 0u, 0u, 0u);
+                    if (m < x_loads && left > 0) xv[m] = w4_eight(src, left, lo, hi);
                 }
             }
-            for (x_u += WAYS; x_u >= u_end;) x_u -= mine;
+            x_src += WAYS * 128;
+            for (x_u += WAYS; x_u >= u_end; x_u -= mine) x_src -= mine * 128;
         };
         auto store_x = [&](int stage) {
 #pragma unroll
