@@ -26,7 +26,7 @@ int launch_w4(const W4LinearArgs &a)
     p.relu = a.relu;
     p.vec = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.K % 8 == 0;
     // By mma.sync, 8 rows of X to an instruction, or from tensor memory, whose MMAs take 64
-    // in the time of 8: 64 x 8192 x 8192 39 and 30 us, 40 x 4096 x 4096 28 and 12, but
+    // in the time of 8: 64 x 8192 x 8192 39 and 26 us, 40 x 4096 x 4096 28 and 11, but
     // 32 x 8192 x 8192 22.3 and 23.1 (and that with 32), 16 x 8192 x 8192 14.5 and 20.2.
     if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
     if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);

@@ -25,11 +25,11 @@
 //
 // Every warp's code between two waits runs alone on its scheduler for most of the time:
 // with a warp per strip for all units a unit took 1400 cycles, of which W's were 1250.
-// Bound by that and by shared memory, where X is stored and read again for every 128
-// rows of W: 64 x 16384 x 8192 fp16 53 us (87 us by mma.sync with bf16, here 58),
-// 64 x 4096 x 4096 12.7 us (32), 64 x 2048 x 2048 8.8 us (12.6), 64 x 1024 x 8192 13.4 us
-// (27).  With 32 rows of X and a 32-column operand it took as long as mma.sync, with 16
-// a third longer.
+// With two it is bound by instructions (74 % of the issue slots at 64 x 16384 x 8192):
+// the codes' conversion and X's way into shared memory, again for every 128 rows of W.
+// 64 x 16384 x 8192 bf16 50 us (87 by mma.sync), 64 x 4096 x 4096 fp16 11.1 us (32),
+// 64 x 2048 x 2048 7.7 us (12.6), 64 x 1024 x 8192 bf16 12 us (27).  With 32 rows of X and
+// a 32-column operand it took as long as mma.sync, with 16 a third longer.
 //
 // K may be divided over the blocks of a cluster, whose sums are added through
 // distributed shared memory.  Every wait is bounded: on expiry the site is recorded in
