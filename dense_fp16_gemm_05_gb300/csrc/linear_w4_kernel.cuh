@@ -8,11 +8,12 @@
 // as the 16-row operand and up to 8 rows of X as the 8-column one: the codes are
 // laid out so that one 16-byte load per lane is the operand of four such products,
 // and q - z is exact in 16 bits, so what is rounded is the fp32 sum alone; a
-// group's sum is scaled in fp32.  (For more than 32 rows of X: linear_w4_tmem.cuh.)
+// group's sum is scaled in fp32.  (For more than 32 rows of X, and for
+// more than 16 beside a large weight: linear_w4_tmem.cuh.)
 //
 // 1 x 4096 x 4096 takes 4.5 us, 1 x 16384 x 8192 16.9 us (4.1 TB/s), 8 x 16384 x 8192 bf16
-// with zero points 22 us, 16 x 16384 x 8192 29.4 us, 32 x 16384 x 8192 44 us; with
-// the products left out the copies alone take 13 to 17 us at that size.  With one row of
+// with zero points 22 us, 16 x 16384 x 8192 29.4 us, 24 x 1024 x 8192 8.7 us; with
+// the products left out the copies alone take 13 to 17 us at 16384 x 8192.  With one row of
 // X the copies and the conversion of the codes share the time, with more it is the
 // instructions: for eight codes of a lane some 11 of conversion, and the mma.sync.
 //

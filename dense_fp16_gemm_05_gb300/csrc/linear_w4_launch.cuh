@@ -25,13 +25,16 @@ int launch_w4(const W4LinearArgs &a)
     p.units = (p.k_tiles + 1) / 2;
     p.relu = a.relu;
     p.vec = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.K % 8 == 0;
-    // By mma.sync, 8 rows of X to an instruction, or from tensor memory, whose MMAs take 64
-    // in the time of 8: 64 x 8192 x 8192 39 and 26 us, 40 x 4096 x 4096 28 and 11, but
-    // 32 x 8192 x 8192 22.3 and 23.1 (and that with 32), 16 x 8192 x 8192 14.5 and 20.2.
+    // By mma.sync, 8 rows of X to an instruction, or from tensor memory, whose MMAs take up
+    // to 64 in the time of 8: 64 x 8192 x 8192 39 and 26 us, 40 x 4096 x 4096 28 and 11.  Up
+    // to 32 rows only if the weight is large and X on the 16-byte grid (32 x 8192 x 8192
+    // 22.3 and 20.0 us, 24 x 4096 x 4096 9.9 and 9.1, but 24 x 1024 x 8192 8.7 and 9.5,
+    // 32 x 16383 x 8191 57 and 65), up to 16 not at all (16 x 8192 x 8192 14.5 and 16.8).
     if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
     if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);
-    if (p.M <= 32) return launch_w4_kernel<T, 4, G>(p, a);
-    return launch_w4_tmem<T, G>(p, a);
+    if (p.M > 32) return launch_w4_tmem<T, 64, G>(p, a);
+    if (p.vec && p.N * p.K >= 1 << 24) return launch_w4_tmem<T, 32, G>(p, a);
+    return launch_w4_kernel<T, 4, G>(p, a);
 }
 
 }  // namespace gemm_sm103

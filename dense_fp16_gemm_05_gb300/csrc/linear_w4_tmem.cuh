@@ -1,12 +1,12 @@
-// linear_w4_tmem.cuh -- the products of linear_w4_kernel.cuh for 33 to 64 rows of X, by
+// linear_w4_tmem.cuh -- the products of linear_w4_kernel.cuh for 17 to 64 rows of X, by
 // the tensor core's own path: by mma.sync 64 rows ran at 250 TFLOP/s, an eighth of what
 // it does, and with so many rows that, not W's bytes, was what a call took.
 //
 // A block takes 128 rows of W (8 strips) times some of its columns, 128 at a time (a
 // unit).  W's codes become 16-bit q - z in registers and go to tensor memory, which
 // tcgen05.mma takes as its 128-row operand: what a lane has of a strip's 16 rows is what
-// one store of the shape 16 x 256 bits takes from it.  X's rows are the 64-column operand,
-// in shared memory.  A store places two words of a lane side by side, of the four that
+// one store of the shape 16 x 256 bits takes from it.  X's rows are the operand of 32 or
+// 64 columns, in shared memory.  A store places two words of a lane side by side, of the four that
 // hold its eight neighbouring columns: the product's columns run in the order
 //   32 h + 16 k + 4 t + i  for the column  32 h + 8 t + 4 k + i   (t, i < 4, k < 2),
 // and X's 8-byte pieces are put down in it.  As in the other kernel a scale group's
@@ -14,12 +14,12 @@
 // in fp32 on the way into the sums, which a thread keeps for its row of W: q - z is
 // exact and nothing is rounded to 16 bits but the result.
 //
-//   warps 0 - 7   sums: one row of W and half of the columns per thread; scales through
-//                 rings of their own
-//   warps 8 - 23  W, a strip and every other unit each, through rings of asynchronous
+//   warps 0 - 3   sums: one row of W and 32 columns per thread (0 - 7 for 64 columns);
+//                 scales through rings of their own
+//   16 warps      W, a strip and every other unit each, through rings of asynchronous
 //                 copies; and some rows of X, by registers (8-byte asynchronous copies of
 //                 a warp took some 25 cycles each and were the bound)
-//   warp 24       allocates tensor memory; issues the MMAs, and one commit per unit (or
+//   last warp     allocates tensor memory; issues the MMAs, and one commit per unit (or
 //                 two), which tells everybody that it is done: a commit holds the lane
 //                 for 100 cycles and more
 //
@@ -28,8 +28,9 @@
 // With two it is bound by instructions (74 % of the issue slots at 64 x 16384 x 8192):
 // the codes' conversion and X's way into shared memory, again for every 128 rows of W.
 // 64 x 16384 x 8192 bf16 50 us (87 by mma.sync), 64 x 4096 x 4096 fp16 11.1 us (32),
-// 64 x 2048 x 2048 7.7 us (12.6), 64 x 1024 x 8192 bf16 12 us (27).  With 32 rows of X and
-// a 32-column operand it took as long as mma.sync, with 16 a third longer.
+// 64 x 2048 x 2048 7.7 us (12.6), 64 x 1024 x 8192 bf16 12 us (27),
+// 32 x 16384 x 8192 40 us (44).  With 16 rows of X and a 16-column operand it takes longer
+// than mma.sync (33 us, 29).
 //
 // K may be divided over the blocks of a cluster, whose sums are added through
 // distributed shared memory.  Every wait is bounded: on expiry the site is recorded in
@@ -101,13 +102,14 @@ struct W4TmemExtra {
     int32_t withhold; // test hook: 1 = W's operands are not handed over; 0 in every normal call
 };
 
-template <int G>
+// NX: columns of the MMA, rows of X.
+template <int NX, int G>
 struct W4TmemShape {
-    static constexpr int NX = 64;                       // columns of the MMA: rows of X
     static constexpr int U = 128 / G;                   // scale groups of a unit
     static constexpr int STRIPS = 8, WAYS = 2;          // warps of W: a strip, every other unit
-    static constexpr int THREADS = 32 * (8 + STRIPS * WAYS + 1);
-    static constexpr int COLS = NX / 2;                 // of a warp that sums
+    static constexpr int SUMS = NX == 64 ? 8 : 4;       // warps that sum
+    static constexpr int THREADS = 32 * (SUMS + STRIPS * WAYS + 1);
+    static constexpr int COLS = NX * 4 / SUMS;          // of a warp that sums
     static constexpr int DEPTH = 8;                    // units of W under way
     static constexpr int SLOT = 1024 + U * 16;          // bytes: codes, zero points
     static constexpr int S_DEPTH = 8, S_SLOT = 64 * U;  // scales of two strips
@@ -120,7 +122,7 @@ struct W4TmemShape {
     static constexpr int UNITS_DONE = 8;                // barriers of units, more than are under way
     static constexpr int X_OFF = 0, RING_OFF = A_STAGES * X_STAGE;
     static constexpr int S_OFF = RING_OFF + STRIPS * DEPTH * SLOT;
-    static constexpr int CTL_OFF = S_OFF + 8 * S_DEPTH * S_SLOT;
+    static constexpr int CTL_OFF = S_OFF + SUMS * S_DEPTH * S_SLOT;
     static constexpr int BARS = UNITS_DONE * PARTS + A_STAGES + D_SLOTS + 1;
     static constexpr int BYTES = 1024 + CTL_OFF + BARS * 8 + 16;   // 1024: alignment
     static_assert(NX * 128 * 4 <= RING_OFF, "a cluster's sums, in the place of X");
@@ -129,14 +131,14 @@ struct W4TmemShape {
     static_assert(BYTES <= 227 * 1024, "shared memory of a block");
 };
 
-template <class T, int G>
-__global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm103a(W4Params<T> p, W4TmemExtra e)
+template <class T, int NX, int G>
+__global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem_sm103a(W4Params<T> p, W4TmemExtra e)
 {
     using Codes = W4Codes<T>;
-    using Shape = W4TmemShape<G>;
-    constexpr int NX = Shape::NX, U = Shape::U, D = Shape::DEPTH, AS = Shape::A_STAGES, DS = Shape::D_SLOTS;
+    using Shape = W4TmemShape<NX, G>;
+    constexpr int U = Shape::U, D = Shape::DEPTH, AS = Shape::A_STAGES, DS = Shape::D_SLOTS;
     constexpr int WAYS = Shape::WAYS, DW = D / WAYS;   // of a warp of W
-    constexpr int kMmaWarp = 8 + Shape::STRIPS * WAYS;
+    constexpr int SUMS = Shape::SUMS, kMmaWarp = SUMS + Shape::STRIPS * WAYS;
     constexpr int COLS = Shape::COLS, PARTS = Shape::PARTS, PART = Shape::PART, UD = Shape::UNITS_DONE;
     extern __shared__ uint8_t smem_w4[];
     const uint32_t raw = smem_addr(smem_w4), base = (raw + 1023u) & ~1023u;
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm1
     if (threadIdx.x == 0) {
         for (int i = 0; i < UD * PARTS; ++i) mbar_init(done(i), 1);
         for (int i = 0; i < AS; ++i) mbar_init(full(i), Shape::STRIPS);
-        for (int i = 0; i < DS; ++i) mbar_init(d_free(i), 8);
+        for (int i = 0; i < DS; ++i) mbar_init(d_free(i), SUMS);
         mbar_init(drain, 1);
         *abort.local = 0;
         fence_mbar_init();
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm1
     griddep_wait();
     griddep_launch_dependents();
 
-    if (warp < 8) {
+    if (warp < SUMS) {
         // ---------------------------------------------------------------- sums
         // The first 8 U lanes copy this warp's scales, of strips 2 quarter and 2 quarter + 1.
         const int quarter = warp & 3, first_col = (warp >> 2) * COLS;
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm1
         // ---------------------------------------------------------------- W and X
         // Strip j of the eight, of which a quarter of TMEM has two, and units way, way +
         // WAYS, ... of the block's.
-        const int j = (warp & 3) * 2 + ((warp >> 2) & 1), way = (warp - 8) >> 3;
+        const int j = (warp & 3) * 2 + (((warp - SUMS) >> 2) & 1), way = (warp - SUMS) >> 3;
         const int g = lane >> 2;
         const uint8_t *ring = mem + Shape::RING_OFF + (way * Shape::STRIPS + j) * (DW * Shape::SLOT);
         const uint32_t q_to = smem_addr(ring) + lane * 16, z_to = smem_addr(ring) + 1024 + lane * 8;
@@ -493,17 +495,17 @@ __global__ void __launch_bounds__(W4TmemShape<G>::THREADS, 1) linear_w4_tmem_sm1
     cluster_wait();
 }
 
-template <class T, int G>
+template <class T, int NX, int G>
 int launch_w4_tmem(W4Params<T> p, const W4LinearArgs &a)
 {
-    using Shape = W4TmemShape<G>;
-    auto kern = linear_w4_tmem_sm103a<T, G>;
+    using Shape = W4TmemShape<NX, G>;
+    auto kern = linear_w4_tmem_sm103a<T, NX, G>;
     static std::atomic<int> prepared[kMaxDevices];
     static W4Clusters clusters[kMaxDevices];
     if (!w4_prepare(kern, Shape::THREADS, Shape::BYTES, a, prepared, clusters)) return GEMM_ERR_LAUNCH;
     const int groups = (p.strips + Shape::STRIPS - 1) / Shape::STRIPS;
-    // Blocks of a cluster for each group of strips: a unit takes some 850 ns, the
-    // exchange of the sums as many as this.
+    // Blocks of a cluster for each group of strips: a unit takes some 720 ns (32 columns:
+    // 600), the exchange of the sums as many as this.
     static constexpr float kExchange[] = {0.0f, 1000.0f, 1500.0f, 2500.0f};
     float least = 1e30f;
     int slices = 1;
@@ -511,7 +513,7 @@ int launch_w4_tmem(W4Params<T> p, const W4LinearArgs &a)
         const int most = clusters[a.device].most[l].load(std::memory_order_relaxed);
         if (most == 0 || (l > 0 && groups > most)) continue;
         const int units = (p.units + (1 << l) - 1) >> l;
-        const float cost = static_cast<float>((groups + most - 1) / most * units) * 850.0f + kExchange[l];
+        const float cost = static_cast<float>((groups + most - 1) / most * units) * (NX == 64 ? 720.0f : 600.0f) + kExchange[l];
         if (cost >= least) continue;
         least = cost;
         slices = 1 << l;

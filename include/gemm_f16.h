@@ -633,8 +633,8 @@ int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8
               int64_t K, int group, int relu, void *stream);
 
 /*
- * linear_w4_selftest_timeout -- exercises the bounded waits of linear_w4's kernel for
- * more than 32 rows of X (a test hook as gemm_f16_selftest_timeout; C is left alone).
+ * linear_w4_selftest_timeout -- exercises the bounded waits of linear_w4's tensor
+ * memory kernel, here for more than 32 rows of X (a test hook as gemm_f16_selftest_timeout; C is left alone).
  * W's operands are not handed to the tensor core and a wait may take timeout_cycles
  * (2^16 .. 2^32) SM clocks; gemm_f16_check then returns GEMM_ERR_TIMEOUT (site 3).
  */

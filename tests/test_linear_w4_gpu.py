@@ -305,3 +305,18 @@ def test_wait_runs_out_and_context_survives(g, N, K):
     assert g.lib().linear_w4_selftest_timeout(*args, 1, None) == g.GEMM_ERR_INVALID_ARG
     few = args[:6] + (32,) + args[7:]
     assert g.lib().linear_w4_selftest_timeout(*few, 1 << 20, None) == g.GEMM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("xt", ["fp16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(17, 4096, 4096), (32, 16400, 1024), (24, 8200, 2056), (31, 65600, 256), (20, 130, 131072),
+                                   (32, 140000, 120)])
+def test_some_rows_beside_a_large_weight(g, M, N, K, group, xt):
+    W = packed(g, N, K, group, group == 64, DTYPES[xt], M + N + K)
+    gen = torch.Generator().manual_seed(K)
+    X = torch.randn((M, K), generator=gen).to(DTYPES[xt]).to(DEV)
+    C = check(g, X, W, N, group, relu=M % 2 == 0)
+    buf = torch.full((M * N + 64,), 7.0, dtype=X.dtype, device=DEV)
+    out = buf[32:32 + M * N].reshape(M, N)
+    assert torch.equal(g.linear_w4(X, *W, N=N, group=group, relu=M % 2 == 0, C=out), C)
+    assert (buf[:32] == 7).all() and (buf[32 + M * N:] == 7).all()
