@@ -11,6 +11,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sm103_ptx.cuh"
 
@@ -27,6 +28,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 }
 
 __device__ __forceinline__ uint32_t fp8_magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// The largest of |m|, |x.x| and |x.y|, NaN if one of them is, in one instruction.
+__device__ __forceinline__ float fp8_largest(float m, float2 x)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(x.x), "f"(x.y));
+    return r;
+}
 
 // Scale of a block whose largest |x| has the bit pattern `amax` (NaN above
 // infinity), and what its elements are converted with.  kTies: see codes().
@@ -73,17 +81,32 @@ struct Fp8Block {
         }
     }
 
+    // Calls f(std::integral_constant<int, way>{}) for the way that the block's elements are
+    // converted: decided once for all of them.
+    template <class F>
+    __device__ __forceinline__ void by_way(F f) const
+    {
+        if (pow2 || (!kTies && !near_limits)) {
+            f(std::integral_constant<int, 0>{});
+        } else if (!near_limits) {
+            if constexpr (kTies) f(std::integral_constant<int, 1>{});
+        } else {
+            f(std::integral_constant<int, 2>{});
+        }
+    }
+
     // Two elements' codes.  With kTies 448 x / a is the product with 1 / a put right by
     // its remainder (P. Markstein, IBM J. Res. Dev. 34, 1990): a quotient half way
     // between two codes, which 16-bit elements often give, stays there.  Elements that
     // are results in fp32 are multiplied with 448 / a.
+    template <int kWay>
     __device__ __forceinline__ uint32_t codes(float2 x) const
     {
         float2 q;
         const float2 inv2 = make_float2(inv, inv);
-        if (pow2 || (!kTies && !near_limits)) {
+        if constexpr (kWay == 0) {
             q = mul_f32x2(x, inv2);
-        } else if (!near_limits) {
+        } else if constexpr (kWay == 1) {
             const float2 t = mul_f32x2(x, make_float2(448.0f, 448.0f));
             q = mul_f32x2(t, inv2);
             q = fma_f32x2(fma_f32x2(q, make_float2(-a, -a), t), inv2, q);

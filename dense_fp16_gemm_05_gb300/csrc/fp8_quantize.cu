@@ -89,21 +89,24 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows(QuantParams<T
         const uint32_t i = first + static_cast<uint32_t>(u * S);
         if (lane == 0 && i < p.total) Fp8Block<true>::store(p.S, i, m, p.pow2 != 0);
         const Fp8Block<true> b(m, p.pow2 != 0);
+        b.by_way([&](auto way) {
+            constexpr int W8 = decltype(way)::value;
 #pragma unroll
-        for (int j = 0; j < E / V; ++j) {
-            if (j * L * V >= left[u]) continue;
-            uint8_t *q = p.Q + at[u] + j * L * V;
-            if constexpr (V == 1) {
-                *q = static_cast<uint8_t>(b.codes(make_float2(x[u][j][0], 0.0f)));
-            } else {
-                uint32_t c[V / 4];
+            for (int j = 0; j < E / V; ++j) {
+                if (j * L * V >= left[u]) continue;
+                uint8_t *q = p.Q + at[u] + j * L * V;
+                if constexpr (V == 1) {
+                    *q = static_cast<uint8_t>(b.template codes<W8>(make_float2(x[u][j][0], 0.0f)));
+                } else {
+                    uint32_t c[V / 4];
 #pragma unroll
-                for (int e = 0; e < V / 4; ++e)
-                    c[e] = b.codes(x[u][j].pair(2 * e)) | (b.codes(x[u][j].pair(2 * e + 1)) << 16);
-                if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
-                else *reinterpret_cast<uint32_t *>(q) = c[0];
+                    for (int e = 0; e < V / 4; ++e)
+                        c[e] = b.template codes<W8>(x[u][j].pair(2 * e)) | (b.template codes<W8>(x[u][j].pair(2 * e + 1)) << 16);
+                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
+                    else *reinterpret_cast<uint32_t *>(q) = c[0];
+                }
             }
-        }
+        });
     }
 }
 
@@ -138,6 +141,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
     for (int i = 0; i < 8; ++i) m = max(m, sh[i]);
     if (threadIdx.x == 0) Fp8Block<true>::store(p.S, blockIdx.x, m, p.pow2 != 0);
     const Fp8Block<true> b(m, p.pow2 != 0);
+    b.by_way([&](auto way) {
+        constexpr int W8 = decltype(way)::value;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -146,16 +151,17 @@ __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
             if (row >= p.rows || k >= p.K) continue;
             uint8_t *q = p.Q + row * p.K + k;
             if constexpr (V == 1) {
-                *q = static_cast<uint8_t>(b.codes(make_float2(x[r][j][0], 0.0f)));
+                *q = static_cast<uint8_t>(b.template codes<W8>(make_float2(x[r][j][0], 0.0f)));
             } else {
                 uint32_t c[V / 4];
 #pragma unroll
                 for (int e = 0; e < V / 4; ++e)
-                    c[e] = b.codes(x[r][j].pair(2 * e)) | (b.codes(x[r][j].pair(2 * e + 1)) << 16);
+                    c[e] = b.template codes<W8>(x[r][j].pair(2 * e)) | (b.template codes<W8>(x[r][j].pair(2 * e + 1)) << 16);
                 if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
                 else *reinterpret_cast<uint32_t *>(q) = c[0];
             }
         }
+    });
 }
 
 template <class T, int V>

@@ -210,9 +210,11 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
         constexpr int L = RL;
 #pragma unroll
         for (int i0 = 0; i0 < NV; i0 += G) {
-            uint32_t m = 0;
+            static_assert(G * V % 2 == 0, "pairs");
+            float largest = 0.0f;
 #pragma unroll
-            for (int e = i0 * V; e < (i0 + G) * V; ++e) m = max(m, fp8_magnitude(ln_half(h[e / 2], e)));
+            for (int e = i0 * V / 2; e < (i0 + G) * V / 2; ++e) largest = fp8_largest(largest, h[e]);
+            uint32_t m = __float_as_uint(largest);
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             const int k0 = column(i0);
@@ -220,24 +222,28 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
             if ((t & (L - 1)) == 0 && k0 < p.dim)
                 Fp8Block<false>::store(p.S, row * p.blocks + (kOne ? 0 : k0 / kFp8Block), m, p.pow2 != 0);
             const Fp8Block<false> b(m, p.pow2 != 0);
+            b.by_way([&](auto way) {
+                constexpr int W8 = decltype(way)::value;
 #pragma unroll
-            for (int i = i0; i < i0 + G; ++i) {
-                const int k = column(i);
-                if (k >= p.dim) continue;
-                uint8_t *q = p.Q + at + k;
-                if constexpr (V == 1) {
-                    *q = static_cast<uint8_t>(b.codes(make_float2(ln_half(h[i / 2], i), 0.0f)));
-                } else if constexpr (V == 2) {
-                    *reinterpret_cast<uint16_t *>(q) = static_cast<uint16_t>(b.codes(h[i]));
-                } else {
-                    uint32_t c[V / 4];
+                for (int i = i0; i < i0 + G; ++i) {
+                    const int k = column(i);
+                    if (k >= p.dim) continue;
+                    uint8_t *q = p.Q + at + k;
+                    if constexpr (V == 1) {
+                        *q = static_cast<uint8_t>(b.template codes<W8>(make_float2(ln_half(h[i / 2], i), 0.0f)));
+                    } else if constexpr (V == 2) {
+                        *reinterpret_cast<uint16_t *>(q) = static_cast<uint16_t>(b.template codes<W8>(h[i]));
+                    } else {
+                        uint32_t c[V / 4];
 #pragma unroll
-                    for (int j = 0; j < V / 4; ++j)
-                        c[j] = b.codes(h[i * (V / 2) + 2 * j]) | (b.codes(h[i * (V / 2) + 2 * j + 1]) << 16);
-                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
-                    else *reinterpret_cast<uint32_t *>(q) = c[0];
+                        for (int j = 0; j < V / 4; ++j)
+                            c[j] = b.template codes<W8>(h[i * (V / 2) + 2 * j]) |
+                                   (b.template codes<W8>(h[i * (V / 2) + 2 * j + 1]) << 16);
+                        if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
+                        else *reinterpret_cast<uint32_t *>(q) = c[0];
+                    }
                 }
-            }
+            });
         }
     }
 }
@@ -297,11 +303,13 @@ __global__ void __launch_bounds__(1024) rms_norm_fwd_long(RmsParams<T, W> p)
             m = __reduce_max_sync(0xffffffffu, m);
             if (lane == 0) Fp8Block<false>::store(p.S, row * p.blocks + k0 / kFp8Block, m, p.pow2 != 0);
             const Fp8Block<false> b(m, p.pow2 != 0);
+            b.by_way([&](auto way) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t k = k0 + j * 32 + lane;
-                if (k < p.dim) p.Q[at + k] = static_cast<uint8_t>(b.codes(make_float2(y[j], 0.0f)));
-            }
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t k = k0 + j * 32 + lane;
+                    if (k < p.dim) p.Q[at + k] = static_cast<uint8_t>(b.template codes<decltype(way)::value>(make_float2(y[j], 0.0f)));
+                }
+            });
         }
     }
 }
