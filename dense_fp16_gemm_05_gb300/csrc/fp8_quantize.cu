@@ -47,8 +47,9 @@ __device__ __forceinline__ uint32_t pack_magnitude(const LnPack<T, V> &x)
 // Blocks of a row: kUnroll of them per group of eight lanes (single elements: a warp),
 // their loads under way together.  V: elements per load, 16 bytes or one.  With
 // 16 lanes and one 16-byte pack each the scale's arithmetic came to a third of the
-// instructions (8192 x 8192 bf16 with fp32 scales 50 us, 37 us so; fp16 with powers
-// of two 38 us and 31 us, 6.5 TB/s).
+// instructions (8192 x 8192 bf16 with fp32 scales 50 us, 37 us so, 33.7 us since the way
+// of conversion is decided once per block; fp16 with powers of two 38 us and 31 us,
+// 6.5 TB/s).
 constexpr int kQuantThreads = 256, kUnroll = 2;
 __host__ __device__ constexpr int quant_lanes(int v) { return v > 1 ? 8 : 32; }
 
