@@ -12,7 +12,7 @@
 // more than 16 beside a large weight: linear_w4_tmem.cuh.)
 //
 // 1 x 4096 x 4096 takes 4.5 us, 1 x 16384 x 8192 16.9 us (4.1 TB/s), 8 x 16384 x 8192 bf16
-// with zero points 22 us, 16 x 16384 x 8192 29.4 us, 24 x 1024 x 8192 8.7 us; with
+// with zero points 22 us, 16 x 16384 x 8192 27.9 us, 24 x 1024 x 8192 8.7 us; with
 // the products left out the copies alone take 13 to 17 us at 16384 x 8192.  With one row of
 // X the copies and the conversion of the codes share the time, with more it is the
 // instructions: for eight codes of a lane some 11 of conversion, and the mma.sync.
@@ -174,9 +174,9 @@ struct W4Shape {
     static constexpr int COLS = NT * 8;
     static constexpr int U = 128 / G;                     // scale groups of a unit
     static constexpr int SLOT = 1024 + U * 48;            // bytes: codes, scales, zero points
-    static constexpr int DEPTH = NT <= 2 ? 6 : 4;         // units under way per warp
+    static constexpr int DEPTH = NT == 1 ? 6 : 4;         // units under way per warp
     static constexpr int RING = kW4Warps * DEPTH * SLOT;
-    static constexpr int X_UNITS = NT <= 2 ? 8 : 4;       // of a chunk of X, at least DEPTH
+    static constexpr int X_UNITS = NT == 2 ? 16 : 8;       // of a chunk of X, at least DEPTH
     static constexpr int SUMS = kW4Warps * 16 * (COLS + 1) * 4;
 };
 
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
         const int n = u_end - u_begin;
         seek(static_cast<int>(blockIdx.x) * p.rw + rw, u_begin);
         clear();
-        copy_x(x_mem, u_begin, min(XU, n));
+        copy_x(x_mem, u_begin, XU);
 #pragma unroll
         for (int i = 0; i < D; ++i) {
             if (i < n) fetch(i * Shape::SLOT, u_begin + i);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) linear_w4_kernel(W4Params<T> p)
             w4_wait<D - 1>();
             if (x_unit == 0) {
                 __syncthreads();   // this chunk is there, and the one before is done with
-                if (i + XU < n) copy_x(x_mem + (x_buffer ^ 1) * p.x_bytes, u_begin + i + XU, min(XU, n - i - XU));
+                if (i + XU < n) copy_x(x_mem + (x_buffer ^ 1) * p.x_bytes, u_begin + i + XU, XU);
             } else {
                 __syncwarp();
             }
