@@ -19,7 +19,6 @@ struct QuantParams {
     uint32_t blocks;     // of a row
     uint32_t total;      // rows * blocks
     uint32_t magic, shift;   // total / blocks by multiplication
-    int32_t pow2;
 };
 
 // Largest magnitude of a pack as an fp32 bit pattern, NaN's above infinity's; 16-bit
@@ -47,13 +46,13 @@ __device__ __forceinline__ uint32_t pack_magnitude(const LnPack<T, V> &x)
 // Blocks of a row: kUnroll of them per group of eight lanes (single elements: a warp),
 // their loads under way together.  V: elements per load, 16 bytes or one.  With
 // 16 lanes and one 16-byte pack each the scale's arithmetic came to a third of the
-// instructions (8192 x 8192 bf16 with fp32 scales 50 us, 37 us so, 33.7 us since the way
-// of conversion is decided once per block; fp16 with powers of two 38 us and 31 us,
-// 6.5 TB/s).
+// instructions (8192 x 8192 bf16 with fp32 scales 50 us, 37 us so, 34 us since the way of
+// conversion is decided once per block; fp16 with powers of two 38 us and 31 us, 30.5 us,
+// 6.6 TB/s, since that kind of scale has a kernel of its own).
 constexpr int kQuantThreads = 256, kUnroll = 2;
 __host__ __device__ constexpr int quant_lanes(int v) { return v > 1 ? 8 : 32; }
 
-template <class T, int V>
+template <class T, int V, bool kPow2>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows(QuantParams<T> p)
 {
     constexpr int L = quant_lanes(V);               // of a block
@@ -88,8 +87,8 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows(QuantParams<T
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const uint32_t i = first + static_cast<uint32_t>(u * S);
-        if (lane == 0 && i < p.total) Fp8Block<true>::store(p.S, i, m, p.pow2 != 0);
-        const Fp8Block<true> b(m, p.pow2 != 0);
+        if (lane == 0 && i < p.total) Fp8Block<true>::store(p.S, i, m, kPow2);
+        const Fp8Block<true> b(m, kPow2);
         b.by_way([&](auto way) {
             constexpr int W8 = decltype(way)::value;
 #pragma unroll
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows(QuantParams<T
 }
 
 // A block of 128 x 128 elements per block of threads, 64 elements per thread.
-template <class T, int V>
+template <class T, int V, bool kPow2>
 __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
 {
     constexpr int L = kFp8Block / V < 32 ? kFp8Block / V : 32;   // lanes of a row
@@ -140,8 +139,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, sh[i]);
-    if (threadIdx.x == 0) Fp8Block<true>::store(p.S, blockIdx.x, m, p.pow2 != 0);
-    const Fp8Block<true> b(m, p.pow2 != 0);
+    if (threadIdx.x == 0) Fp8Block<true>::store(p.S, blockIdx.x, m, kPow2);
+    const Fp8Block<true> b(m, kPow2);
     b.by_way([&](auto way) {
         constexpr int W8 = decltype(way)::value;
 #pragma unroll
@@ -165,15 +164,21 @@ __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
     });
 }
 
-template <class T, int V>
-int launch_packs(const QuantParams<T> &p, int block_rows, cudaStream_t stream)
+template <class T, int V, bool kPow2>
+int launch_kind(const QuantParams<T> &p, int block_rows, cudaStream_t stream)
 {
     if (block_rows != 1)
-        return ln_launch(fp8_quantize_square<T, V>,
+        return ln_launch(fp8_quantize_square<T, V, kPow2>,
                          dim3(static_cast<unsigned>((p.rows + kFp8Block - 1) / kFp8Block * p.blocks), 1, 1), 256, stream,
                          p);
     constexpr uint32_t per = kQuantThreads / quant_lanes(V) * kUnroll;
-    return ln_launch(fp8_quantize_rows<T, V>, dim3((p.total + per - 1) / per, 1, 1), kQuantThreads, stream, p);
+    return ln_launch(fp8_quantize_rows<T, V, kPow2>, dim3((p.total + per - 1) / per, 1, 1), kQuantThreads, stream, p);
+}
+
+template <class T, int V>
+int launch_packs(const QuantParams<T> &p, const Fp8QuantArgs &a)
+{
+    return a.pow2 ? launch_kind<T, V, true>(p, a.block_rows, a.stream) : launch_kind<T, V, false>(p, a.block_rows, a.stream);
 }
 
 template <class T>
@@ -187,7 +192,6 @@ int quantize(const Fp8QuantArgs &a)
     p.K = a.K;
     p.blocks = static_cast<uint32_t>((a.K + kFp8Block - 1) / kFp8Block);
     p.total = static_cast<uint32_t>(a.rows * static_cast<int64_t>(p.blocks));
-    p.pow2 = a.pow2;
     // Division of i < 2^31 by d: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d),
     // floor(i m / 2^(31 + s)) is the quotient (T. Granlund and P. L. Montgomery,
     // PLDI 1994); m < 2^32, and i m / 2^31 is the high word of 2 i m.
@@ -198,8 +202,8 @@ int quantize(const Fp8QuantArgs &a)
     constexpr int V = 16 / sizeof(T);
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.X) | (static_cast<uintptr_t>(a.K) * sizeof(T));
     if ((bits & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.Q) & (V - 1)) == 0)
-        return launch_packs<T, V>(p, a.block_rows, a.stream);
-    return launch_packs<T, 1>(p, a.block_rows, a.stream);
+        return launch_packs<T, V>(p, a);
+    return launch_packs<T, 1>(p, a);
 }
 
 }  // namespace
