@@ -37,27 +37,32 @@ __device__ __forceinline__ float fp8_largest(float m, float2 x)
 }
 
 // Scale of a block whose largest |x| has the bit pattern `amax` (NaN above
-// infinity), and what its elements are converted with.  kTies: see codes().
-template <bool kTies>
+// infinity), and what its elements are converted with.
 struct Fp8Block {
-    float a, inv;
+    float inv, rest;   // 448 / (a k) as the sum of two numbers, or 1 / S
+    float k;           // a power of two
     bool pow2, near_limits;
 
     __device__ __forceinline__ Fp8Block(uint32_t amax, bool pow2_)
     {
         pow2 = pow2_;
-        a = __uint_as_float(amax);
         near_limits = false;
+        k = 1.0f;
+        rest = 0.0f;
         if (amax >= 0x7F800000u) {
-            a = inv = __uint_as_float(0x7FC00000u);
+            inv = __uint_as_float(0x7FC00000u);
         } else if (pow2) {
             inv = __uint_as_float((254u - byte_of(amax)) << 23);
         } else if (amax == 0u) {
-            a = inv = 1.0f;
+            inv = 1.0f;
         } else {
-            // 1 / a and 448 x stay clear of fp32's limits.
+            float a = __uint_as_float(amax);
+            // The quotient and what it lacks stay clear of fp32's limits.
             near_limits = a < 0x1p-100f || a > 0x1p100f;
-            inv = (kTies ? 1.0f : 448.0f) / a;
+            if (near_limits) k = a < 1.0f ? 0x1p100f : 0x1p-100f;
+            a *= k;
+            inv = 448.0f / a;
+            rest = fmaf(-inv, a, 448.0f) * inv * (1.0f / 448.0f);   // the remainder is exact
         }
     }
 
@@ -86,33 +91,22 @@ struct Fp8Block {
     template <class F>
     __device__ __forceinline__ void by_way(F f) const
     {
-        if (pow2 || (!kTies && !near_limits)) {
-            f(std::integral_constant<int, 0>{});
-        } else if (!near_limits) {
-            if constexpr (kTies) f(std::integral_constant<int, 1>{});
-        } else {
-            f(std::integral_constant<int, 2>{});
-        }
+        if (pow2) f(std::integral_constant<int, 0>{});
+        else if (!near_limits) f(std::integral_constant<int, 1>{});
+        else f(std::integral_constant<int, 2>{});
     }
 
-    // Two elements' codes.  With kTies 448 x / a is the product with 1 / a put right by
-    // its remainder (P. Markstein, IBM J. Res. Dev. 34, 1990): a quotient half way
-    // between two codes, which 16-bit elements often give, stays there.  Elements that
-    // are results in fp32 are multiplied with 448 / a.
+    // Two elements' codes.  448 x / a is x inv + x rest with one rounding of note: a
+    // quotient half way between two codes, which 16-bit elements often give, stays there
+    // (the product with a rounded 448 / a alone put one in thirteen of them on either side).
     template <int kWay>
     __device__ __forceinline__ uint32_t codes(float2 x) const
     {
-        float2 q;
         const float2 inv2 = make_float2(inv, inv);
-        if constexpr (kWay == 0) {
-            q = mul_f32x2(x, inv2);
-        } else if constexpr (kWay == 1) {
-            const float2 t = mul_f32x2(x, make_float2(448.0f, 448.0f));
-            q = mul_f32x2(t, inv2);
-            q = fma_f32x2(fma_f32x2(q, make_float2(-a, -a), t), inv2, q);
-        } else {
-            q = make_float2(0.875f * x.x / a * 512.0f, 0.875f * x.y / a * 512.0f);
-        }
+        if constexpr (kWay == 2) x = mul_f32x2(x, make_float2(k, k));
+        float2 q;
+        if constexpr (kWay == 0) q = mul_f32x2(x, inv2);
+        else q = fma_f32x2(x, inv2, mul_f32x2(x, make_float2(rest, rest)));
         return e4m3x2(q.x, q.y);
     }
 };

@@ -46,9 +46,10 @@ __device__ __forceinline__ uint32_t pack_magnitude(const LnPack<T, V> &x)
 // Blocks of a row: kUnroll of them per group of eight lanes (single elements: a warp),
 // their loads under way together.  V: elements per load, 16 bytes or one.  With
 // 16 lanes and one 16-byte pack each the scale's arithmetic came to a third of the
-// instructions (8192 x 8192 bf16 with fp32 scales 50 us, 37 us so, 34 us since the way of
-// conversion is decided once per block; fp16 with powers of two 38 us and 31 us, 30.5 us,
-// 6.6 TB/s, since that kind of scale has a kernel of its own).
+// instructions (8192 x 8192 bf16 with fp32 scales 50 us, 37 us so, 33 us since the way of
+// conversion is decided once per block and a quotient takes two instructions; fp16 with
+// powers of two 38 us and 31 us, 30.5 us, 6.6 TB/s, since that kind of scale has a kernel
+// of its own).
 constexpr int kQuantThreads = 256, kUnroll = 2;
 __host__ __device__ constexpr int quant_lanes(int v) { return v > 1 ? 8 : 32; }
 
@@ -87,8 +88,8 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_rows(QuantParams<T
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const uint32_t i = first + static_cast<uint32_t>(u * S);
-        if (lane == 0 && i < p.total) Fp8Block<true>::store(p.S, i, m, kPow2);
-        const Fp8Block<true> b(m, kPow2);
+        if (lane == 0 && i < p.total) Fp8Block::store(p.S, i, m, kPow2);
+        const Fp8Block b(m, kPow2);
         b.by_way([&](auto way) {
             constexpr int W8 = decltype(way)::value;
 #pragma unroll
@@ -139,8 +140,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, sh[i]);
-    if (threadIdx.x == 0) Fp8Block<true>::store(p.S, blockIdx.x, m, kPow2);
-    const Fp8Block<true> b(m, kPow2);
+    if (threadIdx.x == 0) Fp8Block::store(p.S, blockIdx.x, m, kPow2);
+    const Fp8Block b(m, kPow2);
     b.by_way([&](auto way) {
         constexpr int W8 = decltype(way)::value;
 #pragma unroll

@@ -39,8 +39,8 @@ __host__ __device__ constexpr int rms_threads(int tpr) { return tpr < 0 ? -tpr :
 // Lanes that take neighbouring packs, and the packs of each that follow at once: of
 // narrow packs, a warp's 128 columns; for FP8 output, 128 columns of eight lanes, so
 // that a scale is worked out once for 16 elements of a lane (8192 x 8192 bf16 with a
-// residual: 82 us with 16 lanes and eight elements, 71.5 us so; 69.5 us, 6.8 TB/s, since
-// the way of conversion is decided once per block).
+// residual: 82 us with 16 lanes and eight elements, 71.5 us so; 70.7 us, 6.7 TB/s, since
+// the way of conversion is decided once per block.  Without a residual, fp16, 44.4 us).
 __host__ __device__ constexpr int rms_lanes(int tpr, int v, bool fp8) { return tpr > 0 && tpr < 32 ? tpr : (v >= 4 && fp8 ? 8 : 32); }
 __host__ __device__ constexpr int rms_run(int tpr, int v, bool fp8)
 {
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
             const int k0 = column(i0);
             if (!in) continue;
             if ((t & (L - 1)) == 0 && k0 < p.dim)
-                Fp8Block<false>::store(p.S, row * p.blocks + (kOne ? 0 : k0 / kFp8Block), m, p.pow2 != 0);
-            const Fp8Block<false> b(m, p.pow2 != 0);
+                Fp8Block::store(p.S, row * p.blocks + (kOne ? 0 : k0 / kFp8Block), m, p.pow2 != 0);
+            const Fp8Block b(m, p.pow2 != 0);
             b.by_way([&](auto way) {
                 constexpr int W8 = decltype(way)::value;
 #pragma unroll
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(1024) rms_norm_fwd_long(RmsParams<T, W> p)
         }
         if constexpr (kFp8) {
             m = __reduce_max_sync(0xffffffffu, m);
-            if (lane == 0) Fp8Block<false>::store(p.S, row * p.blocks + k0 / kFp8Block, m, p.pow2 != 0);
-            const Fp8Block<false> b(m, p.pow2 != 0);
+            if (lane == 0) Fp8Block::store(p.S, row * p.blocks + k0 / kFp8Block, m, p.pow2 != 0);
+            const Fp8Block b(m, p.pow2 != 0);
             b.by_way([&](auto way) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
