@@ -80,3 +80,29 @@ def test_norms_codes_half_way_between_two(g, dim, xt, off_grid):
     assert torch.equal(S[:, 0].cpu(), (y[:, :128].abs().amax(1) / 448).float())
     want = (y[:, :128] * 448 / y[:, :128].abs().amax(1, keepdim=True)).float().to(torch.float8_e4m3fn)
     assert torch.equal(Q[:, :128].cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("exponent", [-149, -140, -131, -120, 80, 100])
+def test_codes_of_blocks_near_the_ends_of_fp32(g, exponent, block_rows):
+    """Whole numbers of up to 20 bits times a power of two, subnormals of few bits among them: the nearest codes."""
+    gen = torch.Generator().manual_seed(exponent + 200)
+    n = torch.randint(-2 ** 20, 2 ** 20, (64, 512), generator=gen).double()
+    n *= torch.exp2(-torch.randint(0, 20, (64, 512), generator=gen).double())
+    n[:8] = torch.randint(-5, 6, (8, 512), generator=gen).double()   # subnormals of three bits
+    x = (n.round() * 2.0 ** exponent).float() + 0.0   # no -0
+    Q, S = g.fp8_quantize(x.to(DEV), block_rows=block_rows)
+    assert g.check() == g.GEMM_OK and torch.isfinite(S).all()
+    b = x.double().reshape(64, 4, 128)
+    a = b.abs().amax(2, keepdim=True)
+    if block_rows == 128:
+        a = a.amax(0, keepdim=True)
+    assert (a > 0).all()
+    v = (b * 448 / a).reshape(64, 512)
+    want = v.float().to(torch.float8_e4m3fn)
+    # The quotient is off by less than 2^-23, and exact half way between two codes.
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    from_middle = ((v / step).abs() % 1 - 0.5).abs() * step
+    clear = (from_middle == 0) | (from_middle > 2.0 ** -23 * v.abs())
+    assert clear.double().mean() > 0.999
+    assert torch.equal(Q.cpu().view(torch.uint8)[clear], want.view(torch.uint8)[clear])
