@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem
             }
             __syncwarp();
             next_w(slot);
+            w4_commit();   // in front of the wait that may give up: w4_wait<0> below covers it
             slot = slot == (DW - 1) * Shape::SLOT ? 0u : slot + Shape::SLOT;
             if (i >= AS) {
                 const int before = i - AS;
@@ -447,7 +448,6 @@ __global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem
                 if (!__all_sync(0xffffffffu, got)) break;
                 tc_fence_after_sync();
             }
-            w4_commit();
             store_x(i % AS);
             load_x();   // of the warp's next unit
             tmem_store_16x256b_x8(a_lane + (i % AS) * 64, r);
