@@ -34,7 +34,7 @@
 //
 // K may be divided over the blocks of a cluster, whose sums are added through
 // distributed shared memory.  Every wait is bounded: on expiry the site is recorded in
-// the device status word and the block leaves.
+// the device status word and the block leaves, and no block of its cluster stores.
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -99,7 +99,7 @@ __device__ __forceinline__ bool w4_elect_one()
 struct W4TmemExtra {
     uint64_t limit;   // SM clocks of a wait
     unsigned long long *status;
-    int32_t withhold; // test hook: 1 = W's operands are not handed over; 0 in every normal call
+    int32_t withhold; // test hook: 1 = the last block of a cluster hands over none of W's operands; 0 in every normal call
 };
 
 // NX: columns of the MMA, rows of X.
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem
         // WAYS, ... of the block's.
         const int j = (warp & 3) * 2 + (((warp - SUMS) >> 2) & 1), way = (warp - SUMS) >> 3;
         const int g = lane >> 2;
+        const bool withheld = e.withhold != 0 && slice == slices - 1;
         const uint8_t *ring = mem + Shape::RING_OFF + (way * Shape::STRIPS + j) * (DW * Shape::SLOT);
         const uint32_t q_to = smem_addr(ring) + lane * 16, z_to = smem_addr(ring) + 1024 + lane * 8;
         const bool side = p.Z && lane < 2 * U;
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0 && e.withhold == 0) mbar_arrive(full(i % AS));
+            if (lane == 0 && !withheld) mbar_arrive(full(i % AS));
         }
     }
     w4_wait<0>();   // nothing of this thread's copies is under way
@@ -470,6 +471,11 @@ __global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem
     const float *ordered = reinterpret_cast<const float *>(mem + Shape::X_OFF);
     cluster_arrive();
     cluster_wait();
+    // A block that gave up has left no sums: then nobody stores.
+    uint32_t gave_up = 0;
+    if (lane < slices)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(gave_up) : "r"(mapa_shared(abort.addr, static_cast<uint32_t>(lane))) : "memory");
+    const bool complete = !__any_sync(0xffffffffu, gave_up != 0);
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 128;
     for (int o = 4 * (static_cast<int>(threadIdx.x) + slice * Shape::THREADS); o < p.M * 128; o += 4 * slices * Shape::THREADS) {
         const uint32_t at = smem_addr(ordered + o);
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(W4TmemShape<NX, G>::THREADS, 1) linear_w4_tmem
             for (int i = 0; i < 8; ++i)
                 if (i < slices) v += part[i][b];
             if (p.relu) v = v > 0.0f ? v : 0.0f;
-            if (n + b < p.N && *abort.local == 0) p.C[m * p.N + n + b] = ln_round<T>(v);
+            if (n + b < p.N && complete) p.C[m * p.N + n + b] = ln_round<T>(v);
         }
     }
     cluster_arrive();   // nobody leaves while its sums are read

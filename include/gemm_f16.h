@@ -635,9 +635,10 @@ int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8
 /*
  * linear_w4_selftest_timeout -- exercises the bounded waits of linear_w4's tensor
  * memory kernel, here for more than 32 rows of X (a test hook as
- * gemm_f16_selftest_timeout; C is left alone).  W's operands are not handed to the
- * tensor core and a wait may take timeout_cycles (2^16 .. 2^32) SM clocks;
- * gemm_f16_check then returns GEMM_ERR_TIMEOUT (site 3).
+ * gemm_f16_selftest_timeout; C is left alone).  Of the blocks that share K, the last
+ * hands none of W's operands to the tensor core, the others do; a wait may take
+ * timeout_cycles (2^16 .. 2^32) SM clocks; gemm_f16_check then returns
+ * GEMM_ERR_TIMEOUT (site 3).
  */
 int linear_w4_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C,
                                int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles, void *stream);
