@@ -531,7 +531,9 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
     // unit of each of a block's sixteen warps takes 450 with 8 rows of X, 1030 with 32,
     // and with fewer warps as much less, down to eleven; a group of strips ends with 500,
     // more among the blocks of a cluster, and a quarter for each output; X comes with 60
-    // bytes each, 20 where its rows are off the 16-byte grid, and in chunks half hidden.
+    // bytes each, 20 where its rows cannot lie on the 16-byte grid, and in chunks half
+    // hidden.  (Where they could and do not is not counted, so that the order of the sums
+    // does not go by X's address.)
     const int64_t room = kW4Budget - Shape::RING - 2 * Shape::SUMS;   // for a kept X
     const float unit_cost = NT == 1 ? 450.0f : (NT == 2 ? 650.0f : 1030.0f);
     static constexpr uint8_t kDivisions[][2] = {{16, 1}, {15, 1}, {14, 1}, {8, 2}, {7, 2}, {6, 2},
@@ -542,7 +544,7 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
         const int sl = 1 << l, units = (p.units + sl - 1) / sl, most = clusters[a.device].most[l].load(std::memory_order_relaxed);
         if (most == 0) continue;
         const int64_t x_bytes = p.M * w4_x_row(units);
-        const float x_cost = static_cast<float>(x_bytes) / (p.vec ? 60.0f : 20.0f);
+        const float x_cost = static_cast<float>(x_bytes) / (p.K % 8 == 0 ? 60.0f : 20.0f);
         const float end = sl == 1 ? 500.0f : (sl == 2 ? 1500.0f : (sl == 4 ? 3000.0f : 4000.0f));
         const bool fits = x_bytes <= room;
         for (const auto &d : kDivisions) {

@@ -624,9 +624,9 @@ int w4_quantize(const void *W, int type, void *Q, void *S, uint8_t *Z, int64_t N
  *   C  (M, N) row-major of X's type, overlapping no input
  *
  * Any N and K.  X and C are aligned to their element; rows of X on the 16-byte
- * grid take the vectorised path.  The division of K among
- * blocks depends on the sizes and the GPU alone and every sum has a fixed
- * order, so equal calls give equal bits.  M == 0 or N == 0: no-op; K == 0: C = +0.
+ * grid take the vectorised path.  The division of K among blocks depends on the
+ * sizes and the GPU alone and every sum has a fixed order, so equal values give
+ * equal bits, wherever X lies.  M == 0 or N == 0: no-op; K == 0: C = +0.
  * Only enqueues on `stream`, allocates nothing.
  */
 int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C, int64_t M, int64_t N,
