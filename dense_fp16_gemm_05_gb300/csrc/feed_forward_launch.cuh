@@ -1,6 +1,6 @@
 // feed_forward_launch.cuh -- arguments of the operators around a feed-forward
 // block that are not norms: FP8 quantisation (fp8_quantize.cu), dropout
-// (dropout.cu) and products with 4-bit weights (w4_quantize.cu, linear_w4.cu).
+// (dropout.cu) and products with 4-bit weights (w4_quantize.cu, linear_w4_g*.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -53,6 +53,9 @@ struct W4QuantArgs {
 };
 int launch_w4_quantize(const W4QuantArgs &a);
 
+// Which products go through tensor memory (both sides' times: linear_w4_launch.cuh).
+inline bool w4_by_tmem(int64_t M, int64_t N, int64_t K) { return M > 32 || (M > 16 && K % 8 == 0 && N * K >= 1 << 24); }
+
 struct W4LinearArgs {
     const void *X = nullptr, *Q = nullptr, *S = nullptr;
     const uint8_t *Z = nullptr;
@@ -62,7 +65,7 @@ struct W4LinearArgs {
     int sm_count = 0, device = 0;
     cudaStream_t stream = nullptr;
     unsigned long long *status = nullptr;       // device status word
-    int withhold = 0;                           // test hook (linear_w4_selftest_timeout)
+    int withhold = 0;                           // test hook (linear_w4_selftest_timeout, ..._few_...)
     uint64_t timeout_cycles = 0;                // 0: the normal budget
 };
 // One scale group width each.

@@ -1464,14 +1464,29 @@ extern "C" int linear_w4(const void *X, int type, const void *Q, const void *S, 
     return run_linear_w4(X, type, Q, S, Z, C, M, N, K, group, relu, stream, 0, 0);
 }
 
+static int w4_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C,
+                               int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles, void *stream)
+{
+    if (timeout_cycles < (1ull << 16) || timeout_cycles > (1ull << 32))
+        return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
+    return run_linear_w4(X, type, Q, S, Z, C, M, N, K, group, 0, stream, 1, timeout_cycles);
+}
+
 extern "C" int linear_w4_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z,
                                           void *C, int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles,
                                           void *stream)
 {
-    if (M <= 32 || N == 0 || K == 0) return reject(GEMM_ERR_INVALID_ARG, "the kernel with waits takes more than 32 rows of X");
-    if (timeout_cycles < (1ull << 16) || timeout_cycles > (1ull << 32))
-        return reject(GEMM_ERR_INVALID_ARG, "timeout_cycles outside 2^16 .. 2^32");
-    return run_linear_w4(X, type, Q, S, Z, C, M, N, K, group, 0, stream, 1, timeout_cycles);
+    if (M <= 32 || N == 0 || K == 0) return reject(GEMM_ERR_INVALID_ARG, "this hook takes more than 32 rows of X");
+    return w4_selftest_timeout(X, type, Q, S, Z, C, M, N, K, group, timeout_cycles, stream);
+}
+
+extern "C" int linear_w4_few_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z,
+                                              void *C, int64_t M, int64_t N, int64_t K, int group,
+                                              uint64_t timeout_cycles, void *stream)
+{
+    if (check_sizes(M, N, K, 0) != GEMM_OK || M > 32 || !w4_by_tmem(M, N, K))
+        return reject(GEMM_ERR_INVALID_ARG, "these sizes' kernel has no waits, or more than 32 rows of X");
+    return w4_selftest_timeout(X, type, Q, S, Z, C, M, N, K, group, timeout_cycles, stream);
 }
 
 extern "C" int gemm_fp8_launch_info(int64_t M, int64_t N, int64_t K, int *grid_ctas, int *tiles)

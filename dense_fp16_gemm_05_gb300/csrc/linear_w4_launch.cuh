@@ -36,8 +36,7 @@ int launch_w4(const W4LinearArgs &a)
     if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
     if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);
     if (p.M > 32) return launch_w4_tmem<T, 64, G>(p, a);
-    if (p.K % 8 == 0 && p.N * p.K >= 1 << 24) return launch_w4_tmem<T, 32, G>(p, a);
-    return launch_w4_kernel<T, 4, G>(p, a);
+    return w4_by_tmem(p.M, p.N, p.K) ? launch_w4_tmem<T, 32, G>(p, a) : launch_w4_kernel<T, 4, G>(p, a);
 }
 
 }  // namespace gemm_sm103

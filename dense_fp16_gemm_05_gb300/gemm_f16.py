@@ -148,6 +148,8 @@ def lib() -> ctypes.CDLL:
     L.linear_w4.restype = ci
     L.linear_w4_selftest_timeout.argtypes = [vp, ci, vp, vp, vp, vp, i64, i64, i64, ci, u64, vp]
     L.linear_w4_selftest_timeout.restype = ci
+    L.linear_w4_few_selftest_timeout.argtypes = L.linear_w4_selftest_timeout.argtypes
+    L.linear_w4_few_selftest_timeout.restype = ci
     pi = ctypes.POINTER(ctypes.c_int)
     L.gemm_fp8_launch_info.argtypes = [i64, i64, i64, pi, pi]
     L.gemm_fp8_launch_info.restype = ci

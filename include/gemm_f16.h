@@ -643,6 +643,13 @@ int linear_w4(const void *X, int type, const void *Q, const void *S, const uint8
 int linear_w4_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C,
                                int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles, void *stream);
 
+/*
+ * linear_w4_few_selftest_timeout -- the same for 17 to 32 rows of X beside a weight
+ * of at least 2^24 elements, K a multiple of 8: what that kernel takes of them.
+ */
+int linear_w4_few_selftest_timeout(const void *X, int type, const void *Q, const void *S, const uint8_t *Z, void *C,
+                                   int64_t M, int64_t N, int64_t K, int group, uint64_t timeout_cycles, void *stream);
+
 /* Launch geometry of gemm_fp8_block_scaled for this problem on the current
  * device: persistent grid in CTAs (CTA pairs over 256 x 256 output tiles) and
  * the number of tiles.  Either pointer may be NULL.  Launches nothing. */
