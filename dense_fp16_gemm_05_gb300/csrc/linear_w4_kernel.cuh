@@ -549,7 +549,7 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
         const bool fits = x_bytes <= room;
         for (const auto &d : kDivisions) {
             const int rw = d[0], kw = d[1];
-            if (kw > units) break;
+            if (kw > units) continue;
             const int rounds = ((p.strips + rw - 1) / rw + most - 1) / most, warps = rw * kw > 11 ? rw * kw : 11;
             const float group = static_cast<float>((units + kw - 1) / kw * warps) * (unit_cost / 16.0f) + end +
                                 static_cast<float>(rw * 4 * p.M);

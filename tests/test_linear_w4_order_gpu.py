@@ -28,3 +28,12 @@ def test_the_place_of_x_does_not_change_a_bit(g, M, N, K, group, xt):  # noqa: F
         there.copy_(X)
         assert torch.equal(g.linear_w4(there, *W, N=N, group=group), want), by
     assert g.check() == g.GEMM_OK
+
+
+# Seven units of 128 columns to a block, alone and in clusters: seven ways of a strip.
+@pytest.mark.parametrize("M,N,K", [(1, 300, 896), (8, 4096, 896), (16, 512, 880), (30, 1024, 850), (8, 2048, 1792),
+                                   (16, 1000, 3584), (5, 1024, 7168), (16, 200, 7050)])
+def test_seven_units_of_a_block(g, M, N, K):  # noqa: F811
+    W = packed(g, N, K, 64, True, torch.bfloat16, M + N + K)
+    X = torch.randn((M, K), device=DEV).bfloat16()
+    check(g, X, W, N, 64, relu=M % 2 == 0)
