@@ -55,8 +55,15 @@ __device__ __forceinline__ void rms_load(LnPack<T, V> &p, const T *src) { p.load
 // Elements above 10^18 have squares whose sum is beyond fp32: such rows' squares are
 // summed again, scaled down.  (A row that holds an infinity has rstd 0 either way.)
 constexpr float kDown = 0x1p-100f;
+// Squares of elements below 2^-63 are subnormal or vanish, which counts where eps does
+// not hide it: where mean and eps are below 2^-110 together, the row's elements (below
+// 2^-39 then, whatever its length) are scaled up and their squares summed again, which
+// stay above 2^-118 and below 2^102.  (The scaled elements in the place of the row's own
+// from there on, for rows whose rstd is beyond fp32, cost 8192 x 8192 to FP8 20 us.)
+constexpr float kUp = 0x1p90f, kSmall = 0x1p-110f;
 
 __device__ __forceinline__ bool rms_beyond(float sum) { return !(sum <= 3.4028235e38f); }
+__device__ __forceinline__ bool rms_below(float sum, float inv_dim, float eps) { return fmaf(sum, inv_dim, eps) < kSmall; }
 __device__ __forceinline__ float rms_rstd(float sum, float inv_dim, float eps) { return 1.0f / sqrtf(sum * inv_dim + eps); }
 
 // kShift: a row that is not whole 16-byte pieces is taken with the pieces that it lies
@@ -152,15 +159,18 @@ __global__ void __launch_bounds__(rms_threads(TPR)) rms_norm_fwd_kernel(RmsParam
     const float sum = ln_row_sum<TPR>(s.x + s.y, sh[0]);
     float rstd = rms_rstd(sum, p.inv_dim, p.eps);
     // The same answer for all lanes that take part in the sum.
-    if (TPR > 0 && TPR < 32 ? __any_sync(0xffffffffu, rms_beyond(sum)) : rms_beyond(sum)) {
+    const bool beyond = rms_beyond(sum), below = rms_below(sum, p.inv_dim, p.eps);
+    if (TPR > 0 && TPR < 32 ? __any_sync(0xffffffffu, beyond || below) : beyond || below) {
+        const float by = beyond ? kDown : kUp;
+        const float2 by2 = make_float2(by, by);
         s = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int m = 0; m < P; ++m) {
-            const float2 d = mul_f32x2(h[m], make_float2(kDown, kDown));
+            const float2 d = mul_f32x2(h[m], by2);
             s = fma_f32x2(d, d, s);
         }
-        const float down = ln_row_sum<TPR>(s.x + s.y, sh[1]);
-        if (rms_beyond(sum)) rstd = kDown * rms_rstd(down, p.inv_dim, p.eps * kDown * kDown);
+        const float again = ln_row_sum<TPR>(s.x + s.y, sh[1]);
+        if (beyond || below) rstd = by * rms_rstd(again, p.inv_dim, p.eps * by * by);
     }
     if (t == 0 && in && p.rstd) p.rstd[row] = rstd;
     const float2 rstd2 = make_float2(rstd, rstd);
@@ -276,15 +286,17 @@ __global__ void __launch_bounds__(1024) rms_norm_fwd_long(RmsParams<T, W> p)
         }
     const float sum = ln_row_sum<1024>(s, sh[0]);
     float rstd = rms_rstd(sum, p.inv_dim, p.eps);
-    if (rms_beyond(sum)) {
+    const bool beyond = rms_beyond(sum);
+    if (beyond || rms_below(sum, p.inv_dim, p.eps)) {
+        const float by = beyond ? kDown : kUp;
         s = 0.0f;
         for (int64_t k0 = first; k0 < p.dim; k0 += 32 * kFp8Block)
             for (int j = 0; j < 4; ++j) {
                 const int64_t k = k0 + j * 32 + lane;
-                const float d = k < p.dim ? ln_float(h[at + k]) * kDown : 0.0f;
+                const float d = k < p.dim ? ln_float(h[at + k]) * by : 0.0f;
                 s = fmaf(d, d, s);
             }
-        rstd = kDown * rms_rstd(ln_row_sum<1024>(s, sh[1]), p.inv_dim, p.eps * kDown * kDown);
+        rstd = by * rms_rstd(ln_row_sum<1024>(s, sh[1]), p.inv_dim, p.eps * by * by);
     }
     if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
     for (int64_t k0 = first; k0 < p.dim; k0 += 32 * kFp8Block) {

@@ -467,7 +467,8 @@ int layer_norm_bwd_selftest_timeout(const void *dY, const void *X, const float *
  *   H = X + R (X itself without a residual),  rstd = 1 / sqrt(sum H^2 / dim + eps),  Y = H rstd gamma
  *
  * in fp32.  H is rounded to X's type, the norm is taken of the rounded H, and Y
- * is rounded once to X's type.
+ * is rounded once to X's type.  Squares beyond fp32 or below it are no matter; an
+ * rstd beyond fp32 (eps = 0 and a root mean square below 2^-128) is an infinity.
  *
  *   X, R, H, Y  device pointers, (rows, dim) row-major, type xtype (enum
  *               gemm_f16_type).  R and H are both given or both NULL; H may be
