@@ -591,8 +591,8 @@ template <class T, class W, int V, int NV, int TPR>
 int launch_one(const RmsBwdParams<T, W> &p, cudaStream_t stream)
 {
     // Threads: those of the template, or the whole warps that NV packs each need.
-    const int packs = (p.dim + V - 1) / V;
-    const int BT = TPR > 0 ? rms_bwd_threads(TPR) : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    const int64_t packs = (static_cast<int64_t>(p.dim) + V - 1) / V;
+    const int BT = TPR > 0 ? rms_bwd_threads(TPR) : static_cast<int>(((packs + NV - 1) / NV + 31) / 32 * 32);
     constexpr int R = TPR > 0 ? rms_bwd_threads(TPR) / TPR : 1;
     const int st = launch(rms_norm_bwd_kernel<T, W, V, NV, TPR>, p, BT,
                           R > 1 ? static_cast<size_t>(R) * p.dim * sizeof(float) : 0, stream);
@@ -604,15 +604,15 @@ template <class T, class W, int NV, int TPR, bool kShift>
 int launch_ring(RmsBwdParams<T, W> p, int device, cudaStream_t stream, bool *done)
 {
     constexpr int V = kPiece<T>;
-    const int packs = (p.dim + (kShift ? 2 * V - 2 : V - 1)) / V;
-    const int threads = TPR > 0 ? TPR : ((packs + NV - 1) / NV + 31) / 32 * 32;
+    const int64_t packs = (static_cast<int64_t>(p.dim) + (kShift ? 2 * V - 2 : V - 1)) / V;
+    const int threads = TPR > 0 ? TPR : static_cast<int>(((packs + NV - 1) / NV + 31) / 32 * 32);
     // Blocks per SM: those of the launch bound, or more where they are small.
     const int fit_blocks = V * NV > 8 ? rms_ring_blocks(TPR, V * NV) : 1024 / threads;
     const int budget = (227 * 1024 - fit_blocks * 2048) / fit_blocks;
     p.arrays = p.dH ? 3 : 2;
     const int64_t stage = p.arrays * static_cast<int64_t>(rms_row_bytes<T, kShift>(p.dim));
     constexpr bool kGammaShared = kShift && sizeof(T) == 2 && TPR != -1024;
-    const int64_t gamma_bytes = kGammaShared ? (p.dim + 2 * V - 1) / V * V * static_cast<int64_t>(sizeof(W)) : 0;
+    const int64_t gamma_bytes = kGammaShared ? (static_cast<int64_t>(p.dim) + 2 * V - 1) / V * V * static_cast<int64_t>(sizeof(W)) : 0;
     const int64_t fit = (budget - gamma_bytes) / stage;
     *done = fit >= 1;
     if (fit < 1) return GEMM_OK;
@@ -658,7 +658,7 @@ template <class T, class W, bool kShift>
 int launch_rows(const RmsBwdParams<T, W> &p, int device, cudaStream_t stream)
 {
     constexpr int V = kPiece<T>, N = 8 / V;   // packs of 8 elements
-    const int packs = (p.dim + (kShift ? 2 * V - 2 : V - 1)) / V;
+    const int64_t packs = (static_cast<int64_t>(p.dim) + (kShift ? 2 * V - 2 : V - 1)) / V;
     bool done = false;
     int st = GEMM_OK;
     // Thread counts as for layer norm: rows that fill a power of 2 of threads, then
@@ -682,7 +682,7 @@ int launch_rows(const RmsBwdParams<T, W> &p, int device, cudaStream_t stream)
 template <class T, class W, int V>
 int launch_short(const RmsBwdParams<T, W> &p, cudaStream_t stream)
 {
-    const int packs = (p.dim + V - 1) / V;
+    const int64_t packs = (static_cast<int64_t>(p.dim) + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
     if constexpr (V > 2) {
         // Short rows (a head's width) share a warp.

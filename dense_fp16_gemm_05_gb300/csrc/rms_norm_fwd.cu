@@ -332,8 +332,8 @@ int launch_one(const RmsParams<T, W> &p, cudaStream_t stream)
 {
     // Threads: those of the template, or the whole warps that NV packs each need.
     constexpr int C = rms_run(TPR, V, kFp8);
-    const int runs = (p.dim + (kShift ? V - 1 : 0) + V * C - 1) / (V * C);   // C packs each
-    const int BT = TPR > 0 ? rms_threads(TPR) : ((runs + NV / C - 1) / (NV / C) + 31) / 32 * 32;
+    const int64_t runs = (static_cast<int64_t>(p.dim) + (kShift ? V - 1 : 0) + V * C - 1) / (V * C);   // C packs each
+    const int BT = TPR > 0 ? rms_threads(TPR) : static_cast<int>(((runs + NV / C - 1) / (NV / C) + 31) / 32 * 32);
     constexpr int R = TPR > 0 ? rms_threads(TPR) / TPR : 1;
     return ln_launch(rms_norm_fwd_kernel<T, W, V, NV, TPR, kFp8, kShift>,
                      dim3(static_cast<unsigned>((p.rows + R - 1) / R), 1, 1), BT, stream, p);
@@ -342,7 +342,7 @@ int launch_one(const RmsParams<T, W> &p, cudaStream_t stream)
 template <class T, class W, bool kFp8, int V>
 int launch_packs(const RmsParams<T, W> &p, cudaStream_t stream)
 {
-    const int packs = (p.dim + V - 1) / V;
+    const int64_t packs = (static_cast<int64_t>(p.dim) + V - 1) / V;
     constexpr int N = 8 / V;   // packs of 8 elements
     if constexpr (V > 2) {
         if (packs <= 8 * N) return launch_one<T, W, kFp8, V, N, 8>(p, stream);
@@ -400,7 +400,7 @@ int forward(const RmsNormArgs &a)
         const uintptr_t x = reinterpret_cast<uintptr_t>(a.X), y = reinterpret_cast<uintptr_t>(a.Y);
         const uintptr_t r = a.R ? reinterpret_cast<uintptr_t>(a.R) : x, h = a.R ? reinterpret_cast<uintptr_t>(a.H) : x;
         constexpr int N = 8 / V;   // packs of 8 elements
-        const int packs = (p.dim + 2 * V - 2) / V;
+        const int64_t packs = (static_cast<int64_t>(p.dim) + 2 * V - 2) / V;
         if ((((x ^ y) | (x ^ r) | (x ^ h)) & 15u) == 0 && p.dim >= (pack == 1 ? 768 : 2560) &&
             p.rows * p.dim >= (sizeof(T) == 2 ? 1 << 22 : 1 << 23)) {
             if (packs <= 128 * 2 * N) return launch_one<T, W, false, V, 2 * N, -128, true>(p, a.stream);
