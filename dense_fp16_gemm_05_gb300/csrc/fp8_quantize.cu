@@ -145,23 +145,23 @@ __global__ void __launch_bounds__(256) fp8_quantize_square(QuantParams<T> p)
     b.by_way([&](auto way) {
         constexpr int W8 = decltype(way)::value;
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int64_t row = row0 + r * RS, k = k0 + j * L * V;
-            if (row >= p.rows || k >= p.K) continue;
-            uint8_t *q = p.Q + row * p.K + k;
-            if constexpr (V == 1) {
-                *q = static_cast<uint8_t>(b.template codes<W8>(make_float2(x[r][j][0], 0.0f)));
-            } else {
-                uint32_t c[V / 4];
+            for (int j = 0; j < J; ++j) {
+                const int64_t row = row0 + r * RS, k = k0 + j * L * V;
+                if (row >= p.rows || k >= p.K) continue;
+                uint8_t *q = p.Q + row * p.K + k;
+                if constexpr (V == 1) {
+                    *q = static_cast<uint8_t>(b.template codes<W8>(make_float2(x[r][j][0], 0.0f)));
+                } else {
+                    uint32_t c[V / 4];
 #pragma unroll
-                for (int e = 0; e < V / 4; ++e)
-                    c[e] = b.template codes<W8>(x[r][j].pair(2 * e)) | (b.template codes<W8>(x[r][j].pair(2 * e + 1)) << 16);
-                if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
-                else *reinterpret_cast<uint32_t *>(q) = c[0];
+                    for (int e = 0; e < V / 4; ++e)
+                        c[e] = b.template codes<W8>(x[r][j].pair(2 * e)) | (b.template codes<W8>(x[r][j].pair(2 * e + 1)) << 16);
+                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
+                    else *reinterpret_cast<uint32_t *>(q) = c[0];
+                }
             }
-        }
     });
 }
 

@@ -121,7 +121,8 @@ struct W4Codes<__half> {
     {
         return odd ? 0xD400D400u + z * 0x00100010u : 0xE400E400u + z * 0x00010001u;
     }
-    // 1024 + q and, one nibble further up, 1024 + 16 q, times 1/16: all exact.
+    // 1024 + q and, one nibble further up, 1024 + 16 q, times 1/16: all exact (codes put
+    // into the significand of 1024: Y. J. Kim, R. Henry, R. Fahim, H. H. Awadalla, SustaiNLP 2022).
     static __device__ __forceinline__ void operands(uint32_t w, uint32_t lo, uint32_t hi, uint32_t (&a)[4])
     {
 #pragma unroll
@@ -526,14 +527,15 @@ int launch_w4_kernel(W4Params<T> p, const W4LinearArgs &a)
     static W4Clusters clusters[kMaxDevices];
     if (!w4_prepare(kern, kW4Threads, kW4Budget, a, prepared, clusters)) return GEMM_ERR_LAUNCH;
     // The division of the work that costs least by this count of nanoseconds, fitted to
-    // whole calls of 18 shapes (up to 32 x 16384 x 8192) under every division (its
-    // choice was within a tenth of the best of each, but one of the smallest): a
-    // unit of each of a block's sixteen warps takes 450 with 8 rows of X, 1030 with 32,
-    // and with fewer warps as much less, down to eleven; a group of strips ends with 500,
-    // more among the blocks of a cluster, and a quarter for each output; X comes with 60
-    // bytes each, 20 where its rows cannot lie on the 16-byte grid, and in chunks half
-    // hidden.  (Where they could and do not is not counted, so that the order of the sums
-    // does not go by X's address.)
+    // whole calls under every division; of 25 other shapes (1 to 32 rows, up to
+    // 16384 x 8192) it picks the best of all in 23, and in the others one within a
+    // twentieth of it (4 x 1024 x 8192 4.8 us of 4.6).  A
+    // unit of each of a block's sixteen warps takes 450 with 8 rows of X, 650 with 16,
+    // 1030 with 32, and with fewer warps as much less, down to eleven; a group of strips
+    // ends with 500, more among the blocks of a cluster, and a quarter for each output; X
+    // comes with 60 bytes each, 20 where its rows cannot lie on the 16-byte grid, and in
+    // chunks half hidden.  (Where they could and do not is not counted, so that the order
+    // of the sums does not go by X's address.)
     const int64_t room = kW4Budget - Shape::RING - 2 * Shape::SUMS;   // for a kept X
     const float unit_cost = NT == 1 ? 450.0f : (NT == 2 ? 650.0f : 1030.0f);
     static constexpr uint8_t kDivisions[][2] = {{16, 1}, {15, 1}, {14, 1}, {8, 2}, {7, 2}, {6, 2},

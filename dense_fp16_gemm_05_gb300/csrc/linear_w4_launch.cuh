@@ -28,11 +28,11 @@ int launch_w4(const W4LinearArgs &a)
     // By mma.sync, 8 rows of X to an instruction, or from tensor memory, whose MMAs take up
     // to 64 in the time of 8: 64 x 8192 x 8192 39 and 26 us, 40 x 4096 x 4096 28 and 11.  Up
     // to 32 rows only if the weight is large and X's rows can lie on the 16-byte grid
-    // (32 x 8192 x 8192 22.3 and 20.0 us, 24 x 4096 x 4096 9.9 and 9.1, but 24 x 1024 x 8192
-    // 8.7 and 9.5, 32 x 16383 x 8191 57 and 65), up to 16 not at all (16 x 8192 x 8192 14.5
-    // and 16.8).  By K and not by X's address, so that equal values give equal bits wherever
-    // X lies: one element off the grid 32 x 16384 x 8192 takes 54 and 64 us, 32 x 4096 x 11008
-    // 33 and 21.
+    // (32 x 8192 x 8192 23.6 and 22.8 us, 24 x 4096 x 4096 10.3 and 9.4, 32 x 4096 x 11008 29.0
+    // and 17.2, but 24 x 1024 x 8192 8.7 and 9.8, 24 x 2048 x 4096 7.5 and 8.7, 32 x 16383 x 8191
+    // 53.5 and 62.7), up to 16 not at all (16 x 8192 x 8192 14.5 and 16.8).  By K and not by X's
+    // address, so that equal values give equal bits wherever X lies: one element off the grid
+    // 32 x 16384 x 8192 takes 54 and 64 us, 32 x 4096 x 11008 33 and 21.
     if (p.M <= 8) return launch_w4_kernel<T, 1, G>(p, a);
     if (p.M <= 16) return launch_w4_kernel<T, 2, G>(p, a);
     if (p.M > 32) return launch_w4_tmem<T, 64, G>(p, a);

@@ -25,12 +25,12 @@
 //
 // Every warp's code between two waits runs alone on its scheduler for most of the time:
 // with a warp per strip for all units a unit took 1400 cycles, of which W's were 1250.
-// With two it is bound by instructions (74 % of the issue slots at 64 x 16384 x 8192):
+// With two it is bound by instructions (72 % of the issue slots at 64 x 16384 x 8192):
 // the codes' conversion and X's way into shared memory, again for every 128 rows of W.
 // 64 x 16384 x 8192 bf16 50 us (87 by mma.sync), 64 x 4096 x 4096 fp16 11.1 us (32),
 // 64 x 2048 x 2048 7.7 us (12.6), 64 x 1024 x 8192 bf16 12 us (27),
-// 32 x 16384 x 8192 40 us (44).  With 16 rows of X and a 16-column operand it takes longer
-// than mma.sync (33 us, 29).
+// 32 x 16384 x 8192 40 us (41), 32 x 4096 x 11008 17 us (29).  With 16 rows of X and a
+// 16-column operand it takes longer than mma.sync (33 us, 29).
 //
 // K may be divided over the blocks of a cluster, whose sums are added through
 // distributed shared memory.  Every wait is bounded: on expiry the site is recorded in

@@ -504,8 +504,8 @@ int rms_norm_fp8(const void *X, const void *R, const void *gamma, void *H, void 
  *
  * in fp32, each output rounded once; dX is the gradient of X and of R alike.
  * Sums over rows are taken in a fixed order (equal calls give equal bits on one
- * GPU model): a block's rows in fp32, then the blocks' sums without loss, rounded
- * once.
+ * GPU model; how the buffers lie on the 16-byte grid is part of a call): a block's
+ * rows in fp32, then the blocks' sums without loss, rounded once.
  *
  *   dY, H, gamma, rstd  as given to and kept by rms_norm_fwd (H: X itself where
  *                  there was no residual)
@@ -572,7 +572,7 @@ int fp8_quantize(const void *X, int type, void *Q, void *S, int64_t rows, int64_
  *               it draws another mask at every replay
  *
  * A dropped element's value does not matter (an infinity or NaN of X is dropped
- * too).  n == 0: no-op.  Only enqueues on `stream`.
+ * too); a -0 of R comes out as +0 there.  n == 0: no-op.  Only enqueues on `stream`.
  */
 int dropout_philox(const void *X, const void *R, void *Y, int64_t n, int type, double p, uint64_t seed,
                    uint64_t offset, const void *offset_ptr, void *stream);
