@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define GEMM_F16_VERSION 10
+#define GEMM_F16_VERSION 11
 
 /* Return codes.  0 is success; every error is negative. */
 enum gemm_f16_status {
